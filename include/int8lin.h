@@ -289,6 +289,134 @@ int int8_linear_backward_input_int8(const void* G, int dtype, int64_t M, int64_t
 int int8_linear_backward_weight(const void* G, const void* A, int dtype, int64_t M, int64_t N, int64_t K,
                                 void* grad_W, void* stream);
 
+/* ------------------------------------------------------------------------ *
+ * Low-rank adapters of many requests beside a shared projection (lit-gpt PR
+ * #275 fine-tunes low-rank adapters beside frozen quantized weights). The T
+ * token rows lie in n_seg consecutive segments (requests or sequences):
+ * segment j holds rows seg_offsets[j] .. seg_offsets[j + 1] - 1 and uses
+ * adapter seg_adapter[j]. For a row t of adapter a, with factor s[a]:
+ *   V[t, r]   = sum_k A[a, r, k] X[t, k]                           (fp32)
+ *   out[t, n] = D(base[t, n] + s[a] sum_r B[a, n, r] V[t, r])      (fp32 accumulate)
+ * and the gradients
+ *   dV[t, r]     = s[a] sum_n B[a, n, r] G[t, n]                   (fp32)
+ *   grad_X[t, k] = D(base_grad[t, k] + sum_r A[a, r, k] dV[t, r])
+ *   grad_A[a, r, k] = D(sum over the rows t of adapter a of dV[t, r] X[t, k])
+ *   grad_B[a, n, r] = D(s[a] sum over the rows t of adapter a of G[t, n] V[t, r])
+ * V and dV are never rounded below fp32's 24 bits except for the matrix
+ * products with 16-bit operands, where they enter as the sum of two values of
+ * that type (16 bits of mantissa or more).
+ *   X: T x K, out / base: T x N, A: n_adapters x R x K, B: n_adapters x N x R,
+ *   G: T x N, grad_X / base_grad: T x K, all of `dtype`; grad_A, grad_B: as A
+ *   and B; scaling: n_adapters fp32; V: T x R fp32.
+ *   seg_offsets: n_seg + 1 int32 on the device, non-decreasing from 0 to T
+ *   (the first and last are taken as 0 and T; may be NULL when n_seg <= 1).
+ *   Contents that are not non-decreasing give undefined values in the outputs
+ *   but no access outside the tensors. seg_adapter: n_seg int32 on the device,
+ *   NULL for segment j using adapter j. A segment whose adapter lies outside
+ *   [0, n_adapters) has none: out = D(base), V = 0, grad_X = D(base_grad). Empty
+ *   segments are fine; one token per segment is the form for serving single
+ *   tokens.
+ *   base, base_grad: NULL for 0; may be the output itself (updated in place).
+ *   Adapters of different ranks are stored with the largest, padded with zeros.
+ * Forward: V may be NULL (kept for the backward otherwise). Backward: grad_X,
+ * grad_A and grad_B may each be NULL (not computed); V is the forward's. An
+ * adapter without rows gets a zero gradient.
+ * R <= I8L_LORA_MAX_RANK, K and N <= I8L_MAX_COLS, n_adapters <= 65535,
+ * T + n_seg <= 2^30, else I8L_ESHAPE.
+ * ------------------------------------------------------------------------ */
+#define I8L_LORA_MAX_RANK 128
+
+size_t int8_lora_forward_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t n_seg);
+
+int int8_lora_forward(const void* X, int dtype, int64_t T, int64_t K, const void* A, const void* B,
+                      const float* scaling, int64_t n_adapters, int64_t R, int64_t N, const int32_t* seg_offsets,
+                      const int32_t* seg_adapter, int64_t n_seg, const void* base, void* out, float* V,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+size_t int8_lora_backward_workspace_bytes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t n_adapters,
+                                          int64_t n_seg);
+
+int int8_lora_backward(const void* G, const void* X, const float* V, int dtype, int64_t T, int64_t K, const void* A,
+                       const void* B, const float* scaling, int64_t n_adapters, int64_t R, int64_t N,
+                       const int32_t* seg_offsets, const int32_t* seg_adapter, int64_t n_seg, const void* base_grad,
+                       void* grad_X, void* grad_A, void* grad_B, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * Layer norm in front of a projection, and its gradient. Per row of X (T x C):
+ *   mean = sum x / C, rstd = 1 / sqrt(sum (x - mean)^2 / C + eps)      (fp32)
+ *   out  = D((x - mean) rstd w + b)
+ * and with h = (x - mean) rstd, u = G w:
+ *   grad_X = D(rstd (u - mean(u) - h mean(u h)))
+ *   grad_w = Dw(sum over rows of G h), grad_b = Dw(sum over rows of G)
+ * X, out, G, grad_X: T x C of `dtype`; weight, bias and their gradients: C of
+ * `weight_dtype`, which is `dtype` or I8L_F32. bias may be NULL. mean, rstd: T
+ * fp32, written by the forward (each may be NULL) and read by the backward.
+ * grad_X, grad_weight and grad_bias may each be NULL (not computed). out may be
+ * X; grad_X may be G unless a weight or bias gradient is asked for too. T = 0
+ * writes zero weight gradients. C <= I8L_MAX_COLS, else I8L_ESHAPE; an
+ * eps that is negative or NaN is I8L_EINVAL.
+ * ------------------------------------------------------------------------ */
+int int8_layer_norm_forward(const void* X, int dtype, int64_t T, int64_t C, const void* weight, const void* bias,
+                            int weight_dtype, float eps, void* out, float* mean, float* rstd, void* stream);
+
+size_t int8_layer_norm_backward_workspace_bytes(int64_t T, int64_t C);
+
+int int8_layer_norm_backward(const void* G, const void* X, int dtype, int64_t T, int64_t C, const float* mean,
+                             const float* rstd, const void* weight, int weight_dtype, void* grad_X,
+                             void* grad_weight, void* grad_bias, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * AdamW over many tensors in one launch, states in 32 or in 8 bits (lit-gpt PR
+ * #275 reports its runs with an 8-bit optimizer). Per value, with g' = c g
+ * (c = *grad_scale, 1 without):
+ *   m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   w = w (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * every operation rounded to fp32. w is `master` where that is non-NULL (then
+ * p = D(w)), else p itself.
+ * state_bits 32: m, v are n fp32. state_bits 8: m and v are n bytes of e4m3
+ * codes in blocks of 256 values from the tensor's start, m_scale and v_scale
+ * ceil(n / 256) fp32, one scale per block: m = code * scale, and v's codes hold
+ * its root, sqrt(v) = code * scale. The scale is the least power of two, 2^-126
+ * or more, with the block's largest magnitude / scale <= 448; codes round to
+ * nearest even, and a sqrt(v) over 0 keeps at least the smallest code over 0
+ * (2^-9). The step uses m and v before that rounding. A block with an infinity
+ * or NaN in it gets the scale NaN. All-zero bytes and scales are the state
+ * before the first step.
+ * The tensors are described on the host, checked and laid out once:
+ *   int8_adamw_table_bytes: size of the table of these tensors (0: invalid)
+ *   int8_adamw_table_fill: checks them, writes the table to host memory and the
+ *     number of workgroups to *chunks. The caller copies it to device memory
+ *     (16-byte aligned) and keeps it, and the tensors, while steps use it.
+ *   int8_adamw_step: one step of every tensor in the table; `count` and
+ *     `chunks` as they were filled in. step >= 1 counts the steps, this one
+ *     included. grad_scale, found_inf: device fp32, or NULL; *found_inf != 0
+ *     leaves everything as it is.
+ * A beta outside [0, 1), or a negative or non-finite lr, eps or weight_decay is
+ * I8L_EINVAL. Each value is read and written by one thread: no two tensors
+ * may overlap.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  void* p;           /* n of dtype */
+  const void* g;     /* n of dtype */
+  void* m;
+  void* v;
+  float* m_scale;    /* state_bits 8 only */
+  float* v_scale;    /* state_bits 8 only */
+  float* master;     /* n fp32 or NULL */
+  int64_t n;
+  int32_t dtype;
+  int32_t state_bits;
+} i8l_adamw_tensor;
+
+size_t int8_adamw_table_bytes(const i8l_adamw_tensor* tensors, int64_t count);
+int int8_adamw_table_fill(const i8l_adamw_tensor* tensors, int64_t count, void* table, size_t table_bytes,
+                          int64_t* chunks);
+int int8_adamw_step(const void* table, int64_t count, int64_t chunks, double lr, double beta1, double beta2,
+                    double eps, double weight_decay, int64_t step, const float* grad_scale, const float* found_inf,
+                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,6 +20,7 @@ import torch
 
 from . import _lib
 from ._lib import (I8L_BF16, I8L_F16, I8L_F32, I8L_MAX_K, Int8LinError, check, lib)
+from ._tensors import DTYPE_CODE, _check_out, _code, _dev, _empty, _stream
 
 __all__ = [
     "int8_quantize_rowwise", "int8_linear_forward", "int8_linear_backward_input", "quantize_weight",
@@ -28,41 +29,10 @@ __all__ = [
     "outlier_flags_buffer", "silu_outlier_flags", "int8_linear_forward_flagged",
     "Int8LinearFunction", "Int8Linear", "Int8LinError", "forward_workspace", "forward_layout",
     "forward_check", "default_cap", "int8_linear_forward_noalloc", "DTYPE_CODE", "I8L_MAX_K",
+    "lora_forward", "lora_backward", "Int8LoraFunction", "Int8LoraLinear", "I8L_LORA_MAX_RANK",
+    "layer_norm_forward", "layer_norm_backward", "LayerNormFunction", "LayerNorm",
+    "AdamWPlan", "AdamW", "adamw_state",
 ]
-
-DTYPE_CODE = {torch.float32: I8L_F32, torch.float16: I8L_F16, torch.bfloat16: I8L_BF16}
-
-
-def _code(t: torch.Tensor) -> int:
-    try:
-        return DTYPE_CODE[t.dtype]
-    except KeyError:
-        raise TypeError(f"unsupported dtype {t.dtype}; expected float32, float16 or bfloat16") from None
-
-
-def _dev(t: Optional[torch.Tensor], name: str) -> int:
-    if t is None:
-        return 0
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() if t.numel() > 0 else 0
-
-
-def _check_out(t: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype, name: str) -> None:
-    """Caller-provided result tensors must have exactly the size the kernels write."""
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-
-
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _empty(shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device)
-
 
 # ----------------------------------------------------------------------------
 # quantizer
@@ -453,3 +423,8 @@ class Int8LinearTrainable(torch.nn.Module):
 
     def forward(self, x):
         return Int8LinearTrainableFunction.apply(x, self.weight, self.bias, self.threshold)
+
+
+from .lora import I8L_LORA_MAX_RANK, Int8LoraFunction, Int8LoraLinear, lora_backward, lora_forward  # noqa: E402
+from .norm import LayerNorm, LayerNormFunction, layer_norm_backward, layer_norm_forward  # noqa: E402
+from .optim import AdamW, AdamWPlan, adamw_state  # noqa: E402

@@ -17,15 +17,22 @@ I8L_ESCRATCH = -7
 I8L_NOALLOC_SCRATCH_BYTES = 64 << 20
 I8L_MAX_K = 133144
 I8L_MAX_COLS = 262144
+I8L_LORA_MAX_RANK = 128
 
 # every symbol the header declares, with (restype, argtypes)
 _vp, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
 _int = ctypes.c_int
+_f64 = ctypes.c_double
 
 
 class ForwardLayout(ctypes.Structure):
     _fields_ = [("count", _sz), ("idx", _sz), ("scale", _sz), ("codes", _sz), ("sub", _sz), ("wsub", _sz),
                 ("total", _sz)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("p", _vp), ("g", _vp), ("m", _vp), ("v", _vp), ("m_scale", _vp), ("v_scale", _vp), ("master", _vp),
+                ("n", _i64), ("dtype", _i32), ("state_bits", _i32)]
 
 
 SIGNATURES = {
@@ -52,6 +59,18 @@ SIGNATURES = {
     "int8_silu_outlier_flags": (_int, [_vp, _int, _i64, _i64, _f32, _vp, _vp, _sz, _vp]),
     "int8_linear_forward_flagged": (_int, [_vp, _int, _i64, _i64, _vp, _sz, _vp, _vp, _i64, _vp, _i32, _vp, _vp,
                                            _vp, _sz, _vp]),
+    "int8_lora_forward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "int8_lora_forward": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp,
+                                 _vp, _sz, _vp]),
+    "int8_lora_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64]),
+    "int8_lora_backward": (_int, [_vp, _vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp,
+                                  _vp, _vp, _vp, _vp, _sz, _vp]),
+    "int8_layer_norm_forward": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _int, _f32, _vp, _vp, _vp, _vp]),
+    "int8_layer_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "int8_layer_norm_backward": (_int, [_vp, _vp, _int, _i64, _i64, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "int8_adamw_table_bytes": (_sz, [ctypes.POINTER(AdamWTensor), _i64]),
+    "int8_adamw_table_fill": (_int, [ctypes.POINTER(AdamWTensor), _i64, _vp, _sz, ctypes.POINTER(_i64)]),
+    "int8_adamw_step": (_int, [_vp, _i64, _i64, _f64, _f64, _f64, _f64, _f64, _i64, _vp, _vp, _vp]),
 }
 
 

@@ -70,4 +70,55 @@ hipError_t launch_gemm_wgrad(int dt, const void* G, const void* A, int M, int N,
 size_t grad_bias_partial_floats(int M, int N);
 hipError_t launch_grad_bias(int dt, const void* G, int M, int N, float* partial, void* grad_bias, hipStream_t st);
 
+// Adapters beside a shared projection: the tokens 0 .. T - 1 lie in n_seg
+// consecutive segments; segment s holds tokens off[s] .. off[s + 1] - 1 (off[0]
+// and off[n_seg] are taken as 0 and T) of adapter ids[s] (s itself when ids is
+// NULL; none when outside [0, n_adapters)).
+struct LoraSegs {
+  const int32_t* off;
+  const int32_t* ids;
+  int n_seg, n_adapters;
+};
+size_t lora_forward_floats(int T, int K, int N, int R, int n_seg);
+size_t lora_backward_floats(int T, int K, int N, int R, int n_adapters, int n_seg);
+// T >= 1. V (T x R fp32) or NULL; ws: lora_forward_floats() floats.
+hipError_t launch_lora_forward(int dt, const void* X, int T, int K, const void* A, const void* B,
+                               const float* scaling, int R, int N, const LoraSegs& S, const void* base, void* out,
+                               float* V, float* ws, hipStream_t st);
+hipError_t launch_lora_backward(int dt, const void* G, const void* X, const float* V, int T, int K, const void* A,
+                                const void* B, const float* scaling, int R, int N, const LoraSegs& S,
+                                const void* base_grad, void* gX, void* gA, void* gB, float* ws, hipStream_t st);
+
+// Layer norm, T x C of dt, weight and bias of wdt (dt or fp32).
+hipError_t launch_norm_forward(int dt, int wdt, const void* X, int T, int C, const void* w, const void* b, float eps,
+                               void* Y, float* mean, float* rstd, hipStream_t st);
+size_t norm_backward_floats(int T, int C);
+hipError_t launch_norm_backward(int dt, int wdt, const void* G, const void* X, const float* mean, const float* rstd,
+                                int T, int C, const void* w, void* gX, void* gw, void* gb, float* ws,
+                                hipStream_t st);
+
+// AdamW over a table of tensors: chunk c is values [chunk * adamw_chunk(), ...)
+// of its tensor, one workgroup each.
+struct AdamWTensor {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  float* master;
+  int64_t n;
+  int32_t dtype, bits;
+  int32_t vec, pad;   // vec: every pointer on a 16-byte border (codes 8)
+};
+struct AdamWChunk {
+  int32_t tensor, chunk;
+};
+struct AdamWScalars {
+  float beta1, one_beta1, beta2, one_beta2, keep, step_size, inv_root_bc2, eps;
+};
+int adamw_chunk();
+hipError_t launch_adamw(const AdamWTensor* tensors, const AdamWChunk* chunks, int64_t n_chunks, const AdamWScalars& h,
+                        const float* grad_scale, const float* found_inf, hipStream_t st);
+
 }  // namespace i8l

@@ -1,0 +1,173 @@
+"""AdamW over many tensors in one launch, with states in 32 or in 8 bits:
+binding of int8_adamw_* (include/int8lin.h) and an optimizer.
+
+8-bit states are float8_e4m3fn tensors with one power-of-two fp32 scale for
+each block of 256 values: m = code * scale, and the second tensor holds the
+root, sqrt(v) = code * scale.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Sequence, Tuple
+
+import torch
+
+from ._lib import AdamWTensor, check, lib
+from ._tensors import DTYPE_CODE, _code, _dev, _stream
+
+BLOCK = 256   # values that share a scale
+
+
+def adamw_state(p: torch.Tensor, bits: int = 32, master: bool = False) -> dict:
+    """The state of one parameter before the first step: m, v, for 8 bits their scales, and the fp32 master copy
+    if asked for."""
+    if bits not in (8, 32):
+        raise ValueError("state bits must be 8 or 32")
+    n, dev = p.numel(), p.device
+    if bits == 32:
+        s = {"m": torch.zeros(p.shape, dtype=torch.float32, device=dev),
+             "v": torch.zeros(p.shape, dtype=torch.float32, device=dev)}
+    else:
+        blocks = -(-n // BLOCK)
+        s = {"m": torch.zeros(p.shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn),
+             "v": torch.zeros(p.shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn),
+             "m_scale": torch.zeros(blocks, dtype=torch.float32, device=dev),
+             "v_scale": torch.zeros(blocks, dtype=torch.float32, device=dev)}
+    if master:
+        s["master"] = p.detach().to(torch.float32, copy=True)
+    return s
+
+
+class AdamWPlan:
+    """The tensors of an AdamW step, checked and laid out on the device once; `step` is one launch.
+
+    params, grads: tensors of one dtype each pair (fp32, fp16 or bf16); m, v:
+    their states, all fp32 or all float8_e4m3fn (then with m_scale and v_scale);
+    master: fp32 copies or None. The plan reads and writes these very tensors
+    at every step (grads have to be filled in place) and keeps them alive."""
+
+    def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], m: Sequence[torch.Tensor],
+                 v: Sequence[torch.Tensor], m_scale: Optional[Sequence[torch.Tensor]] = None,
+                 v_scale: Optional[Sequence[torch.Tensor]] = None,
+                 master: Optional[Sequence[torch.Tensor]] = None):
+        n = len(params)
+        lists = dict(grads=grads, m=m, v=v, m_scale=m_scale, v_scale=v_scale, master=master)
+        for name, x in lists.items():
+            if x is not None and len(x) != n:
+                raise ValueError(f"{name} must have one tensor for each of the {n} parameters")
+        if n == 0:
+            raise ValueError("no parameters")
+        self.device = params[0].device
+        self._keep = [list(params)] + [list(x) for x in lists.values() if x is not None]
+        self.table, self.count, self.chunks = None, n, 0
+        arr = (AdamWTensor * n)()
+        for i, p in enumerate(params):
+            size = p.numel()
+            low = m[i].dtype == torch.float8_e4m3fn
+            state = torch.float8_e4m3fn if low else torch.float32
+            if p.dtype not in DTYPE_CODE:
+                raise TypeError(f"unsupported dtype {p.dtype}; expected float32, float16 or bfloat16")
+            if grads[i].dtype != p.dtype or grads[i].numel() != size:
+                raise ValueError(f"grads[{i}] must have its parameter's size and dtype")
+            if m[i].dtype != state or v[i].dtype != state or m[i].numel() != size or v[i].numel() != size:
+                raise ValueError(f"m[{i}] and v[{i}] must both be float32 or both float8_e4m3fn, of the "
+                                 "parameter's size")
+            if low:
+                for name, x in (("m_scale", m_scale), ("v_scale", v_scale)):
+                    if x is None or x[i].dtype != torch.float32 or x[i].numel() != -(-size // BLOCK):
+                        raise ValueError(f"{name}[{i}] must be float32 with one value for each {BLOCK}")
+            if master is not None and (master[i].dtype != torch.float32 or master[i].numel() != size):
+                raise ValueError(f"master[{i}] must be float32 of the parameter's size")
+            row = [x for x in (p, grads[i], m[i], v[i], m_scale[i] if low else None, v_scale[i] if low else None,
+                               master[i] if master is not None else None)]
+            if any(x is not None and x.device != self.device for x in row):
+                raise ValueError("all tensors of a plan must be on one GPU")
+            names = ("params", "grads", "m", "v", "m_scale", "v_scale", "master")
+            ptr = [_dev(x, f"{k}[{i}]") or None for x, k in zip(row, names)]
+            arr[i] = AdamWTensor(*ptr, size, _code(p), 8 if low else 32)
+        need = lib.int8_adamw_table_bytes(arr, n)
+        host = torch.zeros(max(need, 1), dtype=torch.uint8)
+        chunks = ctypes.c_int64(0)
+        check(lib.int8_adamw_table_fill(arr, n, host.data_ptr(), need, ctypes.byref(chunks)), "int8_adamw_table_fill")
+        self.chunks = chunks.value
+        self.table = host.to(self.device)
+
+    def step(self, step: int, lr: float, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
+             weight_decay: float = 0.01, grad_scale: Optional[torch.Tensor] = None,
+             found_inf: Optional[torch.Tensor] = None) -> None:
+        """Step number `step` (from 1). grad_scale: fp32 GPU scalar that multiplies the gradients; found_inf: fp32 GPU
+        scalar, anything but 0 leaves all tensors as they are (the caller's step count goes on)."""
+        for name, x in (("grad_scale", grad_scale), ("found_inf", found_inf)):
+            if x is not None and (x.dtype != torch.float32 or x.numel() != 1 or x.device != self.device):
+                raise ValueError(f"{name} must be one float32 value on {self.device}")
+        check(lib.int8_adamw_step(self.table.data_ptr(), self.count, self.chunks, lr, betas[0], betas[1], eps,
+                                  weight_decay, step, 0 if grad_scale is None else grad_scale.data_ptr(),
+                                  0 if found_inf is None else found_inf.data_ptr(), _stream(self.device)),
+              "int8_adamw_step")
+
+
+class AdamW(torch.optim.Optimizer):
+    """AdamW with every parameter of a group updated in one launch.
+
+    state_bits: 32 or 8; master: keep fp32 copies of fp16 / bf16 parameters.
+    The plan of a group is laid out again whenever a gradient or parameter has
+    moved (gradients kept in place with zero_grad(set_to_none=False) never do).
+    Parameters and gradients have to be contiguous."""
+
+    def __init__(self, params, lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 0.01, state_bits: int = 32, master: bool = False):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits,
+                                      master=master))
+        self._plans: dict = {}
+
+    @torch.no_grad()
+    def step(self, closure=None, grad_scale: Optional[torch.Tensor] = None, found_inf: Optional[torch.Tensor] = None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for gi, group in enumerate(self.param_groups):
+            buckets: dict = {}
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                s = self.state[p]
+                if not s:
+                    s.update(adamw_state(p, group["state_bits"], group["master"] and p.dtype != torch.float32))
+                    s["step"] = 0
+                s["step"] += 1
+                buckets.setdefault((p.device, s["step"], "master" in s), []).append(p)
+            live = {}
+            for (device, step, has_master), ps in buckets.items():
+                rows = [(p, p.grad, self.state[p]) for p in ps]
+                where = tuple(x.data_ptr() for p, g, s in rows
+                              for x in (p, g, s["m"], s["v"], s.get("m_scale"), s.get("v_scale"), s.get("master"))
+                              if x is not None) + tuple(p.numel() for p in ps)
+                key = (device, has_master, tuple(id(p) for p in ps))
+                held = self._plans.get(gi, {}).get(key)
+                if held is None or held[0] != where:
+                    low = group["state_bits"] == 8
+                    held = (where, AdamWPlan(
+                        [r[0].detach() for r in rows], [r[1] for r in rows], [r[2]["m"] for r in rows],
+                        [r[2]["v"] for r in rows], [r[2]["m_scale"] for r in rows] if low else None,
+                        [r[2]["v_scale"] for r in rows] if low else None,
+                        [r[2]["master"] for r in rows] if has_master else None))
+                live[key] = held
+                held[1].step(step, group["lr"], group["betas"], group["eps"], group["weight_decay"], grad_scale,
+                             found_inf)
+            self._plans[gi] = live
+        return loss
+
+    def load_state_dict(self, state_dict):
+        """States keep their own types (the base class would turn them into the parameter's)."""
+        super().load_state_dict(state_dict)
+        saved = state_dict["state"]
+        ids = [i for g in state_dict["param_groups"] for i in g["params"]]
+        params = [p for g in self.param_groups for p in g["params"]]
+        for i, p in zip(ids, params):
+            for k, x in saved.get(i, {}).items():
+                if isinstance(x, torch.Tensor):
+                    self.state[p][k] = x.detach().to(p.device, copy=True)
+        self._plans = {}
