@@ -322,7 +322,7 @@ int int8_linear_backward_weight(const void* G, const void* A, int dtype, int64_t
  * grad_A and grad_B may each be NULL (not computed); V is the forward's. An
  * adapter without rows gets a zero gradient.
  * R <= I8L_LORA_MAX_RANK, K and N <= I8L_MAX_COLS, n_adapters <= 65535,
- * T + n_seg <= 2^30, else I8L_ESHAPE.
+ * T <= 2^24, n_seg <= 2^20, else I8L_ESHAPE.
  * ------------------------------------------------------------------------ */
 #define I8L_LORA_MAX_RANK 128
 
@@ -354,7 +354,7 @@ int int8_lora_backward(const void* G, const void* X, const float* V, int dtype, 
  * fp32, written by the forward (each may be NULL) and read by the backward.
  * grad_X, grad_weight and grad_bias may each be NULL (not computed). out may be
  * X; grad_X may be G unless a weight or bias gradient is asked for too. T = 0
- * writes zero weight gradients. C <= I8L_MAX_COLS, else I8L_ESHAPE; an
+ * writes zero weight gradients. C <= I8L_MAX_COLS, T <= 2^24, else I8L_ESHAPE; an
  * eps that is negative or NaN is I8L_EINVAL.
  * ------------------------------------------------------------------------ */
 int int8_layer_norm_forward(const void* X, int dtype, int64_t T, int64_t C, const void* weight, const void* bias,

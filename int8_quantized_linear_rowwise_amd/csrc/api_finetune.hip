@@ -12,7 +12,8 @@
 namespace {
 
 constexpr size_t ALIGN = 256;
-constexpr int64_t MAX_TOKENS = (int64_t)1 << 30;
+constexpr int64_t MAX_TOKENS = (int64_t)1 << 24;   // rows; tiles of 16 rows and their threads stay within a grid axis
+constexpr int64_t MAX_SEGMENTS = (int64_t)1 << 20;
 constexpr int64_t MAX_ADAPTERS = 65535;
 constexpr int64_t MAX_VALUES = (int64_t)1 << 40;
 
@@ -23,7 +24,7 @@ int hip_status(hipError_t e) { return e == hipSuccess ? I8L_OK : I8L_EHIP; }
 // Sizes of an adapter call: I8L_OK, I8L_EINVAL or I8L_ESHAPE.
 int lora_sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t n_adapters, int64_t n_seg) {
   if (T < 0 || K < 0 || N < 0 || R < 0 || n_adapters < 0 || n_seg < 0) return I8L_EINVAL;
-  if (T > MAX_TOKENS || n_seg > MAX_TOKENS || T + n_seg > MAX_TOKENS || K > I8L_MAX_COLS || N > I8L_MAX_COLS ||
+  if (T > MAX_TOKENS || n_seg > MAX_SEGMENTS || K > I8L_MAX_COLS || N > I8L_MAX_COLS ||
       R > I8L_LORA_MAX_RANK || n_adapters > MAX_ADAPTERS || T * K > MAX_VALUES || T * N > MAX_VALUES)
     return I8L_ESHAPE;
   return I8L_OK;
@@ -142,7 +143,7 @@ static int adamw_chunks(const i8l_adamw_tensor* t, int64_t count, int64_t* chunk
     if (t[i].n > MAX_VALUES) return I8L_ESHAPE;
     c += (t[i].n + i8l::adamw_chunk() - 1) / i8l::adamw_chunk();
   }
-  if (c > INT32_MAX) return I8L_ESHAPE;
+  if (c > ((int64_t)1 << 24) - 1) return I8L_ESHAPE;   // one workgroup of 256 threads each
   *chunks = c;
   return I8L_OK;
 }
