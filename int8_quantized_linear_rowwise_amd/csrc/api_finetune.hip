@@ -90,7 +90,7 @@ int int8_lora_backward(const void* G, const void* X, const float* V, int dtype, 
   if ((uintptr_t)ws % ALIGN) return I8L_EINVAL;
   const i8l::LoraSegs S = {seg_offsets, seg_adapter, (int)n_seg, any ? (int)n_adapters : 0};
   return hip_status(i8l::launch_lora_backward(dtype, G, X, V, (int)T, (int)K, A, B, scaling, (int)R, (int)N, S,
-                                              base_grad, grad_X, grad_A, grad_B, static_cast<float*>(ws),
+                                              (int)n_adapters, base_grad, grad_X, grad_A, grad_B, static_cast<float*>(ws),
                                               (hipStream_t)stream));
 }
 

@@ -81,13 +81,16 @@ struct LoraSegs {
 };
 size_t lora_forward_floats(int T, int K, int N, int R, int n_seg);
 size_t lora_backward_floats(int T, int K, int N, int R, int n_adapters, int n_seg);
-// T >= 1. V (T x R fp32) or NULL; ws: lora_forward_floats() floats.
+// Forward: T >= 1, V (T x R fp32) or NULL. ws: lora_*_floats() floats. S.n_adapters
+// is 0 where nothing is to be read of the adapters (no rank); the backward's
+// n_adapters is the one its workspace was sized with.
 hipError_t launch_lora_forward(int dt, const void* X, int T, int K, const void* A, const void* B,
                                const float* scaling, int R, int N, const LoraSegs& S, const void* base, void* out,
                                float* V, float* ws, hipStream_t st);
 hipError_t launch_lora_backward(int dt, const void* G, const void* X, const float* V, int T, int K, const void* A,
                                 const void* B, const float* scaling, int R, int N, const LoraSegs& S,
-                                const void* base_grad, void* gX, void* gA, void* gB, float* ws, hipStream_t st);
+                                int n_adapters, const void* base_grad, void* gX, void* gA, void* gB, float* ws,
+                                hipStream_t st);
 
 // Layer norm, T x C of dt, weight and bias of wdt (dt or fp32).
 hipError_t launch_norm_forward(int dt, int wdt, const void* X, int T, int C, const void* w, const void* b, float eps,

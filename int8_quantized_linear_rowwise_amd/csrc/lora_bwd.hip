@@ -1,113 +1,847 @@
-// Low-rank adapters of many requests beside a shared projection.
+// Low-rank adapters of many requests beside a shared projection: gradients.
 //
-// Token t of adapter a: V[t] = A[a] x[t] (R values, fp32) and
-//   y[t] = D(base[t] + s[a] B[a] V[t]);
-// backward, g = dL/dy:
+// With g = dL/dy, token t of adapter a:
 //   dV[t] = s[a] B[a]^T g[t],  dx[t] = D(base_grad[t] + A[a]^T dV[t]),
 //   dA[a] = D(sum_t dV[t] x[t]^T),  dB[a] = D(s[a] sum_t g[t] V[t]^T).
+// Bound by memory: G, X, base_grad and dx once, T (N + 3 K) elements, against
+// 4 T R (K + N) flops. Each large operand serves two products, one along the
+// features and one along the tokens, so each is read once for both:
+//   g pass: G gives dV (partial sums by column slice) and dB (by token tile);
+//   sum of the slices of dV;
+//   x pass: X and base_grad give dx and dA (partial sums by token tile);
+//   sum of the tiles of dA and dB, in a fixed order.
+// A workgroup takes a slice of columns and a tile of tokens of one adapter;
+// its eight waves split the columns, and each holds its part of the weight
+// gradient in registers while it walks the tokens 32 (fp32: 16) at a time. The
+// rows come into registers as they lie, which is the fragment of the product
+// along the features, and go through LDS to be read transposed for the one
+// along the tokens.
 #include "lora.hpp"
 
 namespace i8l {
 
-constexpr int TM = 16;
+typedef short v4s __attribute__((ext_vector_type(4)));
+#define I8L_LDS(p) ((__attribute__((address_space(3))) v4s*)(p))
 
-// P[t, r] = f sum_k X[t, k] W(r, k); W(r, k) = W[a][r][k], or W[a][k][r] if WT.
-template <int DT, bool WT>
-__global__ __launch_bounds__(256) void k_lora_shrink(const typename Elem<DT>::T* __restrict__ X, int T, int K,
-                                                     const typename Elem<DT>::T* __restrict__ W, int R,
-                                                     const float* __restrict__ scaling, LoraSegs S,
-                                                     float* __restrict__ P) {
-  const LoraTile tl = lora_tile(S, blockIdx.x + 1, T, TM);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n = tl.t1 - tl.t0;
-  const float f = (tl.adapter >= 0 && scaling) ? scaling[tl.adapter] : 1.0f;
-  const typename Elem<DT>::T* Wa = W + (int64_t)max(tl.adapter, 0) * R * K;
-  for (int j = wave; j < n * R; j += 4) {
-    const int t = tl.t0 + j / R, r = j % R;
-    float s = 0.0f;
-    if (tl.adapter >= 0)
-      for (int k = lane; k < K; k += 64)
-        s = __builtin_fmaf(Elem<DT>::to_f32(X[(int64_t)t * K + k]),
-                           Elem<DT>::to_f32(Wa[WT ? (int64_t)k * R + r : (int64_t)r * K + k]), s);
+namespace {
+
+// A wave's tile of ST token rows x WN columns in LDS. 16-bit rows are stored in
+// pairs of 16-byte chunks (16 columns), pair p of row t at p ^ swz(t): the
+// eight rows of one write by eight lanes and the eight rows of a half wave's
+// transposed read fall on distinct banks. fp32 rows are padded by 16 bytes.
+template <int DT, int WN>
+struct Tile {
+  static constexpr int ST = DT == DT_F32 ? 16 : 32;
+  static constexpr int TT = ST / 16;
+  static constexpr int ROWB = DT == DT_F32 ? (WN + 4) * 4 : WN * 2;
+  static constexpr int BYTES = ST * ROWB;
+  static constexpr int PAIRS = WN / 16, ROWS = PAIRS >= 8 ? 1 : 8 / PAIRS;   // rows that span all banks
+  __device__ static __forceinline__ int swz(int t) {
+    return ((t / ROWS) & (PAIRS - 1)) ^ (((t >> 3) & 1) * (PAIRS / 2));
+  }
+  // fragment of row t (the lane's), step ks along the columns
+  __device__ static __forceinline__ void put(char* w, int t, int ks, int q, v4u f) {
+    if constexpr (DT == DT_F32) *reinterpret_cast<v4u*>(w + t * ROWB + 64 * ks + 16 * q) = f;
+    else *reinterpret_cast<v4u*>(w + t * ROWB + 32 * ((2 * ks + (q >> 1)) ^ swz(t)) + 16 * (q & 1)) = f;
+  }
+  // columns 16 nt .. + 15 as rows, the tokens along the contraction
+  __device__ static __forceinline__ v4u get(const char* w, int nt, int lane) {
+    const int c = lane & 15, q = lane >> 4;
+    if constexpr (DT == DT_F32) {
+      v4u f;
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o, 64);
-    if (lane == 0) P[(int64_t)t * R + r] = s * f;
+      for (int j = 0; j < 4; ++j) f[j] = *reinterpret_cast<const uint32_t*>(w + (4 * q + j) * ROWB + 4 * (16 * nt + c));
+      return f;
+    } else {
+      v4s h[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = 8 * q + 4 * i + (c >> 2);
+        h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(I8L_LDS(w + t * ROWB + 32 * (nt ^ swz(t)) + 8 * (c & 3)));
+      }
+      return __builtin_bit_cast(v4u, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
+// fp32 values [token][r] in LDS as operands: `vt` [part][r][token] (rows of 80
+// bytes) for products along the tokens, `vr` [part][token][r] along r.
+template <int DT, int RT>
+struct Small {
+  typedef typename Elem<DT>::T E;
+  static constexpr int ST = DT == DT_F32 ? 16 : 32, RP = 16 * RT, NC = Mx<DT>::NC;
+  static constexpr int LDT = 80 / (int)sizeof(E), LDR = RP + 16 / (int)sizeof(E);
+  static constexpr int VT = NC * RP * LDT * (int)sizeof(E), VR = NC * ST * LDR * (int)sizeof(E);
+  static constexpr int PAIRS = ST / 2 * RP;                  // two tokens of one r
+  static constexpr int PER = (PAIRS + 511) / 512;            // pairs a thread holds
+  __device__ static __forceinline__ void put_t(char* vt, int r, int tp, float a, float b, float unit) {
+    E* p = reinterpret_cast<E*>(vt) + r * LDT + 2 * tp;
+    if constexpr (DT == DT_F32) {
+      *reinterpret_cast<v2f*>(p) = v2f{a, b};
+    } else {
+      const uint32_t x = split2<DT>(a, unit), y = split2<DT>(b, unit);
+      *reinterpret_cast<uint32_t*>(p) = (x & 0xffffu) | (y << 16);
+      *reinterpret_cast<uint32_t*>(p + RP * LDT) = (x >> 16) | (y & 0xffff0000u);
+    }
+  }
+  __device__ static __forceinline__ void put_r(char* vr, int r, int t, float a, float unit) {
+    E* p = reinterpret_cast<E*>(vr) + t * LDR + r;
+    if constexpr (DT == DT_F32) {
+      *p = a;
+    } else {
+      const uint32_t x = split2<DT>(a, unit);
+      p[0] = __builtin_bit_cast(E, (uint16_t)(x & 0xffffu));
+      p[ST * LDR] = __builtin_bit_cast(E, (uint16_t)(x >> 16));
+    }
+  }
+  __device__ static __forceinline__ v4u get_t(const char* vt, int part, int rt, int lane) {
+    return *reinterpret_cast<const v4u*>(reinterpret_cast<const E*>(vt) + (part * RP + 16 * rt + (lane & 15)) * LDT +
+                                         Mx<DT>::EL * (lane >> 4));
+  }
+  __device__ static __forceinline__ v4u get_r(const char* vr, int part, int t, int r) {
+    return *reinterpret_cast<const v4u*>(reinterpret_cast<const E*>(vr) + (part * ST + t) * LDR + r);
+  }
+};
+
+// acc[j][n] += the tile's columns 16 n .. times vt's r 16 j .., along the
+// tokens; the operand with fewer fragments stays in registers.
+template <int DT, int RT, int WN>
+__device__ __forceinline__ void along_tokens(const char* tile, const char* vt, int lane, v4f (&acc)[RT][WN / 16]) {
+  typedef Mx<DT> M;
+  constexpr int NT = WN / 16;
+  if constexpr (NT <= M::NC * RT) {
+    v4u f[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) f[n] = Tile<DT, WN>::get(tile, n, lane);
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int p = 0; p < M::NC; ++p) {
+        const v4u fv = Small<DT, RT>::get_t(vt, p, j, lane);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[j][n] = M::mma(f[n], fv, acc[j][n]);
+      }
+  } else {
+    v4u fv[M::NC][RT];
+#pragma unroll
+    for (int p = 0; p < M::NC; ++p)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) fv[p][j] = Small<DT, RT>::get_t(vt, p, j, lane);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const v4u f = Tile<DT, WN>::get(tile, n, lane);
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int p = 0; p < M::NC; ++p) acc[j][n] = M::mma(f, fv[p][j], acc[j][n]);
+    }
   }
 }
 
-// out[t, n] = D(base[t, n] + f sum_r P[t, r] W(n, r)); W(n, r) = W[a][n][r], or W[a][r][n] if WT.
-template <int DT, bool WT>
-__global__ __launch_bounds__(256) void k_lora_expand(const float* __restrict__ P, int T, int N,
-                                                     const typename Elem<DT>::T* __restrict__ W, int R,
-                                                     const float* __restrict__ scaling, LoraSegs S,
-                                                     const typename Elem<DT>::T* base, typename Elem<DT>::T* out) {
-  const LoraTile tl = lora_tile(S, blockIdx.x + 1, T, TM);
-  const float f = (tl.adapter >= 0 && scaling) ? scaling[tl.adapter] : 1.0f;
-  const typename Elem<DT>::T* Wa = W + (int64_t)max(tl.adapter, 0) * R * N;
-  const int n = blockIdx.y * 256 + threadIdx.x;
-  if (n >= N) return;
-  for (int t = tl.t0; t < tl.t1; ++t) {
-    float s = 0.0f;
-    if (tl.adapter >= 0)
-      for (int r = 0; r < R; ++r)
-        s = __builtin_fmaf(P[(int64_t)t * R + r], Elem<DT>::to_f32(Wa[WT ? (int64_t)r * N + n : (int64_t)n * R + r]),
-                           s);
-    const int64_t at = (int64_t)t * N + n;
-    out[at] = Elem<DT>::from_f32((base ? Elem<DT>::to_f32(base[at]) : 0.0f) + f * s);
-  }
+// Row of sorted position i: the rows themselves without a permutation. A
+// permutation of offsets that make no sense can have holes: its entries are
+// held inside the tensor.
+__device__ __forceinline__ int row_of(const int32_t* perm, int i, int T) {
+  return perm ? (int)min((uint32_t)perm[i], (uint32_t)(T - 1)) : i;
 }
 
-// gW(r, k) = D(f sum_{t of adapter a} P[t, r] X[t, k]), written to gW[a][r][k], or gW[a][k][r] if WT.
-template <int DT, bool WT>
-__global__ __launch_bounds__(256) void k_lora_wgrad(const float* __restrict__ P,
-                                                    const typename Elem<DT>::T* __restrict__ X, int T, int K, int R,
+__device__ __forceinline__ float finite_abs(float v) { return __builtin_isfinite(v) ? __builtin_fabsf(v) : 0.0f; }
+
+}  // namespace
+
+// dV partial sums P[slice][position][Rp] and dB partial sums dBp[tile][n][Rp] of
+// one tile of tokens and 8 WN columns of G. B's fragments for dV stay in
+// registers; the eight waves' parts of dV meet in LDS.
+template <int DT, int RT, int WN>
+__global__ __launch_bounds__(512) void k_lora_gpass(const typename Elem<DT>::T* __restrict__ G, int N, int T,
+                                                    const float* __restrict__ V,
+                                                    const typename Elem<DT>::T* __restrict__ B, int R,
                                                     const float* __restrict__ scaling, LoraSegs S,
-                                                    typename Elem<DT>::T* __restrict__ gW) {
-  const int a = blockIdx.z, r = blockIdx.y, k = blockIdx.x * 256 + threadIdx.x;
-  float s = 0.0f;
-  for (int g = 0; g < S.n_seg; ++g) {
-    if (seg_adapter(S, g) != a) continue;
-    const int t1 = seg_start(S, g + 1, T);
-    for (int t = seg_start(S, g, T); t < t1; ++t)
-      if (k < K) s = __builtin_fmaf(P[(int64_t)t * R + r], Elem<DT>::to_f32(X[(int64_t)t * K + k]), s);
+                                                    const int32_t* __restrict__ perm, int tm, float* __restrict__ P,
+                                                    float* __restrict__ dBp, int32_t* __restrict__ tile_adapter) {
+  typedef Mx<DT> M;
+  typedef typename Elem<DT>::T E;
+  typedef Tile<DT, WN> TL;
+  typedef Small<DT, RT> SM;
+  constexpr int KS = M::KS, EL = M::EL, ST = TL::ST, TT = TL::TT, NK = WN / KS, NT = WN / 16, RP = 16 * RT;
+  constexpr int RW = RP < 64 ? RP : 64, RH = RP / RW, RTH = RW / 16;   // dV meets in LDS up to 64 columns at a time
+  constexpr int LDV = RW + 4;
+  extern __shared__ __attribute__((aligned(16))) char sm[];
+  char* vt = sm + 8 * TL::BYTES;
+  float* red = reinterpret_cast<float*>(vt + SM::VT);
+  float* top8 = red + 8 * ST * LDV;
+
+  const LoraTile tl = lora_tile(S, blockIdx.y + 1, T, tm);
+  const bool none = tl.t1 <= tl.t0 || tl.adapter < 0;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+  if (blockIdx.x == 0 && tid == 0) tile_adapter[blockIdx.y] = none ? -1 : tl.adapter;
+  if (none) return;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  char* mine = sm + wave * TL::BYTES;
+  const int n0 = blockIdx.x * 8 * WN + wave * WN;
+  const bool whole = n0 + WN <= N;
+  const float scale = scaling[tl.adapter];
+
+  // B[a][n][r] with n along the contraction
+  v4u fb[RT][NK];
+  float bunit = 1.0f;
+  if (P) {
+    const E* Ba = B + (int64_t)tl.adapter * N * R;
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+        fb[j][k] = v4u{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < EL; ++e) {
+          const int n = n0 + k * KS + EL * q + e, r = 16 * j + c;
+          const E w = Ba[(int64_t)min(n, N - 1) * R + min(r, R - 1)];
+          frag_set<DT>(fb[j][k], e, n < N && r < R ? w : Elem<DT>::from_f32(0.0f));
+        }
+      }
+    if constexpr (DT == DT_F16) {
+      // denormal weights lose bits in the matrix core (see the forward's
+      // shrink): a power of two takes the wave's largest to 2^14
+      uint32_t top = 0u;   // magnitude bits order as the values do
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) {
+            const uint32_t m = (fb[j][k][e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+            top = max(top, m < 0x7c00u ? m : 0u);
+          }
+      const float most = (float)__builtin_bit_cast(_Float16, (uint16_t)wave_umax(top));
+      bunit = fminf(fmaxf(unit_for(most), 1.0f), 0x1p15f);   // an fp16 value; never shrinks a weight
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+          fb[j][k] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, fb[j][k]) * (_Float16)bunit);
+    }
   }
-  if (scaling) s *= scaling[a];
-  if (k < K) gW[(int64_t)a * R * K + (WT ? (int64_t)k * R + r : (int64_t)r * K + k)] = Elem<DT>::from_f32(s);
+
+  v4f acc[RT][NT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[j][n] = v4f{};
+  float run_top = 0.0f, unit = 1.0f;
+
+  v4u g[TT][NK];
+  float v[SM::PER][2];
+  auto load = [&](int at) {
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const int row = row_of(perm, min(at + 16 * i + c, tl.t1 - 1), T);
+      const E* p = G + (int64_t)row * N + n0 + EL * q;
+      if (whole) {
+#pragma unroll
+        for (int k = 0; k < NK; ++k) g[i][k] = ld16<DT>(p + k * KS);
+      } else {
+#pragma unroll
+        for (int k = 0; k < NK; ++k) g[i][k] = ld_frag<DT>(p + k * KS, N - n0 - EL * q - k * KS);
+      }
+    }
+    if (dBp) {
+#pragma unroll
+      for (int x = 0; x < SM::PER; ++x) {
+        const int e = tid + 512 * x, r = e % RP, t = at + 2 * (e / RP);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[x][h] = e < SM::PAIRS && r < R && t + h < tl.t1 ? V[(int64_t)row_of(perm, t + h, T) * R + r] : 0.0f;
+      }
+    }
+  };
+  load(tl.t0);
+  for (int at = tl.t0; at < tl.t1; at += ST) {
+    if (dBp) {
+      if constexpr (DT == DT_F16) {
+        float top = 0.0f;
+#pragma unroll
+        for (int x = 0; x < SM::PER; ++x) top = fmaxf(top, fmaxf(finite_abs(v[x][0]), finite_abs(v[x][1])));
+        top = wave_max(top);
+        if (lane == 0) top8[wave] = top;
+        __syncthreads();
+        float all = run_top;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) all = fmaxf(all, top8[w]);
+        if (all > run_top) {
+          const float u = unit_for(all), f = u * inv_pow2(unit);
+#pragma unroll
+          for (int j = 0; j < RT; ++j)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[j][n] *= f;
+          unit = u;
+          run_top = all;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < SM::PER; ++x) {
+        const int e = tid + 512 * x;
+        if (e < SM::PAIRS) SM::put_t(vt, e % RP, e / RP, v[x][0], v[x][1], unit);
+      }
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        const bool row = at + 16 * i + c < tl.t1;   // rows past the tile must not meet their zeros in V as NaN
+#pragma unroll
+        for (int k = 0; k < NK; ++k) TL::put(mine, 16 * i + c, k, q, row ? g[i][k] : v4u{0u, 0u, 0u, 0u});
+      }
+    }
+    const bool more = at + ST < tl.t1;
+    if (P) {
+      const float f = DT == DT_F16 ? inv_pow2(bunit) : 1.0f;
+#pragma unroll
+      for (int h = 0; h < RH; ++h) {
+        v4f dv[TT][RTH];
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+          for (int j = 0; j < RTH; ++j) {
+            dv[i][j] = v4f{};
+#pragma unroll
+            for (int k = 0; k < NK; ++k) dv[i][j] = M::mma(g[i][k], fb[h * RTH + j][k], dv[i][j]);
+          }
+        if (h == RH - 1 && more) load(at + ST);
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+          for (int j = 0; j < RTH; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              red[(wave * ST + 16 * i + 4 * q + e) * LDV + 16 * j + c] = dv[i][j][e] * f;
+        __syncthreads();
+        for (int e = tid; e < ST * RW / 4; e += 512) {
+          const int t = e / (RW / 4), r = e % (RW / 4) * 4;
+          v4f s = {};
+#pragma unroll
+          for (int w = 0; w < 8; ++w) s += *reinterpret_cast<const v4f*>(&red[(w * ST + t) * LDV + r]);
+          if (at + t < tl.t1)
+            *reinterpret_cast<v4f*>(P + ((int64_t)blockIdx.x * T + at + t) * RP + h * RW + r) = s * scale;
+        }
+        if (h + 1 < RH) __syncthreads();
+      }
+    } else {
+      if (more) load(at + ST);
+      __syncthreads();
+    }
+    if (dBp) {
+      along_tokens<DT, RT, WN>(mine, vt, lane, acc);
+    }
+    __syncthreads();
+  }
+  if (dBp) {
+    const float f = DT == DT_F16 ? scale * inv_pow2(unit) : scale;
+    float* o = dBp + (int64_t)blockIdx.y * N * RP;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = n0 + 16 * n + 4 * q + e;
+        if (at < N)
+#pragma unroll
+          for (int j = 0; j < RT; ++j) o[(int64_t)at * RP + 16 * j + c] = acc[j][n][e] * f;
+      }
+  }
 }
 
+// dx and the partial sums dAp[tile][r][Kp] of one tile of tokens and 8 WN
+// columns of X. dx is taken transposed, as the forward's expand, with A's
+// fragments in registers.
+template <int DT, int RT, int WN>
+__global__ __launch_bounds__(512) void k_lora_xpass(const typename Elem<DT>::T* __restrict__ X, int K, int T,
+                                                    const float* __restrict__ dV,
+                                                    const typename Elem<DT>::T* __restrict__ A, int R, LoraSegs S,
+                                                    const int32_t* __restrict__ perm, int tm,
+                                                    const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
+                                                    float* __restrict__ dAp, int Kp,
+                                                    int32_t* __restrict__ tile_adapter) {
+  typedef Mx<DT> M;
+  typedef typename Elem<DT>::T E;
+  typedef Tile<DT, WN> TL;
+  typedef Small<DT, RT> SM;
+  constexpr int KS = M::KS, EL = M::EL, ST = TL::ST, TT = TL::TT, NK = WN / KS, NT = WN / 16, RP = 16 * RT;
+  constexpr int UN = M::F32 ? 1 : 2;
+  constexpr int NB = M::F32 ? RT : (RT + 1) / 2, NS = M::F32 ? RT : RT == 1 ? 1 : RT;
+  extern __shared__ __attribute__((aligned(16))) char sm[];
+  char* vt = sm + 8 * TL::BYTES;
+  char* vr = vt + SM::VT;
+  float* top8 = reinterpret_cast<float*>(vr + SM::VR);
 
-size_t lora_backward_floats(int T, int K, int N, int R, int n_adapters, int n_seg) { return (size_t)T * R; }
+  const LoraTile tl = lora_tile(S, blockIdx.y + 1, T, tm);
+  const bool none = tl.t1 <= tl.t0 || tl.adapter < 0;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
+  if (dAp && blockIdx.x == 0 && tid == 0) tile_adapter[blockIdx.y] = none ? -1 : tl.adapter;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  char* mine = sm + wave * TL::BYTES;
+  const int k0 = blockIdx.x * 8 * WN + wave * WN;
+  const bool whole = k0 + WN <= K;
+
+  v4u x[TT][NK], b[TT][NK];
+  int row[TT];
+  float v[SM::PER][2];
+  auto rows = [&](int at) {
+#pragma unroll
+    for (int i = 0; i < TT; ++i) row[i] = row_of(perm, min(at + 16 * i + c, tl.t1 - 1), T);
+  };
+  auto load_rows = [&](const E* from, v4u (&f)[TT][NK]) {
+#pragma unroll
+    for (int i = 0; i < TT; ++i) {
+      const E* p = from + (int64_t)row[i] * K + k0 + EL * q;
+      if (whole) {
+#pragma unroll
+        for (int k = 0; k < NK; ++k) f[i][k] = ld16<DT>(p + k * KS);
+      } else {
+#pragma unroll
+        for (int k = 0; k < NK; ++k) f[i][k] = ld_frag<DT>(p + k * KS, K - k0 - EL * q - k * KS);
+      }
+    }
+  };
+  auto store_rows = [&](int at, int i, int k, v4u f) {
+    if (at + 16 * i + c < tl.t1) {
+      E* p = out + (int64_t)row[i] * K + k0 + EL * q + k * KS;
+      if (whole) st16<DT>(p, f);
+      else st_frag<DT>(p, f, K - k0 - EL * q - k * KS);
+    }
+  };
+
+  if (none) {
+    if (out == nullptr || base == out) return;
+    for (int at = tl.t0; at < tl.t1; at += ST) {
+      rows(at);
+      if (base) load_rows(base, b);
+#pragma unroll
+      for (int i = 0; i < TT; ++i)
+#pragma unroll
+        for (int k = 0; k < NK; ++k) store_rows(at, i, k, base ? b[i][k] : v4u{0u, 0u, 0u, 0u});
+    }
+    return;
+  }
+
+  // A[a][r][k] with r along the contraction, rows k in the order that gives a lane consecutive k of the product
+  v4u fa[NK][UN][NB];
+  if (out) {
+    const E* Aa = A + (int64_t)tl.adapter * R * K;
+#pragma unroll
+    for (int blk = 0; blk < NK; ++blk)
+#pragma unroll
+      for (int u = 0; u < UN; ++u)
+#pragma unroll
+        for (int s = 0; s < NB; ++s) {
+          const int k = k0 + blk * KS + (M::F32 ? c : 8 * (c >> 2) + 4 * u + (c & 3));
+          fa[blk][u][s] = v4u{0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int e = 0; e < EL; ++e) {
+            const int r = (M::F32 ? 16 * s + 4 * q : RT == 1 ? 8 * (q & 1) : 32 * s + 8 * q) + e;
+            const E w = Aa[(int64_t)min(r, R - 1) * K + min(k, K - 1)];
+            frag_set<DT>(fa[blk][u][s], e, k < K && r < R ? w : Elem<DT>::from_f32(0.0f));
+          }
+        }
+  }
+
+  v4f acc[RT][NT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[j][n] = v4f{};
+  float run_top = 0.0f, unit = 1.0f, sub = 1.0f;
+
+  auto load_v = [&](int at) {
+#pragma unroll
+    for (int y = 0; y < SM::PER; ++y) {
+      const int e = tid + 512 * y, r = e % RP, t = at + 2 * (e / RP);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[y][h] = e < SM::PAIRS && r < R && t + h < tl.t1 ? dV[(int64_t)(t + h) * RP + r] : 0.0f;
+    }
+  };
+  rows(tl.t0);
+  if (dAp) load_rows(X, x);
+  if (out && base) load_rows(base, b);
+  load_v(tl.t0);
+  for (int at = tl.t0; at < tl.t1; at += ST) {
+    if constexpr (DT == DT_F16) {
+      float top = 0.0f;
+#pragma unroll
+      for (int y = 0; y < SM::PER; ++y) top = fmaxf(top, fmaxf(finite_abs(v[y][0]), finite_abs(v[y][1])));
+      top = wave_max(top);
+      if (lane == 0) top8[wave] = top;
+      __syncthreads();
+      float all = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) all = fmaxf(all, top8[w]);
+      sub = unit_for(all);                         // dx: the scale of these tokens
+      if (all > run_top) {                         // dA: the scale of all tokens so far
+        const float u = unit_for(all), f = u * inv_pow2(unit);
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) acc[j][n] *= f;
+        unit = u;
+        run_top = all;
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < SM::PER; ++y) {
+      const int e = tid + 512 * y;
+      if (e < SM::PAIRS) {
+        if (dAp) SM::put_t(vt, e % RP, e / RP, v[y][0], v[y][1], unit);
+        if (out) {
+          SM::put_r(vr, e % RP, 2 * (e / RP), v[y][0], sub);
+          SM::put_r(vr, e % RP, 2 * (e / RP) + 1, v[y][1], sub);
+        }
+      }
+    }
+    if (dAp) {
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        const bool in = at + 16 * i + c < tl.t1;
+#pragma unroll
+        for (int k = 0; k < NK; ++k) TL::put(mine, 16 * i + c, k, q, in ? x[i][k] : v4u{0u, 0u, 0u, 0u});
+      }
+    }
+    const int here[2] = {row[0], row[TT - 1]};
+    const bool more = at + ST < tl.t1;
+    if (more) {
+      rows(at + ST);
+      if (dAp) load_rows(X, x);
+      load_v(at + ST);
+    }
+    __syncthreads();
+    if (out) {
+      const float f = DT == DT_F16 ? inv_pow2(sub) : 1.0f;
+#pragma unroll
+      for (int i = 0; i < TT; ++i) {
+        v4u fv[NS];
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          fv[s] = SM::get_r(vr, M::F32 ? 0 : RT == 1 ? q >> 1 : s / NB, 16 * i + c,
+                            M::F32 ? 16 * s + 4 * q : RT == 1 ? 8 * (q & 1) : 32 * (s % NB) + 8 * q);
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          v4f d[UN];
+#pragma unroll
+          for (int u = 0; u < UN; ++u) {
+            d[u] = v4f{};
+#pragma unroll
+            for (int s = 0; s < NS; ++s) d[u] = M::mma(fa[k][u][s % NB], fv[s], d[u]);
+          }
+          float y[EL];
+          frag_f32<DT>(base ? b[i][k] : v4u{0u, 0u, 0u, 0u}, y);
+#pragma unroll
+          for (int e = 0; e < EL; ++e) y[e] = __builtin_fmaf(f, d[e >> 2][e & 3], y[e]);
+          if (at + 16 * i + c < tl.t1) {
+            E* p = out + (int64_t)here[i] * K + k0 + EL * q + k * KS;
+            if (whole) st16<DT>(p, frag_of<DT>(y));
+            else st_frag<DT>(p, frag_of<DT>(y), K - k0 - EL * q - k * KS);
+          }
+        }
+      }
+      if (more && base) load_rows(base, b);
+    }
+    if (dAp) {
+      along_tokens<DT, RT, WN>(mine, vt, lane, acc);
+    }
+    __syncthreads();
+  }
+  if (dAp) {
+    const float f = DT == DT_F16 ? inv_pow2(unit) : 1.0f;
+    float* o = dAp + (int64_t)blockIdx.y * R * Kp;
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+      const int r = 16 * j + c;
+      if (r < R)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int k = k0 + 16 * n + 4 * q;
+          if (k < Kp) *reinterpret_cast<v4f*>(o + (int64_t)r * Kp + k) = acc[j][n] * f;
+        }
+    }
+  }
+}
+
+// dV = the sum of P's slices, four values a thread.
+__global__ __launch_bounds__(256) void k_lora_sum_slices(const float* __restrict__ P, int slices, int64_t n4,
+                                                         float* __restrict__ dV) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const v4f* p = reinterpret_cast<const v4f*>(P) + i;
+  v4f s = {};
+#pragma unroll 8
+  for (int k = 0; k < slices; ++k) s += p[k * n4];
+  reinterpret_cast<v4f*>(dV)[i] = s;
+}
+
+// One weight gradient: sums of tiles [tile][rows][ld] into out [adapter][rows][width].
+struct TileSum {
+  const float* part;
+  const int32_t* adapter;
+  void* out;
+  int tiles, rows, ld, width, blocks;   // blocks: workgroups of 1024 values
+};
+template <int DT>
+__global__ __launch_bounds__(256) void k_lora_sum_tiles(TileSum a, TileSum b) {
+  typedef typename Elem<DT>::T E;
+  __shared__ int list[256];
+  __shared__ int count;
+  const bool first = (int)blockIdx.x < a.blocks;
+  const TileSum s = first ? a : b;
+  const int ad = blockIdx.y;
+  const int64_t e = ((int64_t)(first ? blockIdx.x : blockIdx.x - a.blocks) * 256 + threadIdx.x) * 4;
+  const int64_t each = (int64_t)s.rows * s.ld;
+  const float* p = s.part + min(e, each - 4);
+  v4f sum = {};
+  for (int t0 = 0; t0 < s.tiles; t0 += 256) {
+    // this adapter's tiles among 256, in order
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = t0 + 64 * i + threadIdx.x;
+        const bool mine = t < s.tiles && s.adapter[t] == ad;
+        const uint64_t m = __ballot(mine);
+        if (mine) list[n + __popcll(m & ((1ull << threadIdx.x) - 1))] = t;
+        n += __popcll(m);
+      }
+      if (threadIdx.x == 0) count = n;
+    }
+    __syncthreads();
+    const int n = count;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) sum += *reinterpret_cast<const v4f*>(p + list[i] * each);
+  }
+  if (e >= each) return;
+  const int row = (int)(e / s.ld), col = (int)(e % s.ld);
+  E* o = static_cast<E*>(s.out) + ((int64_t)ad * s.rows + row) * s.width + col;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (col + j < s.width) o[j] = Elem<DT>::from_f32(sum[j]);
+}
+
+// Rows sorted by adapter (in their order within one; rows without an adapter
+// last): workgroup a writes the positions of adapter a's rows, a = n_adapters
+// those without. Every workgroup reads all segments once.
+__global__ __launch_bounds__(256) void k_lora_sort(LoraSegs S, int T, int32_t* __restrict__ perm,
+                                                   int32_t* __restrict__ starts) {
+  __shared__ int64_t part[4];
+  __shared__ int64_t before[257];
+  __shared__ int own[256], first[256], len[256];
+  const int a = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  auto adapter = [&](int s) {
+    const int x = seg_adapter(S, s);
+    return x < 0 ? S.n_adapters : x;
+  };
+  int64_t less = 0;
+  for (int s = tid; s < S.n_seg; s += 256)
+    if (adapter(s) < a) less += max(seg_start(S, s + 1, T) - seg_start(S, s, T), 0);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) less += __shfl_xor(less, o, 64);
+  if (lane == 0) part[wave] = less;
+  __syncthreads();
+  int64_t at = part[0] + part[1] + part[2] + part[3];
+  if (tid == 0) starts[a] = (int)min(at, (int64_t)T);
+  for (int s0 = 0; s0 < S.n_seg; s0 += 256) {
+    const int s = s0 + tid;
+    const bool mine = s < S.n_seg && adapter(s) == a;
+    const int f = mine ? seg_start(S, s, T) : 0;
+    own[tid] = mine;
+    first[tid] = f;
+    len[tid] = mine ? max(seg_start(S, s + 1, T) - f, 0) : 0;
+    __syncthreads();
+    if (tid < 64) {   // prefix sums of 256 lengths, four a lane
+      int64_t v[4], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = sum;
+        sum += len[4 * tid + i];
+      }
+      int64_t inc = sum;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int64_t u = __shfl_up(inc, o, 64);
+        if (tid >= o) inc += u;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) before[4 * tid + i] = inc - sum + v[i];
+      if (tid == 63) before[256] = inc;
+    }
+    __syncthreads();
+    for (int i = wave; i < 256; i += 4)
+      if (own[i])
+        for (int j = lane; j < len[i]; j += 64) {
+          const int64_t p = at + before[i] + j;
+          if (p < T) perm[p] = first[i] + j;
+        }
+    at += before[256];
+    __syncthreads();
+  }
+}
+
+namespace {
+
+// Sizes of the launches and of the workspace; of the shape alone.
+struct Plan {
+  int rt, slices, tm_g, tiles_g, tm_x, tiles_x, kp;
+  bool wide_g, wide_x, sort;
+  size_t p, dv, dbp, dap, ad_g, ad_x, perm, starts, total;   // offsets in floats
+};
+
+int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
+constexpr int wide_g(int rt) { return rt <= 2 ? 128 : rt == 4 ? 64 : 32; }
+constexpr int wide_x(int rt) { return rt <= 4 ? 64 : 32; }
+int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// Tokens of a tile: enough tiles for `want` workgroups, 64 to 2048 tokens.
+int tile_tokens(int T, int slices, int want) {
+  int64_t tm = (int64_t)T * slices / want;
+  tm = (tm + 31) / 32 * 32;
+  return tm < 64 ? 64 : tm > 2048 ? 2048 : (int)tm;
+}
+
+Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
+  Plan p = {};
+  p.rt = rank_tiles(R);
+  const int rp = 16 * p.rt;
+  p.sort = n_seg > 64 && n_seg > n_adapters + 1;
+  const LoraSegs S = {nullptr, nullptr, p.sort ? n_adapters + 1 : n_seg, n_adapters};
+  p.wide_g = (int64_t)cdiv(N, 8 * wide_g(p.rt)) * cdiv(T, 64) >= 256;
+  p.wide_x = (int64_t)cdiv(K, 8 * wide_x(p.rt)) * cdiv(T, 64) >= 256;
+  p.slices = cdiv(N, 8 * (p.wide_g ? wide_g(p.rt) : 32));
+  p.tm_g = tile_tokens(T, p.slices, 256);
+  p.tiles_g = lora_tiles(T, S, p.tm_g);
+  p.tm_x = tile_tokens(T, cdiv(K, 8 * (p.wide_x ? wide_x(p.rt) : 32)), 512);
+  p.tiles_x = lora_tiles(T, S, p.tm_x);
+  p.kp = (K + 15) / 16 * 16;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += (n + 63) / 64 * 64;
+    return o;
+  };
+  p.p = take(p.slices > 1 ? (size_t)p.slices * T * rp : 0);
+  p.dv = take((size_t)T * rp);
+  p.dbp = take((size_t)p.tiles_g * N * rp);
+  p.dap = take((size_t)p.tiles_x * R * p.kp);
+  p.ad_g = take(p.tiles_g);
+  p.ad_x = take(p.tiles_x);
+  p.perm = take(p.sort ? T : 0);
+  p.starts = take(p.sort ? n_adapters + 2 : 0);
+  p.total = at;
+  return p;
+}
+
+template <int DT, int RT, int WN>
+hipError_t g_pass(const Plan& p, const void* G, const float* V, int T, const void* B, const float* scaling, int R,
+                  int N, const LoraSegs& S, const int32_t* perm, float* P, float* dBp, int32_t* ad, hipStream_t st) {
+  typedef typename Elem<DT>::T E;
+  typedef Tile<DT, WN> TL;
+  constexpr int rw = RT < 4 ? 16 * RT : 64;
+  constexpr int lds = 8 * TL::BYTES + Small<DT, RT>::VT + 8 * TL::ST * (rw + 4) * 4 + 32;
+  auto kern = k_lora_gpass<DT, RT, WN>;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = lds_limit_once((const void*)kern, lds, done);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(p.slices, p.tiles_g), dim3(512), lds, st, static_cast<const E*>(G), N, T, V,
+                     static_cast<const E*>(B), R, scaling, S, perm, p.tm_g, P, dBp, ad);
+  return hipGetLastError();
+}
+
+template <int DT, int RT, int WN>
+hipError_t x_pass(const Plan& p, const void* X, int T, int K, const float* dV, const void* A, int R,
+                  const LoraSegs& S, const int32_t* perm, const void* base, void* out, float* dAp, int32_t* ad,
+                  hipStream_t st) {
+  typedef typename Elem<DT>::T E;
+  constexpr int lds = 8 * Tile<DT, WN>::BYTES + Small<DT, RT>::VT + Small<DT, RT>::VR + 32;
+  auto kern = k_lora_xpass<DT, RT, WN>;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = lds_limit_once((const void*)kern, lds, done);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kern, dim3(cdiv(K, 8 * WN), p.tiles_x), dim3(512), lds, st, static_cast<const E*>(X), K, T, dV,
+                     static_cast<const E*>(A), R, S, perm, p.tm_x, static_cast<const E*>(base), static_cast<E*>(out),
+                     dAp, p.kp, ad);
+  return hipGetLastError();
+}
+
+template <int DT, int RT>
+hipError_t backward_t(const Plan& p, const void* G, const void* X, const float* V, int T, int K, const void* A,
+                      const void* B, const float* scaling, int R, int N, const LoraSegs& S0, const void* base_grad,
+                      void* gX, void* gA, void* gB, float* ws, hipStream_t st) {
+  hipError_t e = hipSuccess;
+  const int na = S0.n_adapters;
+  LoraSegs S = S0;
+  const int32_t* perm = nullptr;
+  int32_t* ad_g = reinterpret_cast<int32_t*>(ws + p.ad_g);
+  int32_t* ad_x = reinterpret_cast<int32_t*>(ws + p.ad_x);
+  float* dV = ws + p.dv;
+  const bool want_dv = (gX || gA) && na > 0 && T > 0, rows = T > 0;
+  if (na == 0) S = LoraSegs{nullptr, nullptr, 1, 0};   // no adapter anywhere: one segment without
+  if (rows && p.sort && na > 0) {
+    int32_t* to = reinterpret_cast<int32_t*>(ws + p.perm);
+    int32_t* starts = reinterpret_cast<int32_t*>(ws + p.starts);
+    hipLaunchKernelGGL(k_lora_sort, dim3(na + 1), dim3(256), 0, st, S0, T, to, starts);
+    perm = to;
+    S = LoraSegs{starts, nullptr, na + 1, na};
+  }
+  if (rows && na > 0 && N > 0 && (want_dv || gB)) {
+    float* P = !want_dv ? nullptr : p.slices > 1 ? ws + p.p : dV;
+    float* dBp = gB ? ws + p.dbp : nullptr;
+    e = p.wide_g ? g_pass<DT, RT, wide_g(RT)>(p, G, V, T, B, scaling, R, N, S, perm, P, dBp, ad_g, st)
+                 : g_pass<DT, RT, 32>(p, G, V, T, B, scaling, R, N, S, perm, P, dBp, ad_g, st);
+    if (e != hipSuccess) return e;
+    if (want_dv && p.slices > 1) {
+      const int64_t n4 = (int64_t)T * 4 * RT;
+      hipLaunchKernelGGL(k_lora_sum_slices, dim3(cdiv(n4, 256)), dim3(256), 0, st, P, p.slices, n4, dV);
+    }
+  }
+  const bool no_dv = N == 0;   // dV = 0: nothing reaches A or X
+  if (rows && K > 0 && (gX || (gA && na > 0))) {
+    LoraSegs Sx = S;
+    if (no_dv) Sx.n_adapters = 0;
+    float* dAp = gA && na > 0 ? ws + p.dap : nullptr;
+    e = p.wide_x ? x_pass<DT, RT, wide_x(RT)>(p, X, T, K, dV, A, R, Sx, perm, base_grad, gX, dAp, ad_x, st)
+                 : x_pass<DT, RT, 32>(p, X, T, K, dV, A, R, Sx, perm, base_grad, gX, dAp, ad_x, st);
+    if (e != hipSuccess) return e;
+  }
+  TileSum a = {}, b = {};
+  const int rp = 16 * RT;
+  if (gA && na > 0 && R > 0 && K > 0)
+    a = TileSum{ws + p.dap, ad_x, gA, rows ? p.tiles_x : 0, R, p.kp, K, cdiv((int64_t)R * p.kp, 1024)};
+  if (gB && na > 0 && R > 0 && N > 0)
+    b = TileSum{ws + p.dbp, ad_g, gB, rows ? p.tiles_g : 0, N, rp, R, cdiv((int64_t)N * rp, 1024)};
+  if (a.blocks + b.blocks > 0)
+    hipLaunchKernelGGL(k_lora_sum_tiles<DT>, dim3(a.blocks + b.blocks, na), dim3(256), 0, st, a, b);
+  return hipGetLastError();
+}
 
 template <int DT>
-static hipError_t backward_t(const void* Gv, const void* Xv, const float* V, int T, int K, const void* A,
-                             const void* B, const float* scaling, int R, int N, const LoraSegs& S,
-                             const void* base_grad, void* gX, void* gA, void* gB, float* ws, hipStream_t st) {
-  typedef typename Elem<DT>::T E;
-  const E* G = static_cast<const E*>(Gv);
-  const E* X = static_cast<const E*>(Xv);
-  const int nt = lora_tiles(T, S, TM), na = S.n_adapters;
-  if (T > 0 && R > 0 && (gX || gA))
-    hipLaunchKernelGGL((k_lora_shrink<DT, true>), dim3(nt), dim3(256), 0, st, G, T, N, static_cast<const E*>(B), R,
-                       scaling, S, ws);
-  if (T > 0 && K > 0 && gX)
-    hipLaunchKernelGGL((k_lora_expand<DT, true>), dim3(nt, (K + 255) / 256), dim3(256), 0, st, ws, T, K,
-                       static_cast<const E*>(A), R, nullptr, S, static_cast<const E*>(base_grad), static_cast<E*>(gX));
-  if (gA && na > 0 && R > 0 && K > 0)
-    hipLaunchKernelGGL((k_lora_wgrad<DT, false>), dim3((K + 255) / 256, R, na), dim3(256), 0, st, ws, X, T, K, R,
-                       nullptr, S, static_cast<E*>(gA));
-  if (gB && na > 0 && R > 0 && N > 0)
-    hipLaunchKernelGGL((k_lora_wgrad<DT, true>), dim3((N + 255) / 256, R, na), dim3(256), 0, st, V, G, T, N, R,
-                       scaling, S, static_cast<E*>(gB));
-  return hipGetLastError();
+hipError_t backward_d(const Plan& p, const void* G, const void* X, const float* V, int T, int K, const void* A,
+                      const void* B, const float* scaling, int R, int N, const LoraSegs& S, const void* base_grad,
+                      void* gX, void* gA, void* gB, float* ws, hipStream_t st) {
+  switch (p.rt) {
+    case 1: return backward_t<DT, 1>(p, G, X, V, T, K, A, B, scaling, R, N, S, base_grad, gX, gA, gB, ws, st);
+    case 2: return backward_t<DT, 2>(p, G, X, V, T, K, A, B, scaling, R, N, S, base_grad, gX, gA, gB, ws, st);
+    case 4: return backward_t<DT, 4>(p, G, X, V, T, K, A, B, scaling, R, N, S, base_grad, gX, gA, gB, ws, st);
+    default: return backward_t<DT, 8>(p, G, X, V, T, K, A, B, scaling, R, N, S, base_grad, gX, gA, gB, ws, st);
+  }
+}
+
+}  // namespace
+
+size_t lora_backward_floats(int T, int K, int N, int R, int n_adapters, int n_seg) {
+  return plan_of(T, K, N, R, n_adapters, n_seg).total;
 }
 
 hipError_t launch_lora_backward(int dt, const void* G, const void* X, const float* V, int T, int K, const void* A,
                                 const void* B, const float* scaling, int R, int N, const LoraSegs& S,
-                                const void* base_grad, void* gX, void* gA, void* gB, float* ws, hipStream_t st) {
+                                int n_adapters, const void* base_grad, void* gX, void* gA, void* gB, float* ws,
+                                hipStream_t st) {
+  const Plan p = plan_of(T, K, N, R, n_adapters, S.n_seg);
   switch (dt) {
-    case DT_F32: return backward_t<DT_F32>(G, X, V, T, K, A, B, scaling, R, N, S, base_grad, gX, gA, gB, ws, st);
-    case DT_F16: return backward_t<DT_F16>(G, X, V, T, K, A, B, scaling, R, N, S, base_grad, gX, gA, gB, ws, st);
-    default: return backward_t<DT_BF16>(G, X, V, T, K, A, B, scaling, R, N, S, base_grad, gX, gA, gB, ws, st);
+    case DT_F32: return backward_d<DT_F32>(p, G, X, V, T, K, A, B, scaling, R, N, S, base_grad, gX, gA, gB, ws, st);
+    case DT_F16: return backward_d<DT_F16>(p, G, X, V, T, K, A, B, scaling, R, N, S, base_grad, gX, gA, gB, ws, st);
+    default: return backward_d<DT_BF16>(p, G, X, V, T, K, A, B, scaling, R, N, S, base_grad, gX, gA, gB, ws, st);
   }
 }
 
