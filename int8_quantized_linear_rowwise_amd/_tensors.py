@@ -41,17 +41,34 @@ def _empty(shape, dtype, device):
     return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _same_device(first: torch.Tensor, **others: Optional[torch.Tensor]) -> None:
-    """The kernels run on `first`'s GPU: every other tensor has to be there too."""
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+def _raw_stream(dev: int) -> int:
+    """The current HIP stream of GPU number `dev` (torch.cuda.current_stream builds a Stream object first, 2 us)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _workspace(ws: Optional[torch.Tensor], need: int, device) -> Optional[torch.Tensor]:
+def _gpu(t: torch.Tensor, name: str) -> int:
+    """The number of the GPU that a call's first tensor is on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    return dev
+
+
+def _ptr(t: Optional[torch.Tensor], name: str, dev: int) -> int:
+    """Device pointer of a tensor that has to be contiguous and on GPU number `dev`; 0 for None."""
+    if t is None:
+        return 0
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on GPU {dev}, as the call's first tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _workspace(ws: Optional[torch.Tensor], need: int, device, dev: int) -> Optional[torch.Tensor]:
     """The caller's uint8 workspace if there is one, else a new one (None when nothing is needed)."""
     if ws is None:
         return _empty((need,), torch.uint8, device) if need else None
-    if ws.dtype != torch.uint8 or ws.numel() < need or ws.device != device:
-        raise ValueError(f"workspace must be uint8 on {device} with at least {need} bytes")
+    if ws.dtype != torch.uint8 or ws.numel() < need or ws.get_device() != dev:
+        raise ValueError(f"workspace must be uint8 on GPU {dev} with at least {need} bytes")
     return ws

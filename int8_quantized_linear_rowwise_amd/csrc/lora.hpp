@@ -27,32 +27,68 @@ __device__ __forceinline__ int seg_adapter(const LoraSegs& S, int s) {
 // Segment s is cut number s + min(start(s) / tm + 1, nb), so the segments
 // begun by tile d are counted by a search 64 wide (every lane of the wave):
 // one load for up to 64 segments, two for up to 4096.
+// Up to 64 segments are held one a lane, so that any tile is found without
+// another access to memory.
 struct LoraTile {
   int t0, t1, adapter;
 };
-__device__ __forceinline__ LoraTile lora_tile(const LoraSegs& S, int d, int T, int tm) {
-  const int lane = threadIdx.x & 63;
-  const int nb = (T + tm - 1) / tm, ns = max(S.n_seg, 1);
+struct SegLanes {
+  int start, adapter;   // of segment min(lane, n_seg - 1)
+};
+__device__ __forceinline__ SegLanes seg_lanes(const LoraSegs& S, int T) {
+  const int s = min((int)(threadIdx.x & 63), max(S.n_seg, 1) - 1);
+  return SegLanes{seg_start(S, s, T), seg_adapter(S, s)};
+}
+
+// How many of the ns segments (in order) satisfy a predicate that holds for a
+// first part of them: pred(start, segment).
+template <typename F>
+__device__ __forceinline__ int count_segments(const LoraSegs& S, const SegLanes& L, int T, F pred) {
+  const int lane = threadIdx.x & 63, ns = max(S.n_seg, 1);
+  if (ns <= 64) return __popcll(__ballot(lane < ns && pred(L.start, lane)));
   int lo = 0, len = ns;
   while (len > 0) {
     const int step = (len + 63) >> 6;
     const int off = (lane + 1) * step - 1;
-    const int s = lo + off;
-    const bool in = off < len && s + min(seg_start(S, s, T) / tm + 1, nb) <= d;
+    const bool in = off < len && pred(seg_start(S, lo + off, T), lo + off);
     const int c = __popcll(__ballot(in));
     lo += c * step;
     len = min(step - 1, len - c * step);
   }
+  return lo;
+}
+
+__device__ __forceinline__ LoraTile lora_tile(const LoraSegs& S, const SegLanes& L, int d, int T, int tm) {
+  const int nb = (T + tm - 1) / tm, ns = max(S.n_seg, 1);
+  const int lo = __builtin_amdgcn_readfirstlane(
+      count_segments(S, L, T, [&](int start, int s) { return s + min(start / tm + 1, nb) <= d; }));
+  int first, last, adapter;
+  if (ns <= 64) {
+    first = __builtin_amdgcn_readlane(L.start, max(lo - 1, 0));
+    last = lo < ns ? __builtin_amdgcn_readlane(L.start, min(lo, 63)) : T;
+    adapter = __builtin_amdgcn_readlane(L.adapter, max(lo - 1, 0));
+  } else {
+    first = seg_start(S, lo - 1, T);
+    last = lo < ns ? seg_start(S, lo, T) : T;
+    adapter = seg_adapter(S, max(lo - 1, 0));
+  }
   const int i = d + 1 - lo;
   LoraTile r;
-  r.t0 = min(max((i - 1) * tm, lo > 0 ? seg_start(S, lo - 1, T) : 0), T);
-  r.t1 = min(min(i * tm, T), lo < ns ? seg_start(S, lo, T) : T);
+  r.t0 = min(max((i - 1) * tm, first), T);
+  r.t1 = min(min(i * tm, T), last);
   if (lo <= 0 || i <= 0) r.t1 = r.t0;
-  r.adapter = lo > 0 ? seg_adapter(S, lo - 1) : -1;
+  r.adapter = lo > 0 ? adapter : -1;
   r.t0 = __builtin_amdgcn_readfirstlane(r.t0);
   r.t1 = __builtin_amdgcn_readfirstlane(r.t1);
   r.adapter = __builtin_amdgcn_readfirstlane(r.adapter);
   return r;
+}
+// Number of the first tile of tokens [i tm, (i + 1) tm): i and the segments that start before.
+__device__ __forceinline__ int first_tile(const LoraSegs& S, const SegLanes& L, int i, int T, int tm) {
+  const int64_t at = (int64_t)i * tm;
+  if (at >= T) return (T + tm - 1) / tm + max(S.n_seg, 1);
+  const int lo = count_segments(S, L, T, [&](int start, int) { return start < at; });
+  return __builtin_amdgcn_readfirstlane(i + lo);
 }
 // Tiles 1 .. lora_tiles() are the ones that can hold rows.
 inline int lora_tiles(int T, const LoraSegs& S, int tm) {

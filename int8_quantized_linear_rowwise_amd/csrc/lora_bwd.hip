@@ -10,12 +10,11 @@
 //   sum of the slices of dV;
 //   x pass: X and base_grad give dx and dA (partial sums by token tile);
 //   sum of the tiles of dA and dB, in a fixed order.
-// A workgroup takes a slice of columns and a tile of tokens of one adapter;
-// its eight waves split the columns, and each holds its part of the weight
+// A workgroup takes a slice of columns and a block of tokens, which it walks
+// tile by tile (the block's tokens of one adapter); its eight waves split the columns, and each holds its part of the weight
 // gradient in registers while it walks the tokens 32 (fp32: 16) at a time. The
-// rows come into registers as they lie, which is the fragment of the product
-// along the features, and go through LDS to be read transposed for the one
-// along the tokens.
+// rows go through LDS, from where they are read along the features for the one
+// product and transposed for the one along the tokens.
 #include "lora.hpp"
 
 namespace i8l {
@@ -39,10 +38,36 @@ struct Tile {
   __device__ static __forceinline__ int swz(int t) {
     return ((t / ROWS) & (PAIRS - 1)) ^ (((t >> 3) & 1) * (PAIRS / 2));
   }
-  // fragment of row t (the lane's), step ks along the columns
-  __device__ static __forceinline__ void put(char* w, int t, int ks, int q, v4u f) {
-    if constexpr (DT == DT_F32) *reinterpret_cast<v4u*>(w + t * ROWB + 64 * ks + 16 * q) = f;
-    else *reinterpret_cast<v4u*>(w + t * ROWB + 32 * ((2 * ks + (q >> 1)) ^ swz(t)) + 16 * (q & 1)) = f;
+  // 16-byte chunk ch of row t
+  __device__ static __forceinline__ v4u& at(char* w, int t, int ch) {
+    if constexpr (DT == DT_F32) return *reinterpret_cast<v4u*>(w + t * ROWB + 16 * ch);
+    else return *reinterpret_cast<v4u*>(w + t * ROWB + 32 * ((ch >> 1) ^ swz(t)) + 16 * (ch & 1));
+  }
+  // The tile as it lies in memory: load i of NI takes RPI rows, CPR lanes side by
+  // side on one row. (A fragment's lanes lie on 16 rows each; loading
+  // fragments straight from memory, 16 bytes a request, held these kernels to
+  // about one request a nanosecond and compute unit.)
+  static constexpr int CPR = WN / Mx<DT>::EL, RPI = 64 / CPR, NI = ST / RPI;
+  // Rows r0 + (8 | 4) q .. along the contraction, columns `col` .. of 4 lanes each as rows: with rows that are ranks,
+  // the operand of a product along the ranks. 16-bit: lane c's column is col(c / 4) + c % 4; fp32: col(0) + c.
+  template <typename F>
+  __device__ static __forceinline__ v4u get_cols(const char* w, int r0, F col, int lane) {
+    const int c = lane & 15;
+    if constexpr (DT == DT_F32) {
+      v4u f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = *reinterpret_cast<const uint32_t*>(w + (r0 + j) * ROWB + 4 * (col(0) + c));
+      return f;
+    } else {
+      v4s h[2];
+      const int x = col(c & 3);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = r0 + 4 * i + (c >> 2);
+        h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(I8L_LDS(w + t * ROWB + 32 * ((x >> 4) ^ swz(t)) + 2 * (x & 15)));
+      }
+      return __builtin_bit_cast(v4u, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
   }
   // columns 16 nt .. + 15 as rows, the tokens along the contraction
   __device__ static __forceinline__ v4u get(const char* w, int nt, int lane) {
@@ -149,16 +174,14 @@ __device__ __forceinline__ float finite_abs(float v) { return __builtin_isfinite
 
 }  // namespace
 
-// dV partial sums P[slice][position][Rp] and dB partial sums dBp[tile][n][Rp] of
-// one tile of tokens and 8 WN columns of G. B's fragments for dV stay in
-// registers; the eight waves' parts of dV meet in LDS.
+// One tile of k_lora_gpass.
 template <int DT, int RT, int WN>
-__global__ __launch_bounds__(512) void k_lora_gpass(const typename Elem<DT>::T* __restrict__ G, int N, int T,
-                                                    const float* __restrict__ V,
-                                                    const typename Elem<DT>::T* __restrict__ B, int R,
-                                                    const float* __restrict__ scaling, LoraSegs S,
-                                                    const int32_t* __restrict__ perm, int tm, float* __restrict__ P,
-                                                    float* __restrict__ dBp, int32_t* __restrict__ tile_adapter) {
+__device__ __forceinline__ void g_tile(const typename Elem<DT>::T* __restrict__ G, int N, int T,
+                                       const float* __restrict__ V, const typename Elem<DT>::T* __restrict__ B, int R,
+                                       const float* __restrict__ scaling, const LoraSegs& S,
+                                       const SegLanes& L, const int32_t* __restrict__ perm, int tm,
+                                       float* __restrict__ P,
+                                       float* __restrict__ dBp, int32_t* __restrict__ tile_adapter, int d) {
   typedef Mx<DT> M;
   typedef typename Elem<DT>::T E;
   typedef Tile<DT, WN> TL;
@@ -171,10 +194,13 @@ __global__ __launch_bounds__(512) void k_lora_gpass(const typename Elem<DT>::T* 
   float* red = reinterpret_cast<float*>(vt + SM::VT);
   float* top8 = red + 8 * ST * LDV;
 
-  const LoraTile tl = lora_tile(S, blockIdx.y + 1, T, tm);
+  const LoraTile tl = lora_tile(S, L, d, T, tm);
   const bool none = tl.t1 <= tl.t0 || tl.adapter < 0;
-  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
-  if (blockIdx.x == 0 && tid == 0) tile_adapter[blockIdx.y] = none ? -1 : tl.adapter;
+  // opaque per tile: hoisted out of the tile loop, the addresses made from it cost 50 registers
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, c = lane & 15, q = lane >> 4;
+  if (blockIdx.x == 0 && tid == 0) tile_adapter[d - 1] = none ? -1 : tl.adapter;
   if (none) return;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   char* mine = sm + wave * TL::BYTES;
@@ -229,20 +255,16 @@ __global__ __launch_bounds__(512) void k_lora_gpass(const typename Elem<DT>::T* 
     for (int n = 0; n < NT; ++n) acc[j][n] = v4f{};
   float run_top = 0.0f, unit = 1.0f;
 
-  v4u g[TT][NK];
+  v4u g[TL::NI];
   float v[SM::PER][2];
+  const int lrow = lane / TL::CPR, lch = lane % TL::CPR;
   auto load = [&](int at) {
+    const int left = N - n0 - EL * lch;
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const int row = row_of(perm, min(at + 16 * i + c, tl.t1 - 1), T);
-      const E* p = G + (int64_t)row * N + n0 + EL * q;
-      if (whole) {
-#pragma unroll
-        for (int k = 0; k < NK; ++k) g[i][k] = ld16<DT>(p + k * KS);
-      } else {
-#pragma unroll
-        for (int k = 0; k < NK; ++k) g[i][k] = ld_frag<DT>(p + k * KS, N - n0 - EL * q - k * KS);
-      }
+    for (int i = 0; i < TL::NI; ++i) {
+      const int row = row_of(perm, min(at + TL::RPI * i + lrow, tl.t1 - 1), T);
+      const E* p = G + (int64_t)row * N + n0 + EL * lch;
+      g[i] = whole ? ld16<DT>(p) : ld_frag<DT>(p, left);
     }
     if (dBp) {
 #pragma unroll
@@ -282,14 +304,14 @@ __global__ __launch_bounds__(512) void k_lora_gpass(const typename Elem<DT>::T* 
         const int e = tid + 512 * x;
         if (e < SM::PAIRS) SM::put_t(vt, e % RP, e / RP, v[x][0], v[x][1], unit);
       }
-#pragma unroll
-      for (int i = 0; i < TT; ++i) {
-        const bool row = at + 16 * i + c < tl.t1;   // rows past the tile must not meet their zeros in V as NaN
-#pragma unroll
-        for (int k = 0; k < NK; ++k) TL::put(mine, 16 * i + c, k, q, row ? g[i][k] : v4u{0u, 0u, 0u, 0u});
-      }
     }
-    const bool more = at + ST < tl.t1;
+    // rows past the tile are zeros: a NaN there must not meet their zeros in V
+#pragma unroll
+    for (int i = 0; i < TL::NI; ++i) {
+      const int t = TL::RPI * i + lrow;
+      TL::at(mine, t, lch) = at + t < tl.t1 ? g[i] : v4u{0u, 0u, 0u, 0u};
+    }
+    if (at + ST < tl.t1) load(at + ST);
     if (P) {
       const float f = DT == DT_F16 ? inv_pow2(bunit) : 1.0f;
 #pragma unroll
@@ -301,9 +323,8 @@ __global__ __launch_bounds__(512) void k_lora_gpass(const typename Elem<DT>::T* 
           for (int j = 0; j < RTH; ++j) {
             dv[i][j] = v4f{};
 #pragma unroll
-            for (int k = 0; k < NK; ++k) dv[i][j] = M::mma(g[i][k], fb[h * RTH + j][k], dv[i][j]);
+            for (int k = 0; k < NK; ++k) dv[i][j] = M::mma(TL::at(mine, 16 * i + c, 4 * k + q), fb[h * RTH + j][k], dv[i][j]);
           }
-        if (h == RH - 1 && more) load(at + ST);
 #pragma unroll
         for (int i = 0; i < TT; ++i)
 #pragma unroll
@@ -323,7 +344,6 @@ __global__ __launch_bounds__(512) void k_lora_gpass(const typename Elem<DT>::T* 
         if (h + 1 < RH) __syncthreads();
       }
     } else {
-      if (more) load(at + ST);
       __syncthreads();
     }
     if (dBp) {
@@ -333,7 +353,7 @@ __global__ __launch_bounds__(512) void k_lora_gpass(const typename Elem<DT>::T* 
   }
   if (dBp) {
     const float f = DT == DT_F16 ? scale * inv_pow2(unit) : scale;
-    float* o = dBp + (int64_t)blockIdx.y * N * RP;
+    float* o = dBp + (int64_t)(d - 1) * N * RP;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -346,17 +366,36 @@ __global__ __launch_bounds__(512) void k_lora_gpass(const typename Elem<DT>::T* 
   }
 }
 
-// dx and the partial sums dAp[tile][r][Kp] of one tile of tokens and 8 WN
-// columns of X. dx is taken transposed, as the forward's expand, with A's
-// fragments in registers.
+// dV partial sums P[slice][position][Rp] and dB partial sums dBp[tile][n][Rp] of
+// 8 WN columns of G and one tile of tokens, or with BLOCKS tokens [y tm, (y + 1)
+// tm) tile by tile. B's fragments
+// for dV stay in registers; the eight waves' parts of dV meet in LDS.
+template <int DT, int RT, int WN, bool BLOCKS>
+__global__ __launch_bounds__(512) void k_lora_gpass(const typename Elem<DT>::T* __restrict__ G, int N, int T,
+                                                    const float* __restrict__ V,
+                                                    const typename Elem<DT>::T* __restrict__ B, int R,
+                                                    const float* __restrict__ scaling, LoraSegs S,
+                                                    const int32_t* __restrict__ perm, int tm, float* __restrict__ P,
+                                                    float* __restrict__ dBp, int32_t* __restrict__ tile_adapter) {
+  const SegLanes L = seg_lanes(S, T);
+  if constexpr (!BLOCKS) {
+    g_tile<DT, RT, WN>(G, N, T, V, B, R, scaling, S, L, perm, tm, P, dBp, tile_adapter, blockIdx.y + 1);
+  } else {
+    const int d1 = first_tile(S, L, blockIdx.y + 1, T, tm);
+    for (int d = max(first_tile(S, L, blockIdx.y, T, tm), 1); d < d1; ++d) {
+      g_tile<DT, RT, WN>(G, N, T, V, B, R, scaling, S, L, perm, tm, P, dBp, tile_adapter, d);
+      __syncthreads();
+    }
+  }
+}
+
+// One tile of k_lora_xpass.
 template <int DT, int RT, int WN>
-__global__ __launch_bounds__(512) void k_lora_xpass(const typename Elem<DT>::T* __restrict__ X, int K, int T,
-                                                    const float* __restrict__ dV,
-                                                    const typename Elem<DT>::T* __restrict__ A, int R, LoraSegs S,
-                                                    const int32_t* __restrict__ perm, int tm,
-                                                    const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
-                                                    float* __restrict__ dAp, int Kp,
-                                                    int32_t* __restrict__ tile_adapter) {
+__device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ X, int K, int T,
+                                       const float* __restrict__ dV, const typename Elem<DT>::T* __restrict__ A, int R,
+                                       const LoraSegs& S, const SegLanes& L, const int32_t* __restrict__ perm, int tm,
+                                       const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
+                                       float* __restrict__ dAp, int Kp, int32_t* __restrict__ tile_adapter, int d) {
   typedef Mx<DT> M;
   typedef typename Elem<DT>::T E;
   typedef Tile<DT, WN> TL;
@@ -369,75 +408,72 @@ __global__ __launch_bounds__(512) void k_lora_xpass(const typename Elem<DT>::T* 
   char* vr = vt + SM::VT;
   float* top8 = reinterpret_cast<float*>(vr + SM::VR);
 
-  const LoraTile tl = lora_tile(S, blockIdx.y + 1, T, tm);
+  const LoraTile tl = lora_tile(S, L, d, T, tm);
   const bool none = tl.t1 <= tl.t0 || tl.adapter < 0;
-  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, q = lane >> 4;
-  if (dAp && blockIdx.x == 0 && tid == 0) tile_adapter[blockIdx.y] = none ? -1 : tl.adapter;
+  // opaque per tile: hoisted out of the tile loop, the addresses made from it cost 50 registers
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, c = lane & 15, q = lane >> 4;
+  if (dAp && blockIdx.x == 0 && tid == 0) tile_adapter[d - 1] = none ? -1 : tl.adapter;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   char* mine = sm + wave * TL::BYTES;
   const int k0 = blockIdx.x * 8 * WN + wave * WN;
   const bool whole = k0 + WN <= K;
 
-  v4u x[TT][NK], b[TT][NK];
-  int row[TT];
+  v4u x[TL::NI], b[TL::NI];
   float v[SM::PER][2];
-  auto rows = [&](int at) {
-#pragma unroll
-    for (int i = 0; i < TT; ++i) row[i] = row_of(perm, min(at + 16 * i + c, tl.t1 - 1), T);
+  const int lrow = lane / TL::CPR, lch = lane % TL::CPR, left = K - k0 - EL * lch;
+  auto spot = [&](int at, int i) {
+    return (int64_t)row_of(perm, min(at + TL::RPI * i + lrow, tl.t1 - 1), T) * K + k0 + EL * lch;
   };
-  auto load_rows = [&](const E* from, v4u (&f)[TT][NK]) {
+  auto load_rows = [&](const E* from, int at, v4u (&f)[TL::NI]) {
 #pragma unroll
-    for (int i = 0; i < TT; ++i) {
-      const E* p = from + (int64_t)row[i] * K + k0 + EL * q;
-      if (whole) {
-#pragma unroll
-        for (int k = 0; k < NK; ++k) f[i][k] = ld16<DT>(p + k * KS);
-      } else {
-#pragma unroll
-        for (int k = 0; k < NK; ++k) f[i][k] = ld_frag<DT>(p + k * KS, K - k0 - EL * q - k * KS);
-      }
+    for (int i = 0; i < TL::NI; ++i) {
+      const E* p = from + spot(at, i);
+      f[i] = whole ? ld16<DT>(p) : ld_frag<DT>(p, left);
     }
   };
-  auto store_rows = [&](int at, int i, int k, v4u f) {
-    if (at + 16 * i + c < tl.t1) {
-      E* p = out + (int64_t)row[i] * K + k0 + EL * q + k * KS;
+  auto store_row = [&](int at, int i, v4u f) {
+    if (at + TL::RPI * i + lrow < tl.t1) {
+      E* p = out + spot(at, i);
       if (whole) st16<DT>(p, f);
-      else st_frag<DT>(p, f, K - k0 - EL * q - k * KS);
+      else st_frag<DT>(p, f, left);
     }
   };
 
   if (none) {
     if (out == nullptr || base == out) return;
     for (int at = tl.t0; at < tl.t1; at += ST) {
-      rows(at);
-      if (base) load_rows(base, b);
+      if (base) load_rows(base, at, b);
 #pragma unroll
-      for (int i = 0; i < TT; ++i)
-#pragma unroll
-        for (int k = 0; k < NK; ++k) store_rows(at, i, k, base ? b[i][k] : v4u{0u, 0u, 0u, 0u});
+      for (int i = 0; i < TL::NI; ++i) store_row(at, i, base ? b[i] : v4u{0u, 0u, 0u, 0u});
     }
     return;
   }
 
-  // A[a][r][k] with r along the contraction, rows k in the order that gives a lane consecutive k of the product
+  // A[a][r][k] with r along the contraction, rows k in the order that gives a
+  // lane consecutive k of the product: rows of A through the wave's tile, read
+  // transposed
   v4u fa[NK][UN][NB];
   if (out) {
-    const E* Aa = A + (int64_t)tl.adapter * R * K;
+    const E* Aa = A + (int64_t)tl.adapter * R * K + k0 + EL * lch;
 #pragma unroll
-    for (int blk = 0; blk < NK; ++blk)
+    for (int r0 = 0; r0 < RP; r0 += ST) {
 #pragma unroll
-      for (int u = 0; u < UN; ++u)
+      for (int i = 0; i < TL::NI; ++i) {
+        const int r = r0 + TL::RPI * i + lrow;
+        v4u f = {0u, 0u, 0u, 0u};
+        if (r < R) f = whole ? ld16<DT>(Aa + (int64_t)r * K) : ld_frag<DT>(Aa + (int64_t)r * K, left);
+        TL::at(mine, TL::RPI * i + lrow, lch) = f;
+      }
 #pragma unroll
-        for (int s = 0; s < NB; ++s) {
-          const int k = k0 + blk * KS + (M::F32 ? c : 8 * (c >> 2) + 4 * u + (c & 3));
-          fa[blk][u][s] = v4u{0u, 0u, 0u, 0u};
+      for (int blk = 0; blk < NK; ++blk)
 #pragma unroll
-          for (int e = 0; e < EL; ++e) {
-            const int r = (M::F32 ? 16 * s + 4 * q : RT == 1 ? 8 * (q & 1) : 32 * s + 8 * q) + e;
-            const E w = Aa[(int64_t)min(r, R - 1) * K + min(k, K - 1)];
-            frag_set<DT>(fa[blk][u][s], e, k < K && r < R ? w : Elem<DT>::from_f32(0.0f));
-          }
+        for (int u = 0; u < UN; ++u) {
+          auto col = [&](int g) { return blk * KS + (M::F32 ? 0 : 8 * g + 4 * u); };
+          fa[blk][u][r0 / ST] = TL::get_cols(mine, M::F32 ? 4 * q : RT == 1 ? 8 * (q & 1) : 8 * q, col, lane);
         }
+    }
   }
 
   v4f acc[RT][NT];
@@ -456,9 +492,8 @@ __global__ __launch_bounds__(512) void k_lora_xpass(const typename Elem<DT>::T* 
         v[y][h] = e < SM::PAIRS && r < R && t + h < tl.t1 ? dV[(int64_t)(t + h) * RP + r] : 0.0f;
     }
   };
-  rows(tl.t0);
-  if (dAp) load_rows(X, x);
-  if (out && base) load_rows(base, b);
+  if (dAp) load_rows(X, tl.t0, x);
+  if (out && base) load_rows(base, tl.t0, b);
   load_v(tl.t0);
   for (int at = tl.t0; at < tl.t1; at += ST) {
     if constexpr (DT == DT_F16) {
@@ -495,21 +530,25 @@ __global__ __launch_bounds__(512) void k_lora_xpass(const typename Elem<DT>::T* 
     }
     if (dAp) {
 #pragma unroll
-      for (int i = 0; i < TT; ++i) {
-        const bool in = at + 16 * i + c < tl.t1;
-#pragma unroll
-        for (int k = 0; k < NK; ++k) TL::put(mine, 16 * i + c, k, q, in ? x[i][k] : v4u{0u, 0u, 0u, 0u});
+      for (int i = 0; i < TL::NI; ++i) {
+        const int t = TL::RPI * i + lrow;
+        TL::at(mine, t, lch) = at + t < tl.t1 ? x[i] : v4u{0u, 0u, 0u, 0u};
       }
     }
-    const int here[2] = {row[0], row[TT - 1]};
     const bool more = at + ST < tl.t1;
     if (more) {
-      rows(at + ST);
-      if (dAp) load_rows(X, x);
+      if (dAp) load_rows(X, at + ST, x);
       load_v(at + ST);
     }
     __syncthreads();
+    if (dAp) along_tokens<DT, RT, WN>(mine, vt, lane, acc);
     if (out) {
+      // base through the wave's tile into the product's layout, dx back the same way
+      if (base) {
+#pragma unroll
+        for (int i = 0; i < TL::NI; ++i) TL::at(mine, TL::RPI * i + lrow, lch) = b[i];
+        if (more) load_rows(base, at + ST, b);
+      }
       const float f = DT == DT_F16 ? inv_pow2(sub) : 1.0f;
 #pragma unroll
       for (int i = 0; i < TT; ++i) {
@@ -520,34 +559,29 @@ __global__ __launch_bounds__(512) void k_lora_xpass(const typename Elem<DT>::T* 
                             M::F32 ? 16 * s + 4 * q : RT == 1 ? 8 * (q & 1) : 32 * (s % NB) + 8 * q);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
-          v4f d[UN];
+          v4f w[UN];
 #pragma unroll
           for (int u = 0; u < UN; ++u) {
-            d[u] = v4f{};
+            w[u] = v4f{};
 #pragma unroll
-            for (int s = 0; s < NS; ++s) d[u] = M::mma(fa[k][u][s % NB], fv[s], d[u]);
+            for (int s = 0; s < NS; ++s) w[u] = M::mma(fa[k][u][s % NB], fv[s], w[u]);
           }
+          v4u& place = TL::at(mine, 16 * i + c, 4 * k + q);
           float y[EL];
-          frag_f32<DT>(base ? b[i][k] : v4u{0u, 0u, 0u, 0u}, y);
+          frag_f32<DT>(base ? place : v4u{0u, 0u, 0u, 0u}, y);
 #pragma unroll
-          for (int e = 0; e < EL; ++e) y[e] = __builtin_fmaf(f, d[e >> 2][e & 3], y[e]);
-          if (at + 16 * i + c < tl.t1) {
-            E* p = out + (int64_t)here[i] * K + k0 + EL * q + k * KS;
-            if (whole) st16<DT>(p, frag_of<DT>(y));
-            else st_frag<DT>(p, frag_of<DT>(y), K - k0 - EL * q - k * KS);
-          }
+          for (int e = 0; e < EL; ++e) y[e] = __builtin_fmaf(f, w[e >> 2][e & 3], y[e]);
+          place = frag_of<DT>(y);
         }
       }
-      if (more && base) load_rows(base, b);
-    }
-    if (dAp) {
-      along_tokens<DT, RT, WN>(mine, vt, lane, acc);
+#pragma unroll
+      for (int i = 0; i < TL::NI; ++i) store_row(at, i, TL::at(mine, TL::RPI * i + lrow, lch));
     }
     __syncthreads();
   }
   if (dAp) {
     const float f = DT == DT_F16 ? inv_pow2(unit) : 1.0f;
-    float* o = dAp + (int64_t)blockIdx.y * R * Kp;
+    float* o = dAp + (int64_t)(d - 1) * R * Kp;
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
       const int r = 16 * j + c;
@@ -561,34 +595,61 @@ __global__ __launch_bounds__(512) void k_lora_xpass(const typename Elem<DT>::T* 
   }
 }
 
-// dV = the sum of P's slices, four values a thread.
-__global__ __launch_bounds__(256) void k_lora_sum_slices(const float* __restrict__ P, int slices, int64_t n4,
-                                                         float* __restrict__ dV) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n4) return;
-  const v4f* p = reinterpret_cast<const v4f*>(P) + i;
-  v4f s = {};
-#pragma unroll 8
-  for (int k = 0; k < slices; ++k) s += p[k * n4];
-  reinterpret_cast<v4f*>(dV)[i] = s;
+// dx and the partial sums dAp[tile][r][Kp] of 8 WN columns of X and the same tokens. dx is taken transposed, as the forward's expand,
+// with A's fragments in registers.
+template <int DT, int RT, int WN, bool BLOCKS>
+__global__ __launch_bounds__(512, RT == 1 ? 4 : 2) void k_lora_xpass(const typename Elem<DT>::T* __restrict__ X, int K, int T,
+                                                    const float* __restrict__ dV,
+                                                    const typename Elem<DT>::T* __restrict__ A, int R, LoraSegs S,
+                                                    const int32_t* __restrict__ perm, int tm,
+                                                    const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
+                                                    float* __restrict__ dAp, int Kp,
+                                                    int32_t* __restrict__ tile_adapter) {
+  const SegLanes L = seg_lanes(S, T);
+  if constexpr (!BLOCKS) {
+    x_tile<DT, RT, WN>(X, K, T, dV, A, R, S, L, perm, tm, base, out, dAp, Kp, tile_adapter, blockIdx.y + 1);
+  } else {
+    const int d1 = first_tile(S, L, blockIdx.y + 1, T, tm);
+    for (int d = max(first_tile(S, L, blockIdx.y, T, tm), 1); d < d1; ++d) {
+      x_tile<DT, RT, WN>(X, K, T, dV, A, R, S, L, perm, tm, base, out, dAp, Kp, tile_adapter, d);
+      __syncthreads();
+    }
+  }
 }
 
-// One weight gradient: sums of tiles [tile][rows][ld] into out [adapter][rows][width].
+// One weight gradient: sums of tiles [tile][rows][ld] into out
+// [adapter][rows][width], in tile order.
 struct TileSum {
   const float* part;
   const int32_t* adapter;
   void* out;
-  int tiles, rows, ld, width, blocks;   // blocks: workgroups of 1024 values
+  int tiles, rows, ld, width, blocks;   // blocks: workgroups of 1024 values for an adapter
 };
+// dV: the sum of P's slices, four values a thread.
+struct SliceSum {
+  const float* part;
+  float* out;
+  int64_t n4;
+  int slices, blocks;   // blocks: workgroups of 1024 values
+};
+// Workgroups: the slices' first, then the tiles', adapter after adapter.
 template <int DT>
-__global__ __launch_bounds__(256) void k_lora_sum_tiles(TileSum a, TileSum b) {
+__global__ __launch_bounds__(256) void k_lora_sum(SliceSum v, TileSum s) {
   typedef typename Elem<DT>::T E;
   __shared__ int list[256];
   __shared__ int count;
-  const bool first = (int)blockIdx.x < a.blocks;
-  const TileSum s = first ? a : b;
-  const int ad = blockIdx.y;
-  const int64_t e = ((int64_t)(first ? blockIdx.x : blockIdx.x - a.blocks) * 256 + threadIdx.x) * 4;
+  if ((int)blockIdx.x < v.blocks) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= v.n4) return;
+    const v4f* p = reinterpret_cast<const v4f*>(v.part) + i;
+    v4f sum = {};
+#pragma unroll 8
+    for (int k = 0; k < v.slices; ++k) sum += p[k * v.n4];
+    reinterpret_cast<v4f*>(v.out)[i] = sum;
+    return;
+  }
+  const int id = blockIdx.x - v.blocks, ad = id / s.blocks;
+  const int64_t e = ((int64_t)(id - ad * s.blocks) * 256 + threadIdx.x) * 4;
   const int64_t each = (int64_t)s.rows * s.ld;
   const float* p = s.part + min(e, each - 4);
   v4f sum = {};
@@ -609,7 +670,7 @@ __global__ __launch_bounds__(256) void k_lora_sum_tiles(TileSum a, TileSum b) {
     }
     __syncthreads();
     const int n = count;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < n; ++i) sum += *reinterpret_cast<const v4f*>(p + list[i] * each);
   }
   if (e >= each) return;
@@ -684,7 +745,7 @@ namespace {
 // Sizes of the launches and of the workspace; of the shape alone.
 struct Plan {
   int rt, slices, tm_g, tiles_g, tm_x, tiles_x, kp;
-  bool wide_g, wide_x, sort;
+  bool wide_g, wide_x, sort, by_tile_g, by_tile_x;   // by_tile: a workgroup a tile, where that fills the chip once
   size_t p, dv, dbp, dap, ad_g, ad_x, perm, starts, total;   // offsets in floats
 };
 
@@ -693,26 +754,36 @@ constexpr int wide_g(int rt) { return rt <= 2 ? 128 : rt == 4 ? 64 : 32; }
 constexpr int wide_x(int rt) { return rt <= 4 ? 64 : 32; }
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Tokens of a tile: enough tiles for `want` workgroups, 64 to 2048 tokens.
-int tile_tokens(int T, int slices, int want) {
-  int64_t tm = (int64_t)T * slices / want;
-  tm = (tm + 31) / 32 * 32;
-  return tm < 64 ? 64 : tm > 2048 ? 2048 : (int)tm;
+// Tokens of a workgroup, a multiple of 32 and at least 64: the number of token
+// blocks that fills the chip's 256 compute units `rounds` times, never one more.
+int tile_tokens(int T, int slices, int rounds) {
+  const int blocks = 256 * rounds / slices;
+  const int tm = (cdiv(T, blocks > 0 ? blocks : 1) + 31) / 32 * 32;
+  return tm < 64 ? 64 : tm;
 }
 
 Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
   Plan p = {};
   p.rt = rank_tiles(R);
   const int rp = 16 * p.rt;
+  // Sorted by adapter there are as many partial sums as adapters instead of
+  // segments. Up to 64 segments are cheaper as they are: at 16 segments of four
+  // adapters (16384 tokens, 8192 -> 28672, rank 32) sorting took 13 us and the
+  // rows' indirection 45 us, against 25 us less in partial sums.
   p.sort = n_seg > 64 && n_seg > n_adapters + 1;
   const LoraSegs S = {nullptr, nullptr, p.sort ? n_adapters + 1 : n_seg, n_adapters};
   p.wide_g = (int64_t)cdiv(N, 8 * wide_g(p.rt)) * cdiv(T, 64) >= 256;
   p.wide_x = (int64_t)cdiv(K, 8 * wide_x(p.rt)) * cdiv(T, 64) >= 256;
   p.slices = cdiv(N, 8 * (p.wide_g ? wide_g(p.rt) : 32));
-  p.tm_g = tile_tokens(T, p.slices, 256);
+  p.slices = p.slices > 0 ? p.slices : 1;
+  p.tm_g = tile_tokens(T, p.slices, 1);
   p.tiles_g = lora_tiles(T, S, p.tm_g);
-  p.tm_x = tile_tokens(T, cdiv(K, 8 * (p.wide_x ? wide_x(p.rt) : 32)), 512);
+  const int slices_x = cdiv(K, 8 * (p.wide_x ? wide_x(p.rt) : 32));
+  const int rounds_x = p.rt == 1 ? 2 : 1;   // rank 16 leaves room for two workgroups a unit
+  p.tm_x = tile_tokens(T, slices_x > 0 ? slices_x : 1, rounds_x);
   p.tiles_x = lora_tiles(T, S, p.tm_x);
+  p.by_tile_g = (int64_t)p.tiles_g * p.slices <= 280;
+  p.by_tile_x = (int64_t)p.tiles_x * slices_x <= 280 * rounds_x;
   p.kp = (K + 15) / 16 * 16;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -732,33 +803,33 @@ Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
   return p;
 }
 
-template <int DT, int RT, int WN>
+template <int DT, int RT, int WN, bool BLOCKS>
 hipError_t g_pass(const Plan& p, const void* G, const float* V, int T, const void* B, const float* scaling, int R,
                   int N, const LoraSegs& S, const int32_t* perm, float* P, float* dBp, int32_t* ad, hipStream_t st) {
   typedef typename Elem<DT>::T E;
   typedef Tile<DT, WN> TL;
   constexpr int rw = RT < 4 ? 16 * RT : 64;
   constexpr int lds = 8 * TL::BYTES + Small<DT, RT>::VT + 8 * TL::ST * (rw + 4) * 4 + 32;
-  auto kern = k_lora_gpass<DT, RT, WN>;
+  auto kern = k_lora_gpass<DT, RT, WN, BLOCKS>;
   static std::atomic<uint64_t> done{0};
   const hipError_t e = lds_limit_once((const void*)kern, lds, done);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(p.slices, p.tiles_g), dim3(512), lds, st, static_cast<const E*>(G), N, T, V,
+  hipLaunchKernelGGL(kern, dim3(p.slices, BLOCKS ? cdiv(T, p.tm_g) : p.tiles_g), dim3(512), lds, st, static_cast<const E*>(G), N, T, V,
                      static_cast<const E*>(B), R, scaling, S, perm, p.tm_g, P, dBp, ad);
   return hipGetLastError();
 }
 
-template <int DT, int RT, int WN>
+template <int DT, int RT, int WN, bool BLOCKS>
 hipError_t x_pass(const Plan& p, const void* X, int T, int K, const float* dV, const void* A, int R,
                   const LoraSegs& S, const int32_t* perm, const void* base, void* out, float* dAp, int32_t* ad,
                   hipStream_t st) {
   typedef typename Elem<DT>::T E;
   constexpr int lds = 8 * Tile<DT, WN>::BYTES + Small<DT, RT>::VT + Small<DT, RT>::VR + 32;
-  auto kern = k_lora_xpass<DT, RT, WN>;
+  auto kern = k_lora_xpass<DT, RT, WN, BLOCKS>;
   static std::atomic<uint64_t> done{0};
   const hipError_t e = lds_limit_once((const void*)kern, lds, done);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(cdiv(K, 8 * WN), p.tiles_x), dim3(512), lds, st, static_cast<const E*>(X), K, T, dV,
+  hipLaunchKernelGGL(kern, dim3(cdiv(K, 8 * WN), BLOCKS ? cdiv(T, p.tm_x) : p.tiles_x), dim3(512), lds, st, static_cast<const E*>(X), K, T, dV,
                      static_cast<const E*>(A), R, S, perm, p.tm_x, static_cast<const E*>(base), static_cast<E*>(out),
                      dAp, p.kp, ad);
   return hipGetLastError();
@@ -784,34 +855,42 @@ hipError_t backward_t(const Plan& p, const void* G, const void* X, const float* 
     perm = to;
     S = LoraSegs{starts, nullptr, na + 1, na};
   }
+  const int rp = 16 * RT;
+  SliceSum slices = {};
+  TileSum tiles = {};
   if (rows && na > 0 && N > 0 && (want_dv || gB)) {
     float* P = !want_dv ? nullptr : p.slices > 1 ? ws + p.p : dV;
     float* dBp = gB ? ws + p.dbp : nullptr;
-    e = p.wide_g ? g_pass<DT, RT, wide_g(RT)>(p, G, V, T, B, scaling, R, N, S, perm, P, dBp, ad_g, st)
-                 : g_pass<DT, RT, 32>(p, G, V, T, B, scaling, R, N, S, perm, P, dBp, ad_g, st);
+    auto pass = p.wide_g ? (p.by_tile_g ? g_pass<DT, RT, wide_g(RT), false> : g_pass<DT, RT, wide_g(RT), true>)
+                         : (p.by_tile_g ? g_pass<DT, RT, 32, false> : g_pass<DT, RT, 32, true>);
+    e = pass(p, G, V, T, B, scaling, R, N, S, perm, P, dBp, ad_g, st);
     if (e != hipSuccess) return e;
     if (want_dv && p.slices > 1) {
       const int64_t n4 = (int64_t)T * 4 * RT;
-      hipLaunchKernelGGL(k_lora_sum_slices, dim3(cdiv(n4, 256)), dim3(256), 0, st, P, p.slices, n4, dV);
+      slices = SliceSum{P, dV, n4, p.slices, cdiv(n4, 256)};
     }
   }
+  // beside the sum of dV's slices: dB is whole after the g pass
+  if (gB && na > 0 && R > 0 && N > 0)
+    tiles = TileSum{ws + p.dbp, ad_g, gB, rows ? p.tiles_g : 0, N, rp, R, cdiv((int64_t)N * rp, 1024)};
+  if (slices.blocks + tiles.blocks > 0)
+    hipLaunchKernelGGL(k_lora_sum<DT>, dim3((unsigned)((int64_t)slices.blocks + (int64_t)tiles.blocks * na)), dim3(256),
+                       0, st, slices, tiles);
   const bool no_dv = N == 0;   // dV = 0: nothing reaches A or X
   if (rows && K > 0 && (gX || (gA && na > 0))) {
     LoraSegs Sx = S;
     if (no_dv) Sx.n_adapters = 0;
     float* dAp = gA && na > 0 ? ws + p.dap : nullptr;
-    e = p.wide_x ? x_pass<DT, RT, wide_x(RT)>(p, X, T, K, dV, A, R, Sx, perm, base_grad, gX, dAp, ad_x, st)
-                 : x_pass<DT, RT, 32>(p, X, T, K, dV, A, R, Sx, perm, base_grad, gX, dAp, ad_x, st);
+    auto pass = p.wide_x ? (p.by_tile_x ? x_pass<DT, RT, wide_x(RT), false> : x_pass<DT, RT, wide_x(RT), true>)
+                         : (p.by_tile_x ? x_pass<DT, RT, 32, false> : x_pass<DT, RT, 32, true>);
+    e = pass(p, X, T, K, dV, A, R, Sx, perm, base_grad, gX, dAp, ad_x, st);
     if (e != hipSuccess) return e;
   }
-  TileSum a = {}, b = {};
-  const int rp = 16 * RT;
-  if (gA && na > 0 && R > 0 && K > 0)
-    a = TileSum{ws + p.dap, ad_x, gA, rows ? p.tiles_x : 0, R, p.kp, K, cdiv((int64_t)R * p.kp, 1024)};
-  if (gB && na > 0 && R > 0 && N > 0)
-    b = TileSum{ws + p.dbp, ad_g, gB, rows ? p.tiles_g : 0, N, rp, R, cdiv((int64_t)N * rp, 1024)};
-  if (a.blocks + b.blocks > 0)
-    hipLaunchKernelGGL(k_lora_sum_tiles<DT>, dim3(a.blocks + b.blocks, na), dim3(256), 0, st, a, b);
+  if (gA && na > 0 && R > 0 && K > 0) {
+    tiles = TileSum{ws + p.dap, ad_x, gA, rows ? p.tiles_x : 0, R, p.kp, K, cdiv((int64_t)R * p.kp, 1024)};
+    hipLaunchKernelGGL(k_lora_sum<DT>, dim3((unsigned)((int64_t)tiles.blocks * na)), dim3(256), 0, st, SliceSum{},
+                       tiles);
+  }
   return hipGetLastError();
 }
 

@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from ._lib import I8L_LORA_MAX_RANK, check, lib
-from ._tensors import _check_out, _code, _dev, _empty, _same_device, _stream, _workspace
+from ._tensors import _check_out, _code, _empty, _gpu, _ptr, _raw_stream, _workspace
 
 
 def _segments(seg_offsets, seg_adapter):
@@ -58,21 +58,24 @@ def lora_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scaling: tor
     N = B.shape[1] if B.dim() == 3 else -1
     n, R = _adapters(A, B, scaling, X.dtype, K, N)
     S = _segments(seg_offsets, seg_adapter)
-    _check_out(base, (T, N), X.dtype, "base")
-    _check_out(out, (T, N), X.dtype, "out")
-    _check_out(v, (T, R), torch.float32, "v")
-    _same_device(X, A=A, B=B, scaling=scaling, seg_offsets=seg_offsets, seg_adapter=seg_adapter, base=base, out=out,
-                 v=v)
+    if base is not None:
+        _check_out(base, (T, N), X.dtype, "base")
+    if out is not None:
+        _check_out(out, (T, N), X.dtype, "out")
+    if v is not None:
+        _check_out(v, (T, R), torch.float32, "v")
+    dev = _gpu(X, "X")
     if out is None:
         out = _empty((T, N), X.dtype, X.device)
     if v is None and with_v:
         v = _empty((T, R), torch.float32, X.device)
-    ws = _workspace(workspace, lib.int8_lora_forward_workspace_bytes(T, K, N, R, S), X.device)
-    check(lib.int8_lora_forward(_dev(X, "X"), _code(X), T, K, _dev(A, "A"), _dev(B, "B"), _dev(scaling, "scaling"), n,
-                                R, N, _dev(seg_offsets, "seg_offsets"), _dev(seg_adapter, "seg_adapter"), S,
-                                _dev(base, "base"), _dev(out, "out"), _dev(v, "v"),
-                                ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0,
-                                _stream(X.device)),
+    need = lib.int8_lora_forward_workspace_bytes(T, K, N, R, S)
+    ws = _workspace(workspace, need, X.device, dev)
+    check(lib.int8_lora_forward(_ptr(X, "X", dev), _code(X), T, K, _ptr(A, "A", dev), _ptr(B, "B", dev),
+                                _ptr(scaling, "scaling", dev), n, R, N, _ptr(seg_offsets, "seg_offsets", dev),
+                                _ptr(seg_adapter, "seg_adapter", dev), S, _ptr(base, "base", dev),
+                                _ptr(out, "out", dev), _ptr(v, "v", dev), _ptr(ws, "workspace", dev),
+                                0 if ws is None else ws.numel(), _raw_stream(dev)),
           "int8_lora_forward")
     return (out, v) if with_v else out
 
@@ -98,23 +101,23 @@ def lora_backward(G: torch.Tensor, X: torch.Tensor, V: torch.Tensor, A: torch.Te
         raise ValueError(f"V must be float32 of shape {(T, R)}")
     _check_out(base_grad, (T, K), X.dtype, "base_grad")
     _check_out(grad_X, (T, K), X.dtype, "grad_X")
-    _check_out(grad_A, tuple(A.shape), X.dtype, "grad_A")
-    _check_out(grad_B, tuple(B.shape), X.dtype, "grad_B")
-    _same_device(G, X=X, V=V, A=A, B=B, scaling=scaling, seg_offsets=seg_offsets, seg_adapter=seg_adapter,
-                 base_grad=base_grad, grad_X=grad_X, grad_A=grad_A, grad_B=grad_B)
+    _check_out(grad_A, A.shape, X.dtype, "grad_A")
+    _check_out(grad_B, B.shape, X.dtype, "grad_B")
+    dev = _gpu(G, "G")
     if grad_X is None and with_grad_X:
-        grad_X = _empty((T, K), X.dtype, X.device)
+        grad_X = torch.empty_like(X, memory_format=torch.contiguous_format)
     if grad_A is None and with_grad_A:
-        grad_A = _empty(A.shape, X.dtype, X.device)
+        grad_A = torch.empty_like(A, memory_format=torch.contiguous_format)
     if grad_B is None and with_grad_B:
-        grad_B = _empty(B.shape, X.dtype, X.device)
-    ws = _workspace(workspace, lib.int8_lora_backward_workspace_bytes(T, K, N, R, n, S), X.device)
-    check(lib.int8_lora_backward(_dev(G, "G"), _dev(X, "X"), _dev(V, "V"), _code(X), T, K, _dev(A, "A"), _dev(B, "B"),
-                                 _dev(scaling, "scaling"), n, R, N, _dev(seg_offsets, "seg_offsets"),
-                                 _dev(seg_adapter, "seg_adapter"), S, _dev(base_grad, "base_grad"),
-                                 _dev(grad_X, "grad_X"), _dev(grad_A, "grad_A"), _dev(grad_B, "grad_B"),
-                                 ws.data_ptr() if ws is not None else 0, ws.numel() if ws is not None else 0,
-                                 _stream(X.device)),
+        grad_B = torch.empty_like(B, memory_format=torch.contiguous_format)
+    need = lib.int8_lora_backward_workspace_bytes(T, K, N, R, n, S)
+    ws = _workspace(workspace, need, X.device, dev)
+    check(lib.int8_lora_backward(_ptr(G, "G", dev), _ptr(X, "X", dev), _ptr(V, "V", dev), _code(X), T, K,
+                                 _ptr(A, "A", dev), _ptr(B, "B", dev), _ptr(scaling, "scaling", dev), n, R, N,
+                                 _ptr(seg_offsets, "seg_offsets", dev), _ptr(seg_adapter, "seg_adapter", dev), S,
+                                 _ptr(base_grad, "base_grad", dev), _ptr(grad_X, "grad_X", dev),
+                                 _ptr(grad_A, "grad_A", dev), _ptr(grad_B, "grad_B", dev),
+                                 _ptr(ws, "workspace", dev), 0 if ws is None else ws.numel(), _raw_stream(dev)),
           "int8_lora_backward")
     return grad_X, grad_A, grad_B
 

@@ -7,7 +7,7 @@ from typing import Optional
 import torch
 
 from ._lib import check, lib
-from ._tensors import _check_out, _code, _dev, _empty, _same_device, _stream, _workspace
+from ._tensors import _check_out, _code, _empty, _gpu, _ptr, _raw_stream, _workspace
 
 
 def _weights(X, weight, bias):
@@ -31,16 +31,16 @@ def layer_norm_forward(X: torch.Tensor, weight: torch.Tensor, bias: Optional[tor
     _check_out(out, (T, C), X.dtype, "out")
     _check_out(mean, (T,), torch.float32, "mean")
     _check_out(rstd, (T,), torch.float32, "rstd")
-    _same_device(X, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
+    dev = _gpu(X, "X")
     if out is None:
-        out = _empty((T, C), X.dtype, X.device)
+        out = torch.empty_like(X, memory_format=torch.contiguous_format)
     if mean is None:
         mean = _empty((T,), torch.float32, X.device)
     if rstd is None:
-        rstd = _empty((T,), torch.float32, X.device)
-    check(lib.int8_layer_norm_forward(_dev(X, "X"), _code(X), T, C, _dev(weight, "weight"), _dev(bias, "bias"),
-                                      _code(weight), eps, _dev(out, "out"), _dev(mean, "mean"), _dev(rstd, "rstd"),
-                                      _stream(X.device)),
+        rstd = torch.empty_like(mean)
+    check(lib.int8_layer_norm_forward(_ptr(X, "X", dev), _code(X), T, C, _ptr(weight, "weight", dev),
+                                      _ptr(bias, "bias", dev), _code(weight), eps, _ptr(out, "out", dev),
+                                      _ptr(mean, "mean", dev), _ptr(rstd, "rstd", dev), _raw_stream(dev)),
           "int8_layer_norm_forward")
     return out, mean, rstd
 
@@ -61,20 +61,19 @@ def layer_norm_backward(G: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rs
     _check_out(grad_X, (T, C), X.dtype, "grad_X")
     _check_out(grad_weight, (C,), weight.dtype, "grad_weight")
     _check_out(grad_bias, (C,), weight.dtype, "grad_bias")
-    _same_device(G, X=X, mean=mean, rstd=rstd, weight=weight, grad_X=grad_X, grad_weight=grad_weight,
-                 grad_bias=grad_bias)
+    dev = _gpu(G, "G")
     if grad_X is None and with_grad_X:
-        grad_X = _empty((T, C), X.dtype, X.device)
+        grad_X = torch.empty_like(X, memory_format=torch.contiguous_format)
     if grad_weight is None and with_grad_weight:
-        grad_weight = _empty((C,), weight.dtype, X.device)
+        grad_weight = torch.empty_like(weight, memory_format=torch.contiguous_format)
     if grad_bias is None and with_grad_bias:
-        grad_bias = _empty((C,), weight.dtype, X.device)
-    ws = _workspace(workspace, lib.int8_layer_norm_backward_workspace_bytes(T, C), X.device)
-    check(lib.int8_layer_norm_backward(_dev(G, "G"), _dev(X, "X"), _code(X), T, C, _dev(mean, "mean"),
-                                       _dev(rstd, "rstd"), _dev(weight, "weight"), _code(weight),
-                                       _dev(grad_X, "grad_X"), _dev(grad_weight, "grad_weight"),
-                                       _dev(grad_bias, "grad_bias"), ws.data_ptr() if ws is not None else 0,
-                                       ws.numel() if ws is not None else 0, _stream(X.device)),
+        grad_bias = torch.empty_like(weight, memory_format=torch.contiguous_format)
+    ws = _workspace(workspace, lib.int8_layer_norm_backward_workspace_bytes(T, C), X.device, dev)
+    check(lib.int8_layer_norm_backward(_ptr(G, "G", dev), _ptr(X, "X", dev), _code(X), T, C, _ptr(mean, "mean", dev),
+                                       _ptr(rstd, "rstd", dev), _ptr(weight, "weight", dev), _code(weight),
+                                       _ptr(grad_X, "grad_X", dev), _ptr(grad_weight, "grad_weight", dev),
+                                       _ptr(grad_bias, "grad_bias", dev), _ptr(ws, "workspace", dev),
+                                       0 if ws is None else ws.numel(), _raw_stream(dev)),
           "int8_layer_norm_backward")
     return grad_X, grad_weight, grad_bias
 

@@ -13,7 +13,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from ._lib import AdamWTensor, check, lib
-from ._tensors import DTYPE_CODE, _code, _dev, _stream
+from ._tensors import DTYPE_CODE, _code, _dev, _raw_stream
 
 BLOCK = 256   # values that share a scale
 
@@ -57,7 +57,7 @@ class AdamWPlan:
                 raise ValueError(f"{name} must have one tensor for each of the {n} parameters")
         if n == 0:
             raise ValueError("no parameters")
-        self.device = params[0].device
+        self.device, self.gpu = params[0].device, params[0].get_device()
         self._keep = [list(params)] + [list(x) for x in lists.values() if x is not None]
         self.table, self.count, self.chunks = None, n, 0
         arr = (AdamWTensor * n)()
@@ -98,11 +98,11 @@ class AdamWPlan:
         """Step number `step` (from 1). grad_scale: fp32 GPU scalar that multiplies the gradients; found_inf: fp32 GPU
         scalar, anything but 0 leaves all tensors as they are (the caller's step count goes on)."""
         for name, x in (("grad_scale", grad_scale), ("found_inf", found_inf)):
-            if x is not None and (x.dtype != torch.float32 or x.numel() != 1 or x.device != self.device):
+            if x is not None and (x.dtype != torch.float32 or x.numel() != 1 or x.get_device() != self.gpu):
                 raise ValueError(f"{name} must be one float32 value on {self.device}")
         check(lib.int8_adamw_step(self.table.data_ptr(), self.count, self.chunks, lr, betas[0], betas[1], eps,
                                   weight_decay, step, 0 if grad_scale is None else grad_scale.data_ptr(),
-                                  0 if found_inf is None else found_inf.data_ptr(), _stream(self.device)),
+                                  0 if found_inf is None else found_inf.data_ptr(), _raw_stream(self.gpu)),
               "int8_adamw_step")
 
 
