@@ -193,6 +193,17 @@ __device__ __forceinline__ v4u frag_of(const float (&x)[Mx<DT>::EL]) {
   return f;
 }
 
+// Rows of CW 16-byte chunks in LDS, chunk ch of row r at ch ^ (r / W): the rows
+// of a fragment read (8 lanes, one chunk of 8 rows) and the chunks of a row
+// written side by side fall on distinct banks.
+template <int CW>
+struct Rows {
+  static constexpr int W = CW < 16 ? 16 / CW : 1, MASK = (CW < 16 ? CW : 16) - 1;
+  __device__ static __forceinline__ v4u& at(char* p, int r, int ch) {
+    return *reinterpret_cast<v4u*>(p + (r * CW + (ch ^ ((r / W) & MASK))) * 16);
+  }
+};
+
 // V and dV are fp32 and enter products with 16-bit operands as hi + lo, two
 // values of that type: hi is v rounded, lo the rest rounded, together within
 // 2^-17 of v (bf16; 2^-22 in fp16). Rounding V to 16 bits once instead would

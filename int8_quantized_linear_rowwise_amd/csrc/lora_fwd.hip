@@ -19,42 +19,41 @@ namespace {
 constexpr int MAX_SPLITS = 8;
 
 // acc[i][j] += X's rows 16 i .. of the tile times A[a]'s rows 16 j .., over the
-// contraction steps s0 .. s1 - 1 that fall to `wave` of NW: pairs of steps in
-// turn, 128 bytes of each row. Fragments come straight from memory, as both
-// operands lie along k. Rows past the tile or the rank repeat the last one:
-// they only reach products that are not used.
+// contraction steps s0 .. s1 - 1 that fall to `wave` of NW. A wave takes pairs
+// of steps: 128 bytes of each row, eight lanes side by side, UU pairs with all
+// their loads in flight; they reach the fragments' layout through the wave's
+// 2 KB a 16 rows in LDS. (Fragments loaded straight from memory, 16 rows at
+// once, run at about one 16-byte request a nanosecond and compute unit: 4096
+// tokens of 4096 features at rank 64 took 43 us.) Rows past the tile or the
+// rank only reach products that are not used.
 //
 // fp16 weights below 2^-14 are denormals, whose products the matrix core sums
 // with the absolute error of products of 2^-14: V of an adapter that is small
 // throughout lost up to 10 of its 24 bits. So A is multiplied by 2^14 (exact)
 // until a value of 2 or more is met, from where the sums go on without.
-template <int DT, int RT, int TMT, int NW, int U, bool FULL>
+template <int DT, int RT, int TMT, int NW, int U>
 __device__ __forceinline__ void shrink_steps(const typename Elem<DT>::T* __restrict__ X, int K,
                                              const typename Elem<DT>::T* __restrict__ A, int R, const LoraTile& tl,
-                                             int s0, int s1, int wave, int lane, v4f (&acc)[TMT][RT]) {
+                                             int s0, int s1, int wave, int lane, char* mine, v4f (&acc)[TMT][RT]) {
   typedef Mx<DT> M;
   typedef typename Elem<DT>::T E;
   constexpr int KS = M::KS, EL = M::EL;
-  const int c = lane & 15, q = lane >> 4;
-  const E* x[TMT];
-  const E* w[RT];
-#pragma unroll
-  for (int i = 0; i < TMT; ++i) x[i] = X + (int64_t)min(tl.t0 + 16 * i + c, tl.t1 - 1) * K + EL * q;
-#pragma unroll
-  for (int j = 0; j < RT; ++j) w[j] = A + ((int64_t)tl.adapter * R + min(16 * j + c, R - 1)) * K + EL * q;
+  const int c = lane & 15, q = lane >> 4, lrow = lane >> 3, lch = lane & 7;
+  const int n_tok = tl.t1 - tl.t0;
+  const E* Xt = X + (int64_t)tl.t0 * K;
+  const E* Aa = A + (int64_t)tl.adapter * R * K;
 #pragma unroll
   for (int i = 0; i < TMT; ++i)
 #pragma unroll
     for (int j = 0; j < RT; ++j) acc[i][j] = v4f{};
 
   bool lifted = DT == DT_F16;
-  auto lift = [&](auto& f, int count) {
+  auto lift = [&](v4u (&f)[RT]) {
     if constexpr (DT == DT_F16) {
       if (!lifted) return;
       uint32_t any = 0u;
-      for (int u = 0; u < count; ++u)
 #pragma unroll
-        for (int j = 0; j < RT; ++j) any |= (f[u][j][0] | f[u][j][1]) | (f[u][j][2] | f[u][j][3]);
+      for (int j = 0; j < RT; ++j) any |= (f[j][0] | f[j][1]) | (f[j][2] | f[j][3]);
       if (__any((any & 0x40004000u) != 0u)) {   // an exponent of 16 or more: |a| >= 2, infinities and NaN
         lifted = false;
 #pragma unroll
@@ -63,42 +62,50 @@ __device__ __forceinline__ void shrink_steps(const typename Elem<DT>::T* __restr
           for (int j = 0; j < RT; ++j) acc[i][j] *= 0x1p-14f;
         return;
       }
-      for (int u = 0; u < count; ++u)
 #pragma unroll
-        for (int j = 0; j < RT; ++j) f[u][j] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, f[u][j]) * (_Float16)0x1p14f);
+      for (int j = 0; j < RT; ++j) f[j] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, f[j]) * (_Float16)0x1p14f);
     }
   };
-  // Whole pairs of steps, wave after wave, UU of a wave with all their loads in
-  // flight. Tiles begin at different pairs: with all of them at k = 0 rows of a
-  // power-of-two width would meet in a few of the memory's channels.
-  const int whole = FULL ? s1 : min(s1, K / KS), np = max(whole - s0, 0) / 2;
-  const int turn = np > 0 ? (int)((unsigned)(tl.t0 / 16 * 5) % (unsigned)np) : 0;
+  auto products = [&](v4u (&fx)[TMT], v4u (&fw)[RT]) {
+    lift(fw);
+#pragma unroll
+    for (int i = 0; i < TMT; ++i)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) acc[i][j] = M::mma(fx[i], fw[j], acc[i][j]);
+  };
+  const int np = max(min(s1, K / KS) - s0, 0) / 2;   // whole pairs
   int p = wave;
   auto pairs = [&](auto uu) {
     constexpr int UU = decltype(uu)::value;
     for (; p + NW * (UU - 1) < np; p += NW * UU) {
-      v4u fx[2 * UU][TMT], fw[2 * UU][RT];
+      v4u lx[UU][2 * TMT], lw[UU][2 * RT];
 #pragma unroll
       for (int u = 0; u < UU; ++u) {
-        int at = p + NW * u + turn;
-        if (at >= np) at -= np;
-        const int k = (s0 + 2 * at) * KS;
+        const int k = (s0 + 2 * (p + NW * u)) * KS + EL * lch;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int i = 0; i < 2 * TMT; ++i)
+          lx[u][i] = 8 * i + lrow < n_tok ? ld16<DT>(Xt + (int64_t)(8 * i + lrow) * K + k) : v4u{0u, 0u, 0u, 0u};
 #pragma unroll
-          for (int i = 0; i < TMT; ++i) fx[2 * u + h][i] = ld16<DT>(x[i] + k + h * KS);
-#pragma unroll
-          for (int j = 0; j < RT; ++j) fw[2 * u + h][j] = ld16<DT>(w[j] + k + h * KS);
-        }
+        for (int j = 0; j < 2 * RT; ++j)
+          lw[u][j] = 8 * j + lrow < R ? ld16<DT>(Aa + (int64_t)(8 * j + lrow) * K + k) : v4u{0u, 0u, 0u, 0u};
       }
       __builtin_amdgcn_sched_barrier(0);   // else the loads move to their products, a few in flight at a time
-      lift(fw, 2 * UU);
 #pragma unroll
-      for (int u = 0; u < 2 * UU; ++u)
+      for (int u = 0; u < UU; ++u) {
 #pragma unroll
-        for (int i = 0; i < TMT; ++i)
+        for (int i = 0; i < 2 * TMT; ++i) Rows<8>::at(mine, 8 * i + lrow, lch) = lx[u][i];
 #pragma unroll
-          for (int j = 0; j < RT; ++j) acc[i][j] = M::mma(fx[u][i], fw[u][j], acc[i][j]);
+        for (int j = 0; j < 2 * RT; ++j) Rows<8>::at(mine, 16 * TMT + 8 * j + lrow, lch) = lw[u][j];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          v4u fx[TMT], fw[RT];
+#pragma unroll
+          for (int i = 0; i < TMT; ++i) fx[i] = Rows<8>::at(mine, 16 * i + c, 4 * h + q);
+#pragma unroll
+          for (int j = 0; j < RT; ++j) fw[j] = Rows<8>::at(mine, 16 * (TMT + j) + c, 4 * h + q);
+          products(fx, fw);
+        }
+      }
     }
   };
   pairs(std::integral_constant<int, U>{});
@@ -108,17 +115,13 @@ __device__ __forceinline__ void shrink_steps(const typename Elem<DT>::T* __restr
   // what is left of the range: a step without its pair, and k's end
 #pragma unroll 1
   for (int s = s0 + 2 * np + wave; s < s1; s += NW) {
-    const int left = K - s * KS - EL * q;
-    v4u fx[TMT], fw[1][RT];
+    const int k = s * KS + EL * q, left = K - k;
+    v4u fx[TMT], fw[RT];
 #pragma unroll
-    for (int i = 0; i < TMT; ++i) fx[i] = FULL ? ld16<DT>(x[i] + s * KS) : ld_frag<DT>(x[i] + s * KS, left);
+    for (int i = 0; i < TMT; ++i) fx[i] = ld_frag<DT>(Xt + (int64_t)min(16 * i + c, n_tok - 1) * K + k, left);
 #pragma unroll
-    for (int j = 0; j < RT; ++j) fw[0][j] = FULL ? ld16<DT>(w[j] + s * KS) : ld_frag<DT>(w[j] + s * KS, left);
-    lift(fw, 1);
-#pragma unroll
-    for (int i = 0; i < TMT; ++i)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) acc[i][j] = M::mma(fx[i], fw[0][j], acc[i][j]);
+    for (int j = 0; j < RT; ++j) fw[j] = ld_frag<DT>(Aa + (int64_t)min(16 * j + c, R - 1) * K + k, left);
+    products(fx, fw);
   }
   if (lifted)   // every wave its own state: the sums meet in common units
 #pragma unroll
@@ -128,67 +131,71 @@ __device__ __forceinline__ void shrink_steps(const typename Elem<DT>::T* __restr
 }
 
 // The columns of a tile's output: out[t, n] = D(base[t, n] + f sum_r V[t, r]
-// B[a][n][r]) in blocks of KS columns. The product is taken transposed (rows n,
-// columns t), so that a lane holds consecutive n of one token: with row m of
-// product u standing for n = 8 (m / 4) + 4 u + m % 4 two 16-bit products give a
-// lane 8 consecutive n, 16 bytes of base and out. The contraction runs over
-// both parts of V against the same B fragments; at rank 16 both parts fill one
-// step.
+// B[a][n][r]) in groups of GC columns, 128 bytes of a row, of one wave. base, B
+// and out cross the wave's LDS between memory's order (lanes side by side on a
+// row) and the product's. The product is taken transposed (rows n, columns t),
+// so that a lane holds consecutive n of one token: with row m of product u
+// standing for n = 8 (m / 4) + 4 u + m % 4 two 16-bit products give a lane 8
+// consecutive n, 16 bytes. The contraction runs over both parts of V against
+// the same B fragments; at rank 16 both parts fill one step. FULL: whole groups
+// and a rank of whole tiles; otherwise B's fragments come straight from memory.
 template <int DT, int RT, int TMT, bool FULL>
 struct Columns {
   typedef Mx<DT> M;
   typedef typename Elem<DT>::T E;
   static constexpr int KS = M::KS, EL = M::EL, TM = 16 * TMT, RP = 16 * RT;
+  static constexpr int GC = 8 * EL;                               // columns of a group: two blocks of KS
   static constexpr int UN = M::F32 ? 1 : 2;                       // products of one block
   static constexpr int NB = M::F32 ? RT : (RT + 1) / 2;           // B fragments of a row
   static constexpr int NS = M::F32 ? RT : RT == 1 ? 1 : RT;       // contraction steps over all parts of V
   static constexpr int LD = M::F32 ? RP + 4 : RP + 8;             // V's row in LDS, in elements
-  struct Block {
-    v4u b[UN][NB], base[TMT];
+  static constexpr int CB = RP / EL;                              // chunks of a row of B
+  static constexpr int LDS = TM * 128 + (FULL ? GC * RP * (int)sizeof(E) : 0);   // a wave's
+  struct Group {
+    v4u base[2 * TMT], b[FULL ? 2 * RT : 1];
   };
   const E* Ba;
   const E* base;
   E* out;
-  int64_t row[TMT];
-  int N, R, n_tok, c, q;
+  int64_t row0;
+  int N, R, n_tok, lane, c, q, lrow, lch;
+  char* mine;
   v4u vf[TMT][NS];
   float f[TMT];
 
-  __device__ __forceinline__ Columns(const LoraTile& tl, const E* B, const E* base_, E* out_, int N_, int R_, int lane)
-      : Ba(B + (int64_t)max(tl.adapter, 0) * N_ * R_), base(base_), out(out_), N(N_), R(R_), n_tok(tl.t1 - tl.t0),
-        c(lane & 15), q(lane >> 4) {
-#pragma unroll
-    for (int i = 0; i < TMT; ++i) row[i] = (int64_t)min(tl.t0 + 16 * i + c, tl.t1 - 1) * N;
-  }
+  __device__ __forceinline__ Columns(const LoraTile& tl, const E* B, const E* base_, E* out_, int N_, int R_, int lane_,
+                                     char* lds)
+      : Ba(B + (int64_t)max(tl.adapter, 0) * N_ * R_), base(base_), out(out_), row0((int64_t)tl.t0 * N_), N(N_), R(R_),
+        n_tok(tl.t1 - tl.t0), lane(lane_), c(lane_ & 15), q(lane_ >> 4), lrow(lane_ >> 3), lch(lane_ & 7), mine(lds) {}
   __device__ static __forceinline__ int r_of(int s, int q) {
     return M::F32 ? 16 * s + 4 * q : RT == 1 ? 8 * (q & 1) : 32 * s + 8 * q;
   }
-  __device__ __forceinline__ void load_base(int blk, Block& k) const {
-    const int n = blk * KS + EL * q;
-    if (base == nullptr) {
+  __device__ __forceinline__ void load_base(int grp, v4u (&b)[2 * TMT]) const {
+    const int n = grp * GC + EL * lch;
 #pragma unroll
-      for (int i = 0; i < TMT; ++i) k.base[i] = v4u{0u, 0u, 0u, 0u};
-    } else if (FULL || (blk + 1) * KS <= N) {
-#pragma unroll
-      for (int i = 0; i < TMT; ++i) k.base[i] = ld16<DT>(base + row[i] + n);
-    } else {
-#pragma unroll
-      for (int i = 0; i < TMT; ++i) k.base[i] = ld_frag<DT>(base + row[i] + n, N - n);
-    }
-  }
-  __device__ __forceinline__ void load(int blk, Block& k) const {
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const int n = blk * KS + (M::F32 ? c : 8 * (c >> 2) + 4 * u + (c & 3));
-      const E* b = Ba + (int64_t)(FULL ? n : min(n, N - 1)) * R;
-#pragma unroll
-      for (int s = 0; s < NB; ++s) {
-        const int r = r_of(s, q);
-        if (FULL || R == RP) k.b[u][s] = ld16<DT>(b + r);
-        else k.b[u][s] = ld_frag<DT>(b + r, R - r);
+    for (int i = 0; i < 2 * TMT; ++i) {
+      b[i] = v4u{0u, 0u, 0u, 0u};
+      if (base && 8 * i + lrow < n_tok) {
+        const E* p = base + row0 + (int64_t)(8 * i + lrow) * N + n;
+        b[i] = FULL ? ld16<DT>(p) : ld_frag<DT>(p, N - n);
       }
     }
-    load_base(blk, k);
+  }
+  __device__ __forceinline__ void load(int grp, Group& k) const {
+    load_base(grp, k.base);
+    if constexpr (FULL) {   // GC rows of B are one piece of memory
+      const E* b = Ba + (int64_t)grp * GC * RP + EL * lane;
+#pragma unroll
+      for (int i = 0; i < 2 * RT; ++i) k.b[i] = ld16<DT>(b + 64 * EL * i);
+    }
+  }
+  __device__ __forceinline__ void store(int grp, int i, v4u y) const {
+    const int n = grp * GC + EL * lch;
+    if (8 * i + lrow < n_tok) {
+      E* p = out + row0 + (int64_t)(8 * i + lrow) * N + n;
+      if (FULL) st16<DT>(p, y);
+      else st_frag<DT>(p, y, N - n);
+    }
   }
   // V's fragments from LDS [part][token][LD]
   __device__ __forceinline__ void take_v(const E* sv) {
@@ -200,38 +207,78 @@ struct Columns {
         vf[i][s] = *reinterpret_cast<const v4u*>(sv + (part * TM + 16 * i + c) * LD + r_of(s % NB, q));
       }
   }
-  __device__ __forceinline__ void store(int blk, int i, v4u y) const {
-    const int n = blk * KS + EL * q;
-    if (16 * i + c < n_tok) {
-      if (FULL || (blk + 1) * KS <= N) st16<DT>(out + row[i] + n, y);
-      else st_frag<DT>(out + row[i] + n, y, N - n);
+  // the group's base and B to LDS, from where `finish` takes them
+  __device__ __forceinline__ void stage(const Group& k) const {
+#pragma unroll
+    for (int i = 0; i < 2 * TMT; ++i) Rows<8>::at(mine, 8 * i + lrow, lch) = k.base[i];
+    if constexpr (FULL) {
+#pragma unroll
+      for (int i = 0; i < 2 * RT; ++i) {
+        const int id = 64 * i + lane;
+        Rows<CB>::at(mine + TM * 128, id / CB, id % CB) = k.b[i];
+      }
     }
   }
-  __device__ __forceinline__ void finish(int blk, const Block& k) const {
+  __device__ __forceinline__ void finish(int grp) const {
 #pragma unroll
-    for (int i = 0; i < TMT; ++i) {
-      v4f acc[UN];
+    for (int blk = 0; blk < 2; ++blk) {
+      v4u b[UN][NB];
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
-        acc[u] = v4f{};
+        const int n = blk * KS + (M::F32 ? c : 8 * (c >> 2) + 4 * u + (c & 3));
 #pragma unroll
-        for (int s = 0; s < NS; ++s) acc[u] = M::mma(k.b[u][s % NB], vf[i][s], acc[u]);
+        for (int s = 0; s < NB; ++s) {
+          const int r = r_of(s, q);
+          if constexpr (FULL) b[u][s] = Rows<CB>::at(mine + TM * 128, n, r / EL);
+          else b[u][s] = ld_frag<DT>(Ba + (int64_t)min(grp * GC + n, N - 1) * R + r, R - r);
+        }
       }
-      float y[EL];
-      frag_f32<DT>(k.base[i], y);
 #pragma unroll
-      for (int j = 0; j < EL; ++j) y[j] = __builtin_fmaf(f[i], acc[j >> 2][j & 3], y[j]);
-      store(blk, i, frag_of<DT>(y));
+      for (int i = 0; i < TMT; ++i) {
+        v4f acc[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          acc[u] = v4f{};
+#pragma unroll
+          for (int s = 0; s < NS; ++s) acc[u] = M::mma(b[u][s % NB], vf[i][s], acc[u]);
+        }
+        v4u& place = Rows<8>::at(mine, 16 * i + c, 4 * blk + q);
+        float y[EL];
+        frag_f32<DT>(place, y);
+#pragma unroll
+        for (int j = 0; j < EL; ++j) y[j] = __builtin_fmaf(f[i], acc[j >> 2][j & 3], y[j]);
+        place = frag_of<DT>(y);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < 2 * TMT; ++i) store(grp, i, Rows<8>::at(mine, 8 * i + lrow, lch));
+  }
+  // groups g0, g0 + step .. of a wave, the first PD of them loaded before
+  template <int PD>
+  __device__ __forceinline__ void prefetch(int g0, int g1, int step, Group (&k)[PD]) const {
+#pragma unroll
+    for (int i = 0; i < PD; ++i)
+      if (g0 + step * i < g1) load(g0 + step * i, k[i]);
+  }
+  template <int PD>
+  __device__ __forceinline__ void all(int g0, int g1, int step, Group (&k)[PD]) const {
+    for (int g = g0; g < g1; g += step * PD)
+#pragma unroll
+      for (int i = 0; i < PD; ++i)
+        if (g + step * i < g1) {
+          stage(k[i]);
+          if (g + step * (i + PD) < g1) load(g + step * (i + PD), k[i]);
+          finish(g + step * i);
+        }
   }
   // a tile without an adapter
-  __device__ __forceinline__ void copy(int b0, int b1, int step) const {
+  __device__ __forceinline__ void copy(int g0, int g1, int step) const {
     if (base == out) return;
-    for (int b = b0; b < b1; b += step) {
-      Block k;
-      load_base(b, k);
+    for (int g = g0; g < g1; g += step) {
+      v4u b[2 * TMT];
+      load_base(g, b);
 #pragma unroll
-      for (int i = 0; i < TMT; ++i) store(b, i, k.base[i]);
+      for (int i = 0; i < 2 * TMT; ++i) store(g, i, b[i]);
     }
   }
 };
@@ -241,20 +288,22 @@ struct Columns {
 // P[split][t][r] = sum over the split's part of k of X[t, k] A[a][r][k], Rp =
 // 16 RT columns (columns past R hold values that are not read). NW waves share
 // a tile; their sums are added in LDS in a fixed order.
-template <int DT, int RT, int TMT, int NW, bool FULL>
+template <int DT, int RT, int TMT, int NW>
 __global__ __launch_bounds__(NW * 64) void k_lora_shrink(const typename Elem<DT>::T* __restrict__ X, int T, int K,
                                                          const typename Elem<DT>::T* __restrict__ A, int R,
                                                          LoraSegs S, float* __restrict__ P) {
-  constexpr int KS = Mx<DT>::KS;
-  __shared__ v4f red[NW / 2][TMT * RT][64];
+  constexpr int KS = Mx<DT>::KS, U = TMT + RT <= 2 ? 4 : TMT + RT <= 5 ? 2 : 1;
+  extern __shared__ __attribute__((aligned(16))) char sm[];
+  v4f(*red)[TMT * RT][64] = reinterpret_cast<v4f(*)[TMT * RT][64]>(sm);
   const LoraTile tl = lora_tile(S, seg_lanes(S, T), blockIdx.x + 1, T, 16 * TMT);
   if (tl.t1 <= tl.t0 || tl.adapter < 0) return;
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int steps = (K + KS - 1) / KS;
-  const int s0 = (int)((int64_t)steps * blockIdx.y / gridDim.y), s1 = (int)((int64_t)steps * (blockIdx.y + 1) / gridDim.y);
+  const int steps = (K + KS - 1) / KS, pairs = (steps + 1) / 2;
+  const int s0 = 2 * (int)((int64_t)pairs * blockIdx.y / gridDim.y);
+  const int s1 = min(2 * (int)((int64_t)pairs * (blockIdx.y + 1) / gridDim.y), steps);
   v4f acc[TMT][RT];
-  shrink_steps<DT, RT, TMT, NW, TMT + RT <= 2 ? 4 : TMT + RT <= 5 ? 2 : 1, FULL>(X, K, A, R, tl, s0, s1, wave, lane, acc);
+  shrink_steps<DT, RT, TMT, NW, U>(X, K, A, R, tl, s0, s1, wave, lane, sm + wave * (TMT + RT) * 2048, acc);
 #pragma unroll
   for (int half = NW / 2; half >= 1; half >>= 1) {
     __syncthreads();
@@ -285,41 +334,40 @@ __global__ __launch_bounds__(NW * 64) void k_lora_shrink(const typename Elem<DT>
 }
 
 // The columns of a tile from V = the sum of the splits of P (also written to
-// `V` by the first column slice).
+// `V` by the first column slice). The first groups of base and B are loaded
+// before V.
 template <int DT, int RT, int TMT, bool FULL>
 __global__ __launch_bounds__(256) void k_lora_expand(const float* __restrict__ P, int splits, int T, int N,
                                                      const typename Elem<DT>::T* __restrict__ B, int R,
                                                      const float* __restrict__ scaling, LoraSegs S,
                                                      const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
-                                                     float* __restrict__ V, int blocks_per_wave) {
+                                                     float* __restrict__ V, int groups_per_wave) {
   typedef Columns<DT, RT, TMT, FULL> C;
   typedef typename Elem<DT>::T E;
   constexpr int TM = C::TM, RP = C::RP, LD = C::LD;
   constexpr bool F32 = DT == DT_F32;
-  __shared__ __attribute__((aligned(16))) E sv[Mx<DT>::NC][TM][LD];
-  __shared__ float sunit[TM];
+  constexpr int PD = TMT == 1 ? (RT <= 2 ? 3 : RT == 4 ? 2 : 1) : 1;
+  extern __shared__ __attribute__((aligned(16))) char sm[];
+  E* sv = reinterpret_cast<E*>(sm);                                    // [part][TM][LD], before the waves' stages
+  float* sunit = reinterpret_cast<float*>(sv + Mx<DT>::NC * TM * LD);   // [TM]
   const LoraTile tl = lora_tile(S, seg_lanes(S, T), blockIdx.x + 1, T, TM);
   const int n_tok = tl.t1 - tl.t0;
   if (n_tok <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int blk0 = blockIdx.y * 4 * blocks_per_wave + wave, n_blk = (N + C::KS - 1) / C::KS;
-  const int blk_end = min(blk0 - wave + 4 * blocks_per_wave, n_blk);
-  C col(tl, B, base, out, N, R, lane);
+  const int first = blockIdx.y * 4 * groups_per_wave;
+  const int g0 = first + wave, g1 = min(first + 4 * groups_per_wave, (N + C::GC - 1) / C::GC);
+  C col(tl, B, base, out, N, R, lane, sm + wave * C::LDS);
 
   if (tl.adapter < 0) {
     if (V && blockIdx.y == 0)
       for (int64_t e = (int64_t)tl.t0 * R + tid; e < (int64_t)tl.t1 * R; e += 256) V[e] = 0.0f;
-    col.copy(blk0, blk_end, 4);
+    col.copy(g0, g1, 4);
     return;
   }
-
-  constexpr int PD = TMT == 1 ? (RT <= 2 ? 6 : RT == 4 ? 3 : 2) : RT == 8 ? 1 : 2;   // blocks in flight
   const float scale = scaling[tl.adapter];
-  typename C::Block k[PD];
-#pragma unroll
-  for (int i = 0; i < PD; ++i)
-    if (blk0 + 4 * i < blk_end) col.load(blk0 + 4 * i, k[i]);
+  typename C::Group k[PD];
+  col.prefetch(g0, g1, 4, k);
 
   // V's parts into LDS: four consecutive r a thread, the threads of a token side by side
   for (int e = tid; e < TM * RP / 4; e += 256) {
@@ -339,8 +387,9 @@ __global__ __launch_bounds__(256) void k_lora_expand(const float* __restrict__ P
       if (r + j >= R) v[j] = 0.0f;
       else if (V && blockIdx.y == 0 && t < n_tok) V[(int64_t)(tl.t0 + t) * R + r + j] = v[j];
     }
+    E* o = sv + t * LD + r;
     if constexpr (F32) {
-      *reinterpret_cast<v4f*>(&sv[0][t][r]) = v;
+      *reinterpret_cast<v4f*>(o) = v;
     } else {
       float unit = 1.0f;
       if constexpr (DT == DT_F16) {
@@ -348,77 +397,71 @@ __global__ __launch_bounds__(256) void k_lora_expand(const float* __restrict__ P
 #pragma unroll
         for (int j = 0; j < 4; ++j) top = fmaxf(top, __builtin_isfinite(v[j]) ? __builtin_fabsf(v[j]) : 0.0f);
 #pragma unroll
-        for (int o = 1; o < RP / 4; o <<= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+        for (int x = 1; x < RP / 4; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, 64));
         unit = unit_for(top);
         if (r == 0) sunit[t] = inv_pow2(unit);
       }
       uint32_t h[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[j] = split2<DT>(v[j], unit);
-      *reinterpret_cast<v2u*>(&sv[0][t][r]) =
-          v2u{(h[0] & 0xffffu) | (h[1] << 16), (h[2] & 0xffffu) | (h[3] << 16)};
-      *reinterpret_cast<v2u*>(&sv[Mx<DT>::NC - 1][t][r]) =
+      *reinterpret_cast<v2u*>(o) = v2u{(h[0] & 0xffffu) | (h[1] << 16), (h[2] & 0xffffu) | (h[3] << 16)};
+      *reinterpret_cast<v2u*>(o + TM * LD) =
           v2u{(h[0] >> 16) | (h[1] & 0xffff0000u), (h[2] >> 16) | (h[3] & 0xffff0000u)};
     }
   }
   __syncthreads();
-  if (blk0 >= blk_end) return;
-  col.take_v(&sv[0][0][0]);
+  col.take_v(sv);
 #pragma unroll
   for (int i = 0; i < TMT; ++i) {
     col.f[i] = scale;
     if constexpr (DT == DT_F16) col.f[i] *= sunit[16 * i + (lane & 15)];
   }
-  for (int b = blk0; b < blk_end; b += 4 * PD)
-#pragma unroll
-    for (int i = 0; i < PD; ++i)
-      if (b + 4 * i < blk_end) {
-        col.finish(b + 4 * i, k[i]);
-        if (b + 4 * (i + PD) < blk_end) col.load(b + 4 * (i + PD), k[i]);
-      }
+  __syncthreads();
+  col.all(g0, g1, 4, k);
 }
 
 // Both in one launch, for tiles of 16 tokens: every workgroup computes the whole
 // V of its tile, which the workgroups of one tile repeat (X and A come from the
-// caches), and its slice of the columns. The first block of base and B is
-// loaded before V's contraction. One request of one token, 4096 x 4096 at rank
-// 16: 4.8 us against 3.9 + 4.4 us and a second launch.
+// caches), and its slice of the columns. The first groups of base and B are
+// loaded before V's contraction.
 template <int DT, int RT, bool FULL>
 __global__ __launch_bounds__(512, 1) void k_lora_short(const typename Elem<DT>::T* __restrict__ X, int T, int K,
-                                                    const typename Elem<DT>::T* __restrict__ A, int R,
-                                                    const float* __restrict__ scaling, LoraSegs S,
-                                                    const typename Elem<DT>::T* __restrict__ B, int N,
-                                                    const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
-                                                    float* __restrict__ V, int blocks_per_wave) {
+                                                       const typename Elem<DT>::T* __restrict__ A, int R,
+                                                       const float* __restrict__ scaling, LoraSegs S,
+                                                       const typename Elem<DT>::T* __restrict__ B, int N,
+                                                       const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
+                                                       float* __restrict__ V, int groups_per_wave) {
   typedef Columns<DT, RT, 1, FULL> C;
   typedef typename Elem<DT>::T E;
-  constexpr int LD = C::LD;
-  __shared__ v4f red[8][RT][64];
-  __shared__ __attribute__((aligned(16))) E sv[Mx<DT>::NC][16][LD];
-  __shared__ float top8[8];
+  constexpr int LD = C::LD, PD = RT <= 2 ? 3 : RT == 4 ? 2 : 1;
+  constexpr int STAGE = (1 + RT) * 2048 > C::LDS ? (1 + RT) * 2048 : C::LDS;
+  extern __shared__ __attribute__((aligned(16))) char sm[];
+  v4f(*red)[RT][64] = reinterpret_cast<v4f(*)[RT][64]>(sm);              // over the waves' stages, between their uses
+  E* sv = reinterpret_cast<E*>(sm + 8 * STAGE);                          // [part][16][LD]
+  float* top8 = reinterpret_cast<float*>(sv + Mx<DT>::NC * 16 * LD);
   const LoraTile tl = lora_tile(S, seg_lanes(S, T), blockIdx.x + 1, T, 16);
   const int n_tok = tl.t1 - tl.t0;
   if (n_tok <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int first = blockIdx.y * 8 * blocks_per_wave, n_blk = (N + C::KS - 1) / C::KS;
-  const int blk0 = first + wave, blk_end = min(first + 8 * blocks_per_wave, n_blk);
-  C col(tl, B, base, out, N, R, lane);
+  char* mine = sm + wave * STAGE;
+  const int first = blockIdx.y * 8 * groups_per_wave;
+  const int g0 = first + wave, g1 = min(first + 8 * groups_per_wave, (N + C::GC - 1) / C::GC);
+  C col(tl, B, base, out, N, R, lane, mine);
   if (tl.adapter < 0) {
     if (V && blockIdx.y == 0)
       for (int64_t e = (int64_t)tl.t0 * R + tid; e < (int64_t)tl.t1 * R; e += 512) V[e] = 0.0f;
-    col.copy(blk0, blk_end, 8);
+    col.copy(g0, g1, 8);
     return;
   }
-  constexpr int PD = RT <= 2 ? 6 : RT == 4 ? 3 : 2;   // blocks in flight
   const float scale = scaling[tl.adapter];
-  typename C::Block k[PD];
-#pragma unroll
-  for (int i = 0; i < PD; ++i)
-    if (blk0 + 8 * i < blk_end) col.load(blk0 + 8 * i, k[i]);
+  typename C::Group k[PD];
+  col.prefetch(g0, g1, 8, k);
   {
     v4f acc[1][RT];
-    shrink_steps<DT, RT, 1, 8, RT == 1 ? 8 : RT == 2 ? 4 : RT == 4 ? 2 : 1, FULL>(X, K, A, R, tl, 0, (K + C::KS - 1) / C::KS, wave, lane, acc);
+    shrink_steps<DT, RT, 1, 8, RT == 1 ? 8 : RT == 2 ? 4 : RT == 4 ? 2 : 1>(X, K, A, R, tl, 0, (K + C::KS - 1) / C::KS,
+                                                                            wave, lane, mine, acc);
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < RT; ++j) red[wave][j][lane] = acc[0][j];
   }
@@ -439,8 +482,8 @@ __global__ __launch_bounds__(512, 1) void k_lora_short(const typename Elem<DT>::
   if constexpr (DT == DT_F16) {
     float top = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)   // rows past the tile repeat its last
-      top = fmaxf(top, __builtin_isfinite(v[e]) ? __builtin_fabsf(v[e]) : 0.0f);
+    for (int e = 0; e < 4; ++e)
+      top = fmaxf(top, 4 * q + e < n_tok && __builtin_isfinite(v[e]) ? __builtin_fabsf(v[e]) : 0.0f);
     top = wave_max(top);
     if (lane == 0) top8[wave] = top;
     __syncthreads();
@@ -451,27 +494,21 @@ __global__ __launch_bounds__(512, 1) void k_lora_short(const typename Elem<DT>::
   if (wave < RT) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+      E* o = sv + (4 * q + e) * LD + r;
       if constexpr (DT == DT_F32) {
-        sv[0][4 * q + e][r] = v[e];
+        *o = v[e];
       } else {
         const uint32_t h = split2<DT>(v[e], unit);
-        sv[0][4 * q + e][r] = __builtin_bit_cast(E, (uint16_t)(h & 0xffffu));
-        sv[Mx<DT>::NC - 1][4 * q + e][r] = __builtin_bit_cast(E, (uint16_t)(h >> 16));
+        o[0] = __builtin_bit_cast(E, (uint16_t)(h & 0xffffu));
+        o[16 * LD] = __builtin_bit_cast(E, (uint16_t)(h >> 16));
       }
     }
   }
   __syncthreads();
-  if (blk0 >= blk_end) return;
-  col.take_v(&sv[0][0][0]);
+  col.take_v(sv);
   col.f[0] = scale;
   if constexpr (DT == DT_F16) col.f[0] *= inv_pow2(unit);
-  for (int b = blk0; b < blk_end; b += 8 * PD)
-#pragma unroll
-    for (int i = 0; i < PD; ++i)
-      if (b + 8 * i < blk_end) {
-        col.finish(b + 8 * i, k[i]);
-        if (b + 8 * (i + PD) < blk_end) col.load(b + 8 * (i + PD), k[i]);
-      }
+  col.all(g0, g1, 8, k);
 }
 
 namespace {
@@ -506,72 +543,92 @@ bool one_launch(int T, int K, int R, int elem, int n_seg) {
   return lora_tiles(T, S, 16) <= 32 && (int64_t)K * R * elem <= 160 * 1024;
 }
 
+// A launch with `lds` bytes of dynamic LDS; over 64 KB the kernel's limit is raised first.
+template <typename... P, typename... Q>
+hipError_t launch(void (*kern)(P...), std::atomic<uint64_t>& done, dim3 grid, int threads, int lds, hipStream_t st,
+                  Q... args) {
+  if (lds > 64 * 1024) {
+    const hipError_t e = lds_limit_once((const void*)kern, lds, done);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kern, grid, dim3(threads), lds, st, args...);
+  return hipGetLastError();
+}
+
 template <int DT, int RT, bool FULL>
-void run_short(const void* Xv, int T, int K, const void* Av, const void* Bv, const float* scaling, int R, int N,
-               const LoraSegs& S, const void* base, void* out, float* V, hipStream_t st) {
+hipError_t run_short(const void* Xv, int T, int K, const void* Av, const void* Bv, const float* scaling, int R, int N,
+                     const LoraSegs& S, const void* base, void* out, float* V, hipStream_t st) {
   typedef typename Elem<DT>::T E;
-  const int tiles = lora_tiles(T, S, 16), blocks = (N + Mx<DT>::KS - 1) / Mx<DT>::KS;
-  int64_t bpw = (int64_t)tiles * blocks / (8 * 256);     // about 256 workgroups: few repeat V
-  bpw = bpw < 1 ? 1 : bpw > 64 ? 64 : bpw;
-  const int slices = blocks > 0 ? (int)((blocks + 8 * bpw - 1) / (8 * bpw)) : V ? 1 : 0;
-  if (slices > 0)
-    hipLaunchKernelGGL((k_lora_short<DT, RT, FULL>), dim3(tiles, slices), dim3(512), 0, st, static_cast<const E*>(Xv), T, K,
-                       static_cast<const E*>(Av), R, scaling, S, static_cast<const E*>(Bv), N,
-                       static_cast<const E*>(base), static_cast<E*>(out), V, (int)bpw);
+  typedef Columns<DT, RT, 1, FULL> C;
+  constexpr int stage = (1 + RT) * 2048 > C::LDS ? (1 + RT) * 2048 : C::LDS;
+  constexpr int lds = 8 * stage + Mx<DT>::NC * 16 * C::LD * (int)sizeof(E) + 32;
+  static std::atomic<uint64_t> done{0};
+  const int tiles = lora_tiles(T, S, 16), groups = (N + C::GC - 1) / C::GC;
+  int64_t gpw = (int64_t)tiles * groups / (8 * 256);     // about 256 workgroups: few repeat V
+  gpw = gpw < 1 ? 1 : gpw > 64 ? 64 : gpw;
+  const int slices = groups > 0 ? (int)((groups + 8 * gpw - 1) / (8 * gpw)) : V ? 1 : 0;
+  if (slices == 0) return hipSuccess;
+  return launch(k_lora_short<DT, RT, FULL>, done, dim3(tiles, slices), 512, lds, st, static_cast<const E*>(Xv), T, K,
+                static_cast<const E*>(Av), R, scaling, S, static_cast<const E*>(Bv), N, static_cast<const E*>(base),
+                static_cast<E*>(out), V, (int)gpw);
 }
 
 template <int DT, int RT, int TMT, bool FULL>
-void run(const void* Xv, int T, int K, const void* Av, const void* Bv, const float* scaling, int R, int N,
-         const LoraSegs& S, const void* base, void* out, float* V, float* ws, hipStream_t st) {
+hipError_t run(const void* Xv, int T, int K, const void* Av, const void* Bv, const float* scaling, int R, int N,
+               const LoraSegs& S, const void* base, void* out, float* V, float* ws, hipStream_t st) {
   typedef typename Elem<DT>::T E;
-  constexpr int KS = Mx<DT>::KS, ST = RT == 8 ? TMT : 1, NW = RT < 8 ? 16 : ST == 4 ? 4 : 8;
-  const int tiles = lora_tiles(T, S, 16 * TMT);
+  typedef Columns<DT, RT, TMT, FULL> C;
+  constexpr int ST = RT == 8 ? TMT : 1, NW = RT < 8 ? 8 : 4;
   const int splits = shrink_splits(T, K, R, S.n_seg);
-  if (S.n_adapters > 0)
-    hipLaunchKernelGGL((k_lora_shrink<DT, RT, ST, NW, FULL>), dim3(lora_tiles(T, S, 16 * ST), splits), dim3(NW * 64),
-                       0, st, static_cast<const E*>(Xv), T, K, static_cast<const E*>(Av), R, S, ws);
-  const int blocks = (N + KS - 1) / KS;
-  int64_t bpw = (int64_t)tiles * blocks / (4 * 1024);
-  bpw = bpw < 1 ? 1 : bpw > 8 ? 8 : bpw;
-  const int slices = blocks > 0 ? (int)((blocks + 4 * bpw - 1) / (4 * bpw)) : V ? 1 : 0;
-  if (slices > 0)
-    hipLaunchKernelGGL((k_lora_expand<DT, RT, TMT, FULL>), dim3(tiles, slices), dim3(256), 0, st, ws, splits, T, N,
-                       static_cast<const E*>(Bv), R, scaling, S, static_cast<const E*>(base), static_cast<E*>(out), V,
-                       (int)bpw);
+  if (S.n_adapters > 0) {
+    constexpr int stage = NW * (ST + RT) * 2048, red = NW / 2 * ST * RT * 1024;
+    static std::atomic<uint64_t> done{0};
+    const hipError_t e = launch(k_lora_shrink<DT, RT, ST, NW>, done, dim3(lora_tiles(T, S, 16 * ST), splits), NW * 64,
+                                stage > red ? stage : red, st, static_cast<const E*>(Xv), T, K,
+                                static_cast<const E*>(Av), R, S, ws);
+    if (e != hipSuccess) return e;
+  }
+  const int tiles = lora_tiles(T, S, 16 * TMT), groups = (N + C::GC - 1) / C::GC;
+  // workgroups that are resident together: two a compute unit with 64 tokens, four with 16
+  constexpr int want = TMT == 4 ? 512 : 1024;
+  int64_t gpw = ((int64_t)tiles * groups + 4 * want - 1) / (4 * want);
+  gpw = gpw < 1 ? 1 : gpw > 16 ? 16 : gpw;
+  const int slices = groups > 0 ? (int)((groups + 4 * gpw - 1) / (4 * gpw)) : V ? 1 : 0;
+  if (slices == 0) return hipSuccess;
+  constexpr int small = Mx<DT>::NC * C::TM * C::LD * (int)sizeof(E) + C::TM * 4;
+  constexpr int lds = 4 * C::LDS > small ? 4 * C::LDS : small;
+  static std::atomic<uint64_t> done{0};
+  return launch(k_lora_expand<DT, RT, TMT, FULL>, done, dim3(tiles, slices), 256, lds, st, (const float*)ws, splits, T,
+                N, static_cast<const E*>(Bv), R, scaling, S, static_cast<const E*>(base), static_cast<E*>(out), V,
+                (int)gpw);
 }
 
 template <int DT, int RT, bool FULL>
-void run_rank(const void* X, int T, int K, const void* A, const void* B, const float* scaling, int R, int N,
+hipError_t run_rank(const void* X, int T, int K, const void* A, const void* B, const float* scaling, int R, int N,
               const LoraSegs& S, const void* base, void* out, float* V, float* ws, hipStream_t st) {
   if (one_launch(T, K, R, Elem<DT>::size, S.n_seg))
-    run_short<DT, RT, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, st);
-  else if (long_tiles(T, S.n_seg))
-    run<DT, RT, 4, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
-  else
-    run<DT, RT, 1, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
+    return run_short<DT, RT, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, st);
+  if (long_tiles(T, S.n_seg)) return run<DT, RT, 4, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
+  return run<DT, RT, 1, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
 }
 
-// Widths of whole steps and a rank of whole tiles run kernels without the code
-// for their ends: a short launch waits for its instructions as for its data.
 template <int DT, int RT>
-void run_size(const void* X, int T, int K, const void* A, const void* B, const float* scaling, int R, int N,
-              const LoraSegs& S, const void* base, void* out, float* V, float* ws, hipStream_t st) {
-  if (K % Mx<DT>::KS == 0 && N % Mx<DT>::KS == 0 && R == 16 * RT)
-    run_rank<DT, RT, true>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
-  else
-    run_rank<DT, RT, false>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
+hipError_t run_size(const void* X, int T, int K, const void* A, const void* B, const float* scaling, int R, int N,
+                    const LoraSegs& S, const void* base, void* out, float* V, float* ws, hipStream_t st) {
+  if (N % (8 * Mx<DT>::EL) == 0 && R == 16 * RT)
+    return run_rank<DT, RT, true>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
+  return run_rank<DT, RT, false>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
 }
 
 template <int DT>
 hipError_t forward_t(const void* X, int T, int K, const void* A, const void* B, const float* scaling, int R, int N,
                      const LoraSegs& S, const void* base, void* out, float* V, float* ws, hipStream_t st) {
   switch (rank_tiles(R)) {
-    case 1: run_size<DT, 1>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st); break;
-    case 2: run_size<DT, 2>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st); break;
-    case 4: run_size<DT, 4>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st); break;
-    default: run_size<DT, 8>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
+    case 1: return run_size<DT, 1>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
+    case 2: return run_size<DT, 2>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
+    case 4: return run_size<DT, 4>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
+    default: return run_size<DT, 8>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
   }
-  return hipGetLastError();
 }
 
 }  // namespace
