@@ -208,46 +208,6 @@ __device__ __forceinline__ void g_tile(const typename Elem<DT>::T* __restrict__ 
   const bool whole = n0 + WN <= N;
   const float scale = scaling[tl.adapter];
 
-  // B[a][n][r] with n along the contraction
-  v4u fb[RT][NK];
-  float bunit = 1.0f;
-  if (P) {
-    const E* Ba = B + (int64_t)tl.adapter * N * R;
-#pragma unroll
-    for (int j = 0; j < RT; ++j)
-#pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        fb[j][k] = v4u{0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int e = 0; e < EL; ++e) {
-          const int n = n0 + k * KS + EL * q + e, r = 16 * j + c;
-          const E w = Ba[(int64_t)min(n, N - 1) * R + min(r, R - 1)];
-          frag_set<DT>(fb[j][k], e, n < N && r < R ? w : Elem<DT>::from_f32(0.0f));
-        }
-      }
-    if constexpr (DT == DT_F16) {
-      // denormal weights lose bits in the matrix core (see the forward's
-      // shrink): a power of two takes the wave's largest to 2^14
-      uint32_t top = 0u;   // magnitude bits order as the values do
-#pragma unroll
-      for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int k = 0; k < NK; ++k)
-#pragma unroll
-          for (int e = 0; e < EL; ++e) {
-            const uint32_t m = (fb[j][k][e >> 1] >> (16 * (e & 1))) & 0x7fffu;
-            top = max(top, m < 0x7c00u ? m : 0u);
-          }
-      const float most = (float)__builtin_bit_cast(_Float16, (uint16_t)wave_umax(top));
-      bunit = fminf(fmaxf(unit_for(most), 1.0f), 0x1p15f);   // an fp16 value; never shrinks a weight
-#pragma unroll
-      for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int k = 0; k < NK; ++k)
-          fb[j][k] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, fb[j][k]) * (_Float16)bunit);
-    }
-  }
-
   v4f acc[RT][NT];
 #pragma unroll
   for (int j = 0; j < RT; ++j)
@@ -276,7 +236,74 @@ __device__ __forceinline__ void g_tile(const typename Elem<DT>::T* __restrict__ 
       }
     }
   };
+  typedef Tile<DT, RP> TB;
+  constexpr bool BYLDS = TB::BYTES <= ST * LDV * 4;
+  v4u lb[BYLDS ? NK : 1][BYLDS ? TB::NI : 1];
+  if constexpr (BYLDS) {
+    const int ch = EL * (lane % TB::CPR);
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+#pragma unroll
+      for (int i = 0; i < TB::NI; ++i) {
+        const int n = n0 + k * KS + TB::RPI * i + lane / TB::CPR;
+        lb[k][i] = v4u{0u, 0u, 0u, 0u};
+        if (P && n < N) lb[k][i] = ld_frag<DT>(B + ((int64_t)tl.adapter * N + n) * R + ch, R - ch);
+      }
+  }
   load(tl.t0);
+
+  // B[a][n][r] with n along the contraction: its rows through the wave's part of
+  // `red`, read transposed (fp32 at rank 128, where that is too small: gathered)
+  v4u fb[RT][NK];
+  float bunit = 1.0f;
+  if (P) {
+    const E* Ba = B + (int64_t)tl.adapter * N * R;
+    if constexpr (BYLDS) {
+      char* w = reinterpret_cast<char*>(red + wave * ST * LDV);
+#pragma unroll
+      for (int k = 0; k < NK; ++k) {
+#pragma unroll
+        for (int i = 0; i < TB::NI; ++i) TB::at(w, TB::RPI * i + lane / TB::CPR, lane % TB::CPR) = lb[k][i];
+#pragma unroll
+        for (int j = 0; j < RT; ++j) fb[j][k] = TB::get(w, j, lane);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          fb[j][k] = v4u{0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int e = 0; e < EL; ++e) {
+            const int n = n0 + k * KS + EL * q + e, r = 16 * j + c;
+            const E w = Ba[(int64_t)min(n, N - 1) * R + min(r, R - 1)];
+            frag_set<DT>(fb[j][k], e, n < N && r < R ? w : Elem<DT>::from_f32(0.0f));
+          }
+        }
+    }
+    if constexpr (DT == DT_F16) {
+      // denormal weights lose bits in the matrix core (see the forward's
+      // shrink): a power of two takes the wave's largest to 2^14
+      uint32_t top = 0u;   // magnitude bits order as the values do
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+#pragma unroll
+          for (int e = 0; e < EL; ++e) {
+            const uint32_t m = (fb[j][k][e >> 1] >> (16 * (e & 1))) & 0x7fffu;
+            top = max(top, m < 0x7c00u ? m : 0u);
+          }
+      const float most = (float)__builtin_bit_cast(_Float16, (uint16_t)wave_umax(top));
+      bunit = fminf(fmaxf(unit_for(most), 1.0f), 0x1p15f);   // an fp16 value; never shrinks a weight
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int k = 0; k < NK; ++k)
+          fb[j][k] = __builtin_bit_cast(v4u, __builtin_bit_cast(v8h, fb[j][k]) * (_Float16)bunit);
+    }
+  }
+
   for (int at = tl.t0; at < tl.t1; at += ST) {
     if (dBp) {
       if constexpr (DT == DT_F16) {
@@ -371,7 +398,7 @@ __device__ __forceinline__ void g_tile(const typename Elem<DT>::T* __restrict__ 
 // tm) tile by tile. B's fragments
 // for dV stay in registers; the eight waves' parts of dV meet in LDS.
 template <int DT, int RT, int WN, bool BLOCKS>
-__global__ __launch_bounds__(512) void k_lora_gpass(const typename Elem<DT>::T* __restrict__ G, int N, int T,
+__global__ __launch_bounds__(512, RT == 1 ? 4 : 2) void k_lora_gpass(const typename Elem<DT>::T* __restrict__ G, int N, int T,
                                                     const float* __restrict__ V,
                                                     const typename Elem<DT>::T* __restrict__ B, int R,
                                                     const float* __restrict__ scaling, LoraSegs S,
@@ -451,6 +478,26 @@ __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ 
     return;
   }
 
+  v4f acc[RT][NT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[j][n] = v4f{};
+  float run_top = 0.0f, unit = 1.0f, sub = 1.0f;
+
+  auto load_v = [&](int at) {
+#pragma unroll
+    for (int y = 0; y < SM::PER; ++y) {
+      const int e = tid + 512 * y, r = e % RP, t = at + 2 * (e / RP);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[y][h] = e < SM::PAIRS && r < R && t + h < tl.t1 ? dV[(int64_t)(t + h) * RP + r] : 0.0f;
+    }
+  };
+  if (dAp) load_rows(X, tl.t0, x);
+  if (out && base) load_rows(base, tl.t0, b);
+  load_v(tl.t0);
+
   // A[a][r][k] with r along the contraction, rows k in the order that gives a
   // lane consecutive k of the product: rows of A through the wave's tile, read
   // transposed
@@ -476,25 +523,6 @@ __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ 
     }
   }
 
-  v4f acc[RT][NT];
-#pragma unroll
-  for (int j = 0; j < RT; ++j)
-#pragma unroll
-    for (int n = 0; n < NT; ++n) acc[j][n] = v4f{};
-  float run_top = 0.0f, unit = 1.0f, sub = 1.0f;
-
-  auto load_v = [&](int at) {
-#pragma unroll
-    for (int y = 0; y < SM::PER; ++y) {
-      const int e = tid + 512 * y, r = e % RP, t = at + 2 * (e / RP);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        v[y][h] = e < SM::PAIRS && r < R && t + h < tl.t1 ? dV[(int64_t)(t + h) * RP + r] : 0.0f;
-    }
-  };
-  if (dAp) load_rows(X, tl.t0, x);
-  if (out && base) load_rows(base, tl.t0, b);
-  load_v(tl.t0);
   for (int at = tl.t0; at < tl.t1; at += ST) {
     if constexpr (DT == DT_F16) {
       float top = 0.0f;
@@ -750,16 +778,16 @@ struct Plan {
 };
 
 int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
-constexpr int wide_g(int rt) { return rt <= 2 ? 128 : rt == 4 ? 64 : 32; }
+constexpr int wide_g(int rt) { return rt == 2 ? 128 : rt <= 4 ? 64 : 32; }
 constexpr int wide_x(int rt) { return rt <= 4 ? 64 : 32; }
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Tokens of a workgroup, a multiple of 32 and at least 64: the number of token
+// Tokens of a workgroup, a multiple of 32: the number of token
 // blocks that fills the chip's 256 compute units `rounds` times, never one more.
 int tile_tokens(int T, int slices, int rounds) {
   const int blocks = 256 * rounds / slices;
   const int tm = (cdiv(T, blocks > 0 ? blocks : 1) + 31) / 32 * 32;
-  return tm < 64 ? 64 : tm;
+  return tm < 32 ? 32 : tm;
 }
 
 Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
@@ -776,14 +804,14 @@ Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
   p.wide_x = (int64_t)cdiv(K, 8 * wide_x(p.rt)) * cdiv(T, 64) >= 256;
   p.slices = cdiv(N, 8 * (p.wide_g ? wide_g(p.rt) : 32));
   p.slices = p.slices > 0 ? p.slices : 1;
-  p.tm_g = tile_tokens(T, p.slices, 1);
+  const int rounds = p.rt == 1 ? 2 : 1;   // rank 16 leaves room for two workgroups a unit
+  p.tm_g = tile_tokens(T, p.slices, rounds);
   p.tiles_g = lora_tiles(T, S, p.tm_g);
   const int slices_x = cdiv(K, 8 * (p.wide_x ? wide_x(p.rt) : 32));
-  const int rounds_x = p.rt == 1 ? 2 : 1;   // rank 16 leaves room for two workgroups a unit
-  p.tm_x = tile_tokens(T, slices_x > 0 ? slices_x : 1, rounds_x);
+  p.tm_x = tile_tokens(T, slices_x > 0 ? slices_x : 1, rounds);
   p.tiles_x = lora_tiles(T, S, p.tm_x);
-  p.by_tile_g = (int64_t)p.tiles_g * p.slices <= 280;
-  p.by_tile_x = (int64_t)p.tiles_x * slices_x <= 280 * rounds_x;
+  p.by_tile_g = (int64_t)p.tiles_g * p.slices <= 280 * rounds;
+  p.by_tile_x = (int64_t)p.tiles_x * slices_x <= 280 * rounds;
   p.kp = (K + 15) / 16 * 16;
   size_t at = 0;
   auto take = [&](size_t n) {

@@ -292,7 +292,7 @@ template <int DT, int RT, int TMT, int NW>
 __global__ __launch_bounds__(NW * 64) void k_lora_shrink(const typename Elem<DT>::T* __restrict__ X, int T, int K,
                                                          const typename Elem<DT>::T* __restrict__ A, int R,
                                                          LoraSegs S, float* __restrict__ P) {
-  constexpr int KS = Mx<DT>::KS, U = TMT + RT <= 2 ? 4 : TMT + RT <= 5 ? 2 : 1;
+  constexpr int KS = Mx<DT>::KS, U = TMT + RT <= 2 ? 4 : TMT + RT <= 6 ? 2 : 1;
   extern __shared__ __attribute__((aligned(16))) char sm[];
   v4f(*red)[TMT * RT][64] = reinterpret_cast<v4f(*)[TMT * RT][64]>(sm);
   const LoraTile tl = lora_tile(S, seg_lanes(S, T), blockIdx.x + 1, T, 16 * TMT);
@@ -522,7 +522,7 @@ bool long_tiles(int T, int n_seg) { return T >= 1024 && T / 48 >= n_seg; }
 // tokens on, and A, read once a tile, comes from L2 (a rank-64 A of 4096
 // features: 512 KB a tile against 128 KB of X from memory); at rank 128 that
 // would be the larger part, so long batches take 64.
-int shrink_tokens(int T, int R, int n_seg) { return R > 64 && long_tiles(T, n_seg) ? 64 : 16; }
+int shrink_tokens(int T, int R, int n_seg) { return !long_tiles(T, n_seg) ? 16 : R > 64 ? 64 : R > 32 ? 32 : 16; }
 
 // Splits of the contraction: about 256 workgroups, each with two steps or more for each of its waves.
 int shrink_splits(int T, int K, int R, int n_seg) {
@@ -578,7 +578,7 @@ hipError_t run(const void* Xv, int T, int K, const void* Av, const void* Bv, con
                const LoraSegs& S, const void* base, void* out, float* V, float* ws, hipStream_t st) {
   typedef typename Elem<DT>::T E;
   typedef Columns<DT, RT, TMT, FULL> C;
-  constexpr int ST = RT == 8 ? TMT : 1, NW = RT < 8 ? 8 : 4;
+  constexpr int ST = TMT == 1 ? 1 : RT == 8 ? 4 : RT == 4 ? 2 : 1, NW = RT < 8 ? 8 : 4;
   const int splits = shrink_splits(T, K, R, S.n_seg);
   if (S.n_adapters > 0) {
     constexpr int stage = NW * (ST + RT) * 2048, red = NW / 2 * ST * RT * 1024;
