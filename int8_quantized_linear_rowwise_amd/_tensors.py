@@ -29,7 +29,7 @@ def _dev(t: Optional[torch.Tensor], name: str) -> int:
 
 def _check_out(t: Optional[torch.Tensor], shape: tuple, dtype: torch.dtype, name: str) -> None:
     """Caller-provided result tensors must have exactly the size the kernels write."""
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is not None and (t.shape != shape or t.dtype != dtype):
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 

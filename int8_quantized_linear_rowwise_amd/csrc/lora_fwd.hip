@@ -533,14 +533,14 @@ int shrink_splits(int T, int K, int R, int n_seg) {
   return want < 1 || most < 1 ? 1 : want < most ? want : most;
 }
 
-// One launch for up to 32 tiles with an A of up to 160 KB. Every workgroup
-// reads A[a] whole, at the 15 to 25 GB/s that one compute unit gets from
-// memory: 128 KB take as long as two launches that split k (8 us), but the
-// second launch costs the host 4 us. With 64 tiles and 11008 columns one launch
-// takes 22 us against 7 + 9.
-bool one_launch(int T, int K, int R, int elem, int n_seg) {
+// One launch for up to 32 tiles with an A of up to 81920 values (it needs no
+// workspace). Every workgroup reads A[a] whole, at the 25 GB/s or so that one
+// compute unit gets from memory: one token, 4096 x 4096 at rank 16, takes 6.8 us
+// against 3.9 + 4.4 us split over k, but a second launch costs the host 4 us.
+// With 64 tiles and 11008 columns one launch took 22 us against 6 + 10.
+bool one_launch(int T, int K, int R, int n_seg) {
   const LoraSegs S = {nullptr, nullptr, n_seg, 0};
-  return lora_tiles(T, S, 16) <= 32 && (int64_t)K * R * elem <= 160 * 1024;
+  return lora_tiles(T, S, 16) <= 32 && (int64_t)K * R <= 81920;
 }
 
 // A launch with `lds` bytes of dynamic LDS; over 64 KB the kernel's limit is raised first.
@@ -606,7 +606,7 @@ hipError_t run(const void* Xv, int T, int K, const void* Av, const void* Bv, con
 template <int DT, int RT, bool FULL>
 hipError_t run_rank(const void* X, int T, int K, const void* A, const void* B, const float* scaling, int R, int N,
               const LoraSegs& S, const void* base, void* out, float* V, float* ws, hipStream_t st) {
-  if (one_launch(T, K, R, Elem<DT>::size, S.n_seg))
+  if (one_launch(T, K, R, S.n_seg))
     return run_short<DT, RT, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, st);
   if (long_tiles(T, S.n_seg)) return run<DT, RT, 4, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
   return run<DT, RT, 1, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
@@ -634,6 +634,7 @@ hipError_t forward_t(const void* X, int T, int K, const void* A, const void* B, 
 }  // namespace
 
 size_t lora_forward_floats(int T, int K, int N, int R, int n_seg) {
+  if (one_launch(T, K, R, n_seg)) return 0;
   return (size_t)shrink_splits(T, K, R, n_seg) * T * 16 * rank_tiles(R);
 }
 

@@ -13,7 +13,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from ._lib import AdamWTensor, check, lib
-from ._tensors import DTYPE_CODE, _code, _dev, _raw_stream
+from ._tensors import DTYPE_CODE, _ptr, _raw_stream
 
 BLOCK = 256   # values that share a scale
 
@@ -61,30 +61,32 @@ class AdamWPlan:
         self._keep = [list(params)] + [list(x) for x in lists.values() if x is not None]
         self.table, self.count, self.chunks = None, n, 0
         arr = (AdamWTensor * n)()
-        for i, p in enumerate(params):
-            size = p.numel()
-            low = m[i].dtype == torch.float8_e4m3fn
+        none = [None] * n
+        names = ("params", "grads", "m", "v", "m_scale", "v_scale", "master")
+        for i, row in enumerate(zip(params, grads, m, v, m_scale or none, v_scale or none, master or none)):
+            p, g, mi, vi, ms, vs, w = row
+            size, dtype = p.numel(), p.dtype
+            low = mi.dtype == torch.float8_e4m3fn
             state = torch.float8_e4m3fn if low else torch.float32
-            if p.dtype not in DTYPE_CODE:
-                raise TypeError(f"unsupported dtype {p.dtype}; expected float32, float16 or bfloat16")
-            if grads[i].dtype != p.dtype or grads[i].numel() != size:
+            if dtype not in DTYPE_CODE:
+                raise TypeError(f"unsupported dtype {dtype}; expected float32, float16 or bfloat16")
+            if g.dtype != dtype or g.numel() != size:
                 raise ValueError(f"grads[{i}] must have its parameter's size and dtype")
-            if m[i].dtype != state or v[i].dtype != state or m[i].numel() != size or v[i].numel() != size:
+            if mi.dtype != state or vi.dtype != state or mi.numel() != size or vi.numel() != size:
                 raise ValueError(f"m[{i}] and v[{i}] must both be float32 or both float8_e4m3fn, of the "
                                  "parameter's size")
             if low:
-                for name, x in (("m_scale", m_scale), ("v_scale", v_scale)):
-                    if x is None or x[i].dtype != torch.float32 or x[i].numel() != -(-size // BLOCK):
+                for name, x in (("m_scale", ms), ("v_scale", vs)):
+                    if x is None or x.dtype != torch.float32 or x.numel() != -(-size // BLOCK):
                         raise ValueError(f"{name}[{i}] must be float32 with one value for each {BLOCK}")
-            if master is not None and (master[i].dtype != torch.float32 or master[i].numel() != size):
+            else:
+                row = (p, g, mi, vi, None, None, w)
+            if w is not None and (w.dtype != torch.float32 or w.numel() != size):
                 raise ValueError(f"master[{i}] must be float32 of the parameter's size")
-            row = [x for x in (p, grads[i], m[i], v[i], m_scale[i] if low else None, v_scale[i] if low else None,
-                               master[i] if master is not None else None)]
-            if any(x is not None and x.device != self.device for x in row):
-                raise ValueError("all tensors of a plan must be on one GPU")
-            names = ("params", "grads", "m", "v", "m_scale", "v_scale", "master")
-            ptr = [_dev(x, f"{k}[{i}]") or None for x, k in zip(row, names)]
-            arr[i] = AdamWTensor(*ptr, size, _code(p), 8 if low else 32)
+            if self.gpu < 0:
+                raise ValueError("parameters must be on a GPU")
+            arr[i] = AdamWTensor(*[_ptr(t, k, self.gpu) or None for t, k in zip(row, names)], size,
+                                 DTYPE_CODE[dtype], 8 if low else 32)
         need = lib.int8_adamw_table_bytes(arr, n)
         host = torch.zeros(max(need, 1), dtype=torch.uint8)
         chunks = ctypes.c_int64(0)

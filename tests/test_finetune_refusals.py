@@ -12,8 +12,9 @@ from tests.test_abi import FAKE, L  # noqa: F401  (fixture: builds the library i
 
 def test_lora_forward_host_errors(L):  # noqa: F811
     f, need = L.lib.int8_lora_forward, L.lib.int8_lora_forward_workspace_bytes
-    base = dict(X=FAKE, dt=2, T=8, K=64, A=FAKE, B=FAKE, s=FAKE, n=2, R=16, N=32, off=FAKE, ids=FAKE, S=3, base=None,
-                out=FAKE, V=None, ws=FAKE, wsb=1 << 40, st=None)
+    # a size that takes a workspace (small ones run without)
+    base = dict(X=FAKE, dt=2, T=8, K=64000, A=FAKE, B=FAKE, s=FAKE, n=2, R=16, N=32, off=FAKE, ids=FAKE, S=3,
+                base=None, out=FAKE, V=None, ws=FAKE, wsb=1 << 40, st=None)
 
     def call(**kw):
         a = dict(base, **kw)
@@ -28,12 +29,12 @@ def test_lora_forward_host_errors(L):  # noqa: F811
     assert call(K=L.I8L_MAX_COLS + 1) == L.I8L_ESHAPE and call(N=L.I8L_MAX_COLS + 1) == L.I8L_ESHAPE
     assert call(T=1 << 31) == L.I8L_ESHAPE and call(S=1 << 31) == L.I8L_ESHAPE and call(n=65536) == L.I8L_ESHAPE
     assert call(T=1 << 29, S=(1 << 29) + 1) == L.I8L_ESHAPE
-    wsb = need(8, 64, 32, 16, 3)
+    wsb = need(8, 64000, 32, 16, 3)
     assert wsb % 256 == 0 and wsb > 0
     assert call(wsb=wsb - 1) == L.I8L_EWORKSPACE and call(ws=0) == L.I8L_EWORKSPACE
     assert call(ws=FAKE + 16) == L.I8L_EINVAL
     assert call(T=0, X=0, out=0, off=0, ws=0, wsb=0) == L.I8L_OK
-    assert need(-1, 64, 32, 16, 3) == 0 and need(8, 64, 32, 129, 3) == 0
+    assert need(-1, 64, 32, 16, 3) == 0 and need(8, 64, 32, 129, 3) == 0 and need(8, 64, 32, 16, 3) == 0
 
 
 def test_lora_backward_host_errors(L):  # noqa: F811
