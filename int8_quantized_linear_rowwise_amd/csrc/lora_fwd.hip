@@ -518,18 +518,17 @@ int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 // 64-token tiles read B once for 64 tokens; they need segments that fill them.
 bool long_tiles(int T, int n_seg) { return T >= 1024 && T / 48 >= n_seg; }
 
-// Tokens of a shrink tile. 16 fill the chip without splitting k from 4096
-// tokens on, and A, read once a tile, comes from L2 (a rank-64 A of 4096
-// features: 512 KB a tile against 128 KB of X from memory); at rank 128 that
-// would be the larger part, so long batches take 64.
-int shrink_tokens(int T, int R, int n_seg) { return !long_tiles(T, n_seg) ? 16 : R > 64 ? 64 : R > 32 ? 32 : 16; }
-
-// Splits of the contraction: about 256 workgroups, each with two steps or more for each of its waves.
-int shrink_splits(int T, int K, int R, int n_seg) {
+// Splits of the contraction: as many workgroups as run together (one a compute
+// unit with 64 tokens), each with two pairs of steps or more for each of its
+// waves. 4096 tokens of 4096 features at rank 64: tiles of 64 tokens in three
+// splits take 15 us, of 32 in two 22 us, of 16 whole 26 us, as A is read once a
+// tile (from L2 at best: 512 KB against 128 KB of X for 16 tokens).
+int shrink_splits(int T, int K, int n_seg) {
   const LoraSegs S = {nullptr, nullptr, n_seg, 0};
-  const int tiles = lora_tiles(T, S, shrink_tokens(T, R, n_seg));
+  const bool big = long_tiles(T, n_seg);
+  const int tiles = lora_tiles(T, S, big ? 64 : 16);
   const int most = K / 512 < MAX_SPLITS ? K / 512 : MAX_SPLITS;
-  const int want = 384 / (tiles > 0 ? tiles : 1);
+  const int want = (big ? 256 : 384) / (tiles > 0 ? tiles : 1);
   return want < 1 || most < 1 ? 1 : want < most ? want : most;
 }
 
@@ -578,12 +577,12 @@ hipError_t run(const void* Xv, int T, int K, const void* Av, const void* Bv, con
                const LoraSegs& S, const void* base, void* out, float* V, float* ws, hipStream_t st) {
   typedef typename Elem<DT>::T E;
   typedef Columns<DT, RT, TMT, FULL> C;
-  constexpr int ST = TMT == 1 ? 1 : RT == 8 ? 4 : RT == 4 ? 2 : 1, NW = RT < 8 ? 8 : 4;
-  const int splits = shrink_splits(T, K, R, S.n_seg);
+  constexpr int NW = RT < 8 ? 8 : 4;
+  const int splits = shrink_splits(T, K, S.n_seg);
   if (S.n_adapters > 0) {
-    constexpr int stage = NW * (ST + RT) * 2048, red = NW / 2 * ST * RT * 1024;
+    constexpr int stage = NW * (TMT + RT) * 2048, red = NW / 2 * TMT * RT * 1024;
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = launch(k_lora_shrink<DT, RT, ST, NW>, done, dim3(lora_tiles(T, S, 16 * ST), splits), NW * 64,
+    const hipError_t e = launch(k_lora_shrink<DT, RT, TMT, NW>, done, dim3(lora_tiles(T, S, 16 * TMT), splits), NW * 64,
                                 stage > red ? stage : red, st, static_cast<const E*>(Xv), T, K,
                                 static_cast<const E*>(Av), R, S, ws);
     if (e != hipSuccess) return e;
@@ -635,7 +634,7 @@ hipError_t forward_t(const void* X, int T, int K, const void* A, const void* B, 
 
 size_t lora_forward_floats(int T, int K, int N, int R, int n_seg) {
   if (one_launch(T, K, R, n_seg)) return 0;
-  return (size_t)shrink_splits(T, K, R, n_seg) * T * 16 * rank_tiles(R);
+  return (size_t)shrink_splits(T, K, n_seg) * T * 16 * rank_tiles(R);
 }
 
 hipError_t launch_lora_forward(int dt, const void* X, int T, int K, const void* A, const void* B,
