@@ -7,9 +7,10 @@
 // 4 T R (K + N) flops. Each large operand serves two products, one along the
 // features and one along the tokens, so each is read once for both:
 //   g pass: G gives dV (partial sums by column slice) and dB (by token tile);
-//   sum of the slices of dV;
+//   sum of the slices of dV and of the tiles of dB, in a fixed order;
 //   x pass: X and base_grad give dx and dA (partial sums by token tile);
-//   sum of the tiles of dA and dB, in a fixed order.
+//   sum of the tiles of dA.
+// Small batches skip the first sum: the x pass adds the slices up itself.
 // A workgroup takes a slice of columns and a block of tokens, which it walks
 // tile by tile (the block's tokens of one adapter); its eight waves split the columns, and each holds its part of the weight
 // gradient in registers while it walks the tokens 32 (fp32: 16) at a time. The
@@ -419,7 +420,7 @@ __global__ __launch_bounds__(512, RT == 1 ? 4 : 2) void k_lora_gpass(const typen
 // One tile of k_lora_xpass.
 template <int DT, int RT, int WN>
 __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ X, int K, int T,
-                                       const float* __restrict__ dV, const typename Elem<DT>::T* __restrict__ A, int R,
+                                       const float* __restrict__ dV, int slices, const typename Elem<DT>::T* __restrict__ A, int R,
                                        const LoraSegs& S, const SegLanes& L, const int32_t* __restrict__ perm, int tm,
                                        const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
                                        float* __restrict__ dAp, int Kp, int32_t* __restrict__ tile_adapter, int d) {
@@ -490,8 +491,17 @@ __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ 
     for (int y = 0; y < SM::PER; ++y) {
       const int e = tid + 512 * y, r = e % RP, t = at + 2 * (e / RP);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        v[y][h] = e < SM::PAIRS && r < R && t + h < tl.t1 ? dV[(int64_t)(t + h) * RP + r] : 0.0f;
+      for (int h = 0; h < 2; ++h) {
+        v[y][h] = 0.0f;
+        if (e < SM::PAIRS && r < R && t + h < tl.t1) {
+          const float* p = dV + (int64_t)(t + h) * RP + r;
+          v[y][h] = p[0];
+          if constexpr (WN == 32) {   // the small batches' form: dV still in slices
+#pragma unroll 4
+            for (int s = 1; s < slices; ++s) v[y][h] += p[(int64_t)s * T * RP];
+          }
+        }
+      }
     }
   };
   if (dAp) load_rows(X, tl.t0, x);
@@ -626,8 +636,8 @@ __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ 
 // dx and the partial sums dAp[tile][r][Kp] of 8 WN columns of X and the same tokens. dx is taken transposed, as the forward's expand,
 // with A's fragments in registers.
 template <int DT, int RT, int WN, bool BLOCKS>
-__global__ __launch_bounds__(512, RT == 1 ? 4 : 2) void k_lora_xpass(const typename Elem<DT>::T* __restrict__ X, int K, int T,
-                                                    const float* __restrict__ dV,
+__global__ __launch_bounds__(512, RT == 1 && DT != DT_F16 ? 4 : 2) void k_lora_xpass(const typename Elem<DT>::T* __restrict__ X, int K, int T,
+                                                    const float* __restrict__ dV, int slices,
                                                     const typename Elem<DT>::T* __restrict__ A, int R, LoraSegs S,
                                                     const int32_t* __restrict__ perm, int tm,
                                                     const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
@@ -635,11 +645,11 @@ __global__ __launch_bounds__(512, RT == 1 ? 4 : 2) void k_lora_xpass(const typen
                                                     int32_t* __restrict__ tile_adapter) {
   const SegLanes L = seg_lanes(S, T);
   if constexpr (!BLOCKS) {
-    x_tile<DT, RT, WN>(X, K, T, dV, A, R, S, L, perm, tm, base, out, dAp, Kp, tile_adapter, blockIdx.y + 1);
+    x_tile<DT, RT, WN>(X, K, T, dV, slices, A, R, S, L, perm, tm, base, out, dAp, Kp, tile_adapter, blockIdx.y + 1);
   } else {
     const int d1 = first_tile(S, L, blockIdx.y + 1, T, tm);
     for (int d = max(first_tile(S, L, blockIdx.y, T, tm), 1); d < d1; ++d) {
-      x_tile<DT, RT, WN>(X, K, T, dV, A, R, S, L, perm, tm, base, out, dAp, Kp, tile_adapter, d);
+      x_tile<DT, RT, WN>(X, K, T, dV, slices, A, R, S, L, perm, tm, base, out, dAp, Kp, tile_adapter, d);
       __syncthreads();
     }
   }
@@ -660,9 +670,9 @@ struct SliceSum {
   int64_t n4;
   int slices, blocks;   // blocks: workgroups of 1024 values
 };
-// Workgroups: the slices' first, then the tiles', adapter after adapter.
+// Workgroups: the slices' first, then a's and b's tiles, adapter after adapter.
 template <int DT>
-__global__ __launch_bounds__(256) void k_lora_sum(SliceSum v, TileSum s) {
+__global__ __launch_bounds__(256) void k_lora_sum(SliceSum v, TileSum a, TileSum b, int adapters) {
   typedef typename Elem<DT>::T E;
   __shared__ int list[256];
   __shared__ int count;
@@ -676,7 +686,10 @@ __global__ __launch_bounds__(256) void k_lora_sum(SliceSum v, TileSum s) {
     reinterpret_cast<v4f*>(v.out)[i] = sum;
     return;
   }
-  const int id = blockIdx.x - v.blocks, ad = id / s.blocks;
+  const int at = blockIdx.x - v.blocks;
+  const bool first = at < a.blocks * adapters;
+  const TileSum s = first ? a : b;
+  const int id = first ? at : at - a.blocks * adapters, ad = id / s.blocks;
   const int64_t e = ((int64_t)(id - ad * s.blocks) * 256 + threadIdx.x) * 4;
   const int64_t each = (int64_t)s.rows * s.ld;
   const float* p = s.part + min(e, each - 4);
@@ -773,7 +786,7 @@ namespace {
 // Sizes of the launches and of the workspace; of the shape alone.
 struct Plan {
   int rt, slices, tm_g, tiles_g, tm_x, tiles_x, kp;
-  bool wide_g, wide_x, sort, by_tile_g, by_tile_x;   // by_tile: a workgroup a tile, where that fills the chip once
+  bool wide_g, wide_x, sort, fold, by_tile_g, by_tile_x;   // by_tile: a workgroup a tile, where that fills the chip once
   size_t p, dv, dbp, dap, ad_g, ad_x, perm, starts, total;   // offsets in floats
 };
 
@@ -810,6 +823,8 @@ Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
   const int slices_x = cdiv(K, 8 * (p.wide_x ? wide_x(p.rt) : 32));
   p.tm_x = tile_tokens(T, slices_x > 0 ? slices_x : 1, rounds);
   p.tiles_x = lora_tiles(T, S, p.tm_x);
+  // few slices of a small batch: the x pass adds them up as it reads them, instead of a launch of its own (4 us)
+  p.fold = !p.wide_x && p.slices > 1 && p.slices <= 8 && (int64_t)p.slices * T * rp * 4 * slices_x <= 4 * 1000 * 1000;
   p.by_tile_g = (int64_t)p.tiles_g * p.slices <= 280 * rounds;
   p.by_tile_x = (int64_t)p.tiles_x * slices_x <= 280 * rounds;
   p.kp = (K + 15) / 16 * 16;
@@ -848,7 +863,7 @@ hipError_t g_pass(const Plan& p, const void* G, const float* V, int T, const voi
 }
 
 template <int DT, int RT, int WN, bool BLOCKS>
-hipError_t x_pass(const Plan& p, const void* X, int T, int K, const float* dV, const void* A, int R,
+hipError_t x_pass(const Plan& p, const void* X, int T, int K, const float* dV, int slices, const void* A, int R,
                   const LoraSegs& S, const int32_t* perm, const void* base, void* out, float* dAp, int32_t* ad,
                   hipStream_t st) {
   typedef typename Elem<DT>::T E;
@@ -858,7 +873,7 @@ hipError_t x_pass(const Plan& p, const void* X, int T, int K, const float* dV, c
   const hipError_t e = lds_limit_once((const void*)kern, lds, done);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, dim3(cdiv(K, 8 * WN), BLOCKS ? cdiv(T, p.tm_x) : p.tiles_x), dim3(512), lds, st, static_cast<const E*>(X), K, T, dV,
-                     static_cast<const E*>(A), R, S, perm, p.tm_x, static_cast<const E*>(base), static_cast<E*>(out),
+                     slices, static_cast<const E*>(A), R, S, perm, p.tm_x, static_cast<const E*>(base), static_cast<E*>(out),
                      dAp, p.kp, ad);
   return hipGetLastError();
 }
@@ -885,7 +900,6 @@ hipError_t backward_t(const Plan& p, const void* G, const void* X, const float* 
   }
   const int rp = 16 * RT;
   SliceSum slices = {};
-  TileSum tiles = {};
   if (rows && na > 0 && N > 0 && (want_dv || gB)) {
     float* P = !want_dv ? nullptr : p.slices > 1 ? ws + p.p : dV;
     float* dBp = gB ? ws + p.dbp : nullptr;
@@ -893,17 +907,22 @@ hipError_t backward_t(const Plan& p, const void* G, const void* X, const float* 
                          : (p.by_tile_g ? g_pass<DT, RT, 32, false> : g_pass<DT, RT, 32, true>);
     e = pass(p, G, V, T, B, scaling, R, N, S, perm, P, dBp, ad_g, st);
     if (e != hipSuccess) return e;
-    if (want_dv && p.slices > 1) {
+    if (want_dv && p.slices > 1 && !p.fold) {
       const int64_t n4 = (int64_t)T * 4 * RT;
       slices = SliceSum{P, dV, n4, p.slices, cdiv(n4, 256)};
     }
   }
-  // beside the sum of dV's slices: dB is whole after the g pass
+  auto sum = [&](const SliceSum& v, const TileSum& a, const TileSum& b) {
+    const int64_t blocks = v.blocks + ((int64_t)a.blocks + b.blocks) * na;
+    if (blocks > 0) hipLaunchKernelGGL(k_lora_sum<DT>, dim3((unsigned)blocks), dim3(256), 0, st, v, a, b, na);
+  };
+  TileSum sum_b = {}, sum_a = {};
   if (gB && na > 0 && R > 0 && N > 0)
-    tiles = TileSum{ws + p.dbp, ad_g, gB, rows ? p.tiles_g : 0, N, rp, R, cdiv((int64_t)N * rp, 1024)};
-  if (slices.blocks + tiles.blocks > 0)
-    hipLaunchKernelGGL(k_lora_sum<DT>, dim3((unsigned)((int64_t)slices.blocks + (int64_t)tiles.blocks * na)), dim3(256),
-                       0, st, slices, tiles);
+    sum_b = TileSum{ws + p.dbp, ad_g, gB, rows ? p.tiles_g : 0, N, rp, R, cdiv((int64_t)N * rp, 1024)};
+  if (slices.blocks > 0) {   // beside the sum of dV's slices: dB is whole after the g pass
+    sum(slices, sum_b, TileSum{});
+    sum_b = TileSum{};
+  }
   const bool no_dv = N == 0;   // dV = 0: nothing reaches A or X
   if (rows && K > 0 && (gX || (gA && na > 0))) {
     LoraSegs Sx = S;
@@ -911,14 +930,12 @@ hipError_t backward_t(const Plan& p, const void* G, const void* X, const float* 
     float* dAp = gA && na > 0 ? ws + p.dap : nullptr;
     auto pass = p.wide_x ? (p.by_tile_x ? x_pass<DT, RT, wide_x(RT), false> : x_pass<DT, RT, wide_x(RT), true>)
                          : (p.by_tile_x ? x_pass<DT, RT, 32, false> : x_pass<DT, RT, 32, true>);
-    e = pass(p, X, T, K, dV, A, R, Sx, perm, base_grad, gX, dAp, ad_x, st);
+    e = pass(p, X, T, K, p.fold ? ws + p.p : dV, p.fold ? p.slices : 1, A, R, Sx, perm, base_grad, gX, dAp, ad_x, st);
     if (e != hipSuccess) return e;
   }
-  if (gA && na > 0 && R > 0 && K > 0) {
-    tiles = TileSum{ws + p.dap, ad_x, gA, rows ? p.tiles_x : 0, R, p.kp, K, cdiv((int64_t)R * p.kp, 1024)};
-    hipLaunchKernelGGL(k_lora_sum<DT>, dim3((unsigned)((int64_t)tiles.blocks * na)), dim3(256), 0, st, SliceSum{},
-                       tiles);
-  }
+  if (gA && na > 0 && R > 0 && K > 0)
+    sum_a = TileSum{ws + p.dap, ad_x, gA, rows ? p.tiles_x : 0, R, p.kp, K, cdiv((int64_t)R * p.kp, 1024)};
+  sum(SliceSum{}, sum_a, sum_b);
   return hipGetLastError();
 }
 

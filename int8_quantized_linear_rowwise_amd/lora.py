@@ -66,7 +66,8 @@ def lora_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scaling: tor
         _check_out(v, (T, R), torch.float32, "v")
     dev = _gpu(X, "X")
     if out is None:
-        out = _empty((T, N), X.dtype, X.device)
+        out = _empty((T, N), X.dtype, X.device) if base is None else \
+            torch.empty_like(base, memory_format=torch.contiguous_format)
     if v is None and with_v:
         v = _empty((T, R), torch.float32, X.device)
     need = lib.int8_lora_forward_workspace_bytes(T, K, N, R, S)
