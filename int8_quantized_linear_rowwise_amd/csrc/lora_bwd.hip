@@ -786,7 +786,7 @@ namespace {
 // Sizes of the launches and of the workspace; of the shape alone.
 struct Plan {
   int rt, slices, tm_g, tiles_g, tm_x, tiles_x, kp;
-  bool wide_g, wide_x, sort, fold, by_tile_g, by_tile_x;   // by_tile: a workgroup a tile, where that fills the chip once
+  bool wide_g, wide_x, sort, fold, by_tile_g, by_tile_x;   // by_tile: a workgroup a tile
   size_t p, dv, dbp, dap, ad_g, ad_x, perm, starts, total;   // offsets in floats
 };
 
@@ -795,12 +795,22 @@ constexpr int wide_g(int rt) { return rt == 2 ? 128 : rt <= 4 ? 64 : 32; }
 constexpr int wide_x(int rt) { return rt <= 4 ? 64 : 32; }
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Tokens of a workgroup, a multiple of 32: the number of token
-// blocks that fills the chip's 256 compute units `rounds` times, never one more.
-int tile_tokens(int T, int slices, int rounds) {
-  const int blocks = 256 * rounds / slices;
+// Tokens of a workgroup, a multiple of 32: the number of token blocks that fills
+// the chip's 256 compute units `rounds` times, never one more. Where the partial
+// weight gradients would then pass 16 MB, at least twice the rank: a tile's is
+// 4 Rp / tm times as much to write and read as its own 16-bit rows (987 tokens
+// of 24 segments, 4480 -> 2792 at rank 64: 81 us with 32 tokens, 69 with 128;
+// 698 tokens of 14, 604 -> 1152: 34 and 38).
+int tile_tokens(int T, int slices, int rounds, int rp, int width, int n_seg) {
+  const int blocks = 256 * rounds / slices, least = 2 * rp;
   const int tm = (cdiv(T, blocks > 0 ? blocks : 1) + 31) / 32 * 32;
-  return tm < 32 ? 32 : tm;
+  const int64_t partial = ((int64_t)cdiv(T, tm > 0 ? tm : 32) + n_seg) * width * rp * 4;
+  return tm < 32 ? 32 : partial > 16 * 1000 * 1000 && tm < least ? least : tm;
+}
+
+// A workgroup for every tile where those run at once, or where the blocks are too few to fill the chip.
+bool one_tile_each(int tiles, int blocks, int slices, int rounds) {
+  return (int64_t)tiles * slices <= 280 * rounds || (int64_t)blocks * slices < 192 * rounds;
 }
 
 Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
@@ -818,15 +828,15 @@ Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
   p.slices = cdiv(N, 8 * (p.wide_g ? wide_g(p.rt) : 32));
   p.slices = p.slices > 0 ? p.slices : 1;
   const int rounds = p.rt == 1 ? 2 : 1;   // rank 16 leaves room for two workgroups a unit
-  p.tm_g = tile_tokens(T, p.slices, rounds);
+  p.tm_g = tile_tokens(T, p.slices, rounds, rp, N, S.n_seg);
   p.tiles_g = lora_tiles(T, S, p.tm_g);
   const int slices_x = cdiv(K, 8 * (p.wide_x ? wide_x(p.rt) : 32));
-  p.tm_x = tile_tokens(T, slices_x > 0 ? slices_x : 1, rounds);
+  p.tm_x = tile_tokens(T, slices_x > 0 ? slices_x : 1, rounds, rp, K, S.n_seg);
   p.tiles_x = lora_tiles(T, S, p.tm_x);
   // few slices of a small batch: the x pass adds them up as it reads them, instead of a launch of its own (4 us)
   p.fold = !p.wide_x && p.slices > 1 && p.slices <= 8 && (int64_t)p.slices * T * rp * 4 * slices_x <= 4 * 1000 * 1000;
-  p.by_tile_g = (int64_t)p.tiles_g * p.slices <= 280 * rounds;
-  p.by_tile_x = (int64_t)p.tiles_x * slices_x <= 280 * rounds;
+  p.by_tile_g = one_tile_each(p.tiles_g, cdiv(T, p.tm_g), p.slices, rounds);
+  p.by_tile_x = one_tile_each(p.tiles_x, cdiv(T, p.tm_x), slices_x, rounds);
   p.kp = (K + 15) / 16 * 16;
   size_t at = 0;
   auto take = [&](size_t n) {
