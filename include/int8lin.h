@@ -322,7 +322,10 @@ int int8_linear_backward_weight(const void* G, const void* A, int dtype, int64_t
  * grad_A and grad_B may each be NULL (not computed); V is the forward's. An
  * adapter without rows gets a zero gradient.
  * R <= I8L_LORA_MAX_RANK, K and N <= I8L_MAX_COLS, n_adapters <= 65535,
- * T <= 2^24, n_seg <= 2^20, else I8L_ESHAPE.
+ * T <= 2^24, n_seg <= 2^20, and n_adapters * max(K, N) * (R rounded up to 16,
+ * 32, 64 or 128) <= 2^33, else I8L_ESHAPE. Apart from base and base_grad no
+ * output may overlap an input. Forward and backward may return 0 as their
+ * workspace's size; workspace may then be NULL.
  * ------------------------------------------------------------------------ */
 #define I8L_LORA_MAX_RANK 128
 
@@ -395,7 +398,8 @@ int int8_layer_norm_backward(const void* G, const void* X, int dtype, int64_t T,
  *     leaves everything as it is.
  * A beta outside [0, 1), or a negative or non-finite lr, eps or weight_decay is
  * I8L_EINVAL. Each value is read and written by one thread: no two tensors
- * may overlap.
+ * may overlap. A captured step keeps the lr, step and other numbers of its
+ * capture; grad_scale and found_inf are read at each replay.
  * ------------------------------------------------------------------------ */
 typedef struct {
   void* p;           /* n of dtype */

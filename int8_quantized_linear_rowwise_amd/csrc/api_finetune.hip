@@ -15,6 +15,7 @@ constexpr size_t ALIGN = 256;
 constexpr int64_t MAX_TOKENS = (int64_t)1 << 24;   // rows; tiles of 16 rows and their threads stay within a grid axis
 constexpr int64_t MAX_SEGMENTS = (int64_t)1 << 20;
 constexpr int64_t MAX_ADAPTERS = 65535;
+constexpr int64_t MAX_ADAPTER_VALUES = (int64_t)1 << 33;
 constexpr int64_t MAX_VALUES = (int64_t)1 << 40;
 
 size_t align_up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
@@ -27,6 +28,9 @@ int lora_sizes(int64_t T, int64_t K, int64_t N, int64_t R, int64_t n_adapters, i
   if (T > MAX_TOKENS || n_seg > MAX_SEGMENTS || K > I8L_MAX_COLS || N > I8L_MAX_COLS ||
       R > I8L_LORA_MAX_RANK || n_adapters > MAX_ADAPTERS || T * K > MAX_VALUES || T * N > MAX_VALUES)
     return I8L_ESHAPE;
+  // adapters padded to a rank of 16, 32, 64 or 128: the gradient's sums take a workgroup for 1024 values of them
+  const int64_t rp = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128;
+  if (n_adapters * rp * (K > N ? K : N) > MAX_ADAPTER_VALUES) return I8L_ESHAPE;
   return I8L_OK;
 }
 

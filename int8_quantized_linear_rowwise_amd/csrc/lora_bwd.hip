@@ -185,7 +185,7 @@ __device__ __forceinline__ void g_tile(const typename Elem<DT>::T* __restrict__ 
                                        const float* __restrict__ scaling, const LoraSegs& S,
                                        const SegLanes& L, const int32_t* __restrict__ perm, int tm,
                                        float* __restrict__ P,
-                                       float* __restrict__ dBp, int32_t* __restrict__ tile_adapter, int d) {
+                                       float* __restrict__ dBp, int32_t* __restrict__ tile_adapter, int slice, int d) {
   typedef Mx<DT> M;
   typedef typename Elem<DT>::T E;
   typedef Tile<DT, WN> TL;
@@ -204,11 +204,11 @@ __device__ __forceinline__ void g_tile(const typename Elem<DT>::T* __restrict__ 
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
   const int lane = tid & 63, c = lane & 15, q = lane >> 4;
-  if (blockIdx.x == 0 && tid == 0) tile_adapter[d - 1] = none ? -1 : tl.adapter;
+  if (slice == 0 && tid == 0) tile_adapter[d - 1] = none ? -1 : tl.adapter;
   if (none) return;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   char* mine = sm + wave * TL::BYTES;
-  const int n0 = blockIdx.x * 8 * WN + wave * WN;
+  const int n0 = slice * 8 * WN + wave * WN;
   const bool whole = n0 + WN <= N;
   const float scale = scaling[tl.adapter];
 
@@ -370,7 +370,7 @@ __device__ __forceinline__ void g_tile(const typename Elem<DT>::T* __restrict__ 
 #pragma unroll
           for (int w = 0; w < 8; ++w) s += *reinterpret_cast<const v4f*>(&red[(w * ST + t) * LDV + r]);
           if (at + t < tl.t1)
-            *reinterpret_cast<v4f*>(P + ((int64_t)blockIdx.x * T + at + t) * RP + h * RW + r) = s * scale;
+            *reinterpret_cast<v4f*>(P + ((int64_t)slice * T + at + t) * RP + h * RW + r) = s * scale;
         }
         if (h + 1 < RH) __syncthreads();
       }
@@ -399,7 +399,8 @@ __device__ __forceinline__ void g_tile(const typename Elem<DT>::T* __restrict__ 
 
 // dV partial sums P[slice][position][Rp] and dB partial sums dBp[tile][n][Rp] of
 // 8 WN columns of G and one tile of tokens, or with BLOCKS tokens [y tm, (y + 1)
-// tm) tile by tile. B's fragments
+// tm) tile by tile. Workgroup y * slices + slice (y as a grid axis of its own
+// would end at 65535). B's fragments
 // for dV stay in registers; the eight waves' parts of dV meet in LDS.
 template <int DT, int RT, int WN, bool BLOCKS>
 __global__ __launch_bounds__(512, RT == 1 ? 4 : 2) void k_lora_gpass(const typename Elem<DT>::T* __restrict__ G, int N, int T,
@@ -407,14 +408,16 @@ __global__ __launch_bounds__(512, RT == 1 ? 4 : 2) void k_lora_gpass(const typen
                                                     const typename Elem<DT>::T* __restrict__ B, int R,
                                                     const float* __restrict__ scaling, LoraSegs S,
                                                     const int32_t* __restrict__ perm, int tm, float* __restrict__ P,
-                                                    float* __restrict__ dBp, int32_t* __restrict__ tile_adapter) {
+                                                    float* __restrict__ dBp, int32_t* __restrict__ tile_adapter,
+                                                    int n_slices) {
   const SegLanes L = seg_lanes(S, T);
+  const int y = blockIdx.x / n_slices, slice = blockIdx.x - y * n_slices;
   if constexpr (!BLOCKS) {
-    g_tile<DT, RT, WN>(G, N, T, V, B, R, scaling, S, L, perm, tm, P, dBp, tile_adapter, blockIdx.y + 1);
+    g_tile<DT, RT, WN>(G, N, T, V, B, R, scaling, S, L, perm, tm, P, dBp, tile_adapter, slice, y + 1);
   } else {
-    const int d1 = first_tile(S, L, blockIdx.y + 1, T, tm);
-    for (int d = max(first_tile(S, L, blockIdx.y, T, tm), 1); d < d1; ++d) {
-      g_tile<DT, RT, WN>(G, N, T, V, B, R, scaling, S, L, perm, tm, P, dBp, tile_adapter, d);
+    const int d1 = first_tile(S, L, y + 1, T, tm);
+    for (int d = max(first_tile(S, L, y, T, tm), 1); d < d1; ++d) {
+      g_tile<DT, RT, WN>(G, N, T, V, B, R, scaling, S, L, perm, tm, P, dBp, tile_adapter, slice, d);
       __syncthreads();
     }
   }
@@ -426,7 +429,8 @@ __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ 
                                        const float* __restrict__ dV, int slices, const typename Elem<DT>::T* __restrict__ A, int R,
                                        const LoraSegs& S, const SegLanes& L, const int32_t* __restrict__ perm, int tm,
                                        const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
-                                       float* __restrict__ dAp, int Kp, int32_t* __restrict__ tile_adapter, int d) {
+                                       float* __restrict__ dAp, int Kp, int32_t* __restrict__ tile_adapter, int slice,
+                                       int d) {
   typedef Mx<DT> M;
   typedef typename Elem<DT>::T E;
   typedef Tile<DT, WN> TL;
@@ -445,10 +449,10 @@ __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ 
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
   const int lane = tid & 63, c = lane & 15, q = lane >> 4;
-  if (dAp && blockIdx.x == 0 && tid == 0) tile_adapter[d - 1] = none ? -1 : tl.adapter;
+  if (dAp && slice == 0 && tid == 0) tile_adapter[d - 1] = none ? -1 : tl.adapter;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   char* mine = sm + wave * TL::BYTES;
-  const int k0 = blockIdx.x * 8 * WN + wave * WN;
+  const int k0 = slice * 8 * WN + wave * WN;
   const bool whole = k0 + WN <= K;
 
   v4u x[TL::NI], b[TL::NI];
@@ -645,14 +649,15 @@ __global__ __launch_bounds__(512, RT == 1 && DT != DT_F16 ? 4 : 2) void k_lora_x
                                                     const int32_t* __restrict__ perm, int tm,
                                                     const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
                                                     float* __restrict__ dAp, int Kp,
-                                                    int32_t* __restrict__ tile_adapter) {
+                                                    int32_t* __restrict__ tile_adapter, int n_slices) {
   const SegLanes L = seg_lanes(S, T);
+  const int y = blockIdx.x / n_slices, slice = blockIdx.x - y * n_slices;
   if constexpr (!BLOCKS) {
-    x_tile<DT, RT, WN>(X, K, T, dV, slices, A, R, S, L, perm, tm, base, out, dAp, Kp, tile_adapter, blockIdx.y + 1);
+    x_tile<DT, RT, WN>(X, K, T, dV, slices, A, R, S, L, perm, tm, base, out, dAp, Kp, tile_adapter, slice, y + 1);
   } else {
-    const int d1 = first_tile(S, L, blockIdx.y + 1, T, tm);
-    for (int d = max(first_tile(S, L, blockIdx.y, T, tm), 1); d < d1; ++d) {
-      x_tile<DT, RT, WN>(X, K, T, dV, slices, A, R, S, L, perm, tm, base, out, dAp, Kp, tile_adapter, d);
+    const int d1 = first_tile(S, L, y + 1, T, tm);
+    for (int d = max(first_tile(S, L, y, T, tm), 1); d < d1; ++d) {
+      x_tile<DT, RT, WN>(X, K, T, dV, slices, A, R, S, L, perm, tm, base, out, dAp, Kp, tile_adapter, slice, d);
       __syncthreads();
     }
   }
@@ -870,8 +875,8 @@ hipError_t g_pass(const Plan& p, const void* G, const float* V, int T, const voi
   static std::atomic<uint64_t> done{0};
   const hipError_t e = lds_limit_once((const void*)kern, lds, done);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(p.slices, BLOCKS ? cdiv(T, p.tm_g) : p.tiles_g), dim3(512), lds, st, static_cast<const E*>(G), N, T, V,
-                     static_cast<const E*>(B), R, scaling, S, perm, p.tm_g, P, dBp, ad);
+  hipLaunchKernelGGL(kern, dim3((unsigned)p.slices * (BLOCKS ? cdiv(T, p.tm_g) : p.tiles_g)), dim3(512), lds, st, static_cast<const E*>(G), N, T, V,
+                     static_cast<const E*>(B), R, scaling, S, perm, p.tm_g, P, dBp, ad, p.slices);
   return hipGetLastError();
 }
 
@@ -885,9 +890,10 @@ hipError_t x_pass(const Plan& p, const void* X, int T, int K, const float* dV, i
   static std::atomic<uint64_t> done{0};
   const hipError_t e = lds_limit_once((const void*)kern, lds, done);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kern, dim3(cdiv(K, 8 * WN), BLOCKS ? cdiv(T, p.tm_x) : p.tiles_x), dim3(512), lds, st, static_cast<const E*>(X), K, T, dV,
+  const int slices_x = cdiv(K, 8 * WN);
+  hipLaunchKernelGGL(kern, dim3((unsigned)slices_x * (BLOCKS ? cdiv(T, p.tm_x) : p.tiles_x)), dim3(512), lds, st, static_cast<const E*>(X), K, T, dV,
                      slices, static_cast<const E*>(A), R, S, perm, p.tm_x, static_cast<const E*>(base), static_cast<E*>(out),
-                     dAp, p.kp, ad);
+                     dAp, p.kp, ad, slices_x);
   return hipGetLastError();
 }
 

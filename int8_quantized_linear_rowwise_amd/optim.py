@@ -93,18 +93,23 @@ class AdamWPlan:
         check(lib.int8_adamw_table_fill(arr, n, host.data_ptr(), need, ctypes.byref(chunks)), "int8_adamw_table_fill")
         self.chunks = chunks.value
         self.table = host.to(self.device)
+        self._stream = _raw_stream(self.gpu)
 
     def step(self, step: int, lr: float, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
              weight_decay: float = 0.01, grad_scale: Optional[torch.Tensor] = None,
              found_inf: Optional[torch.Tensor] = None) -> None:
         """Step number `step` (from 1). grad_scale: fp32 GPU scalar that multiplies the gradients; found_inf: fp32 GPU
-        scalar, anything but 0 leaves all tensors as they are (the caller's step count goes on)."""
+        scalar, anything but 0 leaves all tensors as they are (the caller's step count goes on). A captured step keeps
+        its numbers; only the two scalars are read at each replay."""
         for name, x in (("grad_scale", grad_scale), ("found_inf", found_inf)):
             if x is not None and (x.dtype != torch.float32 or x.numel() != 1 or x.get_device() != self.gpu):
                 raise ValueError(f"{name} must be one float32 value on {self.device}")
+        stream = _raw_stream(self.gpu)
+        if stream != self._stream:     # the table's memory is not given away before this stream is done with it
+            self.table.record_stream(torch.cuda.current_stream(self.device))
         check(lib.int8_adamw_step(self.table.data_ptr(), self.count, self.chunks, lr, betas[0], betas[1], eps,
                                   weight_decay, step, 0 if grad_scale is None else grad_scale.data_ptr(),
-                                  0 if found_inf is None else found_inf.data_ptr(), _raw_stream(self.gpu)),
+                                  0 if found_inf is None else found_inf.data_ptr(), stream),
               "int8_adamw_step")
 
 

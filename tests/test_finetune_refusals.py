@@ -29,6 +29,8 @@ def test_lora_forward_host_errors(L):  # noqa: F811
     assert call(K=L.I8L_MAX_COLS + 1) == L.I8L_ESHAPE and call(N=L.I8L_MAX_COLS + 1) == L.I8L_ESHAPE
     assert call(T=1 << 31) == L.I8L_ESHAPE and call(S=1 << 31) == L.I8L_ESHAPE and call(n=65536) == L.I8L_ESHAPE
     assert call(T=1 << 29, S=(1 << 29) + 1) == L.I8L_ESHAPE
+    assert call(T=(1 << 24) + 1) == L.I8L_ESHAPE and call(S=(1 << 20) + 1) == L.I8L_ESHAPE
+    assert call(n=65535, K=16384, R=1) == L.I8L_ESHAPE       # 65535 x 16384 x 16 (the padded rank) > 2^33
     wsb = need(8, 64000, 32, 16, 3)
     assert wsb % 256 == 0 and wsb > 0
     assert call(wsb=wsb - 1) == L.I8L_EWORKSPACE and call(ws=0) == L.I8L_EWORKSPACE
