@@ -88,6 +88,28 @@ def test_many_segments(I8, dt):
 
 
 @pytest.mark.parametrize("dt", DTS)
+def test_more_adapters_than_segments(I8, dt):
+    """Over 64 segments that are not sorted by adapter, as there are as many adapters; most adapters without rows."""
+    g = torch.Generator().manual_seed(4)
+    T, S, n = 400, 100, 130
+    off = [0] + torch.randint(0, T + 1, (S - 1,), generator=g).sort().values.tolist() + [T]
+    check(I8, dt, T, 72, 40, 8, n, off, torch.randint(0, n, (S,), generator=g).tolist(), what="many adapters")
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("R", [16, 32])
+def test_blocks_of_many_tiles(I8, dt, R):
+    """Long batches of many short segments: a workgroup walks the tiles of its block of tokens, segments end inside
+    and on the blocks' borders (multiples of 32), and some are empty or without an adapter."""
+    g = torch.Generator().manual_seed(5)
+    T, S, n = 6000, 40, 4
+    off = [0] + torch.randint(0, T + 1, (S - 1,), generator=g).sort().values.tolist() + [T]
+    off[10], off[20], off[21] = off[10] // 96 * 96, off[20] // 32 * 32, off[20] // 32 * 32
+    off = sorted(off)
+    check(I8, dt, T, 1024, 4096, R, n, off, torch.randint(-1, n, (S,), generator=g).tolist(), what="blocks")
+
+
+@pytest.mark.parametrize("dt", DTS)
 def test_without_base(I8, dt):
     check(I8, dt, 90, 264, 136, 16, 2, [0, 40, 90], [1, 0], with_base=False, what="no base")
 
