@@ -95,6 +95,16 @@ inline int lora_tiles(int T, const LoraSegs& S, int tm) {
   return (T + tm - 1) / tm + (S.n_seg > 1 ? S.n_seg : 1) - 1;
 }
 
+// Workgroup `bid` of tiles * slices: the eight XCDs take workgroups in turn, so
+// each gets one run of neighbouring tiles, whose rows share an adapter more
+// often than not: its A and B then come through one L2 instead of all eight.
+__device__ __forceinline__ void xcd_order(int bid, int total, int slices, int& tile, int& slice) {
+  const int x = bid & 7, base = total >> 3, rem = total & 7;
+  const int id = x * base + min(x, rem) + (bid >> 3);
+  tile = id / slices;
+  slice = id - tile * slices;
+}
+
 // Matrix-core fragments: 16 bytes a lane. Lane l of a 16-row operand holds row
 // l & 15 and elements EL (l >> 4) .. of one step of KS along the contraction;
 // the product's lane l holds column l & 15 (the second operand's row) and rows

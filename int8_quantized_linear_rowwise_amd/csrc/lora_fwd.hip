@@ -291,17 +291,19 @@ struct Columns {
 template <int DT, int RT, int TMT, int NW>
 __global__ __launch_bounds__(NW * 64) void k_lora_shrink(const typename Elem<DT>::T* __restrict__ X, int T, int K,
                                                          const typename Elem<DT>::T* __restrict__ A, int R,
-                                                         LoraSegs S, float* __restrict__ P) {
+                                                         LoraSegs S, float* __restrict__ P, int splits) {
+  int tile, split;
+  xcd_order(blockIdx.x, gridDim.x, splits, tile, split);
   constexpr int KS = Mx<DT>::KS, U = TMT + RT <= 2 ? 4 : TMT + RT <= 6 ? 2 : 1;
   extern __shared__ __attribute__((aligned(16))) char sm[];
   v4f(*red)[TMT * RT][64] = reinterpret_cast<v4f(*)[TMT * RT][64]>(sm);
-  const LoraTile tl = lora_tile(S, seg_lanes(S, T), blockIdx.x + 1, T, 16 * TMT);
+  const LoraTile tl = lora_tile(S, seg_lanes(S, T), tile + 1, T, 16 * TMT);
   if (tl.t1 <= tl.t0 || tl.adapter < 0) return;
   const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int steps = (K + KS - 1) / KS, pairs = (steps + 1) / 2;
-  const int s0 = 2 * (int)((int64_t)pairs * blockIdx.y / gridDim.y);
-  const int s1 = min(2 * (int)((int64_t)pairs * (blockIdx.y + 1) / gridDim.y), steps);
+  const int s0 = 2 * (int)((int64_t)pairs * split / splits);
+  const int s1 = min(2 * (int)((int64_t)pairs * (split + 1) / splits), steps);
   v4f acc[TMT][RT];
   shrink_steps<DT, RT, TMT, NW, U>(X, K, A, R, tl, s0, s1, wave, lane, sm + wave * (TMT + RT) * 2048, acc);
 #pragma unroll
@@ -320,7 +322,7 @@ __global__ __launch_bounds__(NW * 64) void k_lora_shrink(const typename Elem<DT>
         for (int j = 0; j < RT; ++j) acc[i][j] += red[wave][i * RT + j][lane];
   }
   if (wave == 0) {
-    float* p = P + (int64_t)blockIdx.y * T * (16 * RT);
+    float* p = P + (int64_t)split * T * (16 * RT);
 #pragma unroll
     for (int i = 0; i < TMT; ++i)
 #pragma unroll
@@ -341,7 +343,9 @@ __global__ __launch_bounds__(256) void k_lora_expand(const float* __restrict__ P
                                                      const typename Elem<DT>::T* __restrict__ B, int R,
                                                      const float* __restrict__ scaling, LoraSegs S,
                                                      const typename Elem<DT>::T* base, typename Elem<DT>::T* out,
-                                                     float* __restrict__ V, int groups_per_wave) {
+                                                     float* __restrict__ V, int groups_per_wave, int slices) {
+  int tile, slice;
+  xcd_order(blockIdx.x, gridDim.x, slices, tile, slice);
   typedef Columns<DT, RT, TMT, FULL> C;
   typedef typename Elem<DT>::T E;
   constexpr int TM = C::TM, RP = C::RP, LD = C::LD;
@@ -350,17 +354,17 @@ __global__ __launch_bounds__(256) void k_lora_expand(const float* __restrict__ P
   extern __shared__ __attribute__((aligned(16))) char sm[];
   E* sv = reinterpret_cast<E*>(sm);                                    // [part][TM][LD], before the waves' stages
   float* sunit = reinterpret_cast<float*>(sv + Mx<DT>::NC * TM * LD);   // [TM]
-  const LoraTile tl = lora_tile(S, seg_lanes(S, T), blockIdx.x + 1, T, TM);
+  const LoraTile tl = lora_tile(S, seg_lanes(S, T), tile + 1, T, TM);
   const int n_tok = tl.t1 - tl.t0;
   if (n_tok <= 0) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int first = blockIdx.y * 4 * groups_per_wave;
+  const int first = slice * 4 * groups_per_wave;
   const int g0 = first + wave, g1 = min(first + 4 * groups_per_wave, (N + C::GC - 1) / C::GC);
   C col(tl, B, base, out, N, R, lane, sm + wave * C::LDS);
 
   if (tl.adapter < 0) {
-    if (V && blockIdx.y == 0)
+    if (V && slice == 0)
       for (int64_t e = (int64_t)tl.t0 * R + tid; e < (int64_t)tl.t1 * R; e += 256) V[e] = 0.0f;
     col.copy(g0, g1, 4);
     return;
@@ -385,7 +389,7 @@ __global__ __launch_bounds__(256) void k_lora_expand(const float* __restrict__ P
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (r + j >= R) v[j] = 0.0f;
-      else if (V && blockIdx.y == 0 && t < n_tok) V[(int64_t)(tl.t0 + t) * R + r + j] = v[j];
+      else if (V && slice == 0 && t < n_tok) V[(int64_t)(tl.t0 + t) * R + r + j] = v[j];
     }
     E* o = sv + t * LD + r;
     if constexpr (F32) {
@@ -582,24 +586,24 @@ hipError_t run(const void* Xv, int T, int K, const void* Av, const void* Bv, con
   if (S.n_adapters > 0) {
     constexpr int stage = NW * (TMT + RT) * 2048, red = NW / 2 * TMT * RT * 1024;
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = launch(k_lora_shrink<DT, RT, TMT, NW>, done, dim3(lora_tiles(T, S, 16 * TMT), splits), NW * 64,
+    const hipError_t e = launch(k_lora_shrink<DT, RT, TMT, NW>, done, dim3((unsigned)lora_tiles(T, S, 16 * TMT) * splits), NW * 64,
                                 stage > red ? stage : red, st, static_cast<const E*>(Xv), T, K,
-                                static_cast<const E*>(Av), R, S, ws);
+                                static_cast<const E*>(Av), R, S, ws, splits);
     if (e != hipSuccess) return e;
   }
   const int tiles = lora_tiles(T, S, 16 * TMT), groups = (N + C::GC - 1) / C::GC;
   // workgroups that are resident together: two a compute unit with 64 tokens, four with 16
   constexpr int want = TMT == 4 ? 512 : 1024;
   int64_t gpw = ((int64_t)tiles * groups + 4 * want - 1) / (4 * want);
-  gpw = gpw < 1 ? 1 : gpw > 16 ? 16 : gpw;
+  gpw = gpw < 1 ? 1 : gpw;
   const int slices = groups > 0 ? (int)((groups + 4 * gpw - 1) / (4 * gpw)) : V ? 1 : 0;
   if (slices == 0) return hipSuccess;
   constexpr int small = Mx<DT>::NC * C::TM * C::LD * (int)sizeof(E) + C::TM * 4;
   constexpr int lds = 4 * C::LDS > small ? 4 * C::LDS : small;
   static std::atomic<uint64_t> done{0};
-  return launch(k_lora_expand<DT, RT, TMT, FULL>, done, dim3(tiles, slices), 256, lds, st, (const float*)ws, splits, T,
+  return launch(k_lora_expand<DT, RT, TMT, FULL>, done, dim3((unsigned)tiles * slices), 256, lds, st, (const float*)ws, splits, T,
                 N, static_cast<const E*>(Bv), R, scaling, S, static_cast<const E*>(base), static_cast<E*>(out), V,
-                (int)gpw);
+                (int)gpw, slices);
 }
 
 template <int DT, int RT, bool FULL>
