@@ -127,7 +127,8 @@ __global__ __launch_bounds__(block_of(TPR)) void k_norm_fwd(const typename Elem<
   }
 }
 
-// part: [workgroup][2][Cp] partial dw and db, or NULL. gX may be NULL.
+// part: [workgroup][2][Cp] partial dw and db; NULL for a single workgroup, which
+// writes gw and gb itself, or where neither is wanted. gX, gw, gb may be NULL.
 template <int DT, int WDT, int TPR, int NV>
 __global__ __launch_bounds__(block_of(TPR)) void k_norm_bwd(const typename Elem<DT>::T* G,
                                                             const typename Elem<DT>::T* __restrict__ X,
@@ -135,7 +136,8 @@ __global__ __launch_bounds__(block_of(TPR)) void k_norm_bwd(const typename Elem<
                                                             const float* __restrict__ rstd, int T, int C,
                                                             const typename Elem<WDT>::T* __restrict__ w,
                                                             typename Elem<DT>::T* gX, float* __restrict__ part,
-                                                            int Cp) {
+                                                            int Cp, typename Elem<WDT>::T* __restrict__ gw,
+                                                            typename Elem<WDT>::T* __restrict__ gb) {
   constexpr int EL = Mx<DT>::EL, RPB = block_of(TPR) / TPR;
   // 1024 threads have 128 registers each: no loads in flight for the next row,
   // and w comes from the cache for every row
@@ -210,12 +212,21 @@ __global__ __launch_bounds__(block_of(TPR)) void k_norm_bwd(const typename Elem<
       }
     }
   }
-  if (part == nullptr) return;
+  if (part == nullptr && gw == nullptr && gb == nullptr) return;
   float* p = part + (int64_t)blockIdx.x * 2 * Cp;
   if constexpr (RPB == 1) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * TPR + lane) * EL;
+      if (part == nullptr) {
+#pragma unroll
+        for (int j = 0; j < EL; ++j)
+          if (j < left[i]) {
+            if (gw) gw[c + j] = Elem<WDT>::from_f32(dw[i][j]);
+            if (gb) gb[c + j] = Elem<WDT>::from_f32(db[i][j]);
+          }
+        continue;
+      }
 #pragma unroll
       for (int j = 0; j < EL; j += 4)
         if (c + j < Cp) {
@@ -240,7 +251,12 @@ __global__ __launch_bounds__(block_of(TPR)) void k_norm_bwd(const typename Elem<
 #pragma unroll
       for (int k = 0; k < RPB; ++k) s += meet[2 * k * W + e];
       const int c = e % W;
-      if (c < Cp) p[(e / W) * Cp + c] = s;
+      if (part == nullptr) {
+        typename Elem<WDT>::T* o = e < W ? gw : gb;
+        if (o && c < C) o[c] = Elem<WDT>::from_f32(s);
+      } else if (c < Cp) {
+        p[(e / W) * Cp + c] = s;
+      }
     }
   }
 }
@@ -403,6 +419,7 @@ int norm_parts(int T, int C) {
     return n < 1 ? 1 : n > 32 ? 32 : n;
   }
   const int rows = C <= 128 ? 16 : C <= 1024 ? 4 : 1;    // rows a workgroup takes at once
+  if (T <= 8 * rows) return 1;   // one workgroup finishes within the host's second launch (4 us)
   const int n = (T + rows - 1) / rows;
   const int most = C > 4096 ? 256 : 512;
   return n < 1 ? 1 : n < most ? n : most;
@@ -423,11 +440,12 @@ hipError_t fwd_run(const void* X, int T, int C, const void* w, const void* b, fl
 
 template <int DT, int WDT, int TPR, int NV>
 hipError_t bwd_run(const void* G, const void* X, const float* mean, const float* rstd, int T, int C, const void* w,
-                   void* gX, float* part, hipStream_t st) {
+                   void* gX, float* part, void* gw, void* gb, hipStream_t st) {
   typedef typename Elem<DT>::T E;
+  typedef typename Elem<WDT>::T W;
   hipLaunchKernelGGL((k_norm_bwd<DT, WDT, TPR, NV>), dim3(norm_parts(T, C)), dim3(block_of(TPR)), 0, st,
-                     static_cast<const E*>(G), static_cast<const E*>(X), mean, rstd, T, C,
-                     static_cast<const typename Elem<WDT>::T*>(w), static_cast<E*>(gX), part, pad_cols(C));
+                     static_cast<const E*>(G), static_cast<const E*>(X), mean, rstd, T, C, static_cast<const W*>(w),
+                     static_cast<E*>(gX), part, pad_cols(C), static_cast<W*>(gw), static_cast<W*>(gb));
   return hipGetLastError();
 }
 
@@ -449,8 +467,8 @@ hipError_t fwd_width(const void* X, int T, int C, const void* w, const void* b, 
 }
 template <int DT, int WDT>
 hipError_t bwd_width(const void* G, const void* X, const float* mean, const float* rstd, int T, int C, const void* w,
-                     void* gX, float* part, hipStream_t st) {
-  I8L_NORM_WIDTHS(bwd_run, G, X, mean, rstd, T, C, w, gX, part, st)
+                     void* gX, float* part, void* gw, void* gb, hipStream_t st) {
+  I8L_NORM_WIDTHS(bwd_run, G, X, mean, rstd, T, C, w, gX, part, gw, gb, st)
 }
 
 template <int DT, int WDT>
@@ -474,8 +492,10 @@ hipError_t bwd_t(const void* G, const void* X, const float* mean, const float* r
   if (T > 0) {
     n = norm_parts(T, C);
     if (C <= WIDEST) {
-      const hipError_t e = bwd_width<DT, WDT>(G, X, mean, rstd, T, C, w, gX, sums ? ws : nullptr, st);
-      if (e != hipSuccess) return e;
+      const bool whole = n == 1;
+      const hipError_t e = bwd_width<DT, WDT>(G, X, mean, rstd, T, C, w, gX, sums && !whole ? ws : nullptr,
+                                              whole ? gw : nullptr, whole ? gb : nullptr, st);
+      if (e != hipSuccess || whole) return e;
     } else {
       // the weight gradient first: gX may be G only where there is none
       if (sums)
@@ -496,7 +516,10 @@ hipError_t bwd_t(const void* G, const void* X, const float* mean, const float* r
 
 }  // namespace
 
-size_t norm_backward_floats(int T, int C) { return (size_t)2 * pad_cols(C) * norm_parts(T, C); }
+size_t norm_backward_floats(int T, int C) {
+  const int n = norm_parts(T, C);
+  return n == 1 && C <= WIDEST ? 0 : (size_t)2 * pad_cols(C) * n;
+}
 
 #define I8L_NORM_TYPES(F, ...)                                                    \
   switch (dt * 3 + wdt) {                                                         \
