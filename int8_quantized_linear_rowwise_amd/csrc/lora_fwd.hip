@@ -581,19 +581,19 @@ hipError_t run(const void* Xv, int T, int K, const void* Av, const void* Bv, con
                const LoraSegs& S, const void* base, void* out, float* V, float* ws, hipStream_t st) {
   typedef typename Elem<DT>::T E;
   typedef Columns<DT, RT, TMT, FULL> C;
-  constexpr int NW = RT < 8 ? 8 : 4;
+  constexpr int NW = RT < 8 ? 8 : 4, ST = TMT == 1 ? 1 : 4;   // shrink: its waves and 16-token parts
   const int splits = shrink_splits(T, K, S.n_seg);
   if (S.n_adapters > 0) {
-    constexpr int stage = NW * (TMT + RT) * 2048, red = NW / 2 * TMT * RT * 1024;
+    constexpr int stage = NW * (ST + RT) * 2048, red = NW / 2 * ST * RT * 1024;
     static std::atomic<uint64_t> done{0};
-    const hipError_t e = launch(k_lora_shrink<DT, RT, TMT, NW>, done, dim3((unsigned)lora_tiles(T, S, 16 * TMT) * splits), NW * 64,
+    const hipError_t e = launch(k_lora_shrink<DT, RT, ST, NW>, done, dim3((unsigned)lora_tiles(T, S, 16 * ST) * splits), NW * 64,
                                 stage > red ? stage : red, st, static_cast<const E*>(Xv), T, K,
                                 static_cast<const E*>(Av), R, S, ws, splits);
     if (e != hipSuccess) return e;
   }
   const int tiles = lora_tiles(T, S, 16 * TMT), groups = (N + C::GC - 1) / C::GC;
-  // workgroups that are resident together: two a compute unit with 64 tokens, four with 16
-  constexpr int want = TMT == 4 ? 512 : 1024;
+  // workgroups that are resident together: two a compute unit in long batches, four with 16 tokens
+  constexpr int want = TMT == 1 ? 1024 : 512;
   int64_t gpw = ((int64_t)tiles * groups + 4 * want - 1) / (4 * want);
   gpw = gpw < 1 ? 1 : gpw;
   const int slices = groups > 0 ? (int)((groups + 4 * gpw - 1) / (4 * gpw)) : V ? 1 : 0;
@@ -611,7 +611,8 @@ hipError_t run_rank(const void* X, int T, int K, const void* A, const void* B, c
               const LoraSegs& S, const void* base, void* out, float* V, float* ws, hipStream_t st) {
   if (one_launch(T, K, R, S.n_seg))
     return run_short<DT, RT, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, st);
-  if (long_tiles(T, S.n_seg)) return run<DT, RT, 4, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
+  // 32 tokens at rank 128: B's part in LDS leaves room for two workgroups a compute unit
+  if (long_tiles(T, S.n_seg)) return run<DT, RT, RT == 8 ? 2 : 4, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
   return run<DT, RT, 1, FULL>(X, T, K, A, B, scaling, R, N, S, base, out, V, ws, st);
 }
 
