@@ -358,7 +358,8 @@ int int8_lora_backward(const void* G, const void* X, const float* V, int dtype, 
  * grad_X, grad_weight and grad_bias may each be NULL (not computed). out may be
  * X; grad_X may be G unless a weight or bias gradient is asked for too. T = 0
  * writes zero weight gradients. C <= I8L_MAX_COLS, T <= 2^24, else I8L_ESHAPE; an
- * eps that is negative or NaN is I8L_EINVAL.
+ * eps that is negative or NaN is I8L_EINVAL. A few rows need no workspace (its
+ * size is 0, it may be NULL).
  * ------------------------------------------------------------------------ */
 int int8_layer_norm_forward(const void* X, int dtype, int64_t T, int64_t C, const void* weight, const void* bias,
                             int weight_dtype, float eps, void* out, float* mean, float* rstd, void* stream);

@@ -13,7 +13,7 @@
 // Small batches skip the first sum: the x pass adds the slices up itself. 4096
 // tokens, 4096 -> 11008 at rank 16: 27 + 6 + 28 + 6 us; 16384 tokens of 16
 // sequences, 8192 -> 28672 at rank 32: 235 + 40 + 167 + 7 us, of which the
-// partial sums (300 MB beside 1.75 GB of operands) are about a sixth.
+// partial sums (300 MB beside 1.77 GB of operands) are about a sixth.
 // A workgroup takes a slice of columns and a block of tokens, which it walks
 // tile by tile (the block's tokens of one adapter); its eight waves split the columns, and each holds its part of the weight
 // gradient in registers while it walks the tokens 32 (fp32: 16) at a time. The
