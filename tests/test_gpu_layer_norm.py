@@ -179,3 +179,10 @@ def test_module_and_differences(I8):
             d = float(up.view(-1)[i]) - float(dn.view(-1)[i])
             diff = loss(up, w) - loss(dn, w) if which == 0 else loss(X, up) - loss(X, dn)
             assert abs(diff / d - float(grad.view(-1)[i])) <= lim, (which, i)
+
+
+@pytest.mark.parametrize("C,T", [(64, 64), (64, 65), (128, 64), (1024, 8), (1024, 9), (2048, 4), (2048, 5), (4096, 2),
+                                 (4096, 3), (16384, 1), (16384, 2)])
+def test_few_rows(I8, C, T):
+    """Both sides of where one workgroup takes all rows."""
+    check(I8, "bf16", "f32", T, C)
