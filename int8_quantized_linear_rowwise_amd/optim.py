@@ -151,7 +151,8 @@ class AdamW(torch.optim.Optimizer):
                 rows = [(p, p.grad, self.state[p]) for p in ps]
                 where = tuple(x.data_ptr() for p, g, s in rows
                               for x in (p, g, s["m"], s["v"], s.get("m_scale"), s.get("v_scale"), s.get("master"))
-                              if x is not None) + tuple(p.numel() for p in ps)
+                              if x is not None)
+                where += tuple((p.numel(), p.dtype, g.dtype, p.is_contiguous(), g.is_contiguous()) for p, g, s in rows)
                 key = (device, has_master, tuple(id(p) for p in ps))
                 held = self._plans.get(gi, {}).get(key)
                 if held is None or held[0] != where:
@@ -161,6 +162,9 @@ class AdamW(torch.optim.Optimizer):
                         [r[2]["v"] for r in rows], [r[2]["m_scale"] for r in rows] if low else None,
                         [r[2]["v_scale"] for r in rows] if low else None,
                         [r[2]["master"] for r in rows] if has_master else None))
+                    # every step compares the addresses: old gradients need not be held (their memory is the next
+                    # backward pass's where zero_grad drops them)
+                    held[1]._keep = None
                 live[key] = held
                 held[1].step(step, group["lr"], group["betas"], group["eps"], group["weight_decay"], grad_scale,
                              found_inf)

@@ -1,5 +1,7 @@
 """GPU parity of the AdamW step over many tensors, states in 32 and in 8 bits,
 against the plain 64-bit forms, and of the optimizer built on it."""
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -275,3 +277,28 @@ def test_optimizer_8bit_learns_and_keeps_its_types(I8):
         losses[bits] = float(loss.detach())
     first = float(((A @ target) ** 2).mean())
     assert losses[32] < 1e-2 * first and losses[8] < 1e-2 * first, losses
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_gradients_that_move_are_not_held(I8, bits):
+    """Dropped gradients are freed; new ones at other addresses, in other types or layouts are seen for what they are."""
+    g = torch.Generator().manual_seed(10)
+    draw = lambda: torch.randn(48, 48, generator=g).cuda()  # noqa: E731
+    p, q = (torch.nn.Parameter(torch.ones(48, 48, device="cuda:0")) for _ in range(2))
+    ours, still = I8.AdamW([p], state_bits=bits), I8.AdamW([q], state_bits=bits)
+    q.grad = torch.empty_like(q)
+    for step in range(4):
+        new = draw()
+        p.grad = new.clone()
+        q.grad.copy_(new)
+        ours.step()
+        still.step()
+        assert torch.equal(p, q), step
+        gone = weakref.ref(p.grad)
+        ours.zero_grad(set_to_none=True)
+        assert gone() is None
+    p.grad = draw()
+    ours.step()
+    p.grad = p.grad.t()   # the same address and size, another order
+    with pytest.raises(ValueError, match="contiguous"):
+        ours.step()
