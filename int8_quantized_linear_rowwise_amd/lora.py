@@ -140,6 +140,7 @@ class Int8LoraFunction(torch.autograd.Function):
         return out.reshape(*x.shape[:-1], CB.shape[0])
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, g):
         from . import int8_linear_backward_input
         X, V, CB, SCB, A, B, scaling, seg_offsets, seg_adapter = ctx.saved_tensors

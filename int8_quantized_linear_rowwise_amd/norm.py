@@ -90,6 +90,7 @@ class LayerNormFunction(torch.autograd.Function):
         return out.reshape(x.shape)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, g):
         X, mean, rstd, weight = ctx.saved_tensors
         need = ctx.needs_input_grad

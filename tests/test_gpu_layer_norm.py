@@ -181,6 +181,15 @@ def test_module_and_differences(I8):
             assert abs(diff / d - float(grad.view(-1)[i])) <= lim, (which, i)
 
 
+def test_second_derivatives_are_refused(I8):
+    """The gradients are not differentiable again, and say so."""
+    x = torch.randn(4, 32, device="cuda:0", requires_grad=True)
+    y = I8.LayerNorm(32, device="cuda:0")(x)
+    (g,) = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+
+
 @pytest.mark.parametrize("C,T", [(64, 64), (64, 65), (128, 64), (1024, 8), (1024, 9), (2048, 4), (2048, 5), (4096, 2),
                                  (4096, 3), (16384, 1), (16384, 2)])
 def test_few_rows(I8, C, T):
