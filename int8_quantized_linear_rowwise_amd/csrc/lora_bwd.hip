@@ -954,6 +954,10 @@ hipError_t backward_t(const Plan& p, const void* G, const void* X, const float* 
   }
   if (gA && na > 0 && R > 0 && K > 0)
     sum_a = TileSum{ws + p.dap, ad_x, gA, rows ? p.tiles_x : 0, R, p.kp, K, cdiv((int64_t)R * p.kp, 1024)};
+  if (((int64_t)sum_a.blocks + sum_b.blocks) * na >= 1 << 24) {   // a launch has fewer than 2^32 threads
+    sum(SliceSum{}, sum_a, TileSum{});
+    sum_a = TileSum{};
+  }
   sum(SliceSum{}, sum_a, sum_b);
   return hipGetLastError();
 }
