@@ -119,7 +119,8 @@ class AdamW(torch.optim.Optimizer):
     state_bits: 32 or 8; master: keep fp32 copies of fp16 / bf16 parameters.
     The plan of a group is laid out again whenever a gradient or parameter has
     moved (gradients kept in place with zero_grad(set_to_none=False) never do).
-    Parameters and gradients have to be contiguous."""
+    Parameters and gradients have to be contiguous. A captured step keeps its
+    step number and learning rate; what it uses is held as long as the optimizer."""
 
     def __init__(self, params, lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, state_bits: int = 32, master: bool = False):
@@ -128,6 +129,7 @@ class AdamW(torch.optim.Optimizer):
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits,
                                       master=master))
         self._plans: dict = {}
+        self._captured: list = []
 
     @torch.no_grad()
     def step(self, closure=None, grad_scale: Optional[torch.Tensor] = None, found_inf: Optional[torch.Tensor] = None):
@@ -166,6 +168,8 @@ class AdamW(torch.optim.Optimizer):
                     # backward pass's where zero_grad drops them)
                     held[1]._keep = None
                 live[key] = held
+                if torch.cuda.is_current_stream_capturing():   # a graph's replays read the table and these tensors
+                    self._captured.append((held[1], rows))
                 held[1].step(step, group["lr"], group["betas"], group["eps"], group["weight_decay"], grad_scale,
                              found_inf)
             self._plans[gi] = live

@@ -302,3 +302,39 @@ def test_gradients_that_move_are_not_held(I8, bits):
     p.grad = p.grad.t()   # the same address and size, another order
     with pytest.raises(ValueError, match="contiguous"):
         ours.step()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_captured_step_outlives_moved_gradients(I8, bits):
+    """A graph's replay works on the tensors of its capture after eager steps with other gradients."""
+    g = torch.Generator().manual_seed(11)
+    p, q = (torch.nn.Parameter(torch.ones(3000, device="cuda:0")) for _ in range(2))
+    ours, ref = I8.AdamW([p], state_bits=bits), I8.AdamW([q], state_bits=bits)
+    fixed = torch.randn(3000, generator=g).cuda()
+    q.grad = torch.empty_like(q)
+
+    def twin(grad, number):
+        q.grad.copy_(grad)
+        if number > 1:
+            ref.state[q]["step"] = number - 1
+        ref.step()
+        torch.cuda.synchronize()
+        assert torch.equal(p, q), number
+
+    p.grad = fixed
+    ours.step()
+    twin(fixed, 1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ours.step()
+    graph.replay()
+    twin(fixed, 2)
+    for number in (3, 4):
+        new = torch.randn(3000, generator=g).cuda()
+        p.grad = new.clone()
+        ours.step()
+        twin(new, number)
+        junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda:0") for n in (512, 1024, 4096)]
+        graph.replay()
+        twin(fixed, 2)
+        del junk
