@@ -538,9 +538,14 @@ int shrink_splits(int T, int K, int n_seg) {
 
 // One launch for up to 32 tiles with an A of up to 81920 values (it needs no
 // workspace). Every workgroup reads A[a] whole, at the 25 GB/s or so that one
-// compute unit gets from memory: one token, 4096 x 4096 at rank 16, takes 6.8 us
-// against 3.9 + 4.4 us split over k, but a second launch costs the host 4 us.
-// With 64 tiles and 11008 columns one launch took 22 us against 6 + 10.
+// compute unit gets from memory, but a second launch and a workspace cost the
+// host 5 us. 16-bit, on the GPU, one launch against two: one token, 4096 -> 4096
+// at rank 16, 6.3 and 7.2 us; 64 of 16 adapters, 4096 -> 11008, 7.5 and 8.4; 512
+// of one, 1024 -> 11008 at rank 64, 10.9 and 13.5; at the bound, 5120 at rank
+// 16, 7.2 and 7.2 for one token, 9.0 and 8.3 for the 64. fp32 reads twice the
+// bytes: 10.2 and 7.4, 16 and 10, 23 and 24; there only the host's side gains at
+// the bound, and the workspace's size does not depend on the type. With 64
+// tiles and 11008 columns one launch took 22 us against 6 + 10.
 bool one_launch(int T, int K, int R, int n_seg) {
   const LoraSegs S = {nullptr, nullptr, n_seg, 0};
   return lora_tiles(T, S, 16) <= 32 && (int64_t)K * R <= 81920;
@@ -567,13 +572,13 @@ hipError_t run_short(const void* Xv, int T, int K, const void* Av, const void* B
   constexpr int lds = 8 * stage + Mx<DT>::NC * 16 * C::LD * (int)sizeof(E) + 32;
   static std::atomic<uint64_t> done{0};
   const int tiles = lora_tiles(T, S, 16), groups = (N + C::GC - 1) / C::GC;
-  int64_t gpw = (int64_t)tiles * groups / (8 * 256);     // about 256 workgroups: few repeat V
-  gpw = gpw < 1 ? 1 : gpw > 64 ? 64 : gpw;
-  const int slices = groups > 0 ? (int)((groups + 8 * gpw - 1) / (8 * gpw)) : V ? 1 : 0;
+  // at most 256 workgroups, one a compute unit: a second round would compute V again
+  const int most = 256 / tiles, gpw = groups > 0 ? (groups + 8 * most - 1) / (8 * most) : 1;
+  const int slices = groups > 0 ? (groups + 8 * gpw - 1) / (8 * gpw) : V ? 1 : 0;
   if (slices == 0) return hipSuccess;
   return launch(k_lora_short<DT, RT, FULL>, done, dim3(tiles, slices), 512, lds, st, static_cast<const E*>(Xv), T, K,
                 static_cast<const E*>(Av), R, scaling, S, static_cast<const E*>(Bv), N, static_cast<const E*>(base),
-                static_cast<E*>(out), V, (int)gpw);
+                static_cast<E*>(out), V, gpw);
 }
 
 template <int DT, int RT, int TMT, bool FULL>
