@@ -419,11 +419,12 @@ int norm_parts(int T, int C) {
     return n < 1 ? 1 : n > 32 ? 32 : n;
   }
   const int rows = C <= 128 ? 16 : C <= 1024 ? 4 : 1;    // rows a workgroup takes at once
-  // One workgroup walks few narrow rows and needs no second launch: 8 x 1024 bf16
-  // takes 5.1 us against 6.8, 4 x 2048 7.0 against 6.7 (and the workspace's
-  // allocation less on the host). More than that outlasts the launch it saves: 8
-  // x 4096 takes 15 us against 6.8, 128 x 64 9.6 against 7.0.
-  if (T <= 4 * rows && T * C <= 8192) return 1;
+  // One workgroup walks few narrow rows and needs no second launch and no
+  // workspace (6 us on the host). On the GPU 8 x 1024 bf16 takes 5.1 us against
+  // 6.8, 16 x 1024 6.9 and 6.9, 4 x 4096, the bound, 10 and 6.8, where a call's
+  // host side takes 10.5 and 16.5. More than that outlasts what it saves: 8 x
+  // 4096 takes 15 us, 8 x 16384 36 against 8.6, 128 x 64 9.6 against 7.0.
+  if (T <= 4 * rows && T * C <= 16384) return 1;
   const int n = (T + rows - 1) / rows;
   const int most = C > 4096 ? 256 : 512;
   return n < 1 ? 1 : n < most ? n : most;

@@ -191,7 +191,8 @@ def test_second_derivatives_are_refused(I8):
 
 
 @pytest.mark.parametrize("C,T", [(64, 64), (64, 65), (128, 64), (1024, 8), (1024, 9), (2048, 4), (2048, 5), (4096, 2),
-                                 (4096, 3), (16384, 1), (16384, 2)])
+                                 (4096, 3), (16384, 1), (16384, 2), (1024, 16), (1024, 17), (4096, 4), (4096, 5),
+                                 (8192, 2), (8192, 3)])
 def test_few_rows(I8, C, T):
     """Both sides of where one workgroup takes all rows."""
     check(I8, "bf16", "f32", T, C)
