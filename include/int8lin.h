@@ -25,6 +25,8 @@
  *     never allocates, frees or synchronises, except int8_linear_forward_check
  *     which synchronises by definition). Every call only enqueues work on
  *     `stream` (a hipStream_t passed as void*; NULL = the default stream).
+ *     Kernels run on the calling thread's current device, which must be the
+ *     one of `stream` and of the tensors (the Python binding sees to it).
  *   - Tensors are dense and row-major (last dimension contiguous); leading
  *     batch dimensions are flattened into the row count by the caller.
  *   - dtype: I8L_F32, I8L_F16 or I8L_BF16 (bf16 passed as raw 16-bit words).

@@ -20,7 +20,7 @@ import torch
 
 from . import _lib
 from ._lib import (I8L_BF16, I8L_F16, I8L_F32, I8L_MAX_K, Int8LinError, check, lib)
-from ._tensors import DTYPE_CODE, _check_out, _code, _dev, _empty, _stream
+from ._tensors import DTYPE_CODE, _check_out, _code, _dev, _empty, _on_gpu, _stream
 
 __all__ = [
     "int8_quantize_rowwise", "int8_linear_forward", "int8_linear_backward_input", "quantize_weight",
@@ -64,10 +64,11 @@ def int8_quantize_rowwise(X: torch.Tensor, threshold: float = 6.0, cap: Optional
         ws, wsb = workspace, workspace.numel()
     else:
         ws = _empty((max(wsb, 1),), torch.uint8, dev)
-    check(lib.int8_quantize_rowwise(_dev(X, "X"), _code(X), R, C, float(threshold), _dev(codes, "codes"),
-                                    _dev(scale, "scale"), idx.data_ptr(), count.data_ptr(), sub.data_ptr(), cap,
-                                    ws.data_ptr(), wsb, _stream(dev)),
-          "int8_quantize_rowwise")
+    with _on_gpu(X.get_device()):
+        check(lib.int8_quantize_rowwise(_dev(X, "X"), _code(X), R, C, float(threshold), _dev(codes, "codes"),
+                                        _dev(scale, "scale"), idx.data_ptr(), count.data_ptr(), sub.data_ptr(), cap,
+                                        ws.data_ptr(), wsb, _stream(dev)),
+              "int8_quantize_rowwise")
     return codes, scale, idx[:cap], count, sub[:, :cap]
 
 
@@ -113,8 +114,9 @@ def default_cap(K: int) -> int:
 def forward_check(ws: torch.Tensor, M: int, K: int, N: int, cap: int) -> int:
     """Synchronise and return the outlier count |O| of the last forward on ws."""
     c = ctypes_int32()
-    check(lib.int8_linear_forward_check(ws.data_ptr(), M, K, N, cap, _stream(ws.device), c),
-          "int8_linear_forward")
+    with _on_gpu(ws.get_device()):
+        check(lib.int8_linear_forward_check(ws.data_ptr(), M, K, N, cap, _stream(ws.device), c),
+              "int8_linear_forward")
     return int(c.value)
 
 
@@ -147,10 +149,11 @@ def int8_linear_forward(A: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor, bi
         out = _empty((M, N), A.dtype, A.device)
     if workspace is None:
         workspace = forward_workspace(M, K, N, cap, A.device)
-    check(lib.int8_linear_forward(_dev(A, "A"), _code(A), M, K, _dev(CB, "CB"), _dev(SCB, "SCB"), N,
-                                  _dev(bias, "bias"), float(threshold), cap, _dev(out, "out"), _dev(c32, "c32"),
-                                  workspace.data_ptr(), workspace.numel(), _stream(A.device)),
-          "int8_linear_forward")
+    with _on_gpu(A.get_device()):
+        check(lib.int8_linear_forward(_dev(A, "A"), _code(A), M, K, _dev(CB, "CB"), _dev(SCB, "SCB"), N,
+                                      _dev(bias, "bias"), float(threshold), cap, _dev(out, "out"), _dev(c32, "c32"),
+                                      workspace.data_ptr(), workspace.numel(), _stream(A.device)),
+              "int8_linear_forward")
     return out
 
 
@@ -172,9 +175,11 @@ def int8_linear_forward_noalloc(A: torch.Tensor, CB: torch.Tensor, SCB: torch.Te
     _check_out(out, (M, N), A.dtype, "out")
     if out is None:
         out = _empty((M, N), A.dtype, A.device)
-    check(lib.int8_linear_forward_noalloc(_dev(A, "A"), _code(A), M, K, _dev(CB, "CB"), _dev(SCB, "SCB"), N,
-                                          _dev(bias, "bias"), float(threshold), _dev(out, "out"), _stream(A.device)),
-          "int8_linear_forward_noalloc")
+    with _on_gpu(A.get_device()):
+        check(lib.int8_linear_forward_noalloc(_dev(A, "A"), _code(A), M, K, _dev(CB, "CB"), _dev(SCB, "SCB"), N,
+                                              _dev(bias, "bias"), float(threshold), _dev(out, "out"),
+                                              _stream(A.device)),
+              "int8_linear_forward_noalloc")
     return out
 
 
@@ -199,9 +204,10 @@ def silu_outlier_flags(H: torch.Tensor, threshold: float = 6.0, A: Optional[torc
         flags = outlier_flags_buffer(R, C, H.device)
     elif flags.dtype != torch.int32 or flags.numel() < n:
         raise ValueError(f"flags must be int32 with at least {n} elements")
-    check(lib.int8_silu_outlier_flags(_dev(H, "H"), _code(H), R, C, float(threshold), _dev(A, "A"),
-                                      _dev(flags, "flags"), flags.numel(), _stream(H.device)),
-          "int8_silu_outlier_flags")
+    with _on_gpu(H.get_device()):
+        check(lib.int8_silu_outlier_flags(_dev(H, "H"), _code(H), R, C, float(threshold), _dev(A, "A"),
+                                          _dev(flags, "flags"), flags.numel(), _stream(H.device)),
+              "int8_silu_outlier_flags")
     return A, flags
 
 
@@ -227,12 +233,13 @@ def int8_linear_forward_flagged(A: torch.Tensor, flags: torch.Tensor, CB: torch.
         out = _empty((M, N), A.dtype, A.device)
     if workspace is None:
         workspace = forward_workspace(M, K, N, cap, A.device)
-    check(lib.int8_linear_forward_flagged(_dev(A, "A"), _code(A), M, K, _dev(flags, "flags"), flags.numel(),
-                                          _dev(CB, "CB"),
-                                          _dev(SCB, "SCB"), N, _dev(bias, "bias"), cap, _dev(out, "out"),
-                                          _dev(c32, "c32"), workspace.data_ptr(), workspace.numel(),
-                                          _stream(A.device)),
-          "int8_linear_forward_flagged")
+    with _on_gpu(A.get_device()):
+        check(lib.int8_linear_forward_flagged(_dev(A, "A"), _code(A), M, K, _dev(flags, "flags"), flags.numel(),
+                                              _dev(CB, "CB"),
+                                              _dev(SCB, "SCB"), N, _dev(bias, "bias"), cap, _dev(out, "out"),
+                                              _dev(c32, "c32"), workspace.data_ptr(), workspace.numel(),
+                                              _stream(A.device)),
+              "int8_linear_forward_flagged")
     return out
 
 
@@ -261,11 +268,12 @@ def int8_linear_backward_input(G: torch.Tensor, CB: torch.Tensor, SCB: torch.Ten
     wsb = lib.int8_linear_backward_workspace_bytes(M, N, int(grad_bias is not None))
     if grad_bias is not None and (workspace is None or workspace.numel() < wsb):
         workspace = _empty((max(wsb, 1),), torch.uint8, G.device)
-    check(lib.int8_linear_backward_input(_dev(G, "G"), _code(G), M, N, _dev(CB, "CB"), _dev(SCB, "SCB"), K,
-                                         _dev(grad_A, "grad_A"), _dev(grad_bias, "grad_bias"),
-                                         workspace.data_ptr() if workspace is not None else 0,
-                                         workspace.numel() if workspace is not None else 0, _stream(G.device)),
-          "int8_linear_backward_input")
+    with _on_gpu(G.get_device()):
+        check(lib.int8_linear_backward_input(_dev(G, "G"), _code(G), M, N, _dev(CB, "CB"), _dev(SCB, "SCB"), K,
+                                             _dev(grad_A, "grad_A"), _dev(grad_bias, "grad_bias"),
+                                             workspace.data_ptr() if workspace is not None else 0,
+                                             workspace.numel() if workspace is not None else 0, _stream(G.device)),
+              "int8_linear_backward_input")
     return grad_A, grad_bias
 
 
@@ -299,11 +307,12 @@ def int8_linear_backward_input_int8(G: torch.Tensor, CBt: torch.Tensor, SCBt: to
     wsb = lib.int8_linear_backward_int8_workspace_bytes(M, N, int(grad_bias is not None))
     if workspace is None or workspace.numel() < wsb:
         workspace = _empty((max(wsb, 1),), torch.uint8, G.device)
-    check(lib.int8_linear_backward_input_int8(_dev(G, "G"), _code(G), M, N, _dev(CBt, "CBt"), _dev(SCBt, "SCBt"), K,
-                                              _dev(grad_A, "grad_A"), _dev(grad_bias, "grad_bias"),
-                                              _dev(c32, "c32"), workspace.data_ptr(), workspace.numel(),
-                                              _stream(G.device)),
-          "int8_linear_backward_input_int8")
+    with _on_gpu(G.get_device()):
+        check(lib.int8_linear_backward_input_int8(_dev(G, "G"), _code(G), M, N, _dev(CBt, "CBt"), _dev(SCBt, "SCBt"), K,
+                                                  _dev(grad_A, "grad_A"), _dev(grad_bias, "grad_bias"),
+                                                  _dev(c32, "c32"), workspace.data_ptr(), workspace.numel(),
+                                                  _stream(G.device)),
+              "int8_linear_backward_input_int8")
     return grad_A, grad_bias
 
 
@@ -320,9 +329,10 @@ def int8_linear_backward_weight(G: torch.Tensor, A: torch.Tensor, grad_W: Option
     _check_out(grad_W, (N, K), G.dtype, "grad_W")
     if grad_W is None:
         grad_W = _empty((N, K), G.dtype, G.device)
-    check(lib.int8_linear_backward_weight(_dev(G, "G"), _dev(A, "A"), _code(G), M, N, K, _dev(grad_W, "grad_W"),
-                                          _stream(G.device)),
-          "int8_linear_backward_weight")
+    with _on_gpu(G.get_device()):
+        check(lib.int8_linear_backward_weight(_dev(G, "G"), _dev(A, "A"), _code(G), M, N, K, _dev(grad_W, "grad_W"),
+                                              _stream(G.device)),
+              "int8_linear_backward_weight")
     return grad_W
 
 

@@ -1,6 +1,7 @@
 """What the bindings share: dtype codes, device pointers and result checks."""
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
@@ -44,6 +45,15 @@ def _empty(shape, dtype, device):
 def _raw_stream(dev: int) -> int:
     """The current HIP stream of GPU number `dev` (torch.cuda.current_stream builds a Stream object first, 2 us)."""
     return torch._C._cuda_getCurrentRawStream(dev)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on_gpu(dev: int):
+    """Makes GPU number `dev` the current one (-1: none): a kernel is launched on the current GPU, whatever GPU its
+    stream and its tensors belong to, and the default stream's handle is the same on all of them."""
+    return _HERE if dev < 0 or dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _gpu(t: torch.Tensor, name: str) -> int:

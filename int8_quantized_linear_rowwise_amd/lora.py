@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from ._lib import I8L_LORA_MAX_RANK, check, lib
-from ._tensors import _check_out, _code, _empty, _gpu, _ptr, _raw_stream, _workspace
+from ._tensors import _check_out, _code, _empty, _gpu, _on_gpu, _ptr, _raw_stream, _workspace
 
 
 def _segments(seg_offsets, seg_adapter):
@@ -72,12 +72,13 @@ def lora_forward(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scaling: tor
         v = _empty((T, R), torch.float32, X.device)
     need = lib.int8_lora_forward_workspace_bytes(T, K, N, R, S)
     ws = _workspace(workspace, need, X.device, dev)
-    check(lib.int8_lora_forward(_ptr(X, "X", dev), _code(X), T, K, _ptr(A, "A", dev), _ptr(B, "B", dev),
-                                _ptr(scaling, "scaling", dev), n, R, N, _ptr(seg_offsets, "seg_offsets", dev),
-                                _ptr(seg_adapter, "seg_adapter", dev), S, _ptr(base, "base", dev),
-                                _ptr(out, "out", dev), _ptr(v, "v", dev), _ptr(ws, "workspace", dev),
-                                0 if ws is None else ws.numel(), _raw_stream(dev)),
-          "int8_lora_forward")
+    with _on_gpu(dev):
+        check(lib.int8_lora_forward(_ptr(X, "X", dev), _code(X), T, K, _ptr(A, "A", dev), _ptr(B, "B", dev),
+                                    _ptr(scaling, "scaling", dev), n, R, N, _ptr(seg_offsets, "seg_offsets", dev),
+                                    _ptr(seg_adapter, "seg_adapter", dev), S, _ptr(base, "base", dev),
+                                    _ptr(out, "out", dev), _ptr(v, "v", dev), _ptr(ws, "workspace", dev),
+                                    0 if ws is None else ws.numel(), _raw_stream(dev)),
+              "int8_lora_forward")
     return (out, v) if with_v else out
 
 
@@ -113,13 +114,14 @@ def lora_backward(G: torch.Tensor, X: torch.Tensor, V: torch.Tensor, A: torch.Te
         grad_B = torch.empty_like(B, memory_format=torch.contiguous_format)
     need = lib.int8_lora_backward_workspace_bytes(T, K, N, R, n, S)
     ws = _workspace(workspace, need, X.device, dev)
-    check(lib.int8_lora_backward(_ptr(G, "G", dev), _ptr(X, "X", dev), _ptr(V, "V", dev), _code(X), T, K,
-                                 _ptr(A, "A", dev), _ptr(B, "B", dev), _ptr(scaling, "scaling", dev), n, R, N,
-                                 _ptr(seg_offsets, "seg_offsets", dev), _ptr(seg_adapter, "seg_adapter", dev), S,
-                                 _ptr(base_grad, "base_grad", dev), _ptr(grad_X, "grad_X", dev),
-                                 _ptr(grad_A, "grad_A", dev), _ptr(grad_B, "grad_B", dev),
-                                 _ptr(ws, "workspace", dev), 0 if ws is None else ws.numel(), _raw_stream(dev)),
-          "int8_lora_backward")
+    with _on_gpu(dev):
+        check(lib.int8_lora_backward(_ptr(G, "G", dev), _ptr(X, "X", dev), _ptr(V, "V", dev), _code(X), T, K,
+                                     _ptr(A, "A", dev), _ptr(B, "B", dev), _ptr(scaling, "scaling", dev), n, R, N,
+                                     _ptr(seg_offsets, "seg_offsets", dev), _ptr(seg_adapter, "seg_adapter", dev), S,
+                                     _ptr(base_grad, "base_grad", dev), _ptr(grad_X, "grad_X", dev),
+                                     _ptr(grad_A, "grad_A", dev), _ptr(grad_B, "grad_B", dev),
+                                     _ptr(ws, "workspace", dev), 0 if ws is None else ws.numel(), _raw_stream(dev)),
+              "int8_lora_backward")
     return grad_X, grad_A, grad_B
 
 

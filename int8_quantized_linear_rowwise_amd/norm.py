@@ -7,7 +7,7 @@ from typing import Optional
 import torch
 
 from ._lib import check, lib
-from ._tensors import _check_out, _code, _empty, _gpu, _ptr, _raw_stream, _workspace
+from ._tensors import _check_out, _code, _empty, _gpu, _on_gpu, _ptr, _raw_stream, _workspace
 
 
 def _weights(X, weight, bias):
@@ -38,10 +38,11 @@ def layer_norm_forward(X: torch.Tensor, weight: torch.Tensor, bias: Optional[tor
         mean = _empty((T,), torch.float32, X.device)
     if rstd is None:
         rstd = torch.empty_like(mean)
-    check(lib.int8_layer_norm_forward(_ptr(X, "X", dev), _code(X), T, C, _ptr(weight, "weight", dev),
-                                      _ptr(bias, "bias", dev), _code(weight), eps, _ptr(out, "out", dev),
-                                      _ptr(mean, "mean", dev), _ptr(rstd, "rstd", dev), _raw_stream(dev)),
-          "int8_layer_norm_forward")
+    with _on_gpu(dev):
+        check(lib.int8_layer_norm_forward(_ptr(X, "X", dev), _code(X), T, C, _ptr(weight, "weight", dev),
+                                          _ptr(bias, "bias", dev), _code(weight), eps, _ptr(out, "out", dev),
+                                          _ptr(mean, "mean", dev), _ptr(rstd, "rstd", dev), _raw_stream(dev)),
+              "int8_layer_norm_forward")
     return out, mean, rstd
 
 
@@ -69,12 +70,14 @@ def layer_norm_backward(G: torch.Tensor, X: torch.Tensor, mean: torch.Tensor, rs
     if grad_bias is None and with_grad_bias:
         grad_bias = torch.empty_like(weight, memory_format=torch.contiguous_format)
     ws = _workspace(workspace, lib.int8_layer_norm_backward_workspace_bytes(T, C), X.device, dev)
-    check(lib.int8_layer_norm_backward(_ptr(G, "G", dev), _ptr(X, "X", dev), _code(X), T, C, _ptr(mean, "mean", dev),
-                                       _ptr(rstd, "rstd", dev), _ptr(weight, "weight", dev), _code(weight),
-                                       _ptr(grad_X, "grad_X", dev), _ptr(grad_weight, "grad_weight", dev),
-                                       _ptr(grad_bias, "grad_bias", dev), _ptr(ws, "workspace", dev),
-                                       0 if ws is None else ws.numel(), _raw_stream(dev)),
-          "int8_layer_norm_backward")
+    with _on_gpu(dev):
+        check(lib.int8_layer_norm_backward(_ptr(G, "G", dev), _ptr(X, "X", dev), _code(X), T, C,
+                                           _ptr(mean, "mean", dev), _ptr(rstd, "rstd", dev),
+                                           _ptr(weight, "weight", dev), _code(weight),
+                                           _ptr(grad_X, "grad_X", dev), _ptr(grad_weight, "grad_weight", dev),
+                                           _ptr(grad_bias, "grad_bias", dev), _ptr(ws, "workspace", dev),
+                                           0 if ws is None else ws.numel(), _raw_stream(dev)),
+              "int8_layer_norm_backward")
     return grad_X, grad_weight, grad_bias
 
 

@@ -13,7 +13,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from ._lib import AdamWTensor, check, lib
-from ._tensors import DTYPE_CODE, _ptr, _raw_stream
+from ._tensors import DTYPE_CODE, _on_gpu, _ptr, _raw_stream
 
 BLOCK = 256   # values that share a scale
 
@@ -107,10 +107,11 @@ class AdamWPlan:
         stream = _raw_stream(self.gpu)
         if stream != self._stream:     # the table's memory is not given away before this stream is done with it
             self.table.record_stream(torch.cuda.current_stream(self.device))
-        check(lib.int8_adamw_step(self.table.data_ptr(), self.count, self.chunks, lr, betas[0], betas[1], eps,
-                                  weight_decay, step, 0 if grad_scale is None else grad_scale.data_ptr(),
-                                  0 if found_inf is None else found_inf.data_ptr(), stream),
-              "int8_adamw_step")
+        with _on_gpu(self.gpu):
+            check(lib.int8_adamw_step(self.table.data_ptr(), self.count, self.chunks, lr, betas[0], betas[1], eps,
+                                      weight_decay, step, 0 if grad_scale is None else grad_scale.data_ptr(),
+                                      0 if found_inf is None else found_inf.data_ptr(), stream),
+                  "int8_adamw_step")
 
 
 class AdamW(torch.optim.Optimizer):
