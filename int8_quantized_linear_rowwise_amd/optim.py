@@ -169,7 +169,9 @@ class AdamW(torch.optim.Optimizer):
                     # backward pass's where zero_grad drops them)
                     held[1]._keep = None
                 live[key] = held
-                if torch.cuda.is_current_stream_capturing():   # a graph's replays read the table and these tensors
+                with _on_gpu(held[1].gpu):
+                    capturing = torch.cuda.is_current_stream_capturing()
+                if capturing:   # a graph's replays read the table and these tensors
                     self._captured.append((held[1], rows))
                 held[1].step(step, group["lr"], group["betas"], group["eps"], group["weight_decay"], grad_scale,
                              found_inf)
