@@ -100,7 +100,8 @@ class AdamWPlan:
              found_inf: Optional[torch.Tensor] = None) -> None:
         """Step number `step` (from 1). grad_scale: fp32 GPU scalar that multiplies the gradients; found_inf: fp32 GPU
         scalar, anything but 0 leaves all tensors as they are (the caller's step count goes on). A captured step keeps
-        its numbers; only the two scalars are read at each replay."""
+        its numbers; only the two scalars are read at each replay: the caller keeps them, and the plan, as long
+        as the graph."""
         for name, x in (("grad_scale", grad_scale), ("found_inf", found_inf)):
             if x is not None and (x.dtype != torch.float32 or x.numel() != 1 or x.get_device() != self.gpu):
                 raise ValueError(f"{name} must be one float32 value on {self.device}")
@@ -171,8 +172,9 @@ class AdamW(torch.optim.Optimizer):
                 live[key] = held
                 with _on_gpu(held[1].gpu):
                     capturing = torch.cuda.is_current_stream_capturing()
-                if capturing:   # a graph's replays read the table and these tensors
-                    self._captured.append((held[1], rows))
+                if capturing:   # a graph's replays use the table, these very tensors and the two scalars
+                    self._captured.append((held[1], [(p.detach(), g, dict(s)) for p, g, s in rows], grad_scale,
+                                           found_inf))
                 held[1].step(step, group["lr"], group["betas"], group["eps"], group["weight_decay"], grad_scale,
                              found_inf)
             self._plans[gi] = live
