@@ -8,6 +8,7 @@ root, sqrt(v) = code * scale.
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -16,6 +17,14 @@ from ._lib import AdamWTensor, check, lib
 from ._tensors import DTYPE_CODE, _on_gpu, _ptr, _raw_stream
 
 BLOCK = 256   # values that share a scale
+
+
+def _check_numbers(lr, betas, eps, weight_decay) -> None:
+    for name, x in (("lr", lr), ("eps", eps), ("weight_decay", weight_decay)):
+        if not (0.0 <= x < math.inf):
+            raise ValueError(f"{name} must be a finite number of 0 or more, got {x}")
+    if len(betas) != 2 or not all(0.0 <= b < 1.0 for b in betas):
+        raise ValueError(f"betas must be two numbers in [0, 1), got {betas}")
 
 
 def adamw_state(p: torch.Tensor, bits: int = 32, master: bool = False) -> dict:
@@ -95,6 +104,11 @@ class AdamWPlan:
         self.table = host.to(self.device)
         self._stream = _raw_stream(self.gpu)
 
+    def _check_scalars(self, grad_scale, found_inf) -> None:
+        for name, x in (("grad_scale", grad_scale), ("found_inf", found_inf)):
+            if x is not None and (x.dtype != torch.float32 or x.numel() != 1 or x.get_device() != self.gpu):
+                raise ValueError(f"{name} must be one float32 value on {self.device}")
+
     def step(self, step: int, lr: float, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
              weight_decay: float = 0.01, grad_scale: Optional[torch.Tensor] = None,
              found_inf: Optional[torch.Tensor] = None) -> None:
@@ -102,9 +116,7 @@ class AdamWPlan:
         scalar, anything but 0 leaves all tensors as they are (the caller's step count goes on). A captured step keeps
         its numbers; only the two scalars are read at each replay: the caller keeps them, and the plan, as long
         as the graph."""
-        for name, x in (("grad_scale", grad_scale), ("found_inf", found_inf)):
-            if x is not None and (x.dtype != torch.float32 or x.numel() != 1 or x.get_device() != self.gpu):
-                raise ValueError(f"{name} must be one float32 value on {self.device}")
+        self._check_scalars(grad_scale, found_inf)
         stream = _raw_stream(self.gpu)
         if stream != self._stream:     # the table's memory is not given away before this stream is done with it
             self.table.record_stream(torch.cuda.current_stream(self.device))
@@ -139,25 +151,26 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        # everything is checked and laid out before the first launch: a refused step changes nothing
+        due, plans = [], {}
         for gi, group in enumerate(self.param_groups):
+            _check_numbers(group["lr"], group["betas"], group["eps"], group["weight_decay"])
             buckets: dict = {}
             for p in group["params"]:
                 if p.grad is None:
                     continue
-                s = self.state[p]
+                s = self.state.get(p)
                 if not s:
-                    s.update(adamw_state(p, group["state_bits"], group["master"] and p.dtype != torch.float32))
+                    s = adamw_state(p, group["state_bits"], group["master"] and p.dtype != torch.float32)
                     s["step"] = 0
-                s["step"] += 1
-                buckets.setdefault((p.device, s["step"], "master" in s), []).append(p)
-            live = {}
-            for (device, step, has_master), ps in buckets.items():
-                rows = [(p, p.grad, self.state[p]) for p in ps]
+                buckets.setdefault((p.device, s["step"] + 1, "master" in s), []).append((p, p.grad, s))
+            live = plans[gi] = {}
+            for (device, step, has_master), rows in buckets.items():
                 where = tuple(x.data_ptr() for p, g, s in rows
                               for x in (p, g, s["m"], s["v"], s.get("m_scale"), s.get("v_scale"), s.get("master"))
                               if x is not None)
                 where += tuple((p.numel(), p.dtype, g.dtype, p.is_contiguous(), g.is_contiguous()) for p, g, s in rows)
-                key = (device, has_master, tuple(id(p) for p in ps))
+                key = (device, has_master, tuple(id(r[0]) for r in rows))
                 held = self._plans.get(gi, {}).get(key)
                 if held is None or held[0] != where:
                     low = group["state_bits"] == 8
@@ -169,15 +182,20 @@ class AdamW(torch.optim.Optimizer):
                     # every step compares the addresses: old gradients need not be held (their memory is the next
                     # backward pass's where zero_grad drops them)
                     held[1]._keep = None
+                held[1]._check_scalars(grad_scale, found_inf)
                 live[key] = held
-                with _on_gpu(held[1].gpu):
-                    capturing = torch.cuda.is_current_stream_capturing()
-                if capturing:   # a graph's replays use the table, these very tensors and the two scalars
-                    self._captured.append((held[1], [(p.detach(), g, dict(s)) for p, g, s in rows], grad_scale,
-                                           found_inf))
-                held[1].step(step, group["lr"], group["betas"], group["eps"], group["weight_decay"], grad_scale,
-                             found_inf)
-            self._plans[gi] = live
+                due.append((held[1], step, group, rows))
+        for plan, step, group, rows in due:
+            with _on_gpu(plan.gpu):
+                capturing = torch.cuda.is_current_stream_capturing()
+            if capturing:   # a graph's replays use the table, these very tensors and the two scalars
+                self._captured.append((plan, [(p.detach(), g, dict(s)) for p, g, s in rows], grad_scale, found_inf))
+            plan.step(step, group["lr"], group["betas"], group["eps"], group["weight_decay"], grad_scale, found_inf)
+            for p, _, s in rows:
+                s["step"] = step
+                if step == 1:
+                    self.state[p] = s
+        self._plans = plans
         return loss
 
     def load_state_dict(self, state_dict):

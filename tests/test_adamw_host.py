@@ -2,6 +2,7 @@
 import gc
 import weakref
 
+import pytest
 import torch
 
 from tests._stub_gpu import L, stub  # noqa: F401  (fixtures)
@@ -62,3 +63,38 @@ def test_a_captured_step_holds_its_tensors(stub):  # noqa: F811
     opt.load_state_dict(opt.state_dict())
     gc.collect()
     assert [r() is None for r in gone] == [False] * 3
+
+
+@pytest.mark.parametrize("what", ["layout", "type", "grad_scale", "found_inf", "lr", "betas", "eps", "weight_decay"])
+@pytest.mark.parametrize("before", [0, 2])
+def test_a_refused_step_changes_nothing(stub, what, before):  # noqa: F811
+    """Everything is checked before the first launch: no group is stepped, no step counted, no state made."""
+    a, b = torch.nn.Parameter(torch.ones(4, 6)), torch.nn.Parameter(torch.ones(6, 4).to(torch.bfloat16))
+    for p in (a, b):
+        p.grad = torch.ones_like(p)
+    opt = stub.I8.AdamW([dict(params=[a]), dict(params=[b])], master=True)
+    for _ in range(before):
+        opt.step()
+    launched, made = len(stub.seen), {p: dict(opt.state[p]) for p in opt.state}
+    kw, good = {}, b.grad
+    if what == "layout":
+        b.grad = torch.ones(4, 6).to(torch.bfloat16).t()
+    elif what == "type":
+        b.grad, b.grad_dtype = None, torch.float32
+        b.grad = torch.ones(6, 4)
+    elif what in ("grad_scale", "found_inf"):
+        kw[what] = torch.ones(1, dtype=torch.float64)
+    else:
+        was = opt.param_groups[1][what]
+        opt.param_groups[1][what] = (0.9, 1.0) if what == "betas" else float("inf")
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            opt.step(**kw)
+    assert len(stub.seen) == launched and {p: dict(s) for p, s in opt.state.items()} == made
+    b.grad, b.grad_dtype = None, b.dtype
+    b.grad = good
+    if what in opt.defaults:
+        opt.param_groups[1][what] = was
+    opt.step()
+    assert len(stub.seen) == launched + 2
+    assert [x[8] for x in stub.args[-2:]] == [opt.state[p]["step"] for p in (a, b)] == [before + 1] * 2
