@@ -145,6 +145,13 @@ class AdamW(torch.optim.Optimizer):
         self._plans: dict = {}
         self._captured: list = []
 
+    def __setstate__(self, state):
+        """Plans name the addresses of the states before: a copy, an unpickled optimizer and load_state_dict, which
+        comes through here too, start without. What this optimizer's own captured steps use stays held."""
+        super().__setstate__(state)
+        self._plans = {}
+        self.__dict__.setdefault("_captured", [])
+
     @torch.no_grad()
     def step(self, closure=None, grad_scale: Optional[torch.Tensor] = None, found_inf: Optional[torch.Tensor] = None):
         loss = None

@@ -1,6 +1,8 @@
 """What the AdamW optimizer does on the host, with a library that records its calls instead of a GPU."""
 import gc
+import io
 import weakref
+from copy import deepcopy
 
 import pytest
 import torch
@@ -98,3 +100,25 @@ def test_a_refused_step_changes_nothing(stub, what, before):  # noqa: F811
     opt.step()
     assert len(stub.seen) == launched + 2
     assert [x[8] for x in stub.args[-2:]] == [opt.state[p]["step"] for p in (a, b)] == [before + 1] * 2
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "saved"])
+def test_a_copy_steps_on_its_own(stub, how):  # noqa: F811
+    """A copied optimizer lays out a plan of its own tensors: nothing that it launches names the original's."""
+    opt = stub.I8.AdamW(params(300, 40), state_bits=8)
+    opt.step()
+    own = opt._plans
+    if how == "deepcopy":
+        copy = deepcopy(opt)
+    else:
+        file = io.BytesIO()
+        torch.save(opt, file)
+        file.seek(0)
+        copy = torch.load(file, weights_only=False)
+    for p in copy.param_groups[0]["params"]:
+        p.grad = torch.ones_like(p)
+    copy.step()
+    assert opt._plans is own and stub.args[-1][0] != stub.args[0][0]
+    assert [s["step"] for s in copy.state.values()] == [2, 2] and [s["step"] for s in opt.state.values()] == [1, 1]
+    for s in copy.state.values():
+        assert s["m"].dtype == torch.float8_e4m3fn and s["m_scale"].dtype == torch.float32
