@@ -19,12 +19,14 @@ from ._tensors import DTYPE_CODE, _on_gpu, _ptr, _raw_stream
 BLOCK = 256   # values that share a scale
 
 
-def _check_numbers(lr, betas, eps, weight_decay) -> None:
+def _check_numbers(lr, betas, eps, weight_decay, state_bits=32, **other) -> None:
     for name, x in (("lr", lr), ("eps", eps), ("weight_decay", weight_decay)):
         if not (0.0 <= x < math.inf):
             raise ValueError(f"{name} must be a finite number of 0 or more, got {x}")
     if len(betas) != 2 or not all(0.0 <= b < 1.0 for b in betas):
         raise ValueError(f"betas must be two numbers in [0, 1), got {betas}")
+    if state_bits not in (8, 32):
+        raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
 
 
 def adamw_state(p: torch.Tensor, bits: int = 32, master: bool = False) -> dict:
@@ -138,12 +140,15 @@ class AdamW(torch.optim.Optimizer):
 
     def __init__(self, params, lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, state_bits: int = 32, master: bool = False):
-        if state_bits not in (8, 32):
-            raise ValueError("state_bits must be 8 or 32")
-        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits,
-                                      master=master))
+        defaults = dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits, master=master)
+        _check_numbers(**defaults)
+        super().__init__(params, defaults)
         self._plans: dict = {}
         self._captured: list = []
+
+    def add_param_group(self, param_group):
+        _check_numbers(**{**self.defaults, **param_group})
+        super().add_param_group(param_group)
 
     def __setstate__(self, state):
         """Plans name the addresses of the states before: a copy, an unpickled optimizer and load_state_dict, which
@@ -161,7 +166,7 @@ class AdamW(torch.optim.Optimizer):
         # everything is checked and laid out before the first launch: a refused step changes nothing
         due, plans = [], {}
         for gi, group in enumerate(self.param_groups):
-            _check_numbers(group["lr"], group["betas"], group["eps"], group["weight_decay"])
+            _check_numbers(**group)
             buckets: dict = {}
             for p in group["params"]:
                 if p.grad is None:

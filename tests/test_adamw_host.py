@@ -122,3 +122,20 @@ def test_a_copy_steps_on_its_own(stub, how):  # noqa: F811
     assert [s["step"] for s in copy.state.values()] == [2, 2] and [s["step"] for s in opt.state.values()] == [1, 1]
     for s in copy.state.values():
         assert s["m"].dtype == torch.float8_e4m3fn and s["m_scale"].dtype == torch.float32
+
+
+@pytest.mark.parametrize("kw", [dict(lr=-1.0), dict(lr=float("nan")), dict(betas=(2, 0.9)), dict(betas=(0.9, 1.0)),
+                                dict(betas=(0.9,)), dict(eps=-1e-8), dict(weight_decay=-0.1),
+                                dict(weight_decay=float("inf")), dict(state_bits=16)])
+def test_numbers_out_of_range_are_refused_at_once(stub, kw):  # noqa: F811
+    """By the constructor, for its defaults and for a group's own numbers, and by add_param_group."""
+    (p, q) = params(3, 4)
+    with pytest.raises(ValueError):
+        stub.I8.AdamW([p], **kw)
+    with pytest.raises(ValueError):
+        stub.I8.AdamW([dict(params=[p], **kw)])
+    opt = stub.I8.AdamW([p])
+    with pytest.raises(ValueError):
+        opt.add_param_group(dict(params=[q], **kw))
+    opt.step()
+    assert len(opt.param_groups) == 1 and len(stub.seen) == 1
