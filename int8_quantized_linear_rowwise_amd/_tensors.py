@@ -52,8 +52,9 @@ _HERE = contextlib.nullcontext()
 
 def _on_gpu(dev: int):
     """Makes GPU number `dev` the current one (-1: none): a kernel is launched on the current GPU, whatever GPU its
-    stream and its tensors belong to, and the default stream's handle is the same on all of them."""
-    return _HERE if dev < 0 or dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    stream and its tensors belong to, and the default stream's handle is the same on all of them. (0.25 us where it
+    is current already; torch.cuda.current_device asks for the runtime's start first, 0.12 us more.)"""
+    return _HERE if dev < 0 or dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _gpu(t: torch.Tensor, name: str) -> int:

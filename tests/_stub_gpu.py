@@ -50,7 +50,7 @@ def stub(L, monkeypatch):  # noqa: F811
     monkeypatch.setattr(torch.Tensor, "is_cuda", True)
     monkeypatch.setattr(torch.cuda, "device", Device)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: s.current)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: s.current, raising=False)
     # a stream of GPU 1 is captured, if any
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: s.capturing and s.current == 1)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
