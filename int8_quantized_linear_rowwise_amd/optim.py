@@ -19,6 +19,14 @@ from ._tensors import DTYPE_CODE, _on_gpu, _ptr, _raw_stream
 BLOCK = 256   # values that share a scale
 
 
+def _capturing(dev: int) -> bool:
+    """Whether the current stream of GPU number `dev` is being captured into a graph."""
+    if dev < 0:
+        return False
+    with _on_gpu(dev):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _check_numbers(lr, betas, eps, weight_decay, state_bits=32, **other) -> None:
     for name, x in (("lr", lr), ("eps", eps), ("weight_decay", weight_decay)):
         if not (0.0 <= x < math.inf):
@@ -98,6 +106,9 @@ class AdamWPlan:
                 raise ValueError("parameters must be on a GPU")
             arr[i] = AdamWTensor(*[_ptr(t, k, self.gpu) or None for t, k in zip(row, names)], size,
                                  DTYPE_CODE[dtype], 8 if low else 32)
+        if _capturing(self.gpu):
+            raise RuntimeError("AdamW: the plan of a captured step has to be laid out before the capture (for the "
+                               "optimizer: one ordinary step with the same gradients)")
         need = lib.int8_adamw_table_bytes(arr, n)
         host = torch.zeros(max(need, 1), dtype=torch.uint8)
         chunks = ctypes.c_int64(0)
@@ -118,7 +129,8 @@ class AdamWPlan:
         scalar, anything but 0 leaves all tensors as they are (the caller's step count goes on). A captured step keeps
         its numbers; only the two scalars are read at each replay: the caller keeps them, and the plan, as long
         as the graph."""
-        self._check_scalars(grad_scale, found_inf)
+        if grad_scale is not None or found_inf is not None:
+            self._check_scalars(grad_scale, found_inf)
         stream = _raw_stream(self.gpu)
         if stream != self._stream:     # the table's memory is not given away before this stream is done with it
             self.table.record_stream(torch.cuda.current_stream(self.device))
@@ -136,7 +148,9 @@ class AdamW(torch.optim.Optimizer):
     The plan of a group is laid out again whenever a gradient or parameter has
     moved (gradients kept in place with zero_grad(set_to_none=False) never do).
     Parameters and gradients have to be contiguous. A captured step keeps its
-    step number and learning rate; what it uses is held as long as the optimizer."""
+    step number and learning rate; what it uses is held as long as the optimizer.
+    One ordinary step with the same gradients comes before a capture: it makes the
+    states and lays out the plan."""
 
     def __init__(self, params, lr: float = 1e-3, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, state_bits: int = 32, master: bool = False):
@@ -173,6 +187,9 @@ class AdamW(torch.optim.Optimizer):
                     continue
                 s = self.state.get(p)
                 if not s:
+                    if _capturing(p.get_device()):   # the zeros would be written again at every replay
+                        raise RuntimeError("AdamW: states have to be made before the capture: take one ordinary step "
+                                           "with the same gradients first")
                     s = adamw_state(p, group["state_bits"], group["master"] and p.dtype != torch.float32)
                     s["step"] = 0
                 buckets.setdefault((p.device, s["step"] + 1, "master" in s), []).append((p, p.grad, s))
@@ -198,9 +215,7 @@ class AdamW(torch.optim.Optimizer):
                 live[key] = held
                 due.append((held[1], step, group, rows))
         for plan, step, group, rows in due:
-            with _on_gpu(plan.gpu):
-                capturing = torch.cuda.is_current_stream_capturing()
-            if capturing:   # a graph's replays use the table, these very tensors and the two scalars
+            if _capturing(plan.gpu):   # a graph's replays use the table, these very tensors and the two scalars
                 self._captured.append((plan, [(p.detach(), g, dict(s)) for p, g, s in rows], grad_scale, found_inf))
             plan.step(step, group["lr"], group["betas"], group["eps"], group["weight_decay"], grad_scale, found_inf)
             for p, _, s in rows:

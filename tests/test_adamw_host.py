@@ -139,3 +139,34 @@ def test_numbers_out_of_range_are_refused_at_once(stub, kw):  # noqa: F811
         opt.add_param_group(dict(params=[q], **kw))
     opt.step()
     assert len(opt.param_groups) == 1 and len(stub.seen) == 1
+
+
+@pytest.mark.parametrize("what", ["first step", "other gradients"])
+def test_a_capture_of_a_step_without_its_plan_is_refused(stub, what):  # noqa: F811
+    """Making states (their zeros would be written at every replay) and copying a plan to the GPU do not belong in a
+    graph: one ordinary step with the same gradients comes first. The refused step leaves nothing behind."""
+    (p,) = P = params(300)
+    opt = stub.I8.AdamW(P)
+    done = 0
+    if what == "other gradients":
+        opt.step()
+        p.grad, done = torch.ones(300), 1
+    stub.capturing = True
+    with pytest.raises(RuntimeError, match="before the capture"):
+        opt.step()
+    assert len(stub.seen) == done and len(opt.state) == done and not opt._captured
+    with pytest.raises(RuntimeError, match="before the capture"):
+        stub.I8.AdamWPlan([p.detach()], [p.grad], [torch.zeros(300)], [torch.zeros(300)])
+    stub.capturing = False
+    opt.step()
+    stub.capturing = True
+    opt.step()
+    assert opt.state[p]["step"] == done + 2 and len(opt._captured) == 1
+
+
+def test_parameters_off_the_gpu_are_refused(L):  # noqa: F811
+    import int8_quantized_linear_rowwise_amd as I8
+    opt = I8.AdamW(params(30))
+    with pytest.raises(ValueError, match="GPU"):
+        opt.step()
+    assert not opt.state
