@@ -128,7 +128,7 @@ def lora_backward(G: torch.Tensor, X: torch.Tensor, V: torch.Tensor, A: torch.Te
 class Int8LoraFunction(torch.autograd.Function):
     """The frozen int8 layer with adapters beside it: forward in int8 plus the
     adapters' product, backward through the memory-efficient kernel plus the
-    adapters' gradients. The int8 weight is frozen."""
+    adapters' gradients. The int8 weight is frozen, and scaling is constant."""
 
     @staticmethod
     def forward(ctx, x, CB, SCB, bias, A, B, scaling, seg_offsets, seg_adapter, threshold):
@@ -147,6 +147,8 @@ class Int8LoraFunction(torch.autograd.Function):
         from . import int8_linear_backward_input
         X, V, CB, SCB, A, B, scaling, seg_offsets, seg_adapter = ctx.saved_tensors
         need = ctx.needs_input_grad
+        if need[6]:   # forward cannot tell this from a call under no_grad, which is fine
+            raise ValueError("scaling has no gradient here: the adapters' factors are constants (detach it)")
         g2 = g.reshape(-1, g.shape[-1]).contiguous()
         need_b = ctx.has_bias and need[3]
         gX = gb = None
