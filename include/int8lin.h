@@ -306,7 +306,10 @@ int int8_linear_backward_weight(const void* G, const void* A, int dtype, int64_t
  *   grad_B[a, n, r] = D(s[a] sum over the rows t of adapter a of G[t, n] V[t, r])
  * V and dV are never rounded below fp32's 24 bits except for the matrix
  * products with 16-bit operands, where they enter as the sum of two values of
- * that type (16 bits of mantissa or more).
+ * that type, within 2^-17 of the value. In fp16 these are scaled by a power of
+ * two, and a value below 2^-22 of the largest of its set is off by up to 2^-39
+ * of that one instead; the set is one row of V or dV for out and grad_X (no row
+ * depends on another), and the rows of a tile for grad_A and grad_B.
  *   X: T x K, out / base: T x N, A: n_adapters x R x K, B: n_adapters x N x R,
  *   G: T x N, grad_X / base_grad: T x K, all of `dtype`; grad_A, grad_B: as A
  *   and B; scaling: n_adapters fp32; V: T x R fp32.

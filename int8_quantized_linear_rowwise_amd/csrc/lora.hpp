@@ -218,9 +218,13 @@ struct Rows {
 // values of that type: hi is v rounded, lo the rest rounded, together within
 // 2^-17 of v (bf16; 2^-22 in fp16). Rounding V to 16 bits once instead would
 // add an error of the output's own rounding to every adapter product. An fp16
-// pair covers fp32's range by a power of two per tile that puts the largest
-// magnitude at 2^14: what is 2^-16 of that still has 22 bits, and products
-// with fp16 values stay far inside fp32.
+// pair covers fp32's range by a power of two that puts the largest magnitude
+// of its set at 2^14: values down to 2^-17 of that keep 22 bits, to 2^-22 17
+// bits, and below that an absolute 2^-39 of it; products with fp16 values stay
+// far inside fp32. In products along r (out, grad_X) the set is one token's
+// values, so no token depends on its neighbours. Along the tokens (grad_A,
+// grad_B) one sum meets values of many tokens, and the set is what the tile
+// has met so far.
 template <int DT>
 __device__ __forceinline__ uint32_t split2(float v, float unit) {
   if constexpr (DT == DT_F16) v *= unit;
@@ -230,6 +234,23 @@ __device__ __forceinline__ uint32_t split2(float v, float unit) {
   const typename Elem<DT>::T lo = Elem<DT>::from_f32(__builtin_isfinite(v) ? r : 0.0f);
   return (uint32_t)__builtin_bit_cast(uint16_t, hi) | ((uint32_t)__builtin_bit_cast(uint16_t, lo) << 16);
 }
+// Largest of the W lanes (16, 32 or 64 side by side, all active) that a lane
+// belongs to, of values of 0 or more, whose bits order as they do.
+template <int W>
+__device__ __forceinline__ float lanes_max(float f) {
+  uint32_t v = __float_as_uint(f);
+  if constexpr (W == 64) {
+    v = wave_umax(v);
+  } else {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0xB1, 0xf, 0xf, false));   // quad_perm 1,0,3,2
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x4E, 0xf, 0xf, false));   // quad_perm 2,3,0,1
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x141, 0xf, 0xf, false));  // row_half_mirror
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x140, 0xf, 0xf, false));  // row_mirror
+    if constexpr (W == 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+  }
+  return __uint_as_float(v);
+}
+
 // Power of two that takes a largest magnitude `top` to [2^14, 2^15), and its
 // inverse; 1 for zero, infinities and NaN. Both stay normal fp32 values.
 __device__ __forceinline__ float unit_for(float top) {

@@ -442,6 +442,18 @@ __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ 
   char* vt = sm + 8 * TL::BYTES;
   char* vr = vt + SM::VT;
   float* top8 = reinterpret_cast<float*>(vr + SM::VR);
+  float* tops = top8 + 8;   // fp16: [part][token], the largest of up to 64 of a token's values
+  constexpr int W = RP < 64 ? RP : 64, NP = RP / W;
+  // fp16: the power of two of the tile's token t, and of t and t + 1
+  auto unit_of = [&](int t) { return unit_for(NP == 1 ? tops[t] : fmaxf(tops[t], tops[ST + t])); };
+  auto units_of = [&](int t) {
+    v2f m = *reinterpret_cast<const v2f*>(tops + t);
+    if constexpr (NP == 2) {
+      const v2f o = *reinterpret_cast<const v2f*>(tops + ST + t);
+      m = v2f{fmaxf(m[0], o[0]), fmaxf(m[1], o[1])};
+    }
+    return v2f{unit_for(m[0]), unit_for(m[1])};
+  };
 
   const LoraTile tl = lora_tile(S, L, d, T, tm);
   const bool none = tl.t1 <= tl.t0 || tl.adapter < 0;
@@ -491,7 +503,7 @@ __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ 
   for (int j = 0; j < RT; ++j)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[j][n] = v4f{};
-  float run_top = 0.0f, unit = 1.0f, sub = 1.0f;
+  float run_top = 0.0f, unit = 1.0f;
 
   auto load_v = [&](int at) {
 #pragma unroll
@@ -544,15 +556,22 @@ __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ 
     if constexpr (DT == DT_F16) {
       float top = 0.0f;
 #pragma unroll
-      for (int y = 0; y < SM::PER; ++y) top = fmaxf(top, fmaxf(finite_abs(v[y][0]), finite_abs(v[y][1])));
-      top = wave_max(top);
+      for (int y = 0; y < SM::PER; ++y) {
+        const int e = tid + 512 * y;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float m = lanes_max<W>(finite_abs(v[y][h]));
+          if (e < SM::PAIRS && lane % W == 0) tops[e % RP / W * ST + 2 * (e / RP) + h] = m;
+          top = fmaxf(top, m);
+        }
+      }
+      if constexpr (W < 64) top = lanes_max<64>(top);
       if (lane == 0) top8[wave] = top;
       __syncthreads();
       float all = 0.0f;
 #pragma unroll
       for (int w = 0; w < 8; ++w) all = fmaxf(all, top8[w]);
-      sub = unit_for(all);                         // dx: the scale of these tokens
-      if (all > run_top) {                         // dA: the scale of all tokens so far
+      if (all > run_top) {   // dA: the scale of all tokens so far
         const float u = unit_for(all), f = u * inv_pow2(unit);
 #pragma unroll
         for (int j = 0; j < RT; ++j)
@@ -567,9 +586,12 @@ __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ 
       const int e = tid + 512 * y;
       if (e < SM::PAIRS) {
         if (dAp) SM::put_t(vt, e % RP, e / RP, v[y][0], v[y][1], unit);
-        if (out) {
-          SM::put_r(vr, e % RP, 2 * (e / RP), v[y][0], sub);
-          SM::put_r(vr, e % RP, 2 * (e / RP) + 1, v[y][1], sub);
+        if (out) {   // dx: the scale of the token
+          const int t = 2 * (e / RP);
+          v2f u = {1.0f, 1.0f};
+          if constexpr (DT == DT_F16) u = units_of(t);
+          SM::put_r(vr, e % RP, t, v[y][0], u[0]);
+          SM::put_r(vr, e % RP, t + 1, v[y][1], u[1]);
         }
       }
     }
@@ -594,9 +616,9 @@ __device__ __forceinline__ void x_tile(const typename Elem<DT>::T* __restrict__ 
         for (int i = 0; i < TL::NI; ++i) TL::at(mine, TL::RPI * i + lrow, lch) = b[i];
         if (more) load_rows(base, at + ST, b);
       }
-      const float f = DT == DT_F16 ? inv_pow2(sub) : 1.0f;
 #pragma unroll
       for (int i = 0; i < TT; ++i) {
+        const float f = DT == DT_F16 ? inv_pow2(unit_of(16 * i + c)) : 1.0f;
         v4u fv[NS];
 #pragma unroll
         for (int s = 0; s < NS; ++s)
@@ -885,7 +907,8 @@ hipError_t x_pass(const Plan& p, const void* X, int T, int K, const float* dV, i
                   const LoraSegs& S, const int32_t* perm, const void* base, void* out, float* dAp, int32_t* ad,
                   hipStream_t st) {
   typedef typename Elem<DT>::T E;
-  constexpr int lds = 8 * Tile<DT, WN>::BYTES + Small<DT, RT>::VT + Small<DT, RT>::VR + 32;
+  constexpr int lds = 8 * Tile<DT, WN>::BYTES + Small<DT, RT>::VT + Small<DT, RT>::VR + 32 +
+                      (DT == DT_F16 ? (RT <= 4 ? 1 : 2) * Tile<DT, WN>::ST * 4 : 0);
   auto kern = k_lora_xpass<DT, RT, WN, BLOCKS>;
   static std::atomic<uint64_t> done{0};
   const hipError_t e = lds_limit_once((const void*)kern, lds, done);

@@ -442,7 +442,7 @@ __global__ __launch_bounds__(512, 1) void k_lora_short(const typename Elem<DT>::
   extern __shared__ __attribute__((aligned(16))) char sm[];
   v4f(*red)[RT][64] = reinterpret_cast<v4f(*)[RT][64]>(sm);              // over the waves' stages, between their uses
   E* sv = reinterpret_cast<E*>(sm + 8 * STAGE);                          // [part][16][LD]
-  float* top8 = reinterpret_cast<float*>(sv + Mx<DT>::NC * 16 * LD);
+  float* tops = reinterpret_cast<float*>(sv + Mx<DT>::NC * 16 * LD);     // fp16: [RT][16], a wave's largest of each token
   const LoraTile tl = lora_tile(S, seg_lanes(S, T), blockIdx.x + 1, T, 16);
   const int n_tok = tl.t1 - tl.t0;
   if (n_tok <= 0) return;
@@ -473,7 +473,6 @@ __global__ __launch_bounds__(512, 1) void k_lora_short(const typename Elem<DT>::
   // thread: four tokens of one r
   v4f v = {};
   const int c = lane & 15, q = lane >> 4, r = 16 * wave + c;
-  float unit = 1.0f;
   if (wave < RT) {
 #pragma unroll
     for (int w = 0; w < 8; ++w) v += red[w][wave][lane];
@@ -483,17 +482,21 @@ __global__ __launch_bounds__(512, 1) void k_lora_short(const typename Elem<DT>::
       for (int e = 0; e < 4; ++e)
         if (4 * q + e < n_tok) V[(int64_t)(tl.t0 + 4 * q + e) * R + r] = v[e];
   }
-  if constexpr (DT == DT_F16) {
+  // fp16: the power of two of token t
+  auto unit_of = [&](int t) {
     float top = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      top = fmaxf(top, 4 * q + e < n_tok && __builtin_isfinite(v[e]) ? __builtin_fabsf(v[e]) : 0.0f);
-    top = wave_max(top);
-    if (lane == 0) top8[wave] = top;
-    __syncthreads();
+    for (int w = 0; w < RT; ++w) top = fmaxf(top, tops[16 * w + t]);
+    return unit_for(top);
+  };
+  if constexpr (DT == DT_F16) {
+    if (wave < RT)
 #pragma unroll
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, top8[w]);
-    unit = unit_for(top);
+      for (int e = 0; e < 4; ++e) {
+        const float top = lanes_max<16>(__builtin_isfinite(v[e]) ? __builtin_fabsf(v[e]) : 0.0f);
+        if (c == 0) tops[16 * wave + 4 * q + e] = top;
+      }
+    __syncthreads();
   }
   if (wave < RT) {
 #pragma unroll
@@ -502,7 +505,7 @@ __global__ __launch_bounds__(512, 1) void k_lora_short(const typename Elem<DT>::
       if constexpr (DT == DT_F32) {
         *o = v[e];
       } else {
-        const uint32_t h = split2<DT>(v[e], unit);
+        const uint32_t h = split2<DT>(v[e], DT == DT_F16 ? unit_of(4 * q + e) : 1.0f);
         o[0] = __builtin_bit_cast(E, (uint16_t)(h & 0xffffu));
         o[16 * LD] = __builtin_bit_cast(E, (uint16_t)(h >> 16));
       }
@@ -511,7 +514,7 @@ __global__ __launch_bounds__(512, 1) void k_lora_short(const typename Elem<DT>::
   __syncthreads();
   col.take_v(sv);
   col.f[0] = scale;
-  if constexpr (DT == DT_F16) col.f[0] *= inv_pow2(unit);
+  if constexpr (DT == DT_F16) col.f[0] *= inv_pow2(unit_of(c));
   col.all(g0, g1, 8, k);
 }
 
@@ -569,7 +572,7 @@ hipError_t run_short(const void* Xv, int T, int K, const void* Av, const void* B
   typedef typename Elem<DT>::T E;
   typedef Columns<DT, RT, 1, FULL> C;
   constexpr int stage = (1 + RT) * 2048 > C::LDS ? (1 + RT) * 2048 : C::LDS;
-  constexpr int lds = 8 * stage + Mx<DT>::NC * 16 * C::LD * (int)sizeof(E) + 32;
+  constexpr int lds = 8 * stage + Mx<DT>::NC * 16 * C::LD * (int)sizeof(E) + RT * 16 * 4;
   static std::atomic<uint64_t> done{0};
   const int tiles = lora_tiles(T, S, 16), groups = (N + C::GC - 1) / C::GC;
   // at most 256 workgroups, one a compute unit: a second round would compute V again
