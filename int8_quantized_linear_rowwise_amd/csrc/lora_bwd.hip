@@ -848,10 +848,22 @@ Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
   p.rt = rank_tiles(R);
   const int rp = 16 * p.rt;
   // Sorted by adapter there are as many partial sums as adapters instead of
-  // segments. Up to 64 segments are cheaper as they are: at 16 segments of four
-  // adapters (16384 tokens, 8192 -> 28672, rank 32) sorting took 13 us and the
-  // rows' indirection 45 us, against 25 us less in partial sums.
-  p.sort = n_seg > 64 && n_seg > n_adapters + 1;
+  // segments. The sort takes 13 us, and the rows' indirection slows the passes by
+  // some 0.15 us a MB of rows, so up to 64 segments are sorted where that saves
+  // more than 100 MB and 1.5 times the rows' own bytes (taken as 16-bit ones) of
+  // partial sums, written and read. As they are and sorted, even lengths and
+  // very uneven ones: 64 segments of 4096 tokens, 4096 -> 4096, rank 128, 4
+  // adapters (495 MB beside 134) 191 and 163 us, 342 and 182; 64 of 1024 tokens,
+  // 11008 -> 11008, rank 64, 4 adapters (665 beside 90) 240 and 91, 423 and 97.
+  // On the other side 64 of 8192 tokens, 4096 -> 4096, rank 128, 4 adapters (495
+  // beside 268) 255 and 281, 397 and 300; 64 of 4096 at rank 32 (124 beside 134)
+  // 72 and 88, 131 and 92; 32 of 16384 tokens, 8192 -> 28672, rank 32, 4 adapters
+  // (255 beside 1745), uneven, 454 and 754. More than 64 segments are always
+  // sorted: 200 of 4096 tokens, 4096 -> 4096, 4 adapters, uneven: 196 and 65 at
+  // rank 16, 496 and 129 at rank 64.
+  const double partial = 8.0 * ((double)n_seg - n_adapters - 1) * rp * ((double)K + N);
+  const double row_bytes = 2.0 * T * (N + 3.0 * K);
+  p.sort = n_seg > n_adapters + 1 && (n_seg > 64 || partial > 100e6 + 1.5 * row_bytes);
   const LoraSegs S = {nullptr, nullptr, p.sort ? n_adapters + 1 : n_seg, n_adapters};
   p.wide_g = (int64_t)cdiv(N, 8 * wide_g(p.rt)) * cdiv(T, 64) >= 256;
   p.wide_x = (int64_t)cdiv(K, 8 * wide_x(p.rt)) * cdiv(T, 64) >= 256;

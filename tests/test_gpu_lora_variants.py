@@ -98,8 +98,9 @@ def test_forward(I8, dt, R, columns, form):  # noqa: F811
 
 # rows, columns of the narrow side, segments, adapters: wide slices need (columns / slice) x (rows / 64) of 256 or
 # more, blocks of tiles several segments in a block
-PASSES = {"wide": (2048, 4096, 3, 2), "wide blocks": (4096, 4096, 40, 3), "wide sorted blocks": (4096, 4096, 200, 40),
-          "narrow": (300, 520, 3, 2), "narrow blocks": (6400, 1024, 60, 3), "narrow sorted": (3000, 1000, 300, 5)}
+PASSES = {"wide": (2048, 4096, 3, 2), "wide blocks": (4096, 4096, 40, 40), "wide sorted blocks": (4096, 4096, 200, 40),
+          "narrow": (300, 520, 3, 2), "narrow blocks": (6400, 1024, 60, 3), "narrow sorted": (3000, 1000, 300, 5),
+          "few sorted": (700, 4096, 50, 1)}
 
 
 @pytest.mark.parametrize("dt", DTS)
