@@ -838,9 +838,22 @@ int tile_tokens(int T, int slices, int rounds, int rp, int width, int n_seg) {
   return tm < 32 ? 32 : partial > 16 * 1000 * 1000 && tm < least ? least : tm;
 }
 
-// A workgroup for every tile where those run at once, or where the blocks are too few to fill the chip.
-bool one_tile_each(int tiles, int blocks, int slices, int rounds) {
-  return (int64_t)tiles * slices <= 280 * rounds || (int64_t)blocks * slices < 192 * rounds;
+// A workgroup for every tile, or one for a block of `tm` tokens that walks its
+// tiles. Blocks fill the chip evenly, but a block with many short tiles keeps
+// the others waiting. 4096 -> 4096, blocks and tiles, segments of even and of
+// very uneven lengths: blocks of less than 128 tokens lose (1024 tokens of 12
+// segments at rank 32 38 and 34 us, uneven 49 and 34, of 48 55 and 51, 94 and
+// 54; 4096 of 24 at rank 16 66 and 64, 75 and 58) but where every segment is a
+// block of its own and half the tiles are empty (4096 of 64 at rank 16 62 and
+// 73); so do those that leave compute units idle (2048 at rank 64, 128 blocks x
+// slices, of 12 segments 79 and 63, 102 and 62). From there on blocks win (4096
+// of 3 at rank 32 76 and 85; 8192 uneven of 6 113 and 127; 16384 of 16, 8192 ->
+// 28672, 418 and 483) but for many very uneven segments (8192 of 24 126 and 112,
+// of 48 142 and 128). Tiles that all run at once need no blocks: 264 workgroups
+// at rank 32, a few more than the units, take 75 us against 69, 528 at rank 16,
+// where a unit holds two, 69 against 71.
+bool one_tile_each(int tiles, int blocks, int slices, int rounds, int tm) {
+  return tm < 128 || (int64_t)tiles * slices <= (rounds == 1 ? 256 : 560) || (int64_t)blocks * slices < 192 * rounds;
 }
 
 Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
@@ -877,8 +890,8 @@ Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
   p.tiles_x = lora_tiles(T, S, p.tm_x);
   // few slices of a small batch: the x pass adds them up as it reads them, instead of a launch of its own (4 us)
   p.fold = !p.wide_x && p.slices > 1 && p.slices <= 8 && (int64_t)p.slices * T * rp * 4 * slices_x <= 4 * 1000 * 1000;
-  p.by_tile_g = one_tile_each(p.tiles_g, cdiv(T, p.tm_g), p.slices, rounds);
-  p.by_tile_x = one_tile_each(p.tiles_x, cdiv(T, p.tm_x), slices_x, rounds);
+  p.by_tile_g = one_tile_each(p.tiles_g, cdiv(T, p.tm_g), p.slices, rounds, p.tm_g);
+  p.by_tile_x = one_tile_each(p.tiles_x, cdiv(T, p.tm_x), slices_x, rounds, p.tm_x);
   p.kp = (K + 15) / 16 * 16;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -957,8 +970,9 @@ hipError_t backward_t(const Plan& p, const void* G, const void* X, const float* 
   if (rows && na > 0 && N > 0 && (want_dv || gB)) {
     float* P = !want_dv ? nullptr : p.slices > 1 ? ws + p.p : dV;
     float* dBp = gB ? ws + p.dbp : nullptr;
+    // (at rank 16 batches long enough for blocks of 128 tokens have wide slices)
     auto pass = p.wide_g ? (p.by_tile_g ? g_pass<DT, RT, wide_g(RT), false> : g_pass<DT, RT, wide_g(RT), true>)
-                         : (p.by_tile_g ? g_pass<DT, RT, 32, false> : g_pass<DT, RT, 32, true>);
+                         : (p.by_tile_g ? g_pass<DT, RT, 32, false> : g_pass<DT, RT, 32, (RT > 1)>);
     e = pass(p, G, V, T, B, scaling, R, N, S, perm, P, dBp, ad_g, st);
     if (e != hipSuccess) return e;
     if (want_dv && p.slices > 1 && !p.fold) {
@@ -983,7 +997,7 @@ hipError_t backward_t(const Plan& p, const void* G, const void* X, const float* 
     if (no_dv) Sx.n_adapters = 0;
     float* dAp = gA && na > 0 ? ws + p.dap : nullptr;
     auto pass = p.wide_x ? (p.by_tile_x ? x_pass<DT, RT, wide_x(RT), false> : x_pass<DT, RT, wide_x(RT), true>)
-                         : (p.by_tile_x ? x_pass<DT, RT, 32, false> : x_pass<DT, RT, 32, true>);
+                         : (p.by_tile_x ? x_pass<DT, RT, 32, false> : x_pass<DT, RT, 32, (RT > 1)>);
     e = pass(p, X, T, K, p.fold ? ws + p.p : dV, p.fold ? p.slices : 1, A, R, Sx, perm, base_grad, gX, dAp, ad_x, st);
     if (e != hipSuccess) return e;
   }
