@@ -95,6 +95,9 @@ inline int lora_tiles(int T, const LoraSegs& S, int tm) {
   return (T + tm - 1) / tm + (S.n_seg > 1 ? S.n_seg : 1) - 1;
 }
 
+// The rank's class, in parts of 16.
+inline int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
+
 // Workgroup `bid` of tiles * slices: the eight XCDs take workgroups in turn, so
 // each gets one run of neighbouring tiles, whose rows share an adapter more
 // often than not: its A and B then come through one L2 instead of all eight.

@@ -14,11 +14,12 @@
 // tokens, 4096 -> 11008 at rank 16: 27 + 6 + 28 + 6 us; 16384 tokens of 16
 // sequences, 8192 -> 28672 at rank 32: 235 + 40 + 167 + 7 us, of which the
 // partial sums (300 MB beside 1.77 GB of operands) are about a sixth.
-// A workgroup takes a slice of columns and a block of tokens, which it walks
-// tile by tile (the block's tokens of one adapter); its eight waves split the columns, and each holds its part of the weight
-// gradient in registers while it walks the tokens 32 (fp32: 16) at a time. The
-// rows go through LDS, from where they are read along the features for the one
-// product and transposed for the one along the tokens.
+// A workgroup takes a slice of columns and a token tile (tokens of one adapter),
+// or a block of tokens that it walks tile by tile; its eight waves split the
+// columns, and each holds its part of the weight gradient in registers while it
+// walks the tokens 32 (fp32: 16) at a time. The rows go through LDS, from where
+// they are read along the features for the one product and transposed for the
+// one along the tokens.
 #include "lora.hpp"
 
 namespace i8l {
@@ -820,7 +821,10 @@ struct Plan {
   size_t p, dv, dbp, dap, ad_g, ad_x, perm, starts, total;   // offsets in floats
 };
 
-int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
+// Columns of a wave in wide slices (narrow ones: 32), as many as its registers
+// hold beside the rank. 64 instead of 128 for the g pass of rank 17 to 32: 16384
+// tokens of 16 sequences, 8192 -> 28672, 436 us against 403, 4096 tokens, 4096
+// -> 11008 76 and 75, 4096 -> 4096 55 and 60.
 constexpr int wide_g(int rt) { return rt == 2 ? 128 : rt <= 4 ? 64 : 32; }
 constexpr int wide_x(int rt) { return rt <= 4 ? 64 : 32; }
 int cdiv(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
@@ -878,6 +882,12 @@ Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
   const double row_bytes = 2.0 * T * (N + 3.0 * K);
   p.sort = n_seg > n_adapters + 1 && (n_seg > 64 || partial > 100e6 + 1.5 * row_bytes);
   const LoraSegs S = {nullptr, nullptr, p.sort ? n_adapters + 1 : n_seg, n_adapters};
+  // Wide slices, fewer partial sums of dV, where 64-token tiles of them would
+  // fill the chip. bf16, the g pass wide and narrow: 4096 tokens, 4096 -> 11008,
+  // rank 64 99 and 112 us, rank 32 73 and 81, rank 16 62 and 62; 16384 tokens,
+  // 8192 -> 28672, rank 32 408 and 524. Both passes: 4096 -> 4096, ranks 16, 32
+  // and 64, 4096 tokens 52 61 75 and 46 56 72, 16384 tokens 147 153 183 and 136
+  // 151 196. Below the bound, 1024 tokens, 29 35 51 and 26 32 43.
   p.wide_g = (int64_t)cdiv(N, 8 * wide_g(p.rt)) * cdiv(T, 64) >= 256;
   p.wide_x = (int64_t)cdiv(K, 8 * wide_x(p.rt)) * cdiv(T, 64) >= 256;
   p.slices = cdiv(N, 8 * (p.wide_g ? wide_g(p.rt) : 32));
@@ -888,7 +898,12 @@ Plan plan_of(int T, int K, int N, int R, int n_adapters, int n_seg) {
   const int slices_x = cdiv(K, 8 * (p.wide_x ? wide_x(p.rt) : 32));
   p.tm_x = tile_tokens(T, slices_x > 0 ? slices_x : 1, rounds, rp, K, S.n_seg);
   p.tiles_x = lora_tiles(T, S, p.tm_x);
-  // few slices of a small batch: the x pass adds them up as it reads them, instead of a launch of its own (4 us)
+  // Few slices of a small batch: the x pass adds them up as it reads them, once
+  // a slice of its own, instead of a launch for it. With and without: 64 tokens,
+  // 1024 -> 1024, rank 16 12.8 and 15.2 us; 1024 tokens, 2048 -> 2048, rank 16
+  // (4 MB read) 21.3 and 23.4, rank 64 (17 MB) 60 and 41; 512 tokens, rank 64 (8
+  // MB) 31.8 and 30.4. More slices gain little: 16 of 64 tokens, 4096 -> 4096,
+  // rank 16 14.8 and 15.4, 43 of 1024 -> 11008 17.8 and 17.1.
   p.fold = !p.wide_x && p.slices > 1 && p.slices <= 8 && (int64_t)p.slices * T * rp * 4 * slices_x <= 4 * 1000 * 1000;
   p.by_tile_g = one_tile_each(p.tiles_g, cdiv(T, p.tm_g), p.slices, rounds, p.tm_g);
   p.by_tile_x = one_tile_each(p.tiles_x, cdiv(T, p.tm_x), slices_x, rounds, p.tm_x);

@@ -520,8 +520,6 @@ __global__ __launch_bounds__(512, 1) void k_lora_short(const typename Elem<DT>::
 
 namespace {
 
-int rank_tiles(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
-
 // 64-token tiles read B once for 64 tokens; they need segments that fill them.
 bool long_tiles(int T, int n_seg) { return T >= 1024 && T / 48 >= n_seg; }
 
