@@ -310,6 +310,9 @@ int int8_linear_backward_weight(const void* G, const void* A, int dtype, int64_t
  * two, and a value below 2^-22 of the largest of its set is off by up to 2^-39
  * of that one instead; the set is one row of V or dV for out and grad_X (no row
  * depends on another), and the rows of a tile for grad_A and grad_B.
+ * An infinity or NaN in an operand reaches the outputs that the formulas say
+ * and no others; with 16-bit operands an infinity in A, B, X or G can arrive as
+ * a NaN (it meets both parts of V or dV, one of which may be 0).
  *   X: T x K, out / base: T x N, A: n_adapters x R x K, B: n_adapters x N x R,
  *   G: T x N, grad_X / base_grad: T x K, all of `dtype`; grad_A, grad_B: as A
  *   and B; scaling: n_adapters fp32; V: T x R fp32.
