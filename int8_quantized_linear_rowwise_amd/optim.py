@@ -117,10 +117,13 @@ class AdamWPlan:
         self.table = host.to(self.device)
         self._stream = _raw_stream(self.gpu)
 
-    def _check_scalars(self, grad_scale, found_inf) -> None:
-        for name, x in (("grad_scale", grad_scale), ("found_inf", found_inf)):
-            if x is not None and (x.dtype != torch.float32 or x.numel() != 1 or x.get_device() != self.gpu):
-                raise ValueError(f"{name} must be one float32 value on {self.device}")
+    def _scalar(self, x: Optional[torch.Tensor], name: str) -> int:
+        """Device pointer of one of the step's two scalars, 0 for None."""
+        if x is None:
+            return 0
+        if x.dtype != torch.float32 or x.numel() != 1 or x.get_device() != self.gpu:
+            raise ValueError(f"{name} must be one float32 value on {self.device}")
+        return x.data_ptr()
 
     def step(self, step: int, lr: float, betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
              weight_decay: float = 0.01, grad_scale: Optional[torch.Tensor] = None,
@@ -129,15 +132,13 @@ class AdamWPlan:
         scalar, anything but 0 leaves all tensors as they are (the caller's step count goes on). A captured step keeps
         its numbers; only the two scalars are read at each replay: the caller keeps them, and the plan, as long
         as the graph."""
-        if grad_scale is not None or found_inf is not None:
-            self._check_scalars(grad_scale, found_inf)
+        scale, inf = self._scalar(grad_scale, "grad_scale"), self._scalar(found_inf, "found_inf")
         stream = _raw_stream(self.gpu)
         if stream != self._stream:     # the table's memory is not given away before this stream is done with it
             self.table.record_stream(torch.cuda.current_stream(self.device))
         with _on_gpu(self.gpu):
             check(lib.int8_adamw_step(self.table.data_ptr(), self.count, self.chunks, lr, betas[0], betas[1], eps,
-                                      weight_decay, step, 0 if grad_scale is None else grad_scale.data_ptr(),
-                                      0 if found_inf is None else found_inf.data_ptr(), stream),
+                                      weight_decay, step, scale, inf, stream),
                   "int8_adamw_step")
 
 
@@ -211,7 +212,7 @@ class AdamW(torch.optim.Optimizer):
                     # every step compares the addresses: old gradients need not be held (their memory is the next
                     # backward pass's where zero_grad drops them)
                     held[1]._keep = None
-                held[1]._check_scalars(grad_scale, found_inf)
+                held[1]._scalar(grad_scale, "grad_scale"), held[1]._scalar(found_inf, "found_inf")
                 live[key] = held
                 due.append((held[1], step, group, rows))
         for plan, step, group, rows in due:
