@@ -147,7 +147,8 @@ class AdamW(torch.optim.Optimizer):
 
     state_bits: 32 or 8; master: keep fp32 copies of fp16 / bf16 parameters.
     The plan of a group is laid out again whenever a gradient or parameter has
-    moved (gradients kept in place with zero_grad(set_to_none=False) never do).
+    moved (gradients kept in place with zero_grad(set_to_none=False) never do): a
+    step of 448 tensors takes the host 0.5 ms, 2.3 ms where it is laid out again.
     Parameters and gradients have to be contiguous. A captured step keeps its
     step number and learning rate; what it uses is held as long as the optimizer.
     One ordinary step with the same gradients comes before a capture: it makes the
