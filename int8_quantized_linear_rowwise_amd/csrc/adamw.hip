@@ -9,8 +9,8 @@
 // Bound by memory. A workgroup takes 2048 values of one tensor, 8 a thread, so
 // that bf16 moves 16 bytes a lane and a block of 256 8-bit states is half a
 // wave's; it finds its tensor through a table, so any number of tensors is one
-// launch. 202 M bf16 values with 32-bit states: 798 us, 5.6 TB/s; 41 M in 448
-// tensors with 8-bit states and fp32 masters: 120 us, 5.5 TB/s (a large copy
+// launch. 202 M bf16 values with 32-bit states: 777 us, 5.7 TB/s; 41 M in 448
+// tensors with 8-bit states and fp32 masters: 117 us, 5.4 TB/s (a large copy
 // reaches 4.8 to 5.4).
 //
 // 8-bit states: blocks of 256 values, each with one scale; codes are e4m3.
