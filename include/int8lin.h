@@ -430,6 +430,109 @@ int int8_adamw_step(const void* table, int64_t count, int64_t chunks, double lr,
                     double eps, double weight_decay, int64_t step, const float* grad_scale, const float* found_inf,
                     void* stream);
 
+/* ------------------------------------------------------------------------ *
+ * Norm of all gradients, the factor that clips them, and the clipping: what
+ * int8_adamw_step takes as grad_scale and found_inf. With c = *grad_scale (1
+ * where it is NULL):
+ *   norm      = |c| sqrt(sum over all tensors of g^2)      (norm_type 2)
+ *             = |c| max |g|                                (norm_type I8L_NORM_INF)
+ *   factor    = c min(1, max_norm / (norm + 1e-6))
+ *   found_inf = 1 where norm is not finite in fp32, else 0
+ * so that factor g are the unscaled, clipped gradients (found_inf 1: a step with
+ * them is to be left out). Squares and sums are formed in 64 bits, in a fixed
+ * order. A norm of NaN gives the factor NaN, an infinite one 0. max_norm = +inf:
+ * no clipping, factor = c. clip != 0 also writes g = D(factor g) into every
+ * tensor (nothing is written where factor is 1); the factor has then been
+ * applied.
+ * The list is read on the host during the call and travels with the launches:
+ * no table on the device, nothing kept between calls. A captured call keeps the
+ * addresses and max_norm; grad_scale is read at each replay. norm, factor and
+ * found_inf: one fp32 each on the device, none NULL. count = 0 is fine (norm 0).
+ * With clip no two tensors may overlap. A norm_type that is neither, or a
+ * max_norm that is negative or NaN, is I8L_EINVAL; more than 2^42 values in one
+ * launch's 160 tensors are I8L_ESHAPE.
+ * ------------------------------------------------------------------------ */
+#define I8L_NORM_INF 0
+
+typedef struct {
+  void* g;           /* n of dtype */
+  int64_t n;
+  int32_t dtype;
+  int32_t reserved;  /* 0 */
+} i8l_grad_tensor;
+
+size_t int8_grad_norm_workspace_bytes(const i8l_grad_tensor* grads, int64_t count);
+int int8_grad_norm(const i8l_grad_tensor* grads, int64_t count, int norm_type, double max_norm,
+                   const float* grad_scale, int clip, float* norm, float* factor, float* found_inf, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * Experts: a mixture whose projections are frozen in int8. Every token goes to
+ * k of n_experts experts; the R = T k choices, sorted by expert, are the rows
+ * of the products. Segments are as the adapters have them: segment j holds rows
+ * seg_offsets[j] .. seg_offsets[j + 1] - 1 (the first offset is taken as 0) and
+ * uses expert seg_expert[j] (NULL: expert j). Rows behind the last offset, and
+ * rows of a segment whose expert lies outside [0, n_experts), have none: their
+ * outputs are 0. seg_offsets: n_seg + 1 int32 on the device, non-decreasing;
+ * contents that are not give undefined values but no access outside the
+ * tensors. Offsets and indices are only read on the device: no call waits.
+ *
+ * Sort of T x k choices (int32 or int64: id_bytes 4 or 8), stable by expert:
+ *   seg_offsets[e] = choices of experts below e          (n_experts + 1)
+ *   row_token[r]   = the token of row r, -1 behind the last routed row  (T k)
+ *   position[t, j] = the row of choice (t, j), -1 for one outside
+ *                    [0, n_experts), which is not routed  (T x k)
+ * n_experts <= I8L_SORT_MAX_EXPERTS, T k <= 2^24, else I8L_ESHAPE.
+ * ------------------------------------------------------------------------ */
+#define I8L_SORT_MAX_EXPERTS 1024
+
+size_t int8_expert_sort_workspace_bytes(int64_t T, int64_t k, int64_t n_experts);
+int int8_expert_sort(const void* experts, int id_bytes, int64_t T, int64_t k, int64_t n_experts,
+                     int32_t* seg_offsets, int32_t* row_token, int32_t* position, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Products. X (T x K) is quantized once, row by row, with the outlier columns of
+ * all its rows as in int8_linear_forward; row r is token t = rows[r] (NULL: r,
+ * then R = T) of expert e:
+ *   out[r, n] = D(C32 * SCA[t] * SCB[e, n] / 127^2 + sum_j subA[t, j] * Wdq[e, n, O[j]])
+ * with C32 = sum_k CA[t, k] * CB[e, n, k] exact in int32 and fp32 accumulation.
+ * CB: n_experts x N x K int8, SCB: n_experts x N fp32 (int8_quantize_rowwise of
+ * the n_experts N rows, tau off). rows: R int32 on the device; a value outside
+ * [0, T) makes a row of zeros, and a token may be named any number of times.
+ * out: R x N of `dtype`. K <= I8L_MAX_K, N <= I8L_MAX_COLS, T, R <= 2^24,
+ * n_seg, n_experts <= 65536, else I8L_ESHAPE.
+ *
+ * Input gradient (the weights are frozen): grad_X[r, k] = D(sum_n fp16(G[r, n]) *
+ * Wdq[e, n, k]), R rows; the rows of a token are added up by int8_expert_combine
+ * with gate = NULL. */
+size_t int8_expert_forward_workspace_bytes(int64_t T, int64_t K);
+int int8_expert_forward(const void* X, int dtype, int64_t T, int64_t K, const int32_t* rows, int64_t R,
+                        const int8_t* CB, const float* SCB, int64_t n_experts, int64_t N,
+                        const int32_t* seg_offsets, const int32_t* seg_expert, int64_t n_seg, float threshold,
+                        void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+int int8_expert_backward(const void* G, int dtype, int64_t R, int64_t N, const int8_t* CB, const float* SCB,
+                         int64_t n_experts, int64_t K, const int32_t* seg_offsets, const int32_t* seg_expert,
+                         int64_t n_seg, void* grad_X, void* stream);
+
+/* Weighted sum of each token's rows (Y: R x N of `dtype`), in the order of j:
+ *   out[t] = D(base[t] + sum_j gate[t, j] Y[position[t, j]])     (fp32 accumulate)
+ * gate: T x k fp32, NULL for 1; base: T x N or NULL for 0, may be out itself. A
+ * position outside [0, R) is left out, whatever its gate.
+ * Gradients:
+ *   grad_Y[position[t, j]] = D(gate[t, j] G[t])
+ *   grad_gate[t, j]        = sum_n G[t, n] Y[position[t, j], n]      (fp32)
+ * grad_Y, grad_gate may each be NULL (not computed); Y is read for grad_gate
+ * only. No two positions may name the same row. Rows of grad_Y that no position
+ * names are left as they were, but with n_rows (one int32 on the device: the
+ * sort's last offset) the rows from *n_rows on get 0. grad_gate is 0 where the
+ * position is left out. k <= 64, N <= I8L_MAX_COLS, T, R <= 2^24, else I8L_ESHAPE. */
+int int8_expert_combine(const void* Y, int dtype, int64_t R, int64_t N, const int32_t* position, const float* gate,
+                        const void* base, int64_t T, int64_t k, void* out, void* stream);
+int int8_expert_combine_backward(const void* G, int dtype, int64_t T, int64_t N, const int32_t* position,
+                                 const float* gate, int64_t k, const void* Y, int64_t R, const int32_t* n_rows,
+                                 void* grad_Y, float* grad_gate, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

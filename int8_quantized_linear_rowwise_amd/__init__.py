@@ -31,7 +31,9 @@ __all__ = [
     "forward_check", "default_cap", "int8_linear_forward_noalloc", "DTYPE_CODE", "I8L_MAX_K",
     "lora_forward", "lora_backward", "Int8LoraFunction", "Int8LoraLinear", "I8L_LORA_MAX_RANK",
     "layer_norm_forward", "layer_norm_backward", "LayerNormFunction", "LayerNorm",
-    "AdamWPlan", "AdamW", "adamw_state",
+    "AdamWPlan", "AdamW", "adamw_state", "GradNormPlan", "clip_grad_norm_",
+    "expert_sort", "expert_forward", "expert_backward", "expert_combine", "expert_combine_backward",
+    "Int8ExpertsFunction", "ExpertCombineFunction", "Int8Experts", "I8L_SORT_MAX_EXPERTS",
 ]
 
 # ----------------------------------------------------------------------------
@@ -437,4 +439,7 @@ class Int8LinearTrainable(torch.nn.Module):
 
 from .lora import I8L_LORA_MAX_RANK, Int8LoraFunction, Int8LoraLinear, lora_backward, lora_forward  # noqa: E402
 from .norm import LayerNorm, LayerNormFunction, layer_norm_backward, layer_norm_forward  # noqa: E402
+from .grad_norm import GradNormPlan, clip_grad_norm_  # noqa: E402
 from .optim import AdamW, AdamWPlan, adamw_state  # noqa: E402
+from .experts import (I8L_SORT_MAX_EXPERTS, ExpertCombineFunction, Int8Experts, Int8ExpertsFunction,  # noqa: E402
+                      expert_backward, expert_combine, expert_combine_backward, expert_forward, expert_sort)

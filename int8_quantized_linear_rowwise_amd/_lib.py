@@ -18,6 +18,8 @@ I8L_NOALLOC_SCRATCH_BYTES = 64 << 20
 I8L_MAX_K = 133144
 I8L_MAX_COLS = 262144
 I8L_LORA_MAX_RANK = 128
+I8L_SORT_MAX_EXPERTS = 1024
+I8L_NORM_INF = 0
 
 # every symbol the header declares, with (restype, argtypes)
 _vp, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
@@ -33,6 +35,10 @@ class ForwardLayout(ctypes.Structure):
 class AdamWTensor(ctypes.Structure):
     _fields_ = [("p", _vp), ("g", _vp), ("m", _vp), ("v", _vp), ("m_scale", _vp), ("v_scale", _vp), ("master", _vp),
                 ("n", _i64), ("dtype", _i32), ("state_bits", _i32)]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("g", _vp), ("n", _i64), ("dtype", _i32), ("reserved", _i32)]
 
 
 SIGNATURES = {
@@ -71,6 +77,16 @@ SIGNATURES = {
     "int8_adamw_table_bytes": (_sz, [ctypes.POINTER(AdamWTensor), _i64]),
     "int8_adamw_table_fill": (_int, [ctypes.POINTER(AdamWTensor), _i64, _vp, _sz, ctypes.POINTER(_i64)]),
     "int8_adamw_step": (_int, [_vp, _i64, _i64, _f64, _f64, _f64, _f64, _f64, _i64, _vp, _vp, _vp]),
+    "int8_grad_norm_workspace_bytes": (_sz, [_vp, _i64]),
+    "int8_grad_norm": (_int, [_vp, _i64, _int, _f64, _vp, _int, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "int8_expert_sort_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "int8_expert_sort": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "int8_expert_forward_workspace_bytes": (_sz, [_i64, _i64]),
+    "int8_expert_forward": (_int, [_vp, _int, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _f32, _vp,
+                                   _vp, _sz, _vp]),
+    "int8_expert_backward": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp]),
+    "int8_expert_combine": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp]),
+    "int8_expert_combine_backward": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]),
 }
 
 

@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libint8lin.so")
 BUILD = os.path.join(PKG, "_build")
 SOURCES = ["api.hip", "quantize.hip", "gemm_fwd.hip", "gemm_bwd.hip", "gemm_wgrad.hip",
-           "api_finetune.hip", "lora_fwd.hip", "lora_bwd.hip", "layer_norm.hip", "adamw.hip"]
+           "api_finetune.hip", "lora_fwd.hip", "lora_bwd.hip", "layer_norm.hip", "adamw.hip",
+           "api_experts.hip", "expert_route.hip", "expert_fwd.hip", "expert_bwd.hip", "grad_norm.hip"]
 PEAKS_SRC = "peaks.hip"
 PEAKS_OUT = os.path.join(PKG, "libi8lpeaks.so")
 

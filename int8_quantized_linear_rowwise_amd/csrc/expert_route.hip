@@ -1,0 +1,396 @@
+// Tokens to their experts' rows and back: a stable sort by expert, the weighted
+// sum of each token's rows, and the gradients of that sum.
+#include "expert.hpp"
+
+namespace i8l {
+
+// ---------------------------------------------------------------------------
+// Sort. The R choices are cut into blocks and each block's into one run per
+// wave. Counting goes through LDS atomics (integers: their order is nothing to
+// the result). The place of a choice among those of its expert in the same 64
+// is the number of earlier lanes with the same expert, found by one ballot for
+// each bit of the number; the wave's own cursor for the expert holds the rest,
+// so the sort is stable and the result the same on every run.
+//
+// Bound by launches and by the chains of dependent LDS accesses. One workgroup
+// takes up to 2048 choices in one launch; more take a launch that counts and
+// one that places, in which every workgroup adds up the counts of the others
+// itself instead of waiting for a third.
+constexpr int SORT_WAVES = 8;
+constexpr int SORT_BLOCK = 2048;       // choices of a workgroup, more where there would be over 256 workgroups
+constexpr int SORT_MAX_BLOCKS = 256;
+
+static int sort_per_block(int64_t R) {
+  const int64_t most = (R + SORT_MAX_BLOCKS - 1) / SORT_MAX_BLOCKS;
+  return (int)((most > SORT_BLOCK ? most : SORT_BLOCK) + 511) / 512 * 512;
+}
+static int sort_blocks(int64_t R) {
+  const int pb = sort_per_block(R);
+  return (int)((R + pb - 1) / pb);
+}
+size_t expert_sort_ints(int64_t R, int n_experts) {
+  const int b = sort_blocks(R);
+  return b > 1 ? (size_t)b * (size_t)n_experts : 0;
+}
+
+template <typename ID>
+__device__ __forceinline__ int expert_id(const ID* __restrict__ ids, int i, int E) {
+  const ID v = ids[i];
+  return (v >= 0 && v < (ID)E) ? (int)v : -1;
+}
+
+// Counts of the block's choices by wave and expert, in LDS.
+template <typename ID>
+__device__ __forceinline__ void count_ids(const ID* __restrict__ ids, int lo, int hi, int E, int32_t* hist) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < SORT_WAVES * E; i += 64 * SORT_WAVES) hist[i] = 0;
+  __syncthreads();
+  for (int i = lo + lane; i < hi; i += 64) {
+    const int e = expert_id(ids, i, E);
+    if (e >= 0) atomicAdd(&hist[wave * E + e], 1);
+  }
+  __syncthreads();
+}
+
+template <typename ID>
+__global__ __launch_bounds__(64 * SORT_WAVES) void k_expert_count(const ID* __restrict__ ids, int R, int E,
+                                                                  int per_block, int32_t* __restrict__ counts) {
+  extern __shared__ int32_t hist[];
+  const int run = per_block / SORT_WAVES, wave = threadIdx.x >> 6;
+  const int64_t b0 = (int64_t)blockIdx.x * per_block;
+  const int lo = (int)min((int64_t)R, b0 + (int64_t)wave * run);
+  const int hi = (int)min((int64_t)R, b0 + (int64_t)(wave + 1) * run);
+  count_ids(ids, lo, hi, E, hist);
+  for (int e = threadIdx.x; e < E; e += 64 * SORT_WAVES) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < SORT_WAVES; ++w) n += hist[w * E + e];
+    counts[(int64_t)blockIdx.x * E + e] = n;
+  }
+}
+
+template <typename ID>
+__global__ __launch_bounds__(64 * SORT_WAVES) void k_expert_place(const ID* __restrict__ ids, int R, int k, int E,
+                                                                  int per_block, const int32_t* __restrict__ counts,
+                                                                  int32_t* __restrict__ off,
+                                                                  int32_t* __restrict__ token,
+                                                                  int32_t* __restrict__ position) {
+  extern __shared__ int32_t hist[];                // [SORT_WAVES][E], then one total a wave
+  int32_t* sums = hist + SORT_WAVES * E;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int run = per_block / SORT_WAVES;
+  const int64_t b0 = (int64_t)blockIdx.x * per_block;
+  const int lo = (int)min((int64_t)R, b0 + (int64_t)wave * run);
+  const int hi = (int)min((int64_t)R, b0 + (int64_t)(wave + 1) * run);
+  count_ids(ids, lo, hi, E, hist);
+
+  // per expert: rows of all blocks, and of the blocks before this one
+  int carry = 0;                                   // rows of the experts of earlier passes
+  for (int e0 = 0; e0 < E; e0 += 64 * SORT_WAVES) {
+    const int e = e0 + tid;
+    int all = 0, before = 0, mine = 0;
+    if (e < E) {
+#pragma unroll
+      for (int w = 0; w < SORT_WAVES; ++w) mine += hist[w * E + e];
+      if (counts) {
+        for (int b = 0; b < (int)gridDim.x; ++b) {
+          const int c = counts[(int64_t)b * E + e];
+          all += c;
+          before += b < (int)blockIdx.x ? c : 0;
+        }
+      } else {
+        all = mine;
+      }
+    }
+    int incl = all;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, 64);
+      incl += lane >= o ? v : 0;
+    }
+    if (lane == 63) sums[wave] = incl;
+    __syncthreads();
+    int first = carry, total = 0;
+#pragma unroll
+    for (int w = 0; w < SORT_WAVES; ++w) {
+      const int v = sums[w];
+      first += w < wave ? v : 0;
+      total += v;
+    }
+    first += incl - all;
+    if (e < E) {
+      if (blockIdx.x == 0) off[e] = first;
+      int at = first + before;
+#pragma unroll
+      for (int w = 0; w < SORT_WAVES; ++w) {       // counts become the waves' cursors
+        const int n = hist[w * E + e];
+        hist[w * E + e] = at;
+        at += n;
+      }
+    }
+    carry += total;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && tid == 0) off[E] = carry;
+  // rows behind the last routed one
+  for (int64_t r = (int64_t)carry + blockIdx.x * (64 * SORT_WAVES) + tid; r < R;
+       r += (int64_t)gridDim.x * (64 * SORT_WAVES))
+    token[r] = -1;
+
+  const int bits = 32 - __clz(E);                  // of the numbers 0 .. E
+  volatile int32_t* cursor = hist + wave * E;
+  for (int i0 = lo; i0 < hi; i0 += 64) {
+    const int i = i0 + lane;
+    const int e = i < hi ? expert_id(ids, i, E) : -1;
+    const int key = e < 0 ? E : e;
+    uint64_t same = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t m = __ballot((key >> b) & 1);
+      same &= ((key >> b) & 1) ? m : ~m;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    int row = -1;
+    if (e >= 0) row = cursor[e] + rank;
+    __builtin_amdgcn_wave_barrier();               // every lane has read before the last one of each expert writes
+    if (e >= 0 && rank == __popcll(same) - 1) cursor[e] = row + 1;
+    __builtin_amdgcn_wave_barrier();
+    if (i < hi) {
+      position[i] = row;
+      if (row >= 0) token[row] = i / k;
+    }
+  }
+}
+
+template <typename ID>
+static hipError_t launch_sort_t(const ID* ids, int R, int k, int E, int32_t* off, int32_t* token, int32_t* position,
+                                int32_t* scratch, hipStream_t st) {
+  const int blocks = R > 0 ? sort_blocks(R) : 1, pb = sort_per_block(R);
+  const size_t lds = ((size_t)SORT_WAVES * E + SORT_WAVES) * sizeof(int32_t);
+  if (blocks > 1)
+    hipLaunchKernelGGL(k_expert_count<ID>, dim3(blocks), dim3(64 * SORT_WAVES), lds, st, ids, R, E, pb, scratch);
+  hipLaunchKernelGGL(k_expert_place<ID>, dim3(blocks), dim3(64 * SORT_WAVES), lds, st, ids, R, k, E, pb,
+                     blocks > 1 ? scratch : nullptr, off, token, position);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_sort(const void* experts, int id_bytes, int R, int k, int n_experts, int32_t* off,
+                              int32_t* token, int32_t* position, int32_t* scratch, hipStream_t st) {
+  if (id_bytes == 8)
+    return launch_sort_t(static_cast<const int64_t*>(experts), R, k, n_experts, off, token, position, scratch, st);
+  return launch_sort_t(static_cast<const int32_t*>(experts), R, k, n_experts, off, token, position, scratch, st);
+}
+
+// ---------------------------------------------------------------------------
+// Weighted sum. A thread takes 8 columns of one token and adds its k rows in
+// order, in fp32, then rounds once. Bound by memory: every row is read once.
+
+template <int DT>
+__device__ __forceinline__ void cld(const typename Elem<DT>::T* __restrict__ p, int n, bool vec, float (&f)[8]) {
+  typename Elem<DT>::T e[8];
+  if (vec) {
+    load8<DT>(p, e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = Elem<DT>::to_f32(e[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = j < n ? Elem<DT>::to_f32(p[j]) : 0.0f;
+  }
+}
+template <int DT>
+__device__ __forceinline__ void cst(typename Elem<DT>::T* __restrict__ p, int n, bool vec, const float (&f)[8]) {
+  if (vec) {
+    if constexpr (DT == DT_F32) {
+      reinterpret_cast<v4f*>(p)[0] = v4f{f[0], f[1], f[2], f[3]};
+      reinterpret_cast<v4f*>(p)[1] = v4f{f[4], f[5], f[6], f[7]};
+    } else {
+      v4u w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = (uint32_t)__builtin_bit_cast(uint16_t, Elem<DT>::from_f32(f[2 * j])) |
+               ((uint32_t)__builtin_bit_cast(uint16_t, Elem<DT>::from_f32(f[2 * j + 1])) << 16);
+      *reinterpret_cast<v4u*>(p) = w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) p[j] = Elem<DT>::from_f32(f[j]);
+  }
+}
+
+// Workgroups of 256 threads as (256 / tx) tokens by tx chunks of 8 columns.
+template <int DT, bool VEC>
+__global__ __launch_bounds__(256) void k_expert_combine(const typename Elem<DT>::T* __restrict__ Y, int R, int N,
+                                                        const int32_t* __restrict__ position,
+                                                        const float* __restrict__ gate,
+                                                        const typename Elem<DT>::T* base, int T, int k, int txs,
+                                                        typename Elem<DT>::T* out) {
+  const int tx = threadIdx.x & ((1 << txs) - 1), ty = threadIdx.x >> txs;
+  const int t = blockIdx.x * (256 >> txs) + ty;
+  const int c = (blockIdx.y * (1 << txs) + tx) * 8;
+  if (t >= T || c >= N) return;
+  const int n = min(8, N - c);
+  float s[8] = {};
+  if (base) cld<DT>(base + (int64_t)t * N + c, n, VEC, s);
+  const int32_t* pos = position + (int64_t)t * k;
+  const float* gt = gate ? gate + (int64_t)t * k : nullptr;
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    float f[4][8], w[4];
+    bool has[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = j0 + u < k ? pos[j0 + u] : -1;
+      has[u] = r >= 0 && r < R;
+      w[u] = has[u] ? (gt ? gt[j0 + u] : 1.0f) : 0.0f;
+      if (has[u]) cld<DT>(Y + (int64_t)r * N + c, n, VEC, f[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (has[u]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = __builtin_fmaf(w[u], f[u][e], s[e]);
+      }
+  }
+  cst<DT>(out + (int64_t)t * N + c, n, VEC, s);
+}
+
+template <int DT>
+static hipError_t launch_combine_t(const void* Y, int R, int N, const int32_t* position, const float* gate,
+                                   const void* base, int T, int k, void* out, hipStream_t st) {
+  typedef typename Elem<DT>::T E;
+  const bool vec = N % 8 == 0 && (((uintptr_t)Y | (uintptr_t)base | (uintptr_t)out) % 16 == 0);
+  const int chunks = (N + 7) / 8;
+  int txs = 3;
+  while (txs < 8 && (1 << txs) < chunks) ++txs;
+  const dim3 grid((unsigned)((T + (256 >> txs) - 1) / (256 >> txs)), (unsigned)((chunks + (1 << txs) - 1) >> txs));
+  auto kern = vec ? k_expert_combine<DT, true> : k_expert_combine<DT, false>;
+  hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, static_cast<const E*>(Y), R, N, position, gate,
+                     static_cast<const E*>(base), T, k, txs, static_cast<E*>(out));
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_combine(int dt, const void* Y, int R, int N, const int32_t* position, const float* gate,
+                                 const void* base, int T, int k, void* out, hipStream_t st) {
+  if (dt == DT_F32) return launch_combine_t<DT_F32>(Y, R, N, position, gate, base, T, k, out, st);
+  if (dt == DT_F16) return launch_combine_t<DT_F16>(Y, R, N, position, gate, base, T, k, out, st);
+  return launch_combine_t<DT_BF16>(Y, R, N, position, gate, base, T, k, out, st);
+}
+
+// ---------------------------------------------------------------------------
+// Its gradients. A wave or a workgroup takes one token: each 8 columns of G are
+// read once for four rows at a time, whose products with Y stay in registers
+// until the end of the row; the gradient of each row is written as it is
+// formed. Sums run in a fixed order. The last ZERO_BLOCKS workgroups write
+// zeros into the rows behind the last routed one.
+constexpr int ZERO_BLOCKS = 256;
+
+template <int DT, bool VEC, int TT>   // TT threads a token: 64 or 256
+__global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<DT>::T* __restrict__ G, int T, int N,
+                                                            const int32_t* __restrict__ position,
+                                                            const float* __restrict__ gate, int k,
+                                                            const typename Elem<DT>::T* __restrict__ Y, int R,
+                                                            const int32_t* __restrict__ n_rows,
+                                                            typename Elem<DT>::T* __restrict__ gY,
+                                                            float* __restrict__ ggate) {
+  constexpr int PER = 256 / TT;
+  const int blocks = (T + PER - 1) / PER;
+  if ((int)blockIdx.x >= blocks) {
+    const int64_t from = min(max(n_rows[0], 0), R);
+    const float zero[8] = {};
+    const int chunks = (N + 7) / 8;
+    const int64_t items = (R - from) * (int64_t)chunks;
+    for (int64_t i = (int64_t)(blockIdx.x - blocks) * 256 + threadIdx.x; i < items; i += (int64_t)ZERO_BLOCKS * 256) {
+      const int64_t r = i / chunks;
+      const int c = (int)(i - r * chunks) * 8;
+      cst<DT>(gY + (from + r) * N + c, min(8, N - c), VEC, zero);
+    }
+    return;
+  }
+  __shared__ float part[4][4];
+  const int tid = threadIdx.x % TT, t = (int)blockIdx.x * PER + threadIdx.x / TT;
+  const bool live = t < T;
+  const int32_t* pos = position + (int64_t)(live ? t : 0) * k;
+  const float* gt = gate ? gate + (int64_t)(live ? t : 0) * k : nullptr;
+  const typename Elem<DT>::T* g = G + (int64_t)(live ? t : 0) * N;
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    int64_t row[4];
+    float w[4], dot[4] = {};
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = live && j0 + u < k ? pos[j0 + u] : -1;
+      row[u] = (r >= 0 && r < R) ? (int64_t)r * N : -1;
+      w[u] = row[u] >= 0 ? (gt ? gt[j0 + u] : 1.0f) : 0.0f;
+    }
+    for (int c = tid * 8; c < N; c += TT * 8) {
+      const int n = min(8, N - c);
+      float f[8];
+      cld<DT>(g + c, n, VEC, f);
+      float y[4][8];
+      if (ggate) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (row[u] >= 0) cld<DT>(Y + row[u] + c, n, VEC, y[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (row[u] >= 0) {
+          if (gY) {
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = w[u] * f[e];
+            cst<DT>(gY + row[u] + c, n, VEC, o);
+          }
+          if (ggate) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot[u] = __builtin_fmaf(f[e], y[u][e], dot[u]);
+          }
+        }
+    }
+    if (ggate) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) dot[u] += __shfl_xor(dot[u], o, 64);
+      if constexpr (TT == 256) {
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) part[threadIdx.x >> 6][u] = dot[u];
+        __syncthreads();
+        if (tid < 4 && j0 + tid < k)
+          ggate[(int64_t)t * k + j0 + tid] = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+        __syncthreads();
+      } else if (live && tid == 0) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (j0 + u < k) ggate[(int64_t)t * k + j0 + u] = dot[u];
+      }
+    }
+  }
+}
+
+template <int DT, int TT>
+static hipError_t launch_combine_bwd_t(const void* G, int T, int N, const int32_t* position, const float* gate, int k,
+                                       const void* Y, int R, const int32_t* n_rows, void* gY, float* ggate,
+                                       hipStream_t st) {
+  typedef typename Elem<DT>::T E;
+  const bool vec = N % 8 == 0 && (((uintptr_t)G | (uintptr_t)Y | (uintptr_t)gY) % 16 == 0);
+  const unsigned blocks = (unsigned)((T + 256 / TT - 1) / (256 / TT)) + (n_rows && gY ? ZERO_BLOCKS : 0);
+  if (blocks == 0) return hipSuccess;
+  auto kern = vec ? k_expert_combine_bwd<DT, true, TT> : k_expert_combine_bwd<DT, false, TT>;
+  hipLaunchKernelGGL(kern, dim3(blocks), dim3(256), 0, st, static_cast<const E*>(G), T, N, position, gate, k,
+                     static_cast<const E*>(Y), R, n_rows, static_cast<E*>(gY), ggate);
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_combine_bwd(int dt, const void* G, int T, int N, const int32_t* position, const float* gate,
+                                     int k, const void* Y, int R, const int32_t* n_rows, void* gY, float* ggate,
+                                     hipStream_t st) {
+#define I8L_CB(D)                                                                                           \
+  return N <= 1024 ? launch_combine_bwd_t<D, 64>(G, T, N, position, gate, k, Y, R, n_rows, gY, ggate, st)   \
+                   : launch_combine_bwd_t<D, 256>(G, T, N, position, gate, k, Y, R, n_rows, gY, ggate, st)
+  if (dt == DT_F32) I8L_CB(DT_F32);
+  if (dt == DT_F16) I8L_CB(DT_F16);
+  I8L_CB(DT_BF16);
+#undef I8L_CB
+}
+
+}  // namespace i8l

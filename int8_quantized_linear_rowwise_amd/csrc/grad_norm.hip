@@ -1,0 +1,225 @@
+// Norm of all gradients, the factor that clips them, and the clipping.
+//
+//   norm = c sqrt(sum g^2)  or  c max |g|,   c = *grad_scale (1 without)
+//   factor = c min(1, max_norm / (norm + 1e-6)),   found_inf = norm is not finite
+// Squares are formed and added in 64 bits, so that no finite gradient overflows
+// or vanishes and the sum of any number of values keeps fp32's 24 bits. (The
+// chip's 64-bit vector rate is half its 32-bit rate, far over what memory
+// delivers.) Workgroups add up their chunks in a fixed order, one more
+// workgroup the workgroups' sums: the result is the same on every run.
+//
+// Bound by memory. The list of tensors travels in the kernels' arguments and
+// is put into LDS by every workgroup, so a call needs no table on the device:
+// nothing to lay out, nothing to keep between calls.
+#include <type_traits>
+
+#include "common.hpp"
+#include "kernels.hpp"
+
+namespace i8l {
+
+constexpr int GN_VALUES = 32;                 // values of a thread in one chunk
+constexpr int GN_CHUNK = 256 * GN_VALUES;
+constexpr int GN_GROUPS = 2048;               // workgroups of a launch: eight on each compute unit
+
+int grad_chunk() { return GN_CHUNK; }
+int grad_groups(int64_t chunks) { return (int)(chunks < GN_GROUPS ? chunks : GN_GROUPS); }
+
+// The list in LDS, and the tensor of a chunk.
+struct ListLds {
+  const void* p[GRAD_LIST];
+  int64_t n[GRAD_LIST];
+  int32_t start[GRAD_LIST + 1];
+};
+__device__ __forceinline__ void list_to_lds(const GradList& list, ListLds& s) {
+  for (int i = threadIdx.x; i < list.count; i += 256) {
+    s.p[i] = list.p[i];
+    s.n[i] = list.n[i];
+  }
+  for (int i = threadIdx.x; i <= list.count; i += 256) s.start[i] = list.start[i];
+  __syncthreads();
+}
+// Tensor of chunk c: the last one that starts at or before it (empty tensors have no chunk).
+__device__ __forceinline__ int tensor_of(const ListLds& s, int count, int c) {
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+#pragma unroll
+  for (int b = 0; b < GRAD_LIST; b += 64) n += __popcll(__ballot(b + lane < count && s.start[b + lane] <= c));
+  return __builtin_amdgcn_readfirstlane(n - 1);
+}
+
+// f(group of 8 values, how many of them are in the tensor, their place) for this thread's values of a chunk.
+template <int DT, typename F>
+__device__ __forceinline__ void chunk_values(const void* base, int64_t first, int64_t n, bool vec, F f) {
+  typedef typename Elem<DT>::T T;
+  const T* p = static_cast<const T*>(base);
+  if (vec && first + GN_CHUNK <= n) {
+    T e[GN_VALUES / 8][8];
+#pragma unroll
+    for (int i = 0; i < GN_VALUES / 8; ++i) load8<DT>(p + first + (i * 256 + threadIdx.x) * 8, e[i]);
+#pragma unroll
+    for (int i = 0; i < GN_VALUES / 8; ++i) f(e[i], 8, first + (i * 256 + threadIdx.x) * 8);
+  } else {
+    for (int i = 0; i < GN_VALUES / 8; ++i) {
+      const int64_t at = first + (i * 256 + threadIdx.x) * 8;
+      const int m = (int)min((int64_t)8, n - at);
+      if (m <= 0) break;
+      T e[8] = {};
+      if (vec && m == 8) load8<DT>(p + at, e);
+      else
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < m) e[j] = p[at + j];
+      f(e, m, at);
+    }
+  }
+}
+
+template <bool INF>
+__device__ __forceinline__ double join(double a, double b) {
+  if constexpr (INF) return a != a ? a : (b != b ? b : (a > b ? a : b));   // NaN stays
+  else return a + b;
+}
+// All threads of the workgroup; the result in thread 0.
+template <bool INF>
+__device__ __forceinline__ double join_block(double v, double* lds) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = join<INF>(v, __shfl_xor(v, o, 64));
+  const int waves = blockDim.x >> 6;
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int w = 1; w < waves; ++w) v = join<INF>(v, lds[w]);
+  return v;
+}
+
+template <bool INF>
+__global__ __launch_bounds__(256) void k_grad_partial(const GradList list, double* __restrict__ partial) {
+  __shared__ ListLds s;
+  __shared__ double red[4];
+  list_to_lds(list, s);
+  const int total = s.start[list.count];
+  double sum = 0.0;
+  for (int c = blockIdx.x; c < total; c += gridDim.x) {
+    const int t = tensor_of(s, list.count, c);
+    const int64_t n = s.n[t] >> 2, first = (int64_t)(c - s.start[t]) * GN_CHUNK;
+    const bool vec = (uintptr_t)s.p[t] % 16 == 0;
+    auto one = [&](auto dt) {
+      constexpr int DT = decltype(dt)::value;
+      chunk_values<DT>(s.p[t], first, n, vec, [&](const typename Elem<DT>::T(&e)[8], int, int64_t) {
+        if constexpr (INF) {
+          uint32_t top = 0u;   // magnitudes as integers: infinities and NaN on top
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(Elem<DT>::to_f32(e[j])) & 0x7fffffffu);
+          sum = join<true>(sum, (double)__uint_as_float(top));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const double x = (double)Elem<DT>::to_f32(e[j]);
+            sum = __builtin_fma(x, x, sum);
+          }
+        }
+      });
+    };
+    switch ((int)(s.n[t] & 3)) {
+      case DT_F32: one(std::integral_constant<int, DT_F32>{}); break;
+      case DT_F16: one(std::integral_constant<int, DT_F16>{}); break;
+      default: one(std::integral_constant<int, DT_BF16>{}); break;
+    }
+  }
+  const double v = join_block<INF>(sum, red);
+  if (threadIdx.x == 0) partial[blockIdx.x] = v;
+}
+
+template <bool INF>
+__global__ __launch_bounds__(1024) void k_grad_final(const double* __restrict__ partial, int n, double max_norm,
+                                                     const float* __restrict__ grad_scale, float* __restrict__ norm,
+                                                     float* __restrict__ factor, float* __restrict__ found_inf) {
+  __shared__ double red[16];
+  double v = 0.0;
+  for (int i = threadIdx.x; i < n; i += 1024) v = join<INF>(v, partial[i]);
+  v = join_block<INF>(v, red);
+  if (threadIdx.x == 0) {
+    const double c = grad_scale ? (double)grad_scale[0] : 1.0;
+    const double x = (INF ? v : __builtin_sqrt(v)) * fabs(c);
+    const double r = max_norm / (x + 1e-6);
+    const float f = (float)x;
+    *norm = f;
+    *factor = (float)(max_norm < __builtin_huge_val() && !(r >= 1.0) ? c * r : c);   // a NaN norm: NaN
+    *found_inf = (f - f == 0.0f) ? 0.0f : 1.0f;
+  }
+}
+
+// g = D(factor g), nothing where factor is 1.
+__global__ __launch_bounds__(256) void k_grad_scale(const GradList list, const float* __restrict__ factor) {
+  const float f = factor[0];
+  if (f == 1.0f) return;
+  __shared__ ListLds s;
+  list_to_lds(list, s);
+  const int total = s.start[list.count];
+  for (int c = blockIdx.x; c < total; c += gridDim.x) {
+    const int t = tensor_of(s, list.count, c);
+    const int64_t n = s.n[t] >> 2, first = (int64_t)(c - s.start[t]) * GN_CHUNK;
+    const bool vec = (uintptr_t)s.p[t] % 16 == 0;
+    auto one = [&](auto dt) {
+      constexpr int DT = decltype(dt)::value;
+      typedef typename Elem<DT>::T T;
+      T* p = static_cast<T*>(const_cast<void*>(s.p[t]));
+      chunk_values<DT>(s.p[t], first, n, vec, [&](const T(&e)[8], int m, int64_t at) {
+        T o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = Elem<DT>::from_f32(Elem<DT>::to_f32(e[j]) * f);
+        if (vec && m == 8) {
+          if constexpr (DT == DT_F32) {
+            reinterpret_cast<v4f*>(p + at)[0] = v4f{o[0], o[1], o[2], o[3]};
+            reinterpret_cast<v4f*>(p + at)[1] = v4f{o[4], o[5], o[6], o[7]};
+          } else {
+            v4u w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = (uint32_t)__builtin_bit_cast(uint16_t, o[2 * j]) |
+                     ((uint32_t)__builtin_bit_cast(uint16_t, o[2 * j + 1]) << 16);
+            *reinterpret_cast<v4u*>(p + at) = w;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < m) p[at + j] = o[j];
+        }
+      });
+    };
+    switch ((int)(s.n[t] & 3)) {
+      case DT_F32: one(std::integral_constant<int, DT_F32>{}); break;
+      case DT_F16: one(std::integral_constant<int, DT_F16>{}); break;
+      default: one(std::integral_constant<int, DT_BF16>{}); break;
+    }
+  }
+}
+
+hipError_t launch_grad_partial(const GradList& list, bool inf, double* partial, hipStream_t st) {
+  const int g = grad_groups(list.start[list.count]);
+  if (g == 0) return hipSuccess;
+  if (inf) hipLaunchKernelGGL(k_grad_partial<true>, dim3(g), dim3(256), 0, st, list, partial);
+  else hipLaunchKernelGGL(k_grad_partial<false>, dim3(g), dim3(256), 0, st, list, partial);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_final(const double* partial, int n, bool inf, double max_norm, const float* grad_scale,
+                             float* norm, float* factor, float* found_inf, hipStream_t st) {
+  if (inf)
+    hipLaunchKernelGGL(k_grad_final<true>, dim3(1), dim3(1024), 0, st, partial, n, max_norm, grad_scale, norm, factor,
+                       found_inf);
+  else
+    hipLaunchKernelGGL(k_grad_final<false>, dim3(1), dim3(1024), 0, st, partial, n, max_norm, grad_scale, norm, factor,
+                       found_inf);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_scale(const GradList& list, const float* factor, hipStream_t st) {
+  const int g = grad_groups(list.start[list.count]);
+  if (g == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_grad_scale, dim3(g), dim3(256), 0, st, list, factor);
+  return hipGetLastError();
+}
+
+}  // namespace i8l

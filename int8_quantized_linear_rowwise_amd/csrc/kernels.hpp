@@ -100,6 +100,59 @@ hipError_t launch_norm_backward(int dt, int wdt, const void* G, const void* X, c
                                 int T, int C, const void* w, void* gX, void* gw, void* gb, float* ws,
                                 hipStream_t st);
 
+// Experts: the rows 0 .. R - 1 lie in n_seg consecutive segments; segment s
+// holds rows off[s] .. off[s + 1] - 1 (off[0] is taken as 0) of expert ids[s]
+// (s itself when ids is NULL; none when outside [0, n_experts)). Rows behind
+// off[n_seg] have no expert. off may be NULL only where n_seg is 0.
+struct ExpertSegs {
+  const int32_t* off;
+  const int32_t* ids;
+  int n_seg, n_experts;
+};
+// Stable sort of the R = T k choices by expert. scratch: expert_sort_ints() int32.
+size_t expert_sort_ints(int64_t R, int n_experts);
+hipError_t launch_expert_sort(const void* experts, int id_bytes, int R, int k, int n_experts, int32_t* off,
+                              int32_t* token, int32_t* position, int32_t* scratch, hipStream_t st);
+// out (R x N of dt) = products of the quantized tokens (codes CA, scales SCA, outlier columns) with their rows'
+// experts (CB: n_experts x N x K); row r is token rows[r] (r itself when rows is NULL).
+struct ExpertQuantized {
+  const int8_t* CA;
+  const float* SCA;
+  const uint16_t* sub;
+  int cap;
+  const int32_t* idx;
+  const int32_t* count;
+};
+hipError_t launch_expert_fwd(int dt, const ExpertQuantized& Q, const void* X, int T, const int32_t* rows, int R,
+                             const ExpertSegs& S, const int8_t* CB, const float* SCB, int N, int K, void* out,
+                             hipStream_t st);
+// gX (R x K) = D(fp16(G) Wdq[expert]), G: R x N.
+hipError_t launch_expert_bwd(int dt, const void* G, int R, const ExpertSegs& S, const int8_t* CB, const float* SCB,
+                             int N, int K, void* gX, hipStream_t st);
+// out[t] = D(base[t] + sum_j gate[t, j] Y[position[t, j]]) and its gradients.
+hipError_t launch_expert_combine(int dt, const void* Y, int R, int N, const int32_t* position, const float* gate,
+                                 const void* base, int T, int k, void* out, hipStream_t st);
+hipError_t launch_expert_combine_bwd(int dt, const void* G, int T, int N, const int32_t* position, const float* gate,
+                                     int k, const void* Y, int R, const int32_t* n_rows, void* gY, float* ggate,
+                                     hipStream_t st);
+
+// Norm of many tensors: the list travels in the kernels' arguments, GRAD_LIST
+// tensors a launch.
+constexpr int GRAD_LIST = 160;
+struct GradList {
+  const void* p[GRAD_LIST];
+  int64_t n[GRAD_LIST];          // values << 2 | dtype
+  int32_t start[GRAD_LIST + 1];  // first chunk of each tensor; [count]: all of them
+  int32_t count;
+};
+int grad_chunk();
+// Partial sums of `list` into partial[0 .. grad_groups(chunks) - 1].
+int grad_groups(int64_t chunks);
+hipError_t launch_grad_partial(const GradList& list, bool inf, double* partial, hipStream_t st);
+hipError_t launch_grad_final(const double* partial, int n, bool inf, double max_norm, const float* grad_scale,
+                             float* norm, float* factor, float* found_inf, hipStream_t st);
+hipError_t launch_grad_scale(const GradList& list, const float* factor, hipStream_t st);
+
 // AdamW over a table of tensors: chunk c is values [chunk * adamw_chunk(), ...)
 // of its tensor, one workgroup each.
 struct AdamWTensor {

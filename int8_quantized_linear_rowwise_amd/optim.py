@@ -15,6 +15,7 @@ import torch
 
 from ._lib import AdamWTensor, check, lib
 from ._tensors import DTYPE_CODE, _on_gpu, _ptr, _raw_stream
+from .grad_norm import GradNormPlan
 
 BLOCK = 256   # values that share a scale
 
@@ -226,6 +227,16 @@ class AdamW(torch.optim.Optimizer):
                     self.state[p] = s
         self._plans = plans
         return loss
+
+    def grad_norm(self, max_norm: Optional[float] = None, norm_type: float = 2.0,
+                  grad_scale: Optional[torch.Tensor] = None):
+        """(norm, factor, found_inf) over the gradients of all groups, as GradNormPlan.norm: `step` takes the factor as
+        its grad_scale, which clips without a pass of its own, and found_inf. All gradients have to be on one GPU."""
+        grads = [p.grad for group in self.param_groups for p in group["params"] if p.grad is not None]
+        plan = GradNormPlan(grads)
+        if _capturing(plan.gpu):   # a graph's replays read these very gradients and the scale
+            self._captured.append((plan, grad_scale))
+        return plan.norm(max_norm, norm_type, grad_scale)
 
     def load_state_dict(self, state_dict):
         """States keep their own types (the base class would turn them into the parameter's)."""
