@@ -167,6 +167,297 @@ __global__ __launch_bounds__(256) void k_expert_fwd(ExpertQuantized Q, const typ
   }
 }
 
+// Large tiles: 256 rows by BN features (256, or 128 where 256-wide tiles would
+// leave compute units idle), 8 waves (two per SIMD) of 64 rows by BN / 2, the
+// contraction 128 bytes at a time through two swizzled LDS stages, as in the
+// projection's own kernel; registers hold the next step's tiles. The rows of
+// the activation tile are gathered: a lane keeps the offsets of its four
+// tokens, so the gather costs nothing in the loop. Waves whose 64 rows all lie
+// past the segment only move tiles: a tile of 100 rows takes about half the
+// time of a full one. Requires K % 16 == 0 and codes of less than 2^31 bytes.
+constexpr int EF_OPAN = 2 * 256 * 32;                 // outlier panels P[n][16], Q[row][16] (fp16)
+constexpr int EF_SCALES = (256 + 256) * 4;            // SCB / 127^2, SCA
+template <int DT, int BN>
+__global__ __launch_bounds__(512, 1) void k_expert_fwd_w8(ExpertQuantized Q, const typename Elem<DT>::T* __restrict__ X,
+                                                          int T, const int32_t* __restrict__ rows, int R, ExpertSegs S,
+                                                          const int8_t* __restrict__ CBall,
+                                                          const float* __restrict__ SCBall, int N, int K, int slots,
+                                                          int64_t total, typename Elem<DT>::T* __restrict__ out) {
+  static_assert(BN == 256 || BN == 128, "256- or 128-wide tiles");
+  constexpr int BM = 256, BK = 128, TI = BN / 64, TJ = 2;
+  constexpr int NB = BN / 64;
+  constexpr int STAGE = (BM + BN) * BK, AOFF = BN * BK;
+  constexpr int OT = 256 * 512;
+  constexpr int BASE = 2 * STAGE > OT ? 2 * STAGE : OT;
+  extern __shared__ __attribute__((aligned(16))) int8_t smem[];
+  const int64_t bid = expert_block();
+  if (bid >= total) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 31, lg = lane >> 5;
+  const int wn = wave & 1, wm = wave >> 1;
+  int ts, tn;
+  tile_coords((int)bid, slots, (N + BN - 1) / BN, ts, tn);
+  const ExpertTile tile = expert_tile(S, ts, R, BM);
+  if (tile.r0 >= tile.r1) return;
+  const int r0 = tile.r0, r1 = tile.r1, n0 = tn * BN;
+  const bool has = tile.expert >= 0;
+  const int8_t* CB = CBall + (int64_t)max(tile.expert, 0) * N * K;
+  const float* SCB = SCBall + (int64_t)max(tile.expert, 0) * N;
+
+  const __amdgpu_buffer_rsrc_t rA = make_rsrc(Q.CA, T * K);
+  const __amdgpu_buffer_rsrc_t rB = make_rsrc(CB + (int64_t)n0 * K, has ? min(BN, N - n0) * K : 0);
+  const int lrow = tid >> 3, lc = tid & 7;
+  const int voff = lrow * K + 16 * lc;
+  const int woff = lrow * BK + 16 * (lc ^ lds_swz(lrow));
+  const int sw = lds_swz(lr);
+  int roff[4];
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) roff[ks] = lr * BK + 16 * ((2 * ks + lg) ^ sw);
+  const int pb = wn * (BN / 2) * BK, qb = AOFF + wm * 64 * BK;
+
+  v4u RB[NB], RA[4];
+  auto load_b = [&](int kt) {
+    const int v = (kt + 16 * lc < K) ? voff : OOB_OFFSET;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      RB[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rB, v, kt + 64 * i * K, 0));
+  };
+  load_b(0);
+  int aoff[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + lrow + 64 * i;
+    const int t = (has && r < r1) ? row_token(rows, r, T) : -1;
+    aoff[i] = t >= 0 ? t * K + 16 * lc : OOB_OFFSET;
+  }
+  auto load_a = [&](int kt) {
+    const bool in = kt + 16 * lc < K;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      RA[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rA, in ? aoff[i] : OOB_OFFSET, kt, 0));
+  };
+  auto write_b = [&](int st) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) *reinterpret_cast<v4u*>(smem + st * STAGE + woff + i * 64 * BK) = RB[i];
+  };
+  auto write_a = [&](int st) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<v4u*>(smem + st * STAGE + AOFF + woff + i * 64 * BK) = RA[i];
+  };
+  load_a(0);
+
+  // the tile's scales and tokens, and the panels of the first 16 outlier
+  // columns, while the first operand tiles are in flight
+  char* opan = reinterpret_cast<char*>(smem) + BASE;
+  float* lsb = reinterpret_cast<float*>(opan + EF_OPAN);
+  float* lsa = lsb + 256;
+  const int cnt = has ? *Q.count : 0;
+  const int orow = tid >> 1, oj = (tid & 1) * 8;
+  v8h opP = {}, opQ = {};
+  auto panels = [&](int jo) {
+    const int n = n0 + orow, r = r0 + orow;
+    opP = expert_out_w8(CB, SCB, K, Q.idx, n, orow < BN && n < N, jo + oj, cnt);
+    opQ = expert_out_a8<DT>(Q.sub, Q.cap, X, K, Q.idx, (has && r < r1) ? row_token(rows, r, T) : -1, jo + oj, cnt);
+  };
+  auto put_panels = [&]() {
+    *reinterpret_cast<v8h*>(opan + orow * 32 + oj * 2) = opP;
+    *reinterpret_cast<v8h*>(opan + EF_OPAN / 2 + orow * 32 + oj * 2) = opQ;
+  };
+  if (cnt > 0) panels(0);
+  if (tid < 256) {
+    const int n = n0 + tid;
+    lsb[tid] = (has && tid < BN && n < N) ? SCB[n] * (1.0f / 16129.0f) : 0.0f;
+  } else {
+    const int r = r0 + tid - 256;
+    const int t = (has && r < r1) ? row_token(rows, r, T) : -1;
+    lsa[tid - 256] = t >= 0 ? Q.SCA[t] : 0.0f;
+  }
+
+  v16i acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = v16i{};
+  v4i F[2][TI + TJ];
+  auto fread = [&](int st, int ks, int b) {
+    const int8_t* base = smem + st * STAGE + roff[ks];
+#pragma unroll
+    for (int i = 0; i < TI; ++i) F[b][i] = *reinterpret_cast<const v4i*>(base + pb + i * 32 * BK);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) F[b][TI + j] = *reinterpret_cast<const v4i*>(base + qb + j * 32 * BK);
+  };
+  auto mma = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(F[b][i], F[b][TI + j], acc[i][j], 0, 0, 0);
+  };
+  const int nk = has ? (K + BK - 1) / BK : 0;
+  write_b(0);
+  write_a(0);
+  load_b(BK);
+  load_a(BK);
+  if (cnt > 0) put_panels();
+  __syncthreads();
+  if (r0 + wm * 64 < r1) {
+    fread(0, 0, 0);
+    for (int kt = 0; kt < nk; ++kt) {
+      const int st = kt & 1;
+      const int k2 = (kt + 2) * BK;    // past the end: zeros
+      fread(st, 1, 1);
+      write_b(st ^ 1);
+      load_b(k2);
+      mma(0);
+#pragma unroll
+      for (int q = 0; q < TI * TJ; ++q) {
+        I8L_SGB(SG_MFMA, 1);
+        if (q < TI + TJ) I8L_SGB(SG_DS_R, 1);
+        if (q < NB) {
+          I8L_SGB(SG_DS_W, 1);
+          I8L_SGB(SG_VMEM_R, 1);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      fread(st, 2, 0);
+      write_a(st ^ 1);
+      load_a(k2);
+      mma(1);
+#pragma unroll
+      for (int q = 0; q < TI * TJ; ++q) {
+        I8L_SGB(SG_MFMA, 1);
+        if (q < TI + TJ) I8L_SGB(SG_DS_R, 1);
+        if (q < 4) {
+          I8L_SGB(SG_DS_W, 1);
+          I8L_SGB(SG_VMEM_R, 1);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      fread(st, 3, 1);
+      mma(0);
+#pragma unroll
+      for (int q = 0; q < TI * TJ; ++q) {
+        I8L_SGB(SG_MFMA, 1);
+        if (q < TI + TJ) I8L_SGB(SG_DS_R, 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      mma(1);
+      __syncthreads();
+      fread(st ^ 1, 0, 0);
+    }
+  } else {
+    for (int kt = 0; kt < nk; ++kt) {
+      const int k2 = (kt + 2) * BK;
+      write_b((kt & 1) ^ 1);
+      load_b(k2);
+      write_a((kt & 1) ^ 1);
+      load_a(k2);
+      __syncthreads();
+    }
+  }
+
+  // lane (lr, lg), register r of tile (i, j): feature wn BN / 2 + i 32 + (r / 4) 8 + lg 4 + r % 4, row wm 64 + j 32 + lr
+  const int nl = wn * (BN / 2), ml = wm * 64;
+  // the accumulators become fp32 in place
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const v4f sb = *reinterpret_cast<const v4f*>(lsb + nl + i * 32 + q * 8 + lg * 4);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const float sa = lsa[ml + j * 32 + lr];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          acc[i][j][4 * q + x] = __float_as_int((float)acc[i][j][4 * q + x] * (sa * sb[x]));
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (int jo = 0; jo < cnt; jo += 16) {
+    if (jo > 0) {
+      panels(jo);
+      __syncthreads();
+      put_panels();
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      const v8h P = *reinterpret_cast<const v8h*>(opan + (nl + i * 32 + lr) * 32 + lg * 16);
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const v8h V = *reinterpret_cast<const v8h*>(opan + EF_OPAN / 2 + (ml + j * 32 + lr) * 32 + lg * 16);
+        acc[i][j] = __builtin_bit_cast(
+            v16i, __builtin_amdgcn_mfma_f32_32x32x16_f16(P, V, __builtin_bit_cast(v16f, acc[i][j]), 0, 0, 0));
+      }
+    }
+  }
+  if constexpr (DT == DT_F32) {
+    const bool ov = N % 4 == 0 && (uintptr_t)out % 16 == 0;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      const int r = r0 + ml + j * 32 + lr;
+      if (r >= r1) continue;
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = n0 + nl + i * 32 + q * 8 + lg * 4;
+          int* p = reinterpret_cast<int*>(out) + (int64_t)r * N + n;
+          if (ov && n + 3 < N) {
+            *reinterpret_cast<v4i*>(p) =
+                v4i{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (n + x < N) p[x] = acc[i][j][4 * q + x];
+          }
+        }
+    }
+  } else {
+    // through LDS, stored as whole rows of the tile's columns
+    char* ot = reinterpret_cast<char*>(smem);
+    __syncthreads();   // the operand stages are no longer read
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v2u w;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float a = __int_as_float(acc[i][j][4 * q + 2 * x]), b = __int_as_float(acc[i][j][4 * q + 2 * x + 1]);
+            w[x] = (uint32_t)__builtin_bit_cast(uint16_t, Elem<DT>::from_f32(a)) |
+                   ((uint32_t)__builtin_bit_cast(uint16_t, Elem<DT>::from_f32(b)) << 16);
+          }
+          *reinterpret_cast<v2u*>(ot + otile_off(ml + j * 32 + lr, (nl + i * 32 + q * 8) >> 3) + 8 * lg) = w;
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();
+    otile_store<typename Elem<DT>::T>(ot, out, N, r0, n0, r1, min(N, n0 + BN), wave, lane);
+  }
+}
+
+template <int DT, int BN>
+static hipError_t launch_fwd_w8(const ExpertQuantized& Q, const void* X, int T, const int32_t* rows, int R,
+                                const ExpertSegs& S, const int8_t* CB, const float* SCB, int N, int K, void* out,
+                                hipStream_t st) {
+  typedef typename Elem<DT>::T E;
+  constexpr size_t stages = (size_t)2 * (256 + BN) * 128, otile = (size_t)256 * 512;
+  constexpr size_t lds = (stages > otile ? stages : otile) + EF_OPAN + EF_SCALES;
+  auto kern = k_expert_fwd_w8<DT, BN>;
+  static std::atomic<uint64_t> lds_set{0};
+  const hipError_t e = lds_limit_once((const void*)kern, (int)lds, lds_set);
+  if (e != hipSuccess) return e;
+  const int64_t slots = expert_slots(R, S.n_seg, 256), total = slots * ((N + BN - 1) / BN);
+  hipLaunchKernelGGL(kern, expert_grid(total), dim3(512), lds, st, Q, static_cast<const E*>(X), T, rows, R, S, CB, SCB,
+                     N, K, (int)slots, total, static_cast<E*>(out));
+  return hipGetLastError();
+}
+
 template <int DT>
 static hipError_t launch_fwd_t(const ExpertQuantized& Q, const void* X, int T, const int32_t* rows, int R,
                                const ExpertSegs& S, const int8_t* CB, const float* SCB, int N, int K, void* out,
@@ -174,6 +465,12 @@ static hipError_t launch_fwd_t(const ExpertQuantized& Q, const void* X, int T, c
   typedef typename Elem<DT>::T E;
   const bool kv = K % 16 == 0 && (uintptr_t)CB % 16 == 0;
   const bool ov = N % 4 == 0 && (uintptr_t)out % (4 * sizeof(E)) == 0;
+  if (kv && (int64_t)T * K < ((int64_t)1 << 31) && R >= 128 * (int64_t)S.n_seg && R >= 512) {
+    // 256-wide tiles, unless they would fill at most half of the chip
+    const int64_t tiles = (R + 255) / 256 * ((N + 255) / 256);
+    if (tiles > 128) return launch_fwd_w8<DT, 256>(Q, X, T, rows, R, S, CB, SCB, N, K, out, st);
+    if (tiles >= 32) return launch_fwd_w8<DT, 128>(Q, X, T, rows, R, S, CB, SCB, N, K, out, st);
+  }
   const int64_t slots = expert_slots(R, S.n_seg, 128), total = slots * ((N + 127) / 128);
   auto kern = kv ? (ov ? k_expert_fwd<DT, true, true> : k_expert_fwd<DT, true, false>)
                  : (ov ? k_expert_fwd<DT, false, true> : k_expert_fwd<DT, false, false>);

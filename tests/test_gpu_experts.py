@@ -120,6 +120,17 @@ def test_forward_outlier_columns(I8, dt, outliers):
     run_forward(I8, dt, 150, 320, 264, [0, 30, 150], outliers=outliers)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,k,E,K,N,outliers", [(1500, 2, 4, 272, 1100, 3), (1500, 2, 4, 272, 4100, 40),
+                                                (800, 2, 3, 64, 3000, 1), (2100, 3, 9, 400, 2304, 17),
+                                                (600, 1, 1, 16, 5000, 0)])
+def test_forward_many_rows(I8, dt, T, k, E, K, N, outliers):
+    """Sizes that fill tiles of 256 rows, with contractions and widths that end inside one, more outlier columns than
+    fit beside the tile, and experts of very different numbers of rows."""
+    off, token, _ = X.sort(X.choices(T, k, E, 7, 0.1, skew=1.5), E)
+    run_forward(I8, dt, T, K, N, off.tolist(), rows=token, outliers=outliers)
+
+
 @pytest.mark.parametrize("tau", [0.0, -1.0, float("inf"), float("nan"), 1.0])
 def test_forward_thresholds(I8, tau):
     run_forward(I8, "bf16", 20, 128, 64, [0, 8, 20], tau=tau)
