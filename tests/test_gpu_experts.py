@@ -236,6 +236,14 @@ def test_backward_segments(I8, dt, off):
     run_backward(I8, dt, max(off[-1], 1), 144, 160, off)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,k,E,N,K", [(1500, 2, 4, 264, 1100), (1500, 2, 4, 136, 4100), (800, 2, 3, 64, 3000),
+                                       (2100, 3, 9, 400, 2304), (600, 1, 1, 8, 5000)])
+def test_backward_many_rows(I8, dt, T, k, E, N, K):
+    off, _, _ = X.sort(X.choices(T, k, E, 7, 0.1, skew=1.5), E)
+    run_backward(I8, dt, T * k, N, K, off.tolist())
+
+
 def test_backward_rows_without_expert(I8):
     got = run_backward(I8, "bf16", 11, 80, 96, [0, 3, 6, 9], ids=[1, -1, 5], E=2)
     assert (got[3:] == 0).all() and (got[:3] != 0).any()
