@@ -8,6 +8,7 @@
 // As in the projection's own forward the product is computed transposed (the
 // weights on the matrix core's row side), so that a lane owns four
 // consecutive features of one row.
+#include <stdlib.h>
 #include "expert.hpp"
 
 namespace i8l {
@@ -52,11 +53,7 @@ __global__ __launch_bounds__(256) void k_expert_fwd(ExpertQuantized Q, const typ
     if constexpr (KV) {
       if (k < K) v = *reinterpret_cast<const v4i*>(p + k);
     } else {
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int b = 0; b < 16; ++b)
-        if (k + b < K) w[b >> 2] |= ((uint32_t)(uint8_t)p[k + b]) << (8 * (b & 3));
-      v = v4i{(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+      v = bytes16(p, k, K);
     }
     return v;
   };
@@ -458,6 +455,153 @@ static hipError_t launch_fwd_w8(const ExpertQuantized& Q, const void* X, int T, 
   return hipGetLastError();
 }
 
+// Few rows an expert: tiles of 16 MT rows by 16 features, bound by reading the
+// weights once. Four waves share a tile's contraction, 512 bytes of every row
+// at a time: a wave brings its 16 weight rows of 512 bytes into LDS with lanes
+// side by side on a row (straight from memory into the matrix operands' layout,
+// 16 rows a request, a compute unit gets only one request a nanosecond),
+// 16-byte pieces p of row r at p ^ r, and reads them as operands; the
+// codes, few and shared by all tiles of the expert, come from L2 in the
+// operands' layout. No barrier until the waves' int32 sums meet in LDS (exact,
+// so their order is nothing to the result).
+// Requires K % 16 == 0.
+typedef __attribute__((address_space(3))) void* lds_ptr;
+constexpr int ET_KC = 512;      // bytes of a row a wave takes at a time
+template <int DT, int MT>
+__global__ __launch_bounds__(256) void k_expert_fwd_thin(ExpertQuantized Q, const typename Elem<DT>::T* __restrict__ X,
+                                                         int T, const int32_t* __restrict__ rows, int R, ExpertSegs S,
+                                                         const int8_t* __restrict__ CBall,
+                                                         const float* __restrict__ SCBall, int N, int K, int tiles_n,
+                                                         int64_t total, typename Elem<DT>::T* __restrict__ out) {
+  typedef typename Elem<DT>::T E;
+  constexpr int BM = 16 * MT, BN = 16, STEPS = ET_KC / 64;
+  __shared__ __attribute__((aligned(1024))) int8_t sw[4][BN * ET_KC];
+  const int64_t bid = expert_block();
+  if (bid >= total) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lr = lane & 15, lg = lane >> 4;
+  const int ts = (int)(bid / tiles_n), n0 = (int)(bid - (int64_t)ts * tiles_n) * BN;
+  const ExpertTile tile = expert_tile(S, ts, R, BM);
+  if (tile.r0 >= tile.r1) return;
+  const bool has = tile.expert >= 0;
+  const int8_t* CB = CBall + (int64_t)max(tile.expert, 0) * N * K;
+  const float* SCB = SCBall + (int64_t)max(tile.expert, 0) * N;
+  const __amdgpu_buffer_rsrc_t rB = make_rsrc(CB + (int64_t)n0 * K, has ? min(BN, N - n0) * K : 0);
+  const int nc = has ? (K + ET_KC - 1) / ET_KC : 0;
+
+  int8_t* mine = sw[wave];
+  auto load_w = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = 2 * i + (lane >> 5);
+      const int k = c * ET_KC + 16 * ((lane & 31) ^ row);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr)(mine + i * 1024), 16,
+                                               k < K ? row * K + k : OOB_OFFSET, 0, 0, 0);
+    }
+  };
+  if (wave < nc) load_w(wave);
+
+  int tok[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) {
+    const int r = tile.r0 + 16 * j + lr;
+    tok[j] = (has && r < tile.r1) ? row_token(rows, r, T) : -1;
+  }
+  // wave j finishes tile j: what it needs for that is requested before the contraction
+  const int r = tile.r0 + 16 * wave + lr;      // its token's row
+  const int nb = n0 + 4 * lg;
+  int t = -1, cnt = 0;
+  float sa = 0.0f, sb[4] = {};
+  v8h P = {}, V = {};
+  if (wave < MT && has) {
+    t = r < tile.r1 ? row_token(rows, r, T) : -1;
+    cnt = *Q.count;
+    if (t >= 0) sa = Q.SCA[t];
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (nb + x < N) sb[x] = SCB[nb + x];
+    if (cnt > 0) {
+      P = expert_out_w8(CB, SCB, K, Q.idx, n0 + lr, n0 + lr < N, lg * 8, cnt);
+      V = expert_out_a8<DT>(Q.sub, Q.cap, X, K, Q.idx, t, lg * 8, cnt);
+    }
+  }
+  v4i acc[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) acc[j] = v4i{0, 0, 0, 0};
+  for (int c = wave; c < nc; c += 4) {
+    v4i a[STEPS][MT];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const int k = c * ET_KC + s * 64 + lg * 16;
+        a[s][j] = v4i{0, 0, 0, 0};
+        if (tok[j] >= 0 && k < K) a[s][j] = *reinterpret_cast<const v4i*>(Q.CA + (int64_t)tok[j] * K + k);
+      }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const v4i w = *reinterpret_cast<const v4i*>(mine + lr * ET_KC + 16 * ((4 * s + lg) ^ lr));
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, a[s][j], acc[j], 0, 0, 0);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next piece lands in the same place
+    if (c + 4 < nc) load_w(c + 4);
+  }
+
+  // lane (lr, lg): token lr of tile j, features n0 + 4 lg .. + 3
+  v4i* part = reinterpret_cast<v4i*>(sw[0]);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < MT; ++j) part[(wave * MT + j) * 64 + lane] = acc[j];
+  __syncthreads();
+  if (wave >= MT) return;
+  v4i sum = part[wave * 64 + lane];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) sum += part[(w * MT + wave) * 64 + lane];
+  v4f y;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) y[x] = (float)sum[x] * (sa * (sb[x] * (1.0f / 16129.0f)));
+  if (cnt > 0) y = __builtin_amdgcn_mfma_f32_16x16x32_f16(P, V, y, 0, 0, 0);
+  for (int jo = 32; jo < cnt; jo += 32) {
+    P = expert_out_w8(CB, SCB, K, Q.idx, n0 + lr, n0 + lr < N, jo + lg * 8, cnt);
+    V = expert_out_a8<DT>(Q.sub, Q.cap, X, K, Q.idx, t, jo + lg * 8, cnt);
+    y = __builtin_amdgcn_mfma_f32_16x16x32_f16(P, V, y, 0, 0, 0);
+  }
+  if (r < tile.r1) {
+    E* p = out + (int64_t)r * N + nb;
+    const bool ov = N % 4 == 0 && (uintptr_t)out % (4 * sizeof(E)) == 0;
+    E v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = Elem<DT>::from_f32(y[x]);
+    if (ov && nb + 3 < N) {
+      if constexpr (DT == DT_F32)
+        *reinterpret_cast<v4f*>(p) = y;
+      else
+        *reinterpret_cast<v2u*>(p) =
+            v2u{(uint32_t)__builtin_bit_cast(uint16_t, v[0]) | ((uint32_t)__builtin_bit_cast(uint16_t, v[1]) << 16),
+                (uint32_t)__builtin_bit_cast(uint16_t, v[2]) | ((uint32_t)__builtin_bit_cast(uint16_t, v[3]) << 16)};
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (nb + x < N) p[x] = v[x];
+    }
+  }
+}
+
+template <int DT, int MT>
+static hipError_t launch_fwd_thin(const ExpertQuantized& Q, const void* X, int T, const int32_t* rows, int R,
+                                  const ExpertSegs& S, const int8_t* CB, const float* SCB, int N, int K, void* out,
+                                  hipStream_t st) {
+  typedef typename Elem<DT>::T E;
+  const int tiles_n = (N + 15) / 16;
+  const int64_t total = expert_slots(R, S.n_seg, 16 * MT) * tiles_n;
+  hipLaunchKernelGGL((k_expert_fwd_thin<DT, MT>), expert_grid(total), dim3(256), 0, st, Q, static_cast<const E*>(X), T,
+                     rows, R, S, CB, SCB, N, K, tiles_n, total, static_cast<E*>(out));
+  return hipGetLastError();
+}
+
 template <int DT>
 static hipError_t launch_fwd_t(const ExpertQuantized& Q, const void* X, int T, const int32_t* rows, int R,
                                const ExpertSegs& S, const int8_t* CB, const float* SCB, int N, int K, void* out,
@@ -465,6 +609,13 @@ static hipError_t launch_fwd_t(const ExpertQuantized& Q, const void* X, int T, c
   typedef typename Elem<DT>::T E;
   const bool kv = K % 16 == 0 && (uintptr_t)CB % 16 == 0;
   const bool ov = N % 4 == 0 && (uintptr_t)out % (4 * sizeof(E)) == 0;
+  const char* th = getenv("I8L_THIN");
+  const int64_t thin = th ? atoi(th) : 16;
+  const char* tm = getenv("I8L_THINMT");
+  if (kv && R <= thin * S.n_seg) {
+    if (tm && atoi(tm) == 2) return launch_fwd_thin<DT, 2>(Q, X, T, rows, R, S, CB, SCB, N, K, out, st);
+    return launch_fwd_thin<DT, 1>(Q, X, T, rows, R, S, CB, SCB, N, K, out, st);
+  }
   if (kv && (int64_t)T * K < ((int64_t)1 << 31) && R >= 128 * (int64_t)S.n_seg && R >= 512) {
     // 256-wide tiles, unless they would fill at most half of the chip
     const int64_t tiles = (R + 255) / 256 * ((N + 255) / 256);

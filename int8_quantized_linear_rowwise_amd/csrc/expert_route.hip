@@ -93,10 +93,15 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void k_expert_place(const ID* __re
 #pragma unroll
       for (int w = 0; w < SORT_WAVES; ++w) mine += hist[w * E + e];
       if (counts) {
-        for (int b = 0; b < (int)gridDim.x; ++b) {
-          const int c = counts[(int64_t)b * E + e];
-          all += c;
-          before += b < (int)blockIdx.x ? c : 0;
+        for (int b0 = 0; b0 < (int)gridDim.x; b0 += 16) {   // 16 loads in flight
+          int c[16];
+#pragma unroll
+          for (int u = 0; u < 16; ++u) c[u] = b0 + u < (int)gridDim.x ? counts[(int64_t)(b0 + u) * E + e] : 0;
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            all += c[u];
+            before += b0 + u < (int)blockIdx.x ? c[u] : 0;
+          }
         }
       } else {
         all = mine;
