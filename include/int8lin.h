@@ -504,16 +504,19 @@ int int8_expert_sort(const void* experts, int id_bytes, int64_t T, int64_t k, in
  *
  * Input gradient (the weights are frozen): grad_X[r, k] = D(sum_n fp16(G[r, n]) *
  * Wdq[e, n, k]), R rows; the rows of a token are added up by int8_expert_combine
- * with gate = NULL. */
+ * with gate = NULL. It needs a workspace (for rows of fp16) where G is fp32, N is
+ * no multiple of 8 or G lies off a 16-byte border; the size query looks at no more
+ * of G than its address, and returns 0 otherwise (workspace may then be NULL). */
 size_t int8_expert_forward_workspace_bytes(int64_t T, int64_t K);
 int int8_expert_forward(const void* X, int dtype, int64_t T, int64_t K, const int32_t* rows, int64_t R,
                         const int8_t* CB, const float* SCB, int64_t n_experts, int64_t N,
                         const int32_t* seg_offsets, const int32_t* seg_expert, int64_t n_seg, float threshold,
                         void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+size_t int8_expert_backward_workspace_bytes(const void* G, int dtype, int64_t R, int64_t N);
 int int8_expert_backward(const void* G, int dtype, int64_t R, int64_t N, const int8_t* CB, const float* SCB,
                          int64_t n_experts, int64_t K, const int32_t* seg_offsets, const int32_t* seg_expert,
-                         int64_t n_seg, void* grad_X, void* stream);
+                         int64_t n_seg, void* grad_X, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Weighted sum of each token's rows (Y: R x N of `dtype`), in the order of j:
  *   out[t] = D(base[t] + sum_j gate[t, j] Y[position[t, j]])     (fp32 accumulate)

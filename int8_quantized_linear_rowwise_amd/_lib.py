@@ -84,7 +84,8 @@ SIGNATURES = {
     "int8_expert_forward_workspace_bytes": (_sz, [_i64, _i64]),
     "int8_expert_forward": (_int, [_vp, _int, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _f32, _vp,
                                    _vp, _sz, _vp]),
-    "int8_expert_backward": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp]),
+    "int8_expert_backward_workspace_bytes": (_sz, [_vp, _int, _i64, _i64]),
+    "int8_expert_backward": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _sz, _vp]),
     "int8_expert_combine": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp]),
     "int8_expert_combine_backward": (_int, [_vp, _int, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp]),
 }

@@ -145,17 +145,25 @@ int int8_expert_forward(const void* X, int dtype, int64_t T, int64_t K, const in
   int8_t* CA = reinterpret_cast<int8_t*>(w + L.codes);
   uint16_t* sub = reinterpret_cast<uint16_t*>(w + L.sub);
   hipStream_t st = (hipStream_t)stream;
-  const hipError_t e = i8l::launch_quantize(dtype, X, T, (int)K, threshold, CA, SCA, idx, count, sub, L.cap,
-                                            reinterpret_cast<uint32_t*>(w + L.scratch), st, nullptr, (int)K);
+  const hipError_t e =
+      i8l::quantize_small_fits(T, K, threshold)
+          ? i8l::launch_quantize_small(dtype, X, (int)T, (int)K, threshold, CA, SCA, idx, count, sub, L.cap, st)
+          : i8l::launch_quantize(dtype, X, T, (int)K, threshold, CA, SCA, idx, count, sub, L.cap,
+                                 reinterpret_cast<uint32_t*>(w + L.scratch), st, nullptr, (int)K);
   if (e != hipSuccess) return I8L_EHIP;
   const i8l::ExpertQuantized Q = {CA, SCA, sub, L.cap, idx, count};
   const i8l::ExpertSegs S = {seg_offsets, seg_expert, (int)n_seg, (int)n_experts};
   return hip_status(i8l::launch_expert_fwd(dtype, Q, X, (int)T, rows, (int)R, S, CB, SCB, (int)N, (int)K, out, st));
 }
 
+size_t int8_expert_backward_workspace_bytes(const void* G, int dtype, int64_t R, int64_t N) {
+  if (!valid_dtype(dtype) || R < 0 || N < 0 || R > MAX_ROWS || N > I8L_MAX_COLS || R * N > MAX_VALUES) return 0;
+  return align_up(i8l::expert_bwd_bytes(G, dtype, R, N));
+}
+
 int int8_expert_backward(const void* G, int dtype, int64_t R, int64_t N, const int8_t* CB, const float* SCB,
                          int64_t n_experts, int64_t K, const int32_t* seg_offsets, const int32_t* seg_expert,
-                         int64_t n_seg, void* grad_X, void* stream) {
+                         int64_t n_seg, void* grad_X, void* ws, size_t ws_bytes, void* stream) {
   if (!valid_dtype(dtype)) return I8L_EDTYPE;
   const int rc = product_sizes(R, N, K, n_experts, n_seg);
   if (rc != I8L_OK) return rc;
@@ -163,9 +171,13 @@ int int8_expert_backward(const void* G, int dtype, int64_t R, int64_t N, const i
   if (R > 0 && K > 0 && grad_X == nullptr) return I8L_EINVAL;
   if (R > 0 && N > 0 && G == nullptr) return I8L_EINVAL;
   if (n_experts > 0 && N > 0 && (SCB == nullptr || (K > 0 && CB == nullptr))) return I8L_EINVAL;
+  const size_t need = int8_expert_backward_workspace_bytes(G, dtype, R, N);
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return I8L_EWORKSPACE;
+  if ((uintptr_t)ws % ALIGN) return I8L_EINVAL;
   if (R == 0 || K == 0) return I8L_OK;
   const i8l::ExpertSegs S = {seg_offsets, seg_expert, (int)n_seg, (int)n_experts};
-  return hip_status(i8l::launch_expert_bwd(dtype, G, (int)R, S, CB, SCB, (int)N, (int)K, grad_X, (hipStream_t)stream));
+  return hip_status(
+      i8l::launch_expert_bwd(dtype, G, (int)R, S, CB, SCB, (int)N, (int)K, grad_X, ws, (hipStream_t)stream));
 }
 
 static int combine_sizes(int dtype, int64_t R, int64_t N, int64_t T, int64_t k) {

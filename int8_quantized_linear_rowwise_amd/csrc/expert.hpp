@@ -21,51 +21,70 @@ __device__ __forceinline__ int expert_of(const ExpertSegs& S, int s) {
 
 // Row tiles: every segment is cut into tiles of tm rows from its own start, so
 // a tile lies in one segment. Every wave finds its tile from the offsets alone.
-// Up to 255 segments: a scan of the tile counts, 64 segments at a time, so that
-// only tiles with rows are launched for (but for those of a bound on their
-// number). More: segment s owns the slots from start(s) / tm + s on; its
+// Up to 255 segments: a scan of the tile counts, four times 64 segments, so that
+// the number of tiles is known in the kernel and only tiles with rows are worked
+// on. More: segment s owns the slots from start(s) / tm + s on; its
 // ceil(len / tm) tiles never reach the next segment's, so a search 64 wide finds
 // the segment in two or three loads, and slots that hold no tile end at once.
 struct ExpertTile {
   int r0, r1, expert;   // rows [r0, r1), none where r1 <= r0; expert -1: rows of zeros
 };
 constexpr int SCAN_SEGMENTS = 256;
-__device__ __forceinline__ ExpertTile expert_tile(const ExpertSegs& S, int slot, int R, int tm) {
+struct ExpertScan {
+  int total;            // slots
+  int incl[4];          // of lane l's segment 64 b + l: slots up to and with it
+};
+__device__ __forceinline__ ExpertScan expert_scan(const ExpertSegs& S, int R, int tm) {
   const int lane = threadIdx.x & 63;
-  int s, i;      // segment, and the tile's number in it
-  if (S.n_seg < SCAN_SEGMENTS) {
-    int before = 0;
-    s = S.n_seg + 1;
-    i = 0;
-    for (int s0 = 0; s0 <= S.n_seg; s0 += 64) {
-      const int mine = s0 + lane;
-      const int len = mine <= S.n_seg ? expert_start(S, mine + 1, R) - expert_start(S, mine, R) : 0;
-      const int tiles = len > 0 ? (len + tm - 1) / tm : 0;
-      int incl = tiles;
+  ExpertScan c;
+  if (S.n_seg >= SCAN_SEGMENTS) {
+    c.total = R / tm + S.n_seg + 1;
+    return c;
+  }
+  c.total = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    c.incl[b] = c.total;
+    if (64 * b <= S.n_seg) {
+      const int s = 64 * b + lane;
+      const int len = s <= S.n_seg ? expert_start(S, s + 1, R) - expert_start(S, s, R) : 0;
+      int incl = len > 0 ? (len + tm - 1) / tm : 0;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int v = __shfl_up(incl, o, 64);
         incl += lane >= o ? v : 0;
       }
-      const int total = __builtin_amdgcn_readlane(incl, 63);
-      if (slot < before + total) {
-        const int l = __popcll(__ballot(before + incl <= slot));
-        s = s0 + l;
-        i = slot - before - (l > 0 ? __builtin_amdgcn_readlane(incl, l - 1) : 0);
-        break;
-      }
-      before += total;
+      c.incl[b] += incl;
+      c.total = __builtin_amdgcn_readlane(c.incl[b], 63);
     }
-    if (s > S.n_seg) return ExpertTile{0, 0, -1};
+  }
+  // offsets that are not non-decreasing can count rows twice: no more tiles than were launched for
+  c.total = min(c.total, (R + min(S.n_seg + 1, R) * (tm - 1)) / tm);
+  return c;
+}
+// Slot 0 <= slot < total.
+__device__ __forceinline__ ExpertTile expert_tile(const ExpertSegs& S, const ExpertScan& c, int slot, int R, int tm) {
+  const int lane = threadIdx.x & 63;
+  int s = 0, i;      // segment, and the tile's number in it
+  if (S.n_seg < SCAN_SEGMENTS) {
+    int before = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (64 * b <= S.n_seg) {
+        const int l = __popcll(__ballot(c.incl[b] <= slot));      // segments that end before the slot: a first part
+        s += l;
+        if (l > 0) before = __builtin_amdgcn_readlane(c.incl[b], l - 1);
+      }
+    i = slot - before;
   } else {
     int lo = 0, len = S.n_seg + 1;     // segments whose first slot is <= slot
     while (len > 0) {
       const int step = (len + 63) >> 6;
       const int o = (lane + 1) * step - 1;
       const bool in = o < len && expert_start(S, lo + o, R) / tm + lo + o <= slot;
-      const int c = __popcll(__ballot(in));
-      lo += c * step;
-      len = min(step - 1, len - c * step);
+      const int n = __popcll(__ballot(in));
+      lo += n * step;
+      len = min(step - 1, len - n * step);
     }
     s = max(lo - 1, 0);
     i = slot - (expert_start(S, s, R) / tm + s);
@@ -79,12 +98,48 @@ __device__ __forceinline__ ExpertTile expert_tile(const ExpertSegs& S, int slot,
   t.expert = __builtin_amdgcn_readfirstlane(expert_of(S, s));
   return t;
 }
-// Tiles to launch for: at most one per non-empty segment is not full.
+// Slots to launch for, at least as many as the scan finds: at most one tile of a segment is not full.
 inline int64_t expert_slots(int64_t R, int64_t n_seg, int tm) {
   if (n_seg >= SCAN_SEGMENTS) return R / tm + n_seg + 1;
   const int64_t parts = n_seg + 1 < R ? n_seg + 1 : R;
   return (R + parts * (tm - 1)) / tm;
 }
+
+// Work of a workgroup of the large-tile kernels: tile (slot, column tile), or
+// one of `parts` column parts of it. One workgroup runs on a compute unit at a
+// time, so tiles run in rounds of 256, and a last round of a few tiles takes as
+// long as a full one. Up to SPLIT_2 tiles over the full rounds are cut in two,
+// up to SPLIT_4 in four, which spreads them over idle units.
+// The XCDs take workgroups in turn; each gets one run of neighbouring tiles, in
+// groups of four slots by all columns, whose weights and rows meet in its L2.
+constexpr int ROUND = 256, SPLIT_4 = 64, SPLIT_2 = 128;
+struct ExpertWork {
+  int slot, tc, part, parts;     // slot -1: none
+};
+__device__ __forceinline__ ExpertWork expert_work(int64_t bid, int slots, int tiles_c) {
+  const int nt = slots * tiles_c, rem = nt % ROUND;
+  ExpertWork w = {-1, 0, 0, rem == 0 || rem > SPLIT_2 ? 1 : rem > SPLIT_4 ? 2 : 4};
+  const int full = w.parts > 1 ? nt - rem : nt;      // tiles worked on whole
+  int id;
+  if (bid < full) {
+    const int b = (int)bid, x = b & 7, base = full >> 3, r = full & 7;
+    id = x * base + min(x, r) + (b >> 3);
+    w.parts = 1;
+  } else {
+    const int64_t q = bid - full;
+    if (q >= (int64_t)(nt - full) * w.parts) return w;
+    id = full + (int)q / w.parts;
+    w.part = (int)q % w.parts;
+  }
+  constexpr int GRP = 4;
+  const int group = id / (GRP * tiles_c), first = group * GRP, gsz = min(slots - first, GRP);
+  const int in = id - group * GRP * tiles_c;
+  w.slot = first + in % gsz;
+  w.tc = in / gsz;
+  return w;
+}
+// Workgroups for that: cut tiles take at most 3 SPLIT_4 more.
+inline int64_t expert_groups(int64_t slots, int64_t tiles_c) { return slots * tiles_c + 3 * SPLIT_4; }
 
 // Grid of `total` workgroups in two dimensions (a grid axis holds fewer than 2^32 threads).
 inline dim3 expert_grid(int64_t total) {
@@ -102,7 +157,7 @@ __device__ __forceinline__ int row_token(const int32_t* __restrict__ rows, int r
 // Bytes k .. k + 15 of a row of K bytes at any address, zero past its end: one
 // load of 16 bytes, which global memory takes unaligned; the last piece of a row
 // is loaded so that it ends with the row and shifted into place.
-__device__ __forceinline__ v4i bytes16(const int8_t* row, int k, int K) {
+__device__ __forceinline__ v4u bytes16(const int8_t* row, int k, int K) {
   unsigned __int128 v = 0;
   if (k + 16 <= K) {
     __builtin_memcpy(&v, row + k, 16);
@@ -114,7 +169,7 @@ __device__ __forceinline__ v4i bytes16(const int8_t* row, int k, int K) {
       for (int b = 0; b < K; ++b) v |= (unsigned __int128)(uint8_t)row[b] << (8 * b);   // k is 0
     }
   }
-  return __builtin_bit_cast(v4i, v);
+  return __builtin_bit_cast(v4u, v);
 }
 
 // fp16 outlier values j0 .. j0 + 7 of token t (zero at and past cnt, or for no
@@ -148,6 +203,33 @@ __device__ __forceinline__ v8h expert_out_w8(const int8_t* __restrict__ CB, cons
       if (j0 + e < cnt) p[e] = half_of_f32((float)row[idx[j0 + e]] * sig);
   }
   return p;
+}
+
+// Zeros into columns [c0, c1) of rows [r0, r1), by the whole workgroup: rows without an expert.
+template <typename E>
+__device__ __forceinline__ void expert_zeros(E* out, int64_t ld, int r0, int r1, int c0, int c1) {
+  for (int r = r0; r < r1; ++r)
+    for (int c = c0 + threadIdx.x; c < c1; c += blockDim.x) out[r * ld + c] = E{};
+}
+
+// Four results of one row to p[0 .. 3], of which m lie inside the row; vec: p is on a border of four.
+template <int DT>
+__device__ __forceinline__ void expert_store4(typename Elem<DT>::T* p, const float (&y)[4], int m, bool vec) {
+  typename Elem<DT>::T v[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) v[x] = Elem<DT>::from_f32(y[x]);
+  if (vec && m >= 4) {
+    if constexpr (DT == DT_F32)
+      *reinterpret_cast<v4f*>(p) = v4f{y[0], y[1], y[2], y[3]};
+    else
+      *reinterpret_cast<v2u*>(p) =
+          v2u{(uint32_t)__builtin_bit_cast(uint16_t, v[0]) | ((uint32_t)__builtin_bit_cast(uint16_t, v[1]) << 16),
+              (uint32_t)__builtin_bit_cast(uint16_t, v[2]) | ((uint32_t)__builtin_bit_cast(uint16_t, v[3]) << 16)};
+  } else {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (x < m) p[x] = v[x];
+  }
 }
 
 }  // namespace i8l

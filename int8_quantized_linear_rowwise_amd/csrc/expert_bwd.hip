@@ -4,187 +4,58 @@
 // for the rows r of a segment with expert e; the weights are frozen. The
 // contraction runs along the rows of CB, so each int8 tile is dequantized once
 // per workgroup on its way into LDS, transposed to rows of fp16 along n.
+//
+// Tiles of 256 rows by BK columns, 8 waves (two per SIMD) of 64 rows by BK / 2,
+// 64 rows of CB a step through two swizzled LDS stages, as in the projection's
+// own kernel: the next stage's weights and gradients are loaded two steps
+// ahead, and converted and written between the matrix instructions. Waves whose
+// 64 rows all lie past the segment only move and convert tiles.
+//
+// fp32 gradients, and those whose rows do not start on 16-byte borders, are cast
+// to rows of fp16 first (the same cast that the tiles would do).
 #include <type_traits>
 
 #include "expert.hpp"
 
 namespace i8l {
 
-// Any size and alignment: 128 x 128 tiles, 4 waves of 64 x 64, 64 rows of CB a step.
-template <int DT, bool VEC>
-__global__ __launch_bounds__(256) void k_expert_bwd(const typename Elem<DT>::T* __restrict__ G, int R, ExpertSegs S,
-                                                    const int8_t* __restrict__ CBall, const float* __restrict__ SCBall,
-                                                    int N, int K, int slots, int64_t total,
-                                                    typename Elem<DT>::T* __restrict__ gX) {
-  typedef typename Elem<DT>::T T;
-  constexpr int BM = 128, BK = 128, BNC = 64, LDN = BNC + 8, TI = 2, TJ = 2;
-  __shared__ __attribute__((aligned(16))) _Float16 sW[BK * LDN], sG[BM * LDN];
-  const int64_t bid = expert_block();
-  if (bid >= total) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int lr = lane & 31, lg = lane >> 5;
-  const int wk = wave & 1, wm = wave >> 1;
-  int ts, tk;
-  tile_coords((int)bid, slots, (K + BK - 1) / BK, ts, tk);
-  const ExpertTile tile = expert_tile(S, ts, R, BM);
-  if (tile.r0 >= tile.r1) return;
-  const int r0 = tile.r0, r1 = tile.r1, k0 = tk * BK;
-  const int8_t* CB = CBall + (int64_t)max(tile.expert, 0) * N * K;
-  const float* SCB = SCBall + (int64_t)max(tile.expert, 0) * N;
-
-  v16f acc[TI][TJ];
-#pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) acc[i][j] = v16f{};
-
-  const int nend = tile.expert >= 0 ? N : 0;
-  for (int nc = 0; nc < nend; nc += BNC) {
-    // G: 8 values a thread, rows tid / 8 + 32 i
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = (tid >> 3) + 32 * i, n = nc + (tid & 7) * 8, r = r0 + row;
-      v8h h = {};
-      if (r < r1) {
-        const T* p = G + (int64_t)r * N + n;
-        if (VEC && n < N) {
-          T v[8];
-          load8<DT>(p, v);
-#pragma unroll
-          for (int x = 0; x < 8; ++x) h[x] = to_half<DT>(v[x]);
-        } else if (!VEC) {
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            if (n + x < N) h[x] = to_half<DT>(p[x]);
-        }
-      }
-      *reinterpret_cast<v8h*>(sG + row * LDN + (tid & 7) * 8) = h;
-    }
-    // W: 8 rows by 4 columns a thread
-    {
-      const int kq = tid & 31, ng = tid >> 5;
-      uint32_t w[8];
-      float sig[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int n = nc + 8 * ng + x, k = k0 + 4 * kq;
-        w[x] = 0u;
-        sig[x] = 0.0f;
-        if (n < N) {
-          sig[x] = SCB[n] * (1.0f / 127.0f);
-          const int8_t* p = CB + (int64_t)n * K + k;
-          if (VEC) {
-            if (k < K) w[x] = *reinterpret_cast<const uint32_t*>(p);
-          } else {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              if (k + b < K) w[x] |= ((uint32_t)(uint8_t)p[b]) << (8 * b);
-          }
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        v8h h;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) h[x] = half_of_f32((float)(int)(int8_t)(w[x] >> (8 * c)) * sig[x]);
-        *reinterpret_cast<v8h*>(sW + (4 * kq + c) * LDN + 8 * ng) = h;
-      }
-    }
-    __syncthreads();
-    const _Float16* bW = sW + (wk * 64 + lr) * LDN + lg * 8;
-    const _Float16* bG = sG + (wm * 64 + lr) * LDN + lg * 8;
-#pragma unroll
-    for (int ks = 0; ks < BNC / 16; ++ks) {
-      v8h P[TI], V[TJ];
-#pragma unroll
-      for (int i = 0; i < TI; ++i) P[i] = *reinterpret_cast<const v8h*>(bW + i * 32 * LDN + ks * 16);
-#pragma unroll
-      for (int j = 0; j < TJ; ++j) V[j] = *reinterpret_cast<const v8h*>(bG + j * 32 * LDN + ks * 16);
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(P[i], V[j], acc[i][j], 0, 0, 0);
-    }
-    __syncthreads();
-  }
-
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    const int r = r0 + wm * 64 + j * 32 + lr;
-    if (r >= r1) continue;
-#pragma unroll
-    for (int i = 0; i < TI; ++i)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int k = k0 + wk * 64 + i * 32 + q * 8 + lg * 4;
-        T* p = gX + (int64_t)r * K + k;
-        T v[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) v[x] = Elem<DT>::from_f32(acc[i][j][4 * q + x]);
-        if (VEC && k + 3 < K) {
-          if constexpr (DT == DT_F32)
-            *reinterpret_cast<v4f*>(p) = v4f{v[0], v[1], v[2], v[3]};
-          else
-            *reinterpret_cast<v2u*>(p) =
-                v2u{(uint32_t)__builtin_bit_cast(uint16_t, v[0]) | ((uint32_t)__builtin_bit_cast(uint16_t, v[1]) << 16),
-                    (uint32_t)__builtin_bit_cast(uint16_t, v[2]) | ((uint32_t)__builtin_bit_cast(uint16_t, v[3]) << 16)};
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (k + x < K) p[x] = v[x];
-        }
-      }
-  }
-}
-
-// Large tiles for 16-bit gradients: 256 rows by BK columns (256, or 128 where
-// 256-wide tiles would leave compute units idle), 8 waves (two per SIMD) of 64
-// rows by BK / 2, the contraction 64 rows of CB at a time through two swizzled
-// LDS stages, as in the projection's own kernel: the next stage's weights and
-// gradients are loaded two steps ahead, and converted and written between the
-// matrix instructions. Waves whose 64 rows all lie past the segment only move
-// and convert tiles. Requires N % 8 == 0, K % 4 == 0 and 32-bit offsets within
-// an expert's weight.
-template <int DT, int BK>
-__global__ __launch_bounds__(512, 1) void k_expert_bwd_w8(const typename Elem<DT>::T* __restrict__ G, int R,
-                                                          ExpertSegs S, const int8_t* __restrict__ CBall,
-                                                          const float* __restrict__ SCBall, int N, int K, int slots,
-                                                          int64_t total, typename Elem<DT>::T* __restrict__ gX) {
-  static_assert(DT == DT_F16 || DT == DT_BF16, "16-bit gradients only");
-  static_assert(BK == 256 || BK == 128, "256- or 128-wide tiles");
-  typedef typename Elem<DT>::T T;
+// G is fp16 or bf16 (GT), R rows of ng values (N, or N rounded up to 8 with
+// zeros behind it); the result is OT.
+// UA: N is no multiple of 8 or K of 4, the weights lie off 4-byte borders, or an
+// expert's weight passes 32-bit offsets: loads at any address. A row's last
+// piece is loaded so that it ends with the row, and shifted into place.
+template <int GT, int OT, int BK, bool UA>
+__device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __restrict__ G, int ng,
+                                                const ExpertTile& tile, int k0, const int8_t* __restrict__ CBall,
+                                                const float* __restrict__ SCBall, int N, int K,
+                                                typename Elem<OT>::T* __restrict__ gX, char* bsm) {
+  static_assert(GT == DT_F16 || GT == DT_BF16, "16-bit gradients only");
   constexpr int BM = 256, BNC = 64, TI = BK / 64, TJ = 2;
   constexpr int WR = BK / 32;                  // weight rows a lane converts in a step
   constexpr int ROW = BNC * 2;
   constexpr int STAGE = (BK + BM) * ROW, GOFF = BK * ROW;
-  extern __shared__ __attribute__((aligned(16))) char bsm[];
-  const int64_t bid = expert_block();
-  if (bid >= total) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 31, lg = lane >> 5;
   const int wk = wave & 1, wm = wave >> 1;
-  int ts, tk;
-  tile_coords((int)bid, slots, (K + BK - 1) / BK, ts, tk);
-  const ExpertTile tile = expert_tile(S, ts, R, BM);
-  if (tile.r0 >= tile.r1) return;
-  const int r0 = tile.r0, r1 = tile.r1, k0 = tk * BK;
-  const bool has = tile.expert >= 0;
-  const int8_t* CB = CBall + (int64_t)max(tile.expert, 0) * N * K;
-  const float* SCB = SCBall + (int64_t)max(tile.expert, 0) * N;
+  const int r0 = tile.r0, r1 = tile.r1;
+  const int8_t* CB = CBall + (int64_t)tile.expert * N * K;
+  const float* SCB = SCBall + (int64_t)tile.expert * N;
 
-  const __amdgpu_buffer_rsrc_t rG = make_rsrc(G + (int64_t)r0 * N, has ? (r1 - r0) * N * 2 : 0);
-  const __amdgpu_buffer_rsrc_t rW = make_rsrc(CB + k0, has ? max(0, N * K - k0) : 0);
-  const __amdgpu_buffer_rsrc_t rS = make_rsrc(SCB, has ? N * 4 : 0);
+  const __amdgpu_buffer_rsrc_t rG = make_rsrc(G + (int64_t)r0 * ng, (r1 - r0) * ng * 2);
+  const __amdgpu_buffer_rsrc_t rW = make_rsrc(CB + k0, UA ? 0 : N * K - k0);
+  const __amdgpu_buffer_rsrc_t rS = make_rsrc(SCB, UA ? 0 : N * 4);
 
   // gradient slots: 16-byte chunk gc of rows grow + 64 i (i < 4)
   const int grow = tid >> 3, gc = tid & 7;
-  const int gvoff = grow * N * 2 + 16 * gc;
+  const int gvoff = grow * ng * 2 + 16 * gc;
   const int gwoff = GOFF + grow * ROW + 16 * (gc ^ lds_swz(grow));
   // weights: rows nc + 8 wave + wh .. + WR - 1, bytes 4 kq .. 4 kq + 3
-  const int kq = BK == 256 ? (tid & 63) : (tid & 31);
-  const int wh = BK == 256 ? 0 : 4 * ((tid >> 5) & 1);
+  constexpr int QUADS = BK / 4;                // lanes side by side on a weight row
+  const int kq = lane % QUADS, wh = WR * (lane / QUADS);
   const int wvoff = 4 * kq + wh * K;
+  const int ku = min(k0 + 4 * kq, K - 4);      // UA: where a lane loads, and what it shifts out
+  const int shift = UA ? min(8 * (k0 + 4 * kq - ku), 31) : 0;
   int wwoff[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -202,22 +73,42 @@ __global__ __launch_bounds__(512, 1) void k_expert_bwd_w8(const typename Elem<DT
   float SG[WR];
   auto load_w = [&](int nc) {
     const int n8 = nc + 8 * wave;
+    if constexpr (UA) {
 #pragma unroll
-    for (int e = 0; e < WR; ++e) RW[e] = __builtin_amdgcn_raw_buffer_load_b32(rW, wvoff, (n8 + e) * K, 0);
-    // N % 8 == 0: the eight rows from n8 are all in the matrix or all past it
-    const int so = (n8 < N) ? 4 * (n8 + wh) : OOB_OFFSET;
+      for (int e = 0; e < WR; ++e) {
+        const int n = n8 + wh + e;
+        const int8_t* p = CB + (int64_t)min(n, N - 1) * K;      // past N: its scale is 0
+        if (K >= 4) __builtin_memcpy(&RW[e], p + ku, 4);
+        else {
+          RW[e] = 0u;
+          for (int b = k0 + 4 * kq; b < K; ++b) RW[e] |= (uint32_t)(uint8_t)p[b] << (8 * (b & 3));
+        }
+        SG[e] = n < N ? SCB[n] : 0.0f;
+      }
+    } else {
 #pragma unroll
-    for (int h = 0; h < WR / 4; ++h) {
-      const v4f sv = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rS, so + 16 * h, 0, 0));
+      for (int e = 0; e < WR; ++e) RW[e] = __builtin_amdgcn_raw_buffer_load_b32(rW, wvoff, (n8 + e) * K, 0);
+      // N % 8 == 0: the eight rows from n8 are all in the matrix or all past it
+      const int so = (n8 < N) ? 4 * (n8 + wh) : OOB_OFFSET;
+      if constexpr (WR == 2) {
+        const v2f sv = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rS, so, 0, 0));
+        SG[0] = sv[0];
+        SG[1] = sv[1];
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) SG[4 * h + e] = sv[e];
+        for (int h = 0; h < WR / 4; ++h) {
+          const v4f sv = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rS, so + 16 * h, 0, 0));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) SG[4 * h + e] = sv[e];
+        }
+      }
     }
   };
   auto load_g = [&](int nc) {
-    const int gv = (nc + 8 * gc < N) ? gvoff : OOB_OFFSET;
+    const int gv = (nc + 8 * gc < ng) ? gvoff : OOB_OFFSET;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      RG[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rG, gv, 2 * nc + 128 * i * N, 0));
+      RG[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rG, gv, 2 * nc + 128 * i * ng, 0));
   };
   auto write_w = [&](int st, int c0) {
     float sg[WR];
@@ -228,19 +119,22 @@ __global__ __launch_bounds__(512, 1) void k_expert_bwd_w8(const typename Elem<DT
       uint32_t h[WR / 2];
 #pragma unroll
       for (int e = 0; e < WR / 2; ++e) {
-        const float w0 = (float)(int)(int8_t)(RW[2 * e] >> (8 * c));
-        const float w1 = (float)(int)(int8_t)(RW[2 * e + 1] >> (8 * c));
+        const uint32_t q0 = UA && K >= 4 ? RW[2 * e] >> shift : RW[2 * e];
+        const uint32_t q1 = UA && K >= 4 ? RW[2 * e + 1] >> shift : RW[2 * e + 1];
+        const float w0 = (float)(int)(int8_t)(q0 >> (8 * c));
+        const float w1 = (float)(int)(int8_t)(q1 >> (8 * c));
         h[e] = f32x2_to_f16x2(w0 * sg[2 * e], w1 * sg[2 * e + 1]);
       }
       if constexpr (WR == 8) *reinterpret_cast<v4u*>(bsm + st * STAGE + wwoff[c]) = v4u{h[0], h[1], h[2], h[3]};
-      else *reinterpret_cast<v2u*>(bsm + st * STAGE + wwoff[c]) = v2u{h[0], h[1]};
+      else if constexpr (WR == 4) *reinterpret_cast<v2u*>(bsm + st * STAGE + wwoff[c]) = v2u{h[0], h[1]};
+      else *reinterpret_cast<uint32_t*>(bsm + st * STAGE + wwoff[c]) = h[0];
     }
   };
   auto write_g = [&](int st) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v4u v;
-      if constexpr (DT == DT_F16) {
+      if constexpr (GT == DT_F16) {
         v = RG[i];
       } else {
 #pragma unroll
@@ -271,19 +165,20 @@ __global__ __launch_bounds__(512, 1) void k_expert_bwd_w8(const typename Elem<DT
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(F[b][i], F[b][TI + j], acc[i][j], 0, 0, 0);
   };
   // every matrix instruction of a phase is followed by four conversions, then by its share of the memory work
-  auto spread = [&](auto dsr, auto dsw, auto vm) {
-    constexpr int Rd = decltype(dsr)::value, Wr = decltype(dsw)::value, Gl = decltype(vm)::value;
+  auto spread = [&](auto dsw, auto vm) {
+    constexpr int Wr = decltype(dsw)::value, Gl = decltype(vm)::value;
 #pragma unroll
     for (int q = 0; q < TI * TJ; ++q) {
       I8L_SGB(SG_MFMA, 1);
       I8L_SGB(SG_VALU, 4);
-      if (q < Rd) I8L_SGB(SG_DS_R, 1);
+      if (q < TI + TJ) I8L_SGB(SG_DS_R, 1);
       if (q < Wr) I8L_SGB(SG_DS_W, 1);
       if (q < Gl) I8L_SGB(SG_VMEM_R, 1);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
 
-  const int nn = has ? (N + BNC - 1) / BNC : 0;
+  const int nn = (N + BNC - 1) / BNC;
   load_w(0);
   load_g(0);
   write_w(0, 0);
@@ -300,23 +195,17 @@ __global__ __launch_bounds__(512, 1) void k_expert_bwd_w8(const typename Elem<DT
       fread(st, 1, 1);
       write_w(st ^ 1, 0);
       mma(0);
-      spread(std::integral_constant<int, TI + TJ>{}, std::integral_constant<int, 2>{},
-             std::integral_constant<int, 0>{});
-      __builtin_amdgcn_sched_barrier(0);
+      spread(std::integral_constant<int, 2>{}, std::integral_constant<int, 0>{});
       fread(st, 2, 0);
       write_w(st ^ 1, 2);
       load_w(nc2);
       mma(1);
-      spread(std::integral_constant<int, TI + TJ>{}, std::integral_constant<int, 2>{},
-             std::integral_constant<int, WR + WR / 4>{});
-      __builtin_amdgcn_sched_barrier(0);
+      spread(std::integral_constant<int, 2>{}, std::integral_constant<int, WR + (WR + 3) / 4>{});
       fread(st, 3, 1);
       write_g(st ^ 1);
       load_g(nc2);
       mma(0);
-      spread(std::integral_constant<int, TI + TJ>{}, std::integral_constant<int, 4>{},
-             std::integral_constant<int, 4>{});
-      __builtin_amdgcn_sched_barrier(0);
+      spread(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
       mma(1);
       __syncthreads();
       fread(st ^ 1, 0, 0);
@@ -334,69 +223,136 @@ __global__ __launch_bounds__(512, 1) void k_expert_bwd_w8(const typename Elem<DT
     }
   }
 
-  // lane (lr, lg), register r of tile (i, j): column wk BK / 2 + i 32 + (r / 4) 8 + lg 4 + r % 4, row wm 64 + j 32 + lr;
-  // through LDS, stored as whole rows
-  __syncthreads();   // every wave is done with the operand stages
+  // lane (lr, lg), register r of tile (i, j): column wk BK / 2 + i 32 + (r / 4) 8 + lg 4 + r % 4, row wm 64 + j 32 + lr
+  if constexpr (OT == DT_F32) {
+    const bool ov = K % 4 == 0 && (uintptr_t)gX % 16 == 0;
 #pragma unroll
-  for (int j = 0; j < TJ; ++j)
+    for (int j = 0; j < TJ; ++j) {
+      const int r = r0 + wm * 64 + j * 32 + lr;
+      if (r >= r1) continue;
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+      for (int i = 0; i < TI; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        v2u w;
+        for (int q = 0; q < 4; ++q) {
+          const int k = k0 + wk * (BK / 2) + i * 32 + q * 8 + lg * 4;
+          const float y[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          expert_store4<OT>(gX + (int64_t)r * K + k, y, K - k, ov);
+        }
+    }
+  } else {
+    // through LDS, stored as whole rows of the tile's columns
+    __syncthreads();   // every wave is done with the operand stages
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          w[e] = (uint32_t)__builtin_bit_cast(uint16_t, Elem<DT>::from_f32(acc[i][j][4 * q + 2 * e])) |
-                 ((uint32_t)__builtin_bit_cast(uint16_t, Elem<DT>::from_f32(acc[i][j][4 * q + 2 * e + 1])) << 16);
-        *reinterpret_cast<v2u*>(bsm + otile_off(wm * 64 + j * 32 + lr, wk * (BK / 16) + i * 4 + q) + 8 * lg) = w;
-      }
-  __syncthreads();
-  otile_store<T>(bsm, gX, K, r0, k0, r1, min(K, k0 + BK), wave, lane);
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+      for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v2u w;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            w[e] = (uint32_t)__builtin_bit_cast(uint16_t, Elem<OT>::from_f32(acc[i][j][4 * q + 2 * e])) |
+                   ((uint32_t)__builtin_bit_cast(uint16_t, Elem<OT>::from_f32(acc[i][j][4 * q + 2 * e + 1])) << 16);
+          *reinterpret_cast<v2u*>(bsm + otile_off(wm * 64 + j * 32 + lr, wk * (BK / 16) + i * 4 + q) + 8 * lg) = w;
+        }
+    __syncthreads();
+    otile_store<typename Elem<OT>::T>(bsm, gX, K, r0, k0, r1, min(K, k0 + BK), wave, lane);
+  }
 }
 
-template <int DT, int BK>
-static hipError_t launch_bwd_w8(const void* G, int R, const ExpertSegs& S, const int8_t* CB, const float* SCB, int N,
-                                int K, void* gX, hipStream_t st) {
-  typedef typename Elem<DT>::T E;
-  constexpr size_t stages = (size_t)2 * (BK + 256) * 128, otile = (size_t)256 * 512;
-  constexpr size_t lds = stages > otile ? stages : otile;
-  auto kern = k_expert_bwd_w8<DT, BK>;
-  static std::atomic<uint64_t> lds_set{0};
-  const hipError_t e = lds_limit_once((const void*)kern, (int)lds, lds_set);
+// Tiles 256 wide; the last ones in narrower parts (expert_work).
+template <int GT, int OT, bool UA>
+__global__ __launch_bounds__(512, 1) void k_expert_bwd(const typename Elem<GT>::T* __restrict__ G, int ng, int R,
+                                                       ExpertSegs S, const int8_t* __restrict__ CB,
+                                                       const float* __restrict__ SCB, int N, int K,
+                                                       typename Elem<OT>::T* __restrict__ gX) {
+  extern __shared__ __attribute__((aligned(16))) char bsm[];
+  const ExpertScan scan = expert_scan(S, R, 256);
+  const ExpertWork work = expert_work(expert_block(), scan.total, (K + 255) / 256);
+  if (work.slot < 0) return;
+  const ExpertTile tile = expert_tile(S, scan, work.slot, R, 256);
+  const int k0 = work.tc * 256 + work.part * (256 / work.parts);
+  if (tile.r0 >= tile.r1 || k0 >= K) return;
+  if (tile.expert < 0 || N == 0) return expert_zeros(gX, K, tile.r0, tile.r1, k0, min(K, k0 + 256 / work.parts));
+  if (work.parts == 1) expert_bwd_tile<GT, OT, 256, UA>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
+  else if (work.parts == 2) expert_bwd_tile<GT, OT, 128, UA>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
+  else expert_bwd_tile<GT, OT, 64, UA>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
+}
+
+// Rows of G as fp16, ng values each, zeros behind the N-th.
+template <int DT>
+__global__ __launch_bounds__(256) void k_expert_cast(const typename Elem<DT>::T* __restrict__ G, int64_t R, int N,
+                                                     int ng, bool vec, _Float16* __restrict__ out) {
+  const int chunks = ng / 8;
+  const int64_t items = R * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / chunks;
+    const int c = (int)(i - r * chunks) * 8;
+    const typename Elem<DT>::T* p = G + r * N + c;
+    v8h h = {};
+    if (vec) {
+      typename Elem<DT>::T e[8];
+      load8<DT>(p, e);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = to_half<DT>(e[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < N) h[j] = to_half<DT>(p[j]);
+    }
+    *reinterpret_cast<v8h*>(out + r * ng + c) = h;
+  }
+}
+
+static bool rows_as_fp16(const void* G, int dt, int64_t N) {
+  return dt == DT_F32 || N % 8 != 0 || (uintptr_t)G % 16 != 0;
+}
+size_t expert_bwd_bytes(const void* G, int dt, int64_t R, int64_t N) {
+  return rows_as_fp16(G, dt, N) ? (size_t)R * (size_t)((N + 7) / 8 * 8) * 2 : 0;
+}
+
+template <int GT, int OT>
+static hipError_t launch_bwd_t(const void* G, int ng, int R, const ExpertSegs& S, const int8_t* CB, const float* SCB,
+                               int N, int K, void* gX, hipStream_t st) {
+  constexpr int lds = 2 * (256 + 256) * 128;      // operand stages; the output tile takes their place
+  const bool ua = N % 8 != 0 || K % 4 != 0 || (uintptr_t)CB % 4 != 0 ||
+                  (N + (int64_t)128) * K >= ((int64_t)1 << 31) - 4096;
+  static std::atomic<uint64_t> lds_set[2];
+  auto kern = ua ? k_expert_bwd<GT, OT, true> : k_expert_bwd<GT, OT, false>;
+  const hipError_t e = lds_limit_once((const void*)kern, lds, lds_set[ua]);
   if (e != hipSuccess) return e;
-  const int64_t slots = expert_slots(R, S.n_seg, 256), total = slots * ((K + BK - 1) / BK);
-  hipLaunchKernelGGL(kern, expert_grid(total), dim3(512), lds, st, static_cast<const E*>(G), R, S, CB, SCB, N, K,
-                     (int)slots, total, static_cast<E*>(gX));
+  hipLaunchKernelGGL(kern, expert_grid(expert_groups(expert_slots(R, S.n_seg, 256), (K + 255) / 256)), dim3(512), lds,
+                     st, static_cast<const typename Elem<GT>::T*>(G), ng, R, S, CB, SCB, N, K,
+                     static_cast<typename Elem<OT>::T*>(gX));
   return hipGetLastError();
 }
 
 template <int DT>
-static hipError_t launch_bwd_t(const void* G, int R, const ExpertSegs& S, const int8_t* CB, const float* SCB, int N,
-                               int K, void* gX, hipStream_t st) {
-  typedef typename Elem<DT>::T E;
-  const bool vec = N % 8 == 0 && K % 4 == 0 && (uintptr_t)G % 16 == 0 && (uintptr_t)CB % 4 == 0 &&
-                   (uintptr_t)gX % (4 * sizeof(E)) == 0;
-  if constexpr (DT != DT_F32) {
-    const bool fits = (N + (int64_t)128) * K < ((int64_t)1 << 31) - 4096 && (int64_t)N * 512 < ((int64_t)1 << 31) - 4096;
-    if (vec && N > 0 && fits && R >= 128 * (int64_t)S.n_seg && R >= 512) {
-      // 256-wide tiles, unless they would fill at most half of the chip
-      const int64_t tiles = (R + 255) / 256 * (int64_t)((K + 255) / 256);
-      if (tiles > 128) return launch_bwd_w8<DT, 256>(G, R, S, CB, SCB, N, K, gX, st);
-      if (tiles >= 32) return launch_bwd_w8<DT, 128>(G, R, S, CB, SCB, N, K, gX, st);
-    }
-  }
-  const int64_t slots = expert_slots(R, S.n_seg, 128), total = slots * ((K + 127) / 128);
-  auto kern = vec ? k_expert_bwd<DT, true> : k_expert_bwd<DT, false>;
-  hipLaunchKernelGGL(kern, expert_grid(total), dim3(256), 0, st, static_cast<const E*>(G), R, S, CB, SCB, N, K,
-                     (int)slots, total, static_cast<E*>(gX));
+static hipError_t launch_cast(const void* G, int64_t R, int N, int ng, void* out, hipStream_t st) {
+  const int64_t items = R * (ng / 8);
+  const int64_t groups = (items + 255) / 256;
+  if (groups == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_expert_cast<DT>, dim3((unsigned)(groups < 4096 ? groups : 4096)), dim3(256), 0, st,
+                     static_cast<const typename Elem<DT>::T*>(G), R, N, ng, N % 8 == 0 && (uintptr_t)G % 16 == 0,
+                     static_cast<_Float16*>(out));
   return hipGetLastError();
 }
 
 hipError_t launch_expert_bwd(int dt, const void* G, int R, const ExpertSegs& S, const int8_t* CB, const float* SCB,
-                             int N, int K, void* gX, hipStream_t st) {
-  if (dt == DT_F32) return launch_bwd_t<DT_F32>(G, R, S, CB, SCB, N, K, gX, st);
-  if (dt == DT_F16) return launch_bwd_t<DT_F16>(G, R, S, CB, SCB, N, K, gX, st);
-  return launch_bwd_t<DT_BF16>(G, R, S, CB, SCB, N, K, gX, st);
+                             int N, int K, void* gX, void* ws, hipStream_t st) {
+  if (rows_as_fp16(G, dt, N)) {
+    const int ng = (N + 7) / 8 * 8;
+    hipError_t e;
+    if (dt == DT_F32) e = launch_cast<DT_F32>(G, R, N, ng, ws, st);
+    else if (dt == DT_F16) e = launch_cast<DT_F16>(G, R, N, ng, ws, st);
+    else e = launch_cast<DT_BF16>(G, R, N, ng, ws, st);
+    if (e != hipSuccess) return e;
+    if (dt == DT_F32) return launch_bwd_t<DT_F16, DT_F32>(ws, ng, R, S, CB, SCB, N, K, gX, st);
+    if (dt == DT_F16) return launch_bwd_t<DT_F16, DT_F16>(ws, ng, R, S, CB, SCB, N, K, gX, st);
+    return launch_bwd_t<DT_F16, DT_BF16>(ws, ng, R, S, CB, SCB, N, K, gX, st);
+  }
+  if (dt == DT_F16) return launch_bwd_t<DT_F16, DT_F16>(G, N, R, S, CB, SCB, N, K, gX, st);
+  return launch_bwd_t<DT_BF16, DT_BF16>(G, N, R, S, CB, SCB, N, K, gX, st);
 }
 
 }  // namespace i8l

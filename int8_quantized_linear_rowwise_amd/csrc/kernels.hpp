@@ -36,6 +36,11 @@ hipError_t launch_quantize(int dt, const void* X, int64_t rows, int cols, float 
                            hipStream_t st, const uint32_t* preflags = nullptr, int idx_cap = -1,
                            const OutlierWeights* ow = nullptr);
 
+// The same in one launch for a few rows (idx holds cols entries), where quantize_small_fits().
+bool quantize_small_fits(int64_t rows, int64_t cols, float tau);
+hipError_t launch_quantize_small(int dt, const void* X, int rows, int cols, float tau, int8_t* codes, float* scale,
+                                 int32_t* idx, int32_t* count, uint16_t* sub, int cap, hipStream_t st);
+
 // Producer of a quantizer input: A = D(SiLU(H)) and A's column flag words
 // (quant_scratch_words(rows, cols) words) for tau.
 hipError_t launch_silu_flags(int dt, const void* H, int64_t rows, int cols, float tau, void* A, uint32_t* flags,
@@ -126,9 +131,10 @@ struct ExpertQuantized {
 hipError_t launch_expert_fwd(int dt, const ExpertQuantized& Q, const void* X, int T, const int32_t* rows, int R,
                              const ExpertSegs& S, const int8_t* CB, const float* SCB, int N, int K, void* out,
                              hipStream_t st);
-// gX (R x K) = D(fp16(G) Wdq[expert]), G: R x N.
+// gX (R x K) = D(fp16(G) Wdq[expert]), G: R x N. ws: expert_bwd_bytes() bytes, 16-byte aligned.
+size_t expert_bwd_bytes(const void* G, int dt, int64_t R, int64_t N);
 hipError_t launch_expert_bwd(int dt, const void* G, int R, const ExpertSegs& S, const int8_t* CB, const float* SCB,
-                             int N, int K, void* gX, hipStream_t st);
+                             int N, int K, void* gX, void* ws, hipStream_t st);
 // out[t] = D(base[t] + sum_j gate[t, j] Y[position[t, j]]) and its gradients.
 hipError_t launch_expert_combine(int dt, const void* Y, int R, int N, const int32_t* position, const float* gate,
                                  const void* base, int T, int k, void* out, hipStream_t st);

@@ -668,6 +668,100 @@ __global__ __launch_bounds__(256) void k_rowquant(const typename Elem<DT>::T* __
 }
 
 // ---------------------------------------------------------------------------
+// Few rows, in one launch: a workgroup for each row, which finds the column
+// flags of all rows by itself (they are read from L2, 512 KB at most) instead
+// of waiting for a launch that does. Same codes, scales and outlier values as
+// the two launches. At most 8192 columns, so that a row stays in registers.
+// 64 x 2048 fp16: 7.3 us against 4.8 + 6.4 and the gap between two launches;
+// 1 x 4096 bf16: 4.3 us against 3.8 + 6.1.
+constexpr int QS_THREADS = 512, QS_CHUNKS = 2;
+
+template <int DT, bool VEC>
+__global__ __launch_bounds__(QS_THREADS) void k_quant_small(const typename Elem<DT>::T* __restrict__ X, int rows,
+                                                            int cols, float tau, int cps, int8_t* __restrict__ codes,
+                                                            float* __restrict__ scale, int32_t* __restrict__ idx,
+                                                            int idx_cap, int32_t* __restrict__ count,
+                                                            uint16_t* __restrict__ sub, int cap) {
+#pragma clang fp contract(off)
+  __shared__ uint32_t smask[256];
+  __shared__ int32_t sprefix[256];
+  __shared__ int wsum[QS_THREADS / 64];
+  __shared__ uint32_t red[QS_THREADS / 64];
+  __shared__ int slist[1];
+  constexpr int NW = (DT == DT_F32) ? 8 : 4;
+  const int t = threadIdx.x, nchunk = (cols + 7) >> 3, nwords = (cols + 31) >> 5;
+  const int64_t row = blockIdx.x;
+  v4u ra[QS_CHUNKS], rb[QS_CHUNKS] = {};
+#pragma unroll
+  for (int i = 0; i < QS_CHUNKS; ++i)
+    if (t + i * QS_THREADS < nchunk) load_raw8<DT>(X + row * cols, (t + i * QS_THREADS) * 8, cols, VEC, ra[i], rb[i]);
+  if (t < 256) smask[t] = 0u;
+  __syncthreads();
+  // 2^cps threads side by side on a row, the others on the next rows
+  const int g0 = t >> cps, gs = QS_THREADS >> cps;
+  for (int ci = t & ((1 << cps) - 1); ci < nchunk; ci += QS_THREADS) {
+    uint32_t m[NW] = {};
+    for (int r = g0; r < rows; r += 8 * gs) {
+      v4u a[8], b[8] = {};
+#pragma unroll
+      for (int u = 0; u < 8; ++u)      // past the last row: that row again
+        load_raw8<DT>(X + (int64_t)min(r + u * gs, rows - 1) * cols, ci * 8, cols, VEC, a[u], b[u]);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if constexpr (DT == DT_F32) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            m[d] = max(m[d], a[u][d] & 0x7fffffffu);
+            m[d + 4] = max(m[d + 4], b[u][d] & 0x7fffffffu);
+          }
+        } else {
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            m[d] = __builtin_bit_cast(uint32_t,
+                                      __builtin_elementwise_max(__builtin_bit_cast(us2, m[d]),
+                                                                __builtin_bit_cast(us2, a[u][d] & 0x7fff7fffu)));
+        }
+      }
+    }
+    uint32_t byte = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint32_t v;
+      if constexpr (DT == DT_F32) v = m[e];
+      else v = (m[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+      if (mag_to_half_value<DT>(v) > tau) byte |= 1u << e;
+    }
+    if (byte) atomicOr(&smask[ci >> 2], byte << (8 * (ci & 3)));
+  }
+  __syncthreads();
+  mask_prefix(smask, sprefix, wsum, nwords, row == 0, idx, idx_cap, count, slist, 0);
+  uint32_t om[QS_CHUNKS], mx = 0u;
+#pragma unroll
+  for (int i = 0; i < QS_CHUNKS; ++i) {
+    const int ci = t + i * QS_THREADS;
+    om[i] = 0u;
+    if (ci < nchunk) {
+      om[i] = chunk_mask_bits(smask, ci);
+      mx = max(mx, chunk_absmax<DT, VEC>(ra[i], rb[i], om[i], true));
+    }
+  }
+  mx = wave_umax(mx);
+  if ((t & 63) == 0) red[t >> 6] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < QS_THREADS / 64; ++w) mx = max(mx, red[w]);
+  const float s = mag_to_half_value<DT>(mx);
+  const float inv = (s > 0.0f) ? (127.0f / s) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < QS_CHUNKS; ++i) {
+    const int ci = t + i * QS_THREADS;
+    if (ci < nchunk)
+      chunk_emit<DT, VEC>(codes, sub, cap, cols, smask, sprefix, row, ci, ra[i], rb[i], inv, om[i], true);
+  }
+  if (t == 0) scale[row] = s;
+}
+
+// ---------------------------------------------------------------------------
 // host-side launch sequence
 
 static bool aligned(const void* p, int a) { return ((uintptr_t)p % (uintptr_t)a) == 0; }
@@ -751,6 +845,32 @@ static hipError_t launch_quantize_t(const void* Xv, int64_t rows, int cols, floa
   }
 #undef I8L_RQ
   return hipGetLastError();
+}
+
+bool quantize_small_fits(int64_t rows, int64_t cols, float tau) {
+  return rows > 0 && rows <= 64 && cols > 0 && cols <= 8 * QS_THREADS * QS_CHUNKS && rows * cols <= (1 << 17) &&
+         tau > 0.0f && tau < __builtin_huge_valf();
+}
+
+template <int DT>
+static hipError_t launch_quantize_small_t(const void* Xv, int rows, int cols, float tau, int8_t* codes, float* scale,
+                                          int32_t* idx, int32_t* count, uint16_t* sub, int cap, hipStream_t st) {
+  typedef typename Elem<DT>::T T;
+  const T* X = static_cast<const T*>(Xv);
+  const bool vec = (cols % 8 == 0) && aligned(X, 16) && aligned(codes, 8);
+  int cps = 0;
+  while ((1 << cps) < (cols + 7) / 8 && (1 << cps) < QS_THREADS) ++cps;
+  auto kern = vec ? k_quant_small<DT, true> : k_quant_small<DT, false>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)rows), dim3(QS_THREADS), 0, st, X, rows, cols, tau, cps, codes, scale, idx,
+                     cols, count, sub, cap);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_small(int dt, const void* X, int rows, int cols, float tau, int8_t* codes, float* scale,
+                                 int32_t* idx, int32_t* count, uint16_t* sub, int cap, hipStream_t st) {
+  if (dt == DT_F32) return launch_quantize_small_t<DT_F32>(X, rows, cols, tau, codes, scale, idx, count, sub, cap, st);
+  if (dt == DT_F16) return launch_quantize_small_t<DT_F16>(X, rows, cols, tau, codes, scale, idx, count, sub, cap, st);
+  return launch_quantize_small_t<DT_BF16>(X, rows, cols, tau, codes, scale, idx, count, sub, cap, st);
 }
 
 hipError_t launch_quantize(int dt, const void* X, int64_t rows, int cols, float tau, int8_t* codes, float* scale,

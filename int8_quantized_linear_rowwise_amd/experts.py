@@ -105,7 +105,8 @@ def expert_forward(X: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor, seg_off
 
 
 def expert_backward(G: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor, seg_offsets: torch.Tensor,
-                    seg_expert: Optional[torch.Tensor] = None, grad_X: Optional[torch.Tensor] = None):
+                    seg_expert: Optional[torch.Tensor] = None, grad_X: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None):
     """grad_X[r] = fp16(G[r]) @ dequant(CB of r's expert), one row for each row of G (R x N), in G's dtype; 0 for rows
     without an expert. The rows of a token are added up by expert_combine without a gate."""
     if G.dim() != 2:
@@ -119,10 +120,13 @@ def expert_backward(G: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor, seg_of
     dev = _gpu(G, "G")
     if grad_X is None:
         grad_X = _empty((R, K), G.dtype, G.device)
+    g, code = _ptr(G, "G", dev), _code(G)
+    ws = _workspace(workspace, lib.int8_expert_backward_workspace_bytes(g, code, R, N), G.device, dev)
     with _on_gpu(dev):
-        check(lib.int8_expert_backward(_ptr(G, "G", dev), _code(G), R, N, _ptr(CB, "CB", dev), _ptr(SCB, "SCB", dev),
+        check(lib.int8_expert_backward(g, code, R, N, _ptr(CB, "CB", dev), _ptr(SCB, "SCB", dev),
                                        E, K, _ptr(seg_offsets, "seg_offsets", dev),
                                        _ptr(seg_expert, "seg_expert", dev), S, _ptr(grad_X, "grad_X", dev),
+                                       _ptr(ws, "workspace", dev), 0 if ws is None else ws.numel(),
                                        _raw_stream(dev)),
               "int8_expert_backward")
     return grad_X

@@ -59,7 +59,7 @@ def test_forward_host_errors(L):  # noqa: F811
 
 def test_backward_host_errors(L):  # noqa: F811
     call = caller(L.lib.int8_expert_backward, dict(G=FAKE, dt=1, R=16, N=32, CB=FAKE, SCB=FAKE, E=4, K=64, off=FAKE,
-                                                   ids=None, S=4, gX=FAKE, st=None))
+                                                   ids=None, S=4, gX=FAKE, ws=None, wsb=0, st=None))
     assert call(dt=7) == L.I8L_EDTYPE
     for k in ("R", "N", "E", "K", "S"):
         assert call(**{k: -1}) == L.I8L_EINVAL, k
@@ -67,6 +67,13 @@ def test_backward_host_errors(L):  # noqa: F811
         assert call(**{k: 0}) == L.I8L_EINVAL, k
     assert call(R=(1 << 24) + 1) == L.I8L_ESHAPE and call(S=65537) == L.I8L_ESHAPE
     assert call(R=0, G=0, gX=0) == L.I8L_OK and call(K=0, gX=0, CB=0) == L.I8L_OK
+    need = L.lib.int8_expert_backward_workspace_bytes
+    assert need(FAKE, 1, 16, 32) == 0 and need(FAKE + 2, 1, 16, 32) == 1024
+    assert need(FAKE, 2, 16, 33) == 1280 and need(FAKE, 0, 16, 32) == 1024
+    assert need(FAKE, 1, -1, 32) == 0 and need(FAKE, 5, 16, 32) == 0
+    for bad in (dict(dt=0), dict(N=33, dt=2), dict(G=FAKE + 2)):
+        assert call(**bad) == L.I8L_EWORKSPACE and call(**bad, ws=FAKE, wsb=1023) == L.I8L_EWORKSPACE
+        assert call(**bad, ws=FAKE + 16, wsb=1 << 20) == L.I8L_EINVAL
 
 
 def test_combine_host_errors(L):  # noqa: F811

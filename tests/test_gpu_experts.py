@@ -123,7 +123,9 @@ def test_forward_outlier_columns(I8, dt, outliers):
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("T,k,E,K,N,outliers", [(1500, 2, 4, 272, 1100, 3), (1500, 2, 4, 272, 4100, 40),
                                                 (800, 2, 3, 64, 3000, 1), (2100, 3, 9, 400, 2304, 17),
-                                                (600, 1, 1, 16, 5000, 0)])
+                                                (600, 1, 1, 16, 5000, 0), (1500, 2, 4, 271, 1101, 20),
+                                                (900, 2, 3, 1001, 530, 3), (700, 1, 2, 17, 4099, 1),
+                                                (800, 1, 2, 15, 600, 1), (520, 1, 1, 129, 257, 0)])
 def test_forward_many_rows(I8, dt, T, k, E, K, N, outliers):
     """Sizes that fill tiles of 256 rows, with contractions and widths that end inside one, more outlier columns than
     fit beside the tile, and experts of very different numbers of rows."""
@@ -238,7 +240,9 @@ def test_backward_segments(I8, dt, off):
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("T,k,E,N,K", [(1500, 2, 4, 264, 1100), (1500, 2, 4, 136, 4100), (800, 2, 3, 64, 3000),
-                                       (2100, 3, 9, 400, 2304), (600, 1, 1, 8, 5000)])
+                                       (2100, 3, 9, 400, 2304), (600, 1, 1, 8, 5000), (1500, 2, 4, 263, 1101),
+                                       (800, 2, 3, 65, 3001), (700, 1, 2, 1001, 530), (700, 2, 3, 1, 259),
+                                       (600, 1, 2, 40, 3), (520, 1, 1, 12, 1), (600, 1, 2, 100, 6)])
 def test_backward_many_rows(I8, dt, T, k, E, N, K):
     off, _, _ = X.sort(X.choices(T, k, E, 7, 0.1, skew=1.5), E)
     run_backward(I8, dt, T * k, N, K, off.tolist())
