@@ -168,7 +168,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
       for (int j = 0; j < TJ; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(F[b][i], F[b][TI + j], acc[i][j], 0, 0, 0);
   };
-  // each matrix instruction of a phase is followed by one fragment read of the next and one of `w` tile writes and loads
+  // each matrix instruction of a phase is followed by a fragment read of the next and by its share of the tile traffic
   auto spread = [&](auto writes) {
 #pragma unroll
     for (int q = 0; q < TI * TJ; ++q) {
@@ -221,8 +221,8 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
     }
   }
 
-  // lane (lr, lg), register r of tile (i, j): feature wn BN / 2 + i 32 + (r / 4) 8 + lg 4 + r % 4, row wm 64 + j 32 + lr;
-  // the accumulators become fp32 in place
+  // lane (lr, lg), register r of tile (i, j): feature wn BN / 2 + i 32 + (r / 4) 8 + lg 4 + r % 4, row wm 64 + j 32 + lr
+  // (the accumulators become fp32 in place)
   const int nl = wn * (BN / 2), ml = wm * 64;
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
