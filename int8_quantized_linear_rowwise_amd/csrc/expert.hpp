@@ -154,22 +154,29 @@ __device__ __forceinline__ int row_token(const int32_t* __restrict__ rows, int r
   return (t >= 0 && t < T) ? t : -1;
 }
 
-// Bytes k .. k + 15 of a row of K bytes at any address, zero past its end: one
-// load of 16 bytes, which global memory takes unaligned; the last piece of a row
-// is loaded so that it ends with the row and shifted into place.
-__device__ __forceinline__ v4u bytes16(const int8_t* row, int k, int K) {
-  unsigned __int128 v = 0;
-  if (k + 16 <= K) {
-    __builtin_memcpy(&v, row + k, 16);
-  } else if (k < K) {
-    if (K >= 16) {
-      __builtin_memcpy(&v, row + K - 16, 16);
-      v >>= 8 * (k + 16 - K);
-    } else {
-      for (int b = 0; b < K; ++b) v |= (unsigned __int128)(uint8_t)row[b] << (8 * b);   // k is 0
-    }
+// 16 bytes at any address (global memory takes unaligned loads).
+__device__ __forceinline__ v4u bytes16(const int8_t* p) {
+  v4u v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+// Rows of K >= 16 bytes that are no multiple of 16: the last piece is loaded so
+// that it ends with the row (at tail_at(k)), in both operands alike; in the
+// codes, the bytes that the piece before holds already are cleared.
+__device__ __forceinline__ int tail_at(int k, int K) { return min(k, K - 16); }
+__device__ __forceinline__ v4u tail_clear(v4u v, int k, int K) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int bits = min(max(8 * (k - tail_at(k, K) - 4 * x), 0), 32);
+    v[x] &= (uint32_t)(0xffffffffull << bits);
   }
-  return __builtin_bit_cast(v4u, v);
+  return v;
+}
+// Bytes k .. k + 15 of a row of fewer than 16, zero past its end.
+__device__ __forceinline__ v4u short_row(const int8_t* row, int k, int K) {
+  v4u v = {0u, 0u, 0u, 0u};
+  for (int b = k; b < K; ++b) v[b >> 2] |= (uint32_t)(uint8_t)row[b] << (8 * (b & 3));
+  return v;
 }
 
 // fp16 outlier values j0 .. j0 + 7 of token t (zero at and past cnt, or for no

@@ -21,10 +21,11 @@ namespace i8l {
 
 // G is fp16 or bf16 (GT), R rows of ng values (N, or N rounded up to 8 with
 // zeros behind it); the result is OT.
-// UA: N is no multiple of 8 or K of 4, the weights lie off 4-byte borders, or an
-// expert's weight passes 32-bit offsets: loads at any address. A row's last
-// piece is loaded so that it ends with the row, and shifted into place.
-template <int GT, int OT, int BK, bool UA>
+// AL: 0, N is a multiple of 8, K of 4, the weights lie on 4-byte borders and an
+// expert's weight stays within 32-bit offsets; 1, but for N; 2, none of that:
+// loads at any address, a row's last piece loaded so that it ends with the row
+// and shifted into place.
+template <int GT, int OT, int BK, int AL>
 __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __restrict__ G, int ng,
                                                 const ExpertTile& tile, int k0, const int8_t* __restrict__ CBall,
                                                 const float* __restrict__ SCBall, int N, int K,
@@ -43,8 +44,8 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
   const float* SCB = SCBall + (int64_t)tile.expert * N;
 
   const __amdgpu_buffer_rsrc_t rG = make_rsrc(G + (int64_t)r0 * ng, (r1 - r0) * ng * 2);
-  const __amdgpu_buffer_rsrc_t rW = make_rsrc(CB + k0, UA ? 0 : N * K - k0);
-  const __amdgpu_buffer_rsrc_t rS = make_rsrc(SCB, UA ? 0 : N * 4);
+  const __amdgpu_buffer_rsrc_t rW = make_rsrc(CB + k0, AL == 2 ? 0 : N * K - k0);
+  const __amdgpu_buffer_rsrc_t rS = make_rsrc(SCB, AL == 2 ? 0 : N * 4);
 
   // gradient slots: 16-byte chunk gc of rows grow + 64 i (i < 4)
   const int grow = tid >> 3, gc = tid & 7;
@@ -54,8 +55,8 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
   constexpr int QUADS = BK / 4;                // lanes side by side on a weight row
   const int kq = lane % QUADS, wh = WR * (lane / QUADS);
   const int wvoff = 4 * kq + wh * K;
-  const int ku = min(k0 + 4 * kq, K - 4);      // UA: where a lane loads, and what it shifts out
-  const int shift = UA ? min(8 * (k0 + 4 * kq - ku), 31) : 0;
+  const int ku = min(k0 + 4 * kq, K - 4);      // AL 2: where a lane loads, and what it shifts out
+  const int shift = AL == 2 ? min(8 * (k0 + 4 * kq - ku), 31) : 0;
   int wwoff[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -73,7 +74,7 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
   float SG[WR];
   auto load_w = [&](int nc) {
     const int n8 = nc + 8 * wave;
-    if constexpr (UA) {
+    if constexpr (AL == 2) {
 #pragma unroll
       for (int e = 0; e < WR; ++e) {
         const int n = n8 + wh + e;
@@ -90,7 +91,11 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
       for (int e = 0; e < WR; ++e) RW[e] = __builtin_amdgcn_raw_buffer_load_b32(rW, wvoff, (n8 + e) * K, 0);
       // N % 8 == 0: the eight rows from n8 are all in the matrix or all past it
       const int so = (n8 < N) ? 4 * (n8 + wh) : OOB_OFFSET;
-      if constexpr (WR == 2) {
+      if constexpr (AL == 1) {
+#pragma unroll
+        for (int e = 0; e < WR; ++e)
+          SG[e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rS, 4 * (n8 + wh + e), 0, 0));
+      } else if constexpr (WR == 2) {
         const v2f sv = __builtin_bit_cast(v2f, __builtin_amdgcn_raw_buffer_load_b64(rS, so, 0, 0));
         SG[0] = sv[0];
         SG[1] = sv[1];
@@ -119,8 +124,8 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
       uint32_t h[WR / 2];
 #pragma unroll
       for (int e = 0; e < WR / 2; ++e) {
-        const uint32_t q0 = UA && K >= 4 ? RW[2 * e] >> shift : RW[2 * e];
-        const uint32_t q1 = UA && K >= 4 ? RW[2 * e + 1] >> shift : RW[2 * e + 1];
+        const uint32_t q0 = AL == 2 && K >= 4 ? RW[2 * e] >> shift : RW[2 * e];
+        const uint32_t q1 = AL == 2 && K >= 4 ? RW[2 * e + 1] >> shift : RW[2 * e + 1];
         const float w0 = (float)(int)(int8_t)(q0 >> (8 * c));
         const float w1 = (float)(int)(int8_t)(q1 >> (8 * c));
         h[e] = f32x2_to_f16x2(w0 * sg[2 * e], w1 * sg[2 * e + 1]);
@@ -261,7 +266,7 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
 }
 
 // Tiles 256 wide; the last ones in narrower parts (expert_work).
-template <int GT, int OT, bool UA>
+template <int GT, int OT, int AL>
 __global__ __launch_bounds__(512, 1) void k_expert_bwd(const typename Elem<GT>::T* __restrict__ G, int ng, int R,
                                                        ExpertSegs S, const int8_t* __restrict__ CB,
                                                        const float* __restrict__ SCB, int N, int K,
@@ -274,15 +279,15 @@ __global__ __launch_bounds__(512, 1) void k_expert_bwd(const typename Elem<GT>::
   const int k0 = work.tc * 256 + work.part * (256 / work.parts);
   if (tile.r0 >= tile.r1 || k0 >= K) return;
   if (tile.expert < 0 || N == 0) return expert_zeros(gX, K, tile.r0, tile.r1, k0, min(K, k0 + 256 / work.parts));
-  if (work.parts == 1) expert_bwd_tile<GT, OT, 256, UA>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
-  else if (work.parts == 2) expert_bwd_tile<GT, OT, 128, UA>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
-  else expert_bwd_tile<GT, OT, 64, UA>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
+  if (work.parts == 1) expert_bwd_tile<GT, OT, 256, AL>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
+  else if (work.parts == 2) expert_bwd_tile<GT, OT, 128, AL>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
+  else expert_bwd_tile<GT, OT, 64, AL>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
 }
 
 // Rows of G as fp16, ng values each, zeros behind the N-th.
 template <int DT>
 __global__ __launch_bounds__(256) void k_expert_cast(const typename Elem<DT>::T* __restrict__ G, int64_t R, int N,
-                                                     int ng, bool vec, _Float16* __restrict__ out) {
+                                                     int ng, _Float16* __restrict__ out) {
   const int chunks = ng / 8;
   const int64_t items = R * chunks;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
@@ -290,9 +295,9 @@ __global__ __launch_bounds__(256) void k_expert_cast(const typename Elem<DT>::T*
     const int c = (int)(i - r * chunks) * 8;
     const typename Elem<DT>::T* p = G + r * N + c;
     v8h h = {};
-    if (vec) {
+    if (c + 8 <= N) {      // at any address
       typename Elem<DT>::T e[8];
-      load8<DT>(p, e);
+      __builtin_memcpy(e, p, sizeof(e));
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[j] = to_half<DT>(e[j]);
     } else {
@@ -315,11 +320,11 @@ template <int GT, int OT>
 static hipError_t launch_bwd_t(const void* G, int ng, int R, const ExpertSegs& S, const int8_t* CB, const float* SCB,
                                int N, int K, void* gX, hipStream_t st) {
   constexpr int lds = 2 * (256 + 256) * 128;      // operand stages; the output tile takes their place
-  const bool ua = N % 8 != 0 || K % 4 != 0 || (uintptr_t)CB % 4 != 0 ||
-                  (N + (int64_t)128) * K >= ((int64_t)1 << 31) - 4096;
-  static std::atomic<uint64_t> lds_set[2];
-  auto kern = ua ? k_expert_bwd<GT, OT, true> : k_expert_bwd<GT, OT, false>;
-  const hipError_t e = lds_limit_once((const void*)kern, lds, lds_set[ua]);
+  const bool words = K % 4 == 0 && (uintptr_t)CB % 4 == 0 && (N + (int64_t)128) * K < ((int64_t)1 << 31) - 4096;
+  const int al = !words ? 2 : N % 8 != 0 ? 1 : 0;
+  static std::atomic<uint64_t> lds_set[3];
+  auto kern = al == 2 ? k_expert_bwd<GT, OT, 2> : al == 1 ? k_expert_bwd<GT, OT, 1> : k_expert_bwd<GT, OT, 0>;
+  const hipError_t e = lds_limit_once((const void*)kern, lds, lds_set[al]);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, expert_grid(expert_groups(expert_slots(R, S.n_seg, 256), (K + 255) / 256)), dim3(512), lds,
                      st, static_cast<const typename Elem<GT>::T*>(G), ng, R, S, CB, SCB, N, K,
@@ -333,7 +338,7 @@ static hipError_t launch_cast(const void* G, int64_t R, int N, int ng, void* out
   const int64_t groups = (items + 255) / 256;
   if (groups == 0) return hipSuccess;
   hipLaunchKernelGGL(k_expert_cast<DT>, dim3((unsigned)(groups < 4096 ? groups : 4096)), dim3(256), 0, st,
-                     static_cast<const typename Elem<DT>::T*>(G), R, N, ng, N % 8 == 0 && (uintptr_t)G % 16 == 0,
+                     static_cast<const typename Elem<DT>::T*>(G), R, N, ng,
                      static_cast<_Float16*>(out));
   return hipGetLastError();
 }

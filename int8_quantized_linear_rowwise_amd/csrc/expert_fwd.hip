@@ -25,16 +25,16 @@ namespace i8l {
 // tokens, so the gather costs nothing in the loop. Waves whose 64 rows all lie
 // past the segment only move tiles: a tile of 100 rows takes about half the
 // time of a full one.
-// UA: K (16 at least) is no multiple of 16, the weights lie off 16-byte borders,
-// or the codes pass 2^31 bytes: 16-byte loads at any address instead of buffer
-// loads. A row's last piece is loaded so that it ends with the row, in both
-// operands alike; what it holds of the piece before is cleared in the weights.
+// AL, what K (16 at least) and the weights' address are multiples of: 16; 4, the
+// same loads and the last piece of a row as tail_at has it; 1, or where the codes
+// pass 2^31 bytes, 16-byte loads at any address. 4096 tokens, two of eight
+// experts, 4096 -> 11008 449 us, 4088 -> 11000 AL4 us, 4095 -> 11007 AL1 us.
 constexpr int EF_OPAN = 2 * 256 * 32;                 // outlier panels P[n][16], Q[row][16] (fp16)
 constexpr int EF_SCALES = (256 + 256) * 4;            // SCB / 127^2, SCA
 constexpr int EF_STAGES = 2 * (256 + 256) * 128;      // operand stages; the output tile takes their place
 constexpr int EF_LDS = EF_STAGES + EF_OPAN + EF_SCALES;
 
-template <int DT, int BN, bool UA>
+template <int DT, int BN, int AL>
 __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const typename Elem<DT>::T* __restrict__ X,
                                                 int T, const int32_t* __restrict__ rows, const ExpertTile& tile,
                                                 int n0, const int8_t* __restrict__ CBall,
@@ -61,26 +61,22 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
   const int pb = wn * (BN / 2) * BK, qb = AOFF + wm * 64 * BK;
 
   v4u RB[NB], RA[4];
-  const __amdgpu_buffer_rsrc_t rB = make_rsrc(CB + (int64_t)n0 * K, UA ? 0 : min(BN, N - n0) * K);
+  const __amdgpu_buffer_rsrc_t rB = make_rsrc(CB + (int64_t)n0 * K, AL == 1 ? 0 : min(BN, N - n0) * K);
   const int voff = lrow * K + 16 * lc;
   int boff[NB];
   const int8_t* B0 = CB + (int64_t)n0 * K;
 #pragma unroll
   for (int i = 0; i < NB; ++i) boff[i] = (min(n0 + lrow + 64 * i, N - 1) - n0) * K;   // past N: not stored
   auto load_b = [&](int kt) {
-    if constexpr (UA) {
-      const int k = kt + 16 * lc, at = min(k, K - 16);
+    if constexpr (AL == 1) {
+      const int at = tail_at(kt + 16 * lc, K);
 #pragma unroll
-      for (int i = 0; i < NB; ++i) __builtin_memcpy(&RB[i], B0 + (boff[i] + at), 16);
-      if (kt + BK > K) {
+      for (int i = 0; i < NB; ++i) RB[i] = bytes16(B0 + (boff[i] + at));
+    } else if constexpr (AL == 4) {
+      const int v = lrow * K + tail_at(kt + 16 * lc, K);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int bits = min(max(8 * (k - at - 4 * x), 0), 32);      // of the word: already in the piece before
-          const uint32_t keep = (uint32_t)(0xffffffffull << bits);
-#pragma unroll
-          for (int i = 0; i < NB; ++i) RB[i][x] &= keep;
-        }
-      }
+      for (int i = 0; i < NB; ++i)
+        RB[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rB, v, 64 * i * K, 0));
     } else {
       const int v = (kt + 16 * lc < K) ? voff : OOB_OFFSET;
 #pragma unroll
@@ -89,21 +85,30 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
     }
   };
   load_b(0);
-  const __amdgpu_buffer_rsrc_t rA = make_rsrc(Q.CA, UA ? 0 : T * K);
+  const __amdgpu_buffer_rsrc_t rA = make_rsrc(Q.CA, AL == 1 ? 0 : T * K);
   int aoff[4];
   const int8_t* pA[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = r0 + lrow + 64 * i;
     const int t = r < r1 ? row_token(rows, r, T) : -1;
-    if constexpr (UA) pA[i] = Q.CA + (int64_t)max(t, 0) * K;      // no token: its scale is 0
+    // no token: its scale is 0, whatever its codes
+    if constexpr (AL == 1) pA[i] = Q.CA + (int64_t)max(t, 0) * K;
+    else if constexpr (AL == 4) aoff[i] = max(t, 0) * K;
     else aoff[i] = t >= 0 ? t * K + 16 * lc : OOB_OFFSET;
   }
   auto load_a = [&](int kt) {
-    if constexpr (UA) {
-      const int at = min(kt + 16 * lc, K - 16);
+    if constexpr (AL < 16) {
+      const int k = kt + 16 * lc, at = tail_at(k, K);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) __builtin_memcpy(&RA[i], pA[i] + at, 16);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (AL == 1) RA[i] = bytes16(pA[i] + at);
+        else RA[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rA, aoff[i] + at, 0, 0));
+      }
+      if (kt + BK > K) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) RA[i] = tail_clear(RA[i], k, K);
+      }
     } else {
       const bool in = kt + 16 * lc < K;
 #pragma unroll
@@ -301,7 +306,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
 }
 
 // Tiles 256 wide; the last ones in narrower parts (expert_work).
-template <int DT, bool UA>
+template <int DT, int AL>
 __global__ __launch_bounds__(512, 1) void k_expert_fwd(ExpertQuantized Q, const typename Elem<DT>::T* __restrict__ X,
                                                        int T, const int32_t* __restrict__ rows, int R, ExpertSegs S,
                                                        const int8_t* __restrict__ CB, const float* __restrict__ SCB,
@@ -314,9 +319,9 @@ __global__ __launch_bounds__(512, 1) void k_expert_fwd(ExpertQuantized Q, const 
   const int n0 = work.tc * 256 + work.part * (256 / work.parts);
   if (tile.r0 >= tile.r1 || n0 >= N) return;
   if (tile.expert < 0) return expert_zeros(out, N, tile.r0, tile.r1, n0, min(N, n0 + 256 / work.parts));
-  if (work.parts == 1) expert_fwd_tile<DT, 256, UA>(Q, X, T, rows, tile, n0, CB, SCB, N, K, out, smem);
-  else if (work.parts == 2) expert_fwd_tile<DT, 128, UA>(Q, X, T, rows, tile, n0, CB, SCB, N, K, out, smem);
-  else expert_fwd_tile<DT, 64, UA>(Q, X, T, rows, tile, n0, CB, SCB, N, K, out, smem);
+  if (work.parts == 1) expert_fwd_tile<DT, 256, AL>(Q, X, T, rows, tile, n0, CB, SCB, N, K, out, smem);
+  else if (work.parts == 2) expert_fwd_tile<DT, 128, AL>(Q, X, T, rows, tile, n0, CB, SCB, N, K, out, smem);
+  else expert_fwd_tile<DT, 64, AL>(Q, X, T, rows, tile, n0, CB, SCB, N, K, out, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -332,11 +337,11 @@ __global__ __launch_bounds__(512, 1) void k_expert_fwd(ExpertQuantized Q, const 
 // that eight workgroups on a compute unit cover each other's beginnings and
 // ends: 512 bytes at a time, five workgroups, took 28 us for one token of two
 // 4096 -> 11008 experts instead of 22.
-// UA: as above, through registers; any K.
+// AL: as above; 1 goes through registers and takes any K.
 typedef __attribute__((address_space(3))) void* lds_ptr;
 constexpr int ET_KC = 256;      // bytes of a row a wave takes at a time
-template <int DT, bool UA>
-__global__ __launch_bounds__(256, UA ? 4 : 8) void k_expert_fwd_thin(ExpertQuantized Q,
+template <int DT, int AL>
+__global__ __launch_bounds__(256, AL == 1 ? 6 : 8) void k_expert_fwd_thin(ExpertQuantized Q,
                                                             const typename Elem<DT>::T* __restrict__ X, int T,
                                                             const int32_t* __restrict__ rows, int R, ExpertSegs S,
                                                             const int8_t* __restrict__ CBall,
@@ -358,21 +363,22 @@ __global__ __launch_bounds__(256, UA ? 4 : 8) void k_expert_fwd_thin(ExpertQuant
   if (tile.expert < 0) return expert_zeros(out, N, tile.r0, tile.r1, n0, min(N, n0 + BN));
   const int8_t* CB = CBall + (int64_t)tile.expert * N * K;
   const float* SCB = SCBall + (int64_t)tile.expert * N;
-  const __amdgpu_buffer_rsrc_t rB = make_rsrc(CB + (int64_t)n0 * K, UA ? 0 : min(BN, N - n0) * K);
+  const __amdgpu_buffer_rsrc_t rB = make_rsrc(CB + (int64_t)n0 * K, AL == 1 ? 0 : min(BN, N - n0) * K);
   const int nc = (K + ET_KC - 1) / ET_KC;
 
   int8_t* mine = sw[wave];
+  v4u W[ET_KC / 64];      // AL 1
   auto load_w = [&](int c) {
 #pragma unroll
     for (int i = 0; i < ET_KC / 64; ++i) {
       const int row = (64 / LPR) * i + lane / LPR;
       const int k = c * ET_KC + 16 * ((lane % LPR) ^ row);
-      if constexpr (UA) {
-        const int n = min(n0 + row, N - 1);     // past N: not stored
-        *reinterpret_cast<v4u*>(mine + i * 1024 + lane * 16) = bytes16(CB + (int64_t)n * K, k, K);
+      if constexpr (AL == 1) {
+        const int8_t* p = CB + (int64_t)min(n0 + row, N - 1) * K;     // past N: not stored
+        W[i] = K >= 16 ? bytes16(p + tail_at(k, K)) : short_row(p, k, K);
       } else {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr)(mine + i * 1024), 16,
-                                                 k < K ? row * K + k : OOB_OFFSET, 0, 0, 0);
+        const int at = AL == 4 ? row * K + tail_at(k, K) : k < K ? row * K + k : OOB_OFFSET;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr)(mine + i * 1024), 16, at, 0, 0, 0);
       }
     }
   };
@@ -405,8 +411,23 @@ __global__ __launch_bounds__(256, UA ? 4 : 8) void k_expert_fwd_thin(ExpertQuant
       a[s] = v4i{0, 0, 0, 0};
       if (t >= 0) {
         const int8_t* p = Q.CA + (int64_t)t * K;
-        if constexpr (UA) a[s] = __builtin_bit_cast(v4i, bytes16(p, k, K));
-        else if (k < K) a[s] = *reinterpret_cast<const v4i*>(p + k);
+        if constexpr (AL == 16) {
+          if (k < K) a[s] = *reinterpret_cast<const v4i*>(p + k);
+        } else {
+          const v4u v = K >= 16 ? bytes16(p + tail_at(k, K)) : short_row(p, k, K);
+          a[s] = __builtin_bit_cast(v4i, v);
+        }
+      }
+    }
+    if constexpr (AL == 1) {
+#pragma unroll
+      for (int i = 0; i < ET_KC / 64; ++i) *reinterpret_cast<v4u*>(mine + i * 1024 + lane * 16) = W[i];
+    }
+    if (AL < 16 && K >= 16 && (c + 1) * ET_KC > K) {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const int k = c * ET_KC + s * 64 + lg * 16;
+        a[s] = __builtin_bit_cast(v4i, tail_clear(__builtin_bit_cast(v4u, a[s]), k, K));
       }
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -455,17 +476,20 @@ static hipError_t launch_fwd_t(const ExpertQuantized& Q, const void* X, int T, c
                                const ExpertSegs& S, const int8_t* CB, const float* SCB, int N, int K, void* out,
                                hipStream_t st) {
   typedef typename Elem<DT>::T E;
-  const bool ua = K % 16 != 0 || (uintptr_t)CB % 16 != 0 || (int64_t)T * K >= ((int64_t)1 << 31);
+  const bool far = (int64_t)T * K >= ((int64_t)1 << 31);
+  const int al = K < 16 || K % 4 != 0 || (uintptr_t)CB % 4 != 0 || far ? 1
+                 : K % 16 != 0 || (uintptr_t)CB % 16 != 0              ? 4
+                                                                       : 16;
   if (few_rows(R, S.n_seg, N) || K < 16 || T == 0) {
     const int tiles_n = (N + 15) / 16;
-    auto kern = ua ? k_expert_fwd_thin<DT, true> : k_expert_fwd_thin<DT, false>;
+    auto kern = al == 1 ? k_expert_fwd_thin<DT, 1> : al == 4 ? k_expert_fwd_thin<DT, 4> : k_expert_fwd_thin<DT, 16>;
     hipLaunchKernelGGL(kern, expert_grid(expert_slots(R, S.n_seg, 16) * tiles_n), dim3(256), 0, st, Q,
                        static_cast<const E*>(X), T, rows, R, S, CB, SCB, N, K, tiles_n, static_cast<E*>(out));
     return hipGetLastError();
   }
-  static std::atomic<uint64_t> lds_set[2];
-  auto kern = ua ? k_expert_fwd<DT, true> : k_expert_fwd<DT, false>;
-  const hipError_t e = lds_limit_once((const void*)kern, EF_LDS, lds_set[ua]);
+  static std::atomic<uint64_t> lds_set[3];
+  auto kern = al == 1 ? k_expert_fwd<DT, 1> : al == 4 ? k_expert_fwd<DT, 4> : k_expert_fwd<DT, 16>;
+  const hipError_t e = lds_limit_once((const void*)kern, EF_LDS, lds_set[al == 1 ? 0 : al == 4 ? 1 : 2]);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, expert_grid(expert_groups(expert_slots(R, S.n_seg, 256), (N + 255) / 256)), dim3(512),
                      EF_LDS, st, Q, static_cast<const E*>(X), T, rows, R, S, CB, SCB, N, K, static_cast<E*>(out));
