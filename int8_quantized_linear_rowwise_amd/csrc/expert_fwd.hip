@@ -97,6 +97,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
     else if constexpr (AL == 4) aoff[i] = max(t, 0) * K;
     else aoff[i] = t >= 0 ? t * K + 16 * lc : OOB_OFFSET;
   }
+  int ka = 0;      // AL < 16: first byte of the codes in RA
   auto load_a = [&](int kt) {
     if constexpr (AL < 16) {
       const int k = kt + 16 * lc, at = tail_at(k, K);
@@ -105,10 +106,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
         if constexpr (AL == 1) RA[i] = bytes16(pA[i] + at);
         else RA[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rA, aoff[i] + at, 0, 0));
       }
-      if (kt + BK > K) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) RA[i] = tail_clear(RA[i], k, K);
-      }
+      ka = k;
     } else {
       const bool in = kt + 16 * lc < K;
 #pragma unroll
@@ -122,7 +120,9 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
   };
   auto write_a = [&](int st) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<v4u*>(smem + st * STAGE + AOFF + woff + i * 64 * BK) = RA[i];
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<v4u*>(smem + st * STAGE + AOFF + woff + i * 64 * BK) =
+          AL == 16 ? RA[i] : tail_clear<AL>(RA[i], ka, K);      // every step: a branch costs the loop more
   };
   load_a(0);
 
@@ -427,7 +427,7 @@ __global__ __launch_bounds__(256, AL == 1 ? 6 : 8) void k_expert_fwd_thin(Expert
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
         const int k = c * ET_KC + s * 64 + lg * 16;
-        a[s] = __builtin_bit_cast(v4i, tail_clear(__builtin_bit_cast(v4u, a[s]), k, K));
+        a[s] = __builtin_bit_cast(v4i, tail_clear<AL>(__builtin_bit_cast(v4u, a[s]), k, K));
       }
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
