@@ -81,7 +81,7 @@ SIGNATURES = {
     "int8_grad_norm": (_int, [_vp, _i64, _int, _f64, _vp, _int, _vp, _vp, _vp, _vp, _sz, _vp]),
     "int8_expert_sort_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "int8_expert_sort": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
-    "int8_expert_forward_workspace_bytes": (_sz, [_i64, _i64]),
+    "int8_expert_forward_workspace_bytes": (_sz, [_i64, _i64, _vp, _i64, _i64, _i64]),
     "int8_expert_forward": (_int, [_vp, _int, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _f32, _vp,
                                    _vp, _sz, _vp]),
     "int8_expert_backward_workspace_bytes": (_sz, [_vp, _int, _i64, _i64]),

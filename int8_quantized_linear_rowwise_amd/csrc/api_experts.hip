@@ -115,9 +115,10 @@ int int8_expert_sort(const void* experts, int id_bytes, int64_t T, int64_t k, in
                                             row_token, position, static_cast<int32_t*>(ws), (hipStream_t)stream));
 }
 
-size_t int8_expert_forward_workspace_bytes(int64_t T, int64_t K) {
-  if (T < 0 || K < 0 || T > MAX_ROWS || K > I8L_MAX_K || T * K > MAX_VALUES) return 0;
-  return forward_layout(T, K).total;
+size_t int8_expert_forward_workspace_bytes(int64_t T, int64_t K, const int8_t* CB, int64_t R, int64_t N,
+                                           int64_t n_seg) {
+  if (T < 0 || T > MAX_ROWS || T * K > MAX_VALUES || product_sizes(R, N, K, 0, n_seg) != I8L_OK) return 0;
+  return i8l::expert_fwd_tiny_fits(T, K, CB, R, N, n_seg) ? 0 : forward_layout(T, K).total;
 }
 
 int int8_expert_forward(const void* X, int dtype, int64_t T, int64_t K, const int32_t* rows, int64_t R,
@@ -135,9 +136,14 @@ int int8_expert_forward(const void* X, int dtype, int64_t T, int64_t K, const in
   if (T > 0 && K > 0 && X == nullptr) return I8L_EINVAL;
   if (n_experts > 0 && N > 0 && (SCB == nullptr || (K > 0 && CB == nullptr))) return I8L_EINVAL;
   const Layout L = forward_layout(T, K);
-  if (ws == nullptr || ws_bytes < L.total) return I8L_EWORKSPACE;
+  const bool tiny = i8l::expert_fwd_tiny_fits(T, K, CB, R, N, n_seg);
+  if (!tiny && (ws == nullptr || ws_bytes < L.total)) return I8L_EWORKSPACE;
   if ((uintptr_t)ws % ALIGN) return I8L_EINVAL;
   if (R == 0 || N == 0) return I8L_OK;
+  const i8l::ExpertSegs S = {seg_offsets, seg_expert, (int)n_seg, (int)n_experts};
+  if (tiny)
+    return hip_status(i8l::launch_expert_fwd_tiny(dtype, X, (int)T, threshold, rows, (int)R, S, CB, SCB, (int)N, (int)K,
+                                                  out, (hipStream_t)stream));
   char* w = static_cast<char*>(ws);
   int32_t* count = reinterpret_cast<int32_t*>(w + L.count);
   int32_t* idx = reinterpret_cast<int32_t*>(w + L.idx);
@@ -152,7 +158,6 @@ int int8_expert_forward(const void* X, int dtype, int64_t T, int64_t K, const in
                                  reinterpret_cast<uint32_t*>(w + L.scratch), st, nullptr, (int)K);
   if (e != hipSuccess) return I8L_EHIP;
   const i8l::ExpertQuantized Q = {CA, SCA, sub, L.cap, idx, count};
-  const i8l::ExpertSegs S = {seg_offsets, seg_expert, (int)n_seg, (int)n_experts};
   return hip_status(i8l::launch_expert_fwd(dtype, Q, X, (int)T, rows, (int)R, S, CB, SCB, (int)N, (int)K, out, st));
 }
 

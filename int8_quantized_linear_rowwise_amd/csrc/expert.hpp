@@ -30,6 +30,16 @@ struct ExpertTile {
   int r0, r1, expert;   // rows [r0, r1), none where r1 <= r0; expert -1: rows of zeros
 };
 constexpr int SCAN_SEGMENTS = 256;
+// Sum over the lanes up to and with this one.
+__device__ __forceinline__ int lane_scan(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(v, o, 64);
+    v += lane >= o ? u : 0;
+  }
+  return v;
+}
 struct ExpertScan {
   int total;            // slots
   int incl[4];          // of lane l's segment 64 b + l: slots up to and with it
@@ -48,13 +58,7 @@ __device__ __forceinline__ ExpertScan expert_scan(const ExpertSegs& S, int R, in
     if (64 * b <= S.n_seg) {
       const int s = 64 * b + lane;
       const int len = s <= S.n_seg ? expert_start(S, s + 1, R) - expert_start(S, s, R) : 0;
-      int incl = len > 0 ? (len + tm - 1) / tm : 0;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int v = __shfl_up(incl, o, 64);
-        incl += lane >= o ? v : 0;
-      }
-      c.incl[b] += incl;
+      c.incl[b] += lane_scan(len > 0 ? (len + tm - 1) / tm : 0);
       c.total = __builtin_amdgcn_readlane(c.incl[b], 63);
     }
   }

@@ -14,6 +14,7 @@
 #include <type_traits>
 
 #include "expert.hpp"
+#include "quantize.hpp"
 
 namespace i8l {
 
@@ -28,7 +29,7 @@ namespace i8l {
 // AL, what K (16 at least) and the weights' address are multiples of: 16; 4, the
 // same loads and the last piece of a row as tail_at has it; 1, or where the codes
 // pass 2^31 bytes, 16-byte loads at any address. 4096 tokens, two of eight
-// experts, 4096 -> 11008 449 us, 4088 -> 11000 AL4 us, 4095 -> 11007 AL1 us.
+// experts, 4096 -> 11008 449 us, 4088 -> 11000 516 us, 4095 -> 11007 626 us.
 constexpr int EF_OPAN = 2 * 256 * 32;                 // outlier panels P[n][16], Q[row][16] (fp16)
 constexpr int EF_SCALES = (256 + 256) * 4;            // SCB / 127^2, SCA
 constexpr int EF_STAGES = 2 * (256 + 256) * 128;      // operand stages; the output tile takes their place
@@ -226,7 +227,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
     }
   }
 
-  // lane (lr, lg), register r of tile (i, j): feature wn BN / 2 + i 32 + (r / 4) 8 + lg 4 + r % 4, row wm 64 + j 32 + lr
+  // lane (lr, lg), register r of tile (i, j): feature wn BN / 2 + 32 i + 8 (r / 4) + 4 lg + r % 4, row 64 wm + 32 j + lr
   // (the accumulators become fp32 in place)
   const int nl = wn * (BN / 2), ml = wm * 64;
 #pragma unroll
@@ -338,10 +339,15 @@ __global__ __launch_bounds__(512, 1) void k_expert_fwd(ExpertQuantized Q, const 
 // ends: 512 bytes at a time, five workgroups, took 28 us for one token of two
 // 4096 -> 11008 experts instead of 22.
 // AL: as above; 1 goes through registers and takes any K.
+// KS 1: a wave has a tile of its own and all of its contraction, with no barrier
+// at all; for contractions up to 2048 where that fills the chip. 64 tokens, four
+// of 64 experts, 512 -> 4096: 27 us against 43 with KS 4, 2048: 80 against 90,
+// 4096: 166 against 160; one token, two of eight experts, 2048 -> 11008: 19
+// against 17 (too few workgroups).
 typedef __attribute__((address_space(3))) void* lds_ptr;
 constexpr int ET_KC = 256;      // bytes of a row a wave takes at a time
-template <int DT, int AL>
-__global__ __launch_bounds__(256, AL == 1 ? 6 : 8) void k_expert_fwd_thin(ExpertQuantized Q,
+template <int DT, int AL, int KS>
+__global__ __launch_bounds__(256, AL == 1 ? 4 : 8) void k_expert_fwd_thin(ExpertQuantized Q,
                                                             const typename Elem<DT>::T* __restrict__ X, int T,
                                                             const int32_t* __restrict__ rows, int R, ExpertSegs S,
                                                             const int8_t* __restrict__ CBall,
@@ -349,18 +355,23 @@ __global__ __launch_bounds__(256, AL == 1 ? 6 : 8) void k_expert_fwd_thin(Expert
                                                             int tiles_n, typename Elem<DT>::T* __restrict__ out) {
   typedef typename Elem<DT>::T E;
   constexpr int BM = 16, BN = 16, STEPS = ET_KC / 64, LPR = ET_KC / 16;
+  constexpr int WG_N = KS == 1 ? 4 * BN : BN;      // features of a workgroup
   __shared__ __attribute__((aligned(1024))) int8_t sw[4][BN * ET_KC];
   const int64_t bid = expert_block();
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lg = lane >> 4;
   const int64_t ts = bid / tiles_n;
-  const int n0 = (int)(bid - ts * tiles_n) * BN;
+  const int n0 = (int)(bid - ts * tiles_n) * WG_N + (KS == 1 ? wave * BN : 0);
   const ExpertScan scan = expert_scan(S, R, BM);
   if (ts >= scan.total) return;
   const ExpertTile tile = expert_tile(S, scan, (int)ts, R, BM);
   if (tile.r0 >= tile.r1) return;
-  if (tile.expert < 0) return expert_zeros(out, N, tile.r0, tile.r1, n0, min(N, n0 + BN));
+  if (tile.expert < 0) {
+    const int c0 = (int)(bid - ts * tiles_n) * WG_N;
+    return expert_zeros(out, N, tile.r0, tile.r1, c0, min(N, c0 + WG_N));
+  }
+  if (n0 >= N) return;      // KS 1: no barrier follows
   const int8_t* CB = CBall + (int64_t)tile.expert * N * K;
   const float* SCB = SCBall + (int64_t)tile.expert * N;
   const __amdgpu_buffer_rsrc_t rB = make_rsrc(CB + (int64_t)n0 * K, AL == 1 ? 0 : min(BN, N - n0) * K);
@@ -382,16 +393,17 @@ __global__ __launch_bounds__(256, AL == 1 ? 6 : 8) void k_expert_fwd_thin(Expert
       }
     }
   };
-  if (wave < nc) load_w(wave);
+  const int first = KS == 1 ? 0 : wave;
+  if (first < nc) load_w(first);
 
   const int r = tile.r0 + lr;
   const int t = r < tile.r1 ? row_token(rows, r, T) : -1;
-  // what the first wave needs to finish the tile is requested before the contraction
+  // what the wave that finishes the tile needs for that is requested before the contraction
   const int nb = n0 + 4 * lg;
   int cnt = 0;
   float sa = 0.0f, sb[4] = {};
   v8h P = {}, V = {};
-  if (wave == 0) {
+  if (KS == 1 || wave == 0) {
     cnt = *Q.count;
     if (t >= 0) sa = Q.SCA[t];
 #pragma unroll
@@ -403,7 +415,7 @@ __global__ __launch_bounds__(256, AL == 1 ? 6 : 8) void k_expert_fwd_thin(Expert
     }
   }
   v4i acc = {0, 0, 0, 0};
-  for (int c = wave; c < nc; c += 4) {
+  for (int c = first; c < nc; c += KS) {
     v4i a[STEPS];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
@@ -437,18 +449,20 @@ __global__ __launch_bounds__(256, AL == 1 ? 6 : 8) void k_expert_fwd_thin(Expert
       acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, a[s], acc, 0, 0, 0);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next piece lands in the same place
-    if (c + 4 < nc) load_w(c + 4);
+    if (c + KS < nc) load_w(c + KS);
   }
 
   // lane (lr, lg): the token of row lr, features n0 + 4 lg .. + 3
-  v4i* part = reinterpret_cast<v4i*>(sw[0]);
-  __syncthreads();
-  part[wave * 64 + lane] = acc;
-  __syncthreads();
-  if (wave > 0) return;
-  v4i sum = part[lane];
+  v4i sum = acc;
+  if constexpr (KS > 1) {
+    v4i* part = reinterpret_cast<v4i*>(sw[0]);
+    __syncthreads();
+    part[wave * 64 + lane] = acc;
+    __syncthreads();
+    if (wave > 0) return;
 #pragma unroll
-  for (int w = 1; w < 4; ++w) sum += part[w * 64 + lane];
+    for (int w = 1; w < 4; ++w) sum += part[w * 64 + lane];
+  }
   v4f y;
 #pragma unroll
   for (int x = 0; x < 4; ++x) y[x] = (float)sum[x] * (sa * (sb[x] * (1.0f / 16129.0f)));
@@ -464,11 +478,224 @@ __global__ __launch_bounds__(256, AL == 1 ? 6 : 8) void k_expert_fwd_thin(Expert
   }
 }
 
+// ---------------------------------------------------------------------------
+// Up to four tokens: the kernel above (KS 4), with the quantization in it. Every
+// workgroup quantizes all of the tokens itself, into LDS, while its first
+// weights are on their way: one launch, and nothing to wait for between two. The
+// same flags, scales, codes and outlier values as the quantizer's.
+// One token of two 4096 -> 11008 experts, bf16: 20 us against 26 in two launches.
+constexpr int EQ_TOKENS = 4, EQ_COLS = 4096, EQ_LIST = 256;
+template <int DT, int TM>      // TM: 1 or EQ_TOKENS, at least T
+__global__ __launch_bounds__(256, TM == 1 ? 6 : 4) void k_expert_fwd_tiny(
+    const typename Elem<DT>::T* __restrict__ X, int T, bool vec, float tau, const int32_t* __restrict__ rows, int R,
+    ExpertSegs S, const int8_t* __restrict__ CBall, const float* __restrict__ SCBall, int N, int K, int tiles_n,
+    typename Elem<DT>::T* __restrict__ out) {
+#pragma clang fp contract(off)
+  typedef typename Elem<DT>::T E;
+  constexpr int BN = 16, STEPS = ET_KC / 64, LPR = ET_KC / 16, CH = EQ_COLS / 8 / 256;
+  __shared__ __attribute__((aligned(1024))) int8_t sw[4][BN * ET_KC];
+  __shared__ uint32_t smask[EQ_COLS / 32];
+  __shared__ uint32_t red[TM][4];
+  __shared__ uint16_t slist[EQ_LIST];
+  extern __shared__ __attribute__((aligned(16))) int8_t codes[];      // TM rows of kp
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lg = lane >> 4;
+  const int64_t bid = expert_block();
+  const int64_t ts = bid / tiles_n;
+  const int n0 = (int)(bid - ts * tiles_n) * BN;
+  const ExpertScan scan = expert_scan(S, R, 16);
+  if (ts >= scan.total) return;
+  const ExpertTile tile = expert_tile(S, scan, (int)ts, R, 16);
+  if (tile.r0 >= tile.r1) return;
+  if (tile.expert < 0) return expert_zeros(out, N, tile.r0, tile.r1, n0, min(N, n0 + BN));
+  const int8_t* CB = CBall + (int64_t)tile.expert * N * K;
+  const float* SCB = SCBall + (int64_t)tile.expert * N;
+  const __amdgpu_buffer_rsrc_t rB = make_rsrc(CB + (int64_t)n0 * K, min(BN, N - n0) * K);
+  const int nc = (K + ET_KC - 1) / ET_KC, kp = nc * ET_KC;
+  int8_t* mine = sw[wave];
+  auto load_w = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < ET_KC / 64; ++i) {
+      const int row = (64 / LPR) * i + lane / LPR;
+      const int k = c * ET_KC + 16 * ((lane % LPR) ^ row);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr)(mine + i * 1024), 16, k < K ? row * K + k : OOB_OFFSET, 0,
+                                               0, 0);
+    }
+  };
+  if (wave < nc) load_w(wave);
+
+  // quantization: a thread has chunks tid and tid + 256 of every token
+  const int nchunk = K / 8;
+  v4u ra[TM][CH], rb[TM][CH] = {};
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (t < T && tid + 256 * i < nchunk)
+        load_raw8<DT>(X + (int64_t)t * K, (tid + 256 * i) * 8, K, vec, ra[t][i], rb[t][i]);
+  const bool tau_on = tau > 0.0f && tau < __builtin_huge_valf();
+  uint32_t om[CH], mx[TM] = {};
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    om[i] = 0u;
+    if (tid + 256 * i < nchunk) {
+      if (tau_on) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint32_t m = 0u;
+#pragma unroll
+          for (int t = 0; t < TM; ++t)
+            if (t < T) m = max(m, chunk_mag<DT>(ra[t][i], rb[t][i], e));
+          if (mag_to_half_value<DT>(m) > tau) om[i] |= 1u << e;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < TM; ++t)
+        if (t < T) mx[t] = max(mx[t], chunk_absmax<DT, true>(ra[t][i], rb[t][i], om[i], true));
+    }
+    reinterpret_cast<uint8_t*>(smask)[tid + 256 * i] = (uint8_t)om[i];
+  }
+#pragma unroll
+  for (int t = 0; t < TM; ++t) {
+    mx[t] = wave_umax(mx[t]);
+    if (lane == 0) red[t][wave] = mx[t];
+  }
+  __syncthreads();
+  auto scale = [&](int t) {
+    return mag_to_half_value<DT>(max(max(red[t][0], red[t][1]), max(red[t][2], red[t][3])));
+  };
+#pragma unroll
+  for (int t = 0; t < TM; ++t)
+    if (t < T) {
+      const float s = scale(t), inv = (s > 0.0f) ? (127.0f / s) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+        if (tid + 256 * i < nchunk) {
+          uint32_t lo, hi;
+          chunk_quant8<DT>(ra[t][i], rb[t][i], inv, lo, hi);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if ((om[i] >> e) & 1u) lo &= ~(0xffu << (8 * e));
+            if ((om[i] >> (e + 4)) & 1u) hi &= ~(0xffu << (8 * e));
+          }
+          *reinterpret_cast<v2u*>(codes + t * kp + (tid + 256 * i) * 8) = v2u{lo, hi};
+        }
+    }
+  __syncthreads();
+
+  const int r = tile.r0 + lr;
+  const int t = r < tile.r1 ? row_token(rows, r, T) : -1;
+  // the first wave finishes the tile; what it needs for that is requested before the contraction
+  const int nb = n0 + 4 * lg;
+  int cnt = 0, below = 0;      // outlier columns, and those in the words of the lanes before
+  float sa = 0.0f, sb[4] = {};
+  v8h P = {}, V = {};
+  // columns of rank base .. base + EQ_LIST - 1, ascending
+  auto list = [&](int base) {
+    int j = below - base;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      for (uint32_t m = smask[2 * lane + h]; m != 0u; m &= m - 1u, ++j)
+        if (j >= 0 && j < EQ_LIST) slist[j] = (uint16_t)((2 * lane + h) * 32 + __ffs(m) - 1);
+    __builtin_amdgcn_wave_barrier();
+  };
+  auto operands = [&](int j0, int base) {
+    P = v8h{};
+    V = v8h{};
+    const float sig = n0 + lr < N ? SCB[n0 + lr] * (1.0f / 127.0f) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int j = j0 + lg * 8 + e;
+      if (j < cnt) {
+        const int col = slist[j - base];
+        if (n0 + lr < N) P[e] = half_of_f32((float)CB[(int64_t)(n0 + lr) * K + col] * sig);
+        if (t >= 0) V[e] = to_half<DT>(X[(int64_t)t * K + col]);
+      }
+    }
+  };
+  if (wave == 0) {
+    if (t >= 0) sa = scale(t);
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (nb + x < N) sb[x] = SCB[nb + x];
+    const int n = __popc(smask[2 * lane]) + __popc(smask[2 * lane + 1]);
+    const int incl = lane_scan(n);
+    below = incl - n;
+    cnt = __builtin_amdgcn_readlane(incl, 63);
+    if (cnt > 0) {
+      list(0);
+      operands(0, 0);
+    }
+  }
+  v4i acc = {0, 0, 0, 0};
+  const int8_t* mycodes = codes + max(t, 0) * kp;      // no token: its scale is 0
+  for (int c = wave; c < nc; c += 4) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const v4i w = *reinterpret_cast<const v4i*>(mine + lr * ET_KC + 16 * ((4 * s + lg) ^ lr));
+      const v4i a = *reinterpret_cast<const v4i*>(mycodes + c * ET_KC + s * 64 + lg * 16);
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, a, acc, 0, 0, 0);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // read before the next piece lands in the same place
+    if (c + 4 < nc) load_w(c + 4);
+  }
+  v4i* part = reinterpret_cast<v4i*>(sw[0]);
+  __syncthreads();
+  part[wave * 64 + lane] = acc;
+  __syncthreads();
+  if (wave > 0) return;
+  v4i sum = acc;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) sum += part[w * 64 + lane];
+  v4f y;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) y[x] = (float)sum[x] * (sa * (sb[x] * (1.0f / 16129.0f)));
+  if (cnt > 0) y = __builtin_amdgcn_mfma_f32_16x16x32_f16(P, V, y, 0, 0, 0);
+  for (int jo = 32; jo < cnt; jo += 32) {
+    const int base = jo / EQ_LIST * EQ_LIST;
+    if (jo == base) list(base);
+    operands(jo, base);
+    y = __builtin_amdgcn_mfma_f32_16x16x32_f16(P, V, y, 0, 0, 0);
+  }
+  if (r < tile.r1) {
+    const float v[4] = {y[0], y[1], y[2], y[3]};
+    expert_store4<DT>(out + (int64_t)r * N + nb, v, N - nb, N % 4 == 0 && (uintptr_t)out % (4 * sizeof(E)) == 0);
+  }
+}
+
 // Few rows: up to 10 a segment on average; or up to 64 where large tiles, cut
 // in four, would not fill the chip.
 static bool few_rows(int64_t R, int64_t n_seg, int64_t N) {
   if (R <= 10 * n_seg) return true;
   return R <= 64 * n_seg && expert_slots(R, n_seg, 256) * ((N + 255) / 256) <= 32;
+}
+
+bool expert_fwd_tiny_fits(int64_t T, int64_t K, const int8_t* CB, int64_t R, int64_t N, int64_t n_seg) {
+  return T > 0 && T <= EQ_TOKENS && K > 0 && K <= EQ_COLS && K % 16 == 0 && (uintptr_t)CB % 4 == 0 &&
+         few_rows(R, n_seg, N);
+}
+
+template <int DT>
+static hipError_t launch_tiny_t(const void* X, int T, float tau, const int32_t* rows, int R, const ExpertSegs& S,
+                                const int8_t* CB, const float* SCB, int N, int K, void* out, hipStream_t st) {
+  typedef typename Elem<DT>::T E;
+  const int tiles_n = (N + 15) / 16, tm = T == 1 ? 1 : EQ_TOKENS;
+  auto kern = T == 1 ? k_expert_fwd_tiny<DT, 1> : k_expert_fwd_tiny<DT, EQ_TOKENS>;
+  const size_t lds = (size_t)tm * ((K + ET_KC - 1) / ET_KC * ET_KC);
+  hipLaunchKernelGGL(kern, expert_grid(expert_slots(R, S.n_seg, 16) * tiles_n), dim3(256), lds, st,
+                     static_cast<const E*>(X), T, (uintptr_t)X % 16 == 0, tau, rows, R, S, CB, SCB, N, K, tiles_n,
+                     static_cast<E*>(out));
+  return hipGetLastError();
+}
+
+hipError_t launch_expert_fwd_tiny(int dt, const void* X, int T, float tau, const int32_t* rows, int R,
+                                  const ExpertSegs& S, const int8_t* CB, const float* SCB, int N, int K, void* out,
+                                  hipStream_t st) {
+  if (dt == DT_F32) return launch_tiny_t<DT_F32>(X, T, tau, rows, R, S, CB, SCB, N, K, out, st);
+  if (dt == DT_F16) return launch_tiny_t<DT_F16>(X, T, tau, rows, R, S, CB, SCB, N, K, out, st);
+  return launch_tiny_t<DT_BF16>(X, T, tau, rows, R, S, CB, SCB, N, K, out, st);
 }
 
 template <int DT>
@@ -481,9 +708,16 @@ static hipError_t launch_fwd_t(const ExpertQuantized& Q, const void* X, int T, c
                  : K % 16 != 0 || (uintptr_t)CB % 16 != 0              ? 4
                                                                        : 16;
   if (few_rows(R, S.n_seg, N) || K < 16 || T == 0) {
-    const int tiles_n = (N + 15) / 16;
-    auto kern = al == 1 ? k_expert_fwd_thin<DT, 1> : al == 4 ? k_expert_fwd_thin<DT, 4> : k_expert_fwd_thin<DT, 16>;
-    hipLaunchKernelGGL(kern, expert_grid(expert_slots(R, S.n_seg, 16) * tiles_n), dim3(256), 0, st, Q,
+    const int64_t slots = expert_slots(R, S.n_seg, 16);
+    const bool split = K > 2048 || slots * ((N + 63) / 64) < 1024;
+    const int tiles_n = split ? (N + 15) / 16 : (N + 63) / 64;
+    auto kern = split ? (al == 1   ? k_expert_fwd_thin<DT, 1, 4>
+                         : al == 4 ? k_expert_fwd_thin<DT, 4, 4>
+                                   : k_expert_fwd_thin<DT, 16, 4>)
+                      : (al == 1   ? k_expert_fwd_thin<DT, 1, 1>
+                         : al == 4 ? k_expert_fwd_thin<DT, 4, 1>
+                                   : k_expert_fwd_thin<DT, 16, 1>);
+    hipLaunchKernelGGL(kern, expert_grid(slots * tiles_n), dim3(256), 0, st, Q,
                        static_cast<const E*>(X), T, rows, R, S, CB, SCB, N, K, tiles_n, static_cast<E*>(out));
     return hipGetLastError();
   }

@@ -131,6 +131,12 @@ struct ExpertQuantized {
 hipError_t launch_expert_fwd(int dt, const ExpertQuantized& Q, const void* X, int T, const int32_t* rows, int R,
                              const ExpertSegs& S, const int8_t* CB, const float* SCB, int N, int K, void* out,
                              hipStream_t st);
+// The same in one launch, quantization included, for a few tokens, where expert_fwd_tiny_fits() (of CB it takes the
+// address alone).
+bool expert_fwd_tiny_fits(int64_t T, int64_t K, const int8_t* CB, int64_t R, int64_t N, int64_t n_seg);
+hipError_t launch_expert_fwd_tiny(int dt, const void* X, int T, float tau, const int32_t* rows, int R,
+                                  const ExpertSegs& S, const int8_t* CB, const float* SCB, int N, int K, void* out,
+                                  hipStream_t st);
 // gX (R x K) = D(fp16(G) Wdq[expert]), G: R x N. ws: expert_bwd_bytes() bytes, 16-byte aligned.
 size_t expert_bwd_bytes(const void* G, int dt, int64_t R, int64_t N);
 hipError_t launch_expert_bwd(int dt, const void* G, int R, const ExpertSegs& S, const int8_t* CB, const float* SCB,

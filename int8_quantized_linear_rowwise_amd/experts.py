@@ -93,10 +93,11 @@ def expert_forward(X: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor, seg_off
     dev = _gpu(X, "X")
     if out is None:
         out = _empty((R, N), X.dtype, X.device)
-    ws = _workspace(workspace, lib.int8_expert_forward_workspace_bytes(T, K), X.device, dev)
+    cb = _ptr(CB, "CB", dev)
+    ws = _workspace(workspace, lib.int8_expert_forward_workspace_bytes(T, K, cb, R, N, S), X.device, dev)
     with _on_gpu(dev):
         check(lib.int8_expert_forward(_ptr(X, "X", dev), _code(X), T, K, _ptr(rows, "rows", dev), R,
-                                      _ptr(CB, "CB", dev), _ptr(SCB, "SCB", dev), E, N,
+                                      cb, _ptr(SCB, "SCB", dev), E, N,
                                       _ptr(seg_offsets, "seg_offsets", dev), _ptr(seg_expert, "seg_expert", dev), S,
                                       threshold, _ptr(out, "out", dev), _ptr(ws, "workspace", dev),
                                       0 if ws is None else ws.numel(), _raw_stream(dev)),

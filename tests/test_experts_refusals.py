@@ -50,8 +50,11 @@ def test_forward_host_errors(L):  # noqa: F811
     assert call(R=(1 << 24) + 1) == L.I8L_ESHAPE and call(T=(1 << 24) + 1) == L.I8L_ESHAPE
     assert call(S=65537) == L.I8L_ESHAPE and call(E=65537) == L.I8L_ESHAPE
     assert call(E=65536, N=65536) == L.I8L_ESHAPE             # more scales than an int counts
-    wsb = need(8, 64)
-    assert wsb > 0 and wsb % 256 == 0 and need(-1, 64) == 0 and need(8, L.I8L_MAX_K + 1) == 0
+    wsb = need(8, 64, FAKE, 16, 32, 4)
+    assert wsb > 0 and wsb % 256 == 0
+    assert need(-1, 64, FAKE, 16, 32, 4) == 0 and need(8, L.I8L_MAX_K + 1, FAKE, 16, 32, 4) == 0
+    assert need(4, 64, FAKE, 8, 32, 4) == 0                   # up to four tokens are quantized on the way
+    assert need(4, 64, FAKE + 1, 8, 32, 4) > 0 and need(4, 72, FAKE, 8, 32, 4) > 0 and need(4, 64, FAKE, 999, 32, 4) > 0
     assert call(wsb=wsb - 1) == L.I8L_EWORKSPACE and call(ws=0) == L.I8L_EWORKSPACE
     assert call(ws=FAKE + 16) == L.I8L_EINVAL
     assert call(R=0, out=0) == L.I8L_OK and call(N=0, out=0, CB=0, SCB=0) == L.I8L_OK

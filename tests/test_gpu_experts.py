@@ -133,6 +133,25 @@ def test_forward_many_rows(I8, dt, T, k, E, K, N, outliers):
     run_forward(I8, dt, T, K, N, off.tolist(), rows=token, outliers=outliers)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,k,E,K,N,outliers", [(1, 1, 1, 16, 8, 0), (1, 2, 8, 4096, 136, 4), (1, 3, 3, 272, 50, 17),
+                                                (2, 2, 5, 2064, 33, 300), (3, 2, 4, 1024, 64, 600),
+                                                (4, 2, 4, 4096, 48, 33), (4, 4, 4, 48, 17, 5), (5, 2, 4, 4096, 48, 3),
+                                                (4, 1, 2, 4112, 32, 3)])
+def test_forward_few_tokens(I8, dt, T, k, E, K, N, outliers):
+    """Up to four tokens are quantized in the product's own launch; one more, or one piece more, is not."""
+    off, token, _ = X.sort(X.choices(T, k, E, 7, 0.1), E)
+    a = run_forward(I8, dt, T, K, N, off.tolist(), rows=token, outliers=outliers)
+    run_forward(I8, dt, T, K, N, off.tolist(), rows=token, outliers=outliers, tau=0.0)
+    if T == 4:
+        # beside a fifth token, with the same outlier columns, the rows are the same
+        CB, SCB = gpu(*X.weights(E, N, K, 1))
+        x = X.inputs(T, K, dt, 2, outliers).to(DEV)
+        five = torch.cat([x, x[:1]])
+        off, token = gpu(off, token)
+        assert torch.equal(I8.expert_forward(five, CB, SCB, off, rows=token), a)
+
+
 @pytest.mark.parametrize("tau", [0.0, -1.0, float("inf"), float("nan"), 1.0])
 def test_forward_thresholds(I8, tau):
     run_forward(I8, "bf16", 20, 128, 64, [0, 8, 20], tau=tau)
