@@ -41,8 +41,8 @@ __device__ __forceinline__ int lane_scan(int v) {
   return v;
 }
 struct ExpertScan {
-  int total;            // slots
-  int incl[4];          // of lane l's segment 64 b + l: slots up to and with it
+  int total;                        // slots
+  int incl[4], start[4], end[4];    // of lane l's segment 64 b + l: slots up to and with it, and its rows
 };
 __device__ __forceinline__ ExpertScan expert_scan(const ExpertSegs& S, int R, int tm) {
   const int lane = threadIdx.x & 63;
@@ -57,7 +57,9 @@ __device__ __forceinline__ ExpertScan expert_scan(const ExpertSegs& S, int R, in
     c.incl[b] = c.total;
     if (64 * b <= S.n_seg) {
       const int s = 64 * b + lane;
-      const int len = s <= S.n_seg ? expert_start(S, s + 1, R) - expert_start(S, s, R) : 0;
+      c.start[b] = expert_start(S, s, R);
+      c.end[b] = expert_start(S, s + 1, R);
+      const int len = s <= S.n_seg ? c.end[b] - c.start[b] : 0;
       c.incl[b] += lane_scan(len > 0 ? (len + tm - 1) / tm : 0);
       c.total = __builtin_amdgcn_readlane(c.incl[b], 63);
     }
@@ -69,15 +71,19 @@ __device__ __forceinline__ ExpertScan expert_scan(const ExpertSegs& S, int R, in
 // Slot 0 <= slot < total.
 __device__ __forceinline__ ExpertTile expert_tile(const ExpertSegs& S, const ExpertScan& c, int slot, int R, int tm) {
   const int lane = threadIdx.x & 63;
-  int s = 0, i;      // segment, and the tile's number in it
+  int s = 0, i, start = 0, end = 0;      // segment, the tile's number in it, and its rows
   if (S.n_seg < SCAN_SEGMENTS) {
     int before = 0;
 #pragma unroll
     for (int b = 0; b < 4; ++b)
       if (64 * b <= S.n_seg) {
         const int l = __popcll(__ballot(c.incl[b] <= slot));      // segments that end before the slot: a first part
-        s += l;
         if (l > 0) before = __builtin_amdgcn_readlane(c.incl[b], l - 1);
+        if (s == 64 * b) {      // all of the blocks before
+          start = __builtin_amdgcn_readlane(c.start[b], min(l, 63));
+          end = __builtin_amdgcn_readlane(c.end[b], min(l, 63));
+        }
+        s += l;
       }
     i = slot - before;
   } else {
@@ -91,11 +97,12 @@ __device__ __forceinline__ ExpertTile expert_tile(const ExpertSegs& S, const Exp
       len = min(step - 1, len - n * step);
     }
     s = max(lo - 1, 0);
-    i = slot - (expert_start(S, s, R) / tm + s);
+    start = expert_start(S, s, R);
+    end = expert_start(S, s + 1, R);
+    i = slot - (start / tm + s);
   }
   s = __builtin_amdgcn_readfirstlane(s);
   i = __builtin_amdgcn_readfirstlane(i);
-  const int start = expert_start(S, s, R), end = expert_start(S, s + 1, R);
   ExpertTile t;
   t.r0 = __builtin_amdgcn_readfirstlane(start + i * tm);
   t.r1 = __builtin_amdgcn_readfirstlane(i < 0 ? start + i * tm : min(start + (i + 1) * tm, end));
@@ -120,8 +127,9 @@ constexpr int ROUND = 256, SPLIT_4 = 64, SPLIT_2 = 128;
 struct ExpertWork {
   int slot, tc, part, parts;     // slot -1: none
 };
+template <bool CUT>
 __device__ __forceinline__ ExpertWork expert_work(int64_t bid, int slots, int tiles_c) {
-  const int nt = slots * tiles_c, rem = nt % ROUND;
+  const int nt = slots * tiles_c, rem = CUT ? nt % ROUND : 0;
   ExpertWork w = {-1, 0, 0, rem == 0 || rem > SPLIT_2 ? 1 : rem > SPLIT_4 ? 2 : 4};
   const int full = w.parts > 1 ? nt - rem : nt;      // tiles worked on whole
   int id;
@@ -142,7 +150,7 @@ __device__ __forceinline__ ExpertWork expert_work(int64_t bid, int slots, int ti
   w.tc = in / gsz;
   return w;
 }
-// Workgroups for that: cut tiles take at most 3 SPLIT_4 more.
+// Workgroups for that with CUT: cut tiles take at most 3 SPLIT_4 more.
 inline int64_t expert_groups(int64_t slots, int64_t tiles_c) { return slots * tiles_c + 3 * SPLIT_4; }
 
 // Grid of `total` workgroups in two dimensions (a grid axis holds fewer than 2^32 threads).
@@ -185,13 +193,24 @@ __device__ __forceinline__ v4u short_row(const int8_t* row, int k, int K) {
   return v;
 }
 
+// Outlier columns j0 .. j0 + 7 (0 at and past cnt). They and their number belong
+// to no tile: the kernels ask for the first ones before anything else.
+struct OutlierCols {
+  int c[8];
+};
+__device__ __forceinline__ OutlierCols expert_out_cols(const int32_t* __restrict__ idx, int j0, int cnt) {
+  OutlierCols o;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o.c[e] = j0 + e < cnt ? idx[j0 + e] : 0;
+  return o;
+}
 // fp16 outlier values j0 .. j0 + 7 of token t (zero at and past cnt, or for no
 // token): from the quantizer's staged copy for the first cap columns, beyond
 // them from the input itself.
 template <int DT>
 __device__ __forceinline__ v8h expert_out_a8(const uint16_t* __restrict__ sub, int cap,
-                                             const typename Elem<DT>::T* __restrict__ X, int K,
-                                             const int32_t* __restrict__ idx, int t, int j0, int cnt) {
+                                             const typename Elem<DT>::T* __restrict__ X, int K, const OutlierCols& o,
+                                             int t, int j0, int cnt) {
   v8h q = {};
   if (t >= 0) {
 #pragma unroll
@@ -199,21 +218,21 @@ __device__ __forceinline__ v8h expert_out_a8(const uint16_t* __restrict__ sub, i
       const int j = j0 + e;
       if (j < cnt)
         q[e] = j < cap ? __builtin_bit_cast(_Float16, sub[(int64_t)t * cap + j])
-                       : to_half<DT>(X[(int64_t)t * K + idx[j]]);
+                       : to_half<DT>(X[(int64_t)t * K + o.c[e]]);
     }
   }
   return q;
 }
 // Dequantized weights of those columns, row n of an expert's weight: fp16(CB * fl32(SCB * fl32(1/127))).
 __device__ __forceinline__ v8h expert_out_w8(const int8_t* __restrict__ CB, const float* __restrict__ SCB, int K,
-                                             const int32_t* __restrict__ idx, int n, bool ok, int j0, int cnt) {
+                                             const OutlierCols& o, int n, bool ok, int j0, int cnt) {
   v8h p = {};
   if (ok) {
     const float sig = SCB[n] * (1.0f / 127.0f);
     const int8_t* row = CB + (int64_t)n * K;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (j0 + e < cnt) p[e] = half_of_f32((float)row[idx[j0 + e]] * sig);
+      if (j0 + e < cnt) p[e] = half_of_f32((float)row[o.c[e]] * sig);
   }
   return p;
 }
@@ -223,6 +242,34 @@ template <typename E>
 __device__ __forceinline__ void expert_zeros(E* out, int64_t ld, int r0, int r1, int c0, int c1) {
   for (int r = r0; r < r1; ++r)
     for (int c = c0 + threadIdx.x; c < c1; c += blockDim.x) out[r * ld + c] = E{};
+}
+
+// Output tiles of BM rows by BN 16-bit values in LDS, so that global stores cover
+// whole rows: 16-byte chunk c of row r at chunk position c ^ (r mod BN / 8).
+template <int BN>
+__device__ __forceinline__ int etile_off(int row, int chunk) {
+  return row * (2 * BN) + 16 * (chunk ^ (row & (BN / 8 - 1)));
+}
+template <int BM, int BN, int THREADS, typename E>
+__device__ __forceinline__ void etile_store(const char* ot, E* __restrict__ dst, int64_t ld, int r0, int c0, int r1,
+                                            int c1) {
+  static_assert(sizeof(E) == 2, "16-bit outputs");
+  constexpr int CPR = BN / 8;
+  const bool vec = ld % 8 == 0 && (uintptr_t)dst % 16 == 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < BM * CPR; i += THREADS) {
+    const int row = i / CPR, ch = i % CPR, r = r0 + row, c = c0 + ch * 8;
+    if (r >= r1) continue;
+    const v4u v = *reinterpret_cast<const v4u*>(ot + etile_off<BN>(row, ch));
+    E* p = dst + (int64_t)r * ld + c;
+    if (vec && c + 8 <= c1) {
+      *reinterpret_cast<v4u*>(p) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < c1) p[e] = __builtin_bit_cast(E, (uint16_t)(v[e >> 1] >> (16 * (e & 1))));
+    }
+  }
 }
 
 // Four results of one row to p[0 .. 3], of which m lie inside the row; vec: p is on a border of four.

@@ -273,7 +273,7 @@ __global__ __launch_bounds__(512, 1) void k_expert_bwd(const typename Elem<GT>::
                                                        typename Elem<OT>::T* __restrict__ gX) {
   extern __shared__ __attribute__((aligned(16))) char bsm[];
   const ExpertScan scan = expert_scan(S, R, 256);
-  const ExpertWork work = expert_work(expert_block(), scan.total, (K + 255) / 256);
+  const ExpertWork work = expert_work<true>(expert_block(), scan.total, (K + 255) / 256);
   if (work.slot < 0) return;
   const ExpertTile tile = expert_tile(S, scan, work.slot, R, 256);
   const int k0 = work.tc * 256 + work.part * (256 / work.parts);

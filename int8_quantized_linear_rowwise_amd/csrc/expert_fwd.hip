@@ -30,21 +30,30 @@ namespace i8l {
 // same loads and the last piece of a row as tail_at has it; 1, or where the codes
 // pass 2^31 bytes, 16-byte loads at any address. 4096 tokens, two of eight
 // experts, 4096 -> 11008 449 us, 4088 -> 11000 516 us, 4095 -> 11007 626 us.
-constexpr int EF_OPAN = 2 * 256 * 32;                 // outlier panels P[n][16], Q[row][16] (fp16)
-constexpr int EF_SCALES = (256 + 256) * 4;            // SCB / 127^2, SCA
-constexpr int EF_STAGES = 2 * (256 + 256) * 128;      // operand stages; the output tile takes their place
-constexpr int EF_LDS = EF_STAGES + EF_OPAN + EF_SCALES;
+//
+// Short contractions: 128 rows by 128 features, 4 waves of 64 x 64 and one LDS
+// stage, so that three workgroups share a compute unit and their beginnings and
+// ends (tile, tokens, outlier panels; the output's way to memory), which are most
+// of such a tile's time, cover each other: 4096 tokens,
+// eight of 16 experts, bf16, -> 2048: from 128 80 -> 68 us, from 512 104 -> 96; above
+// 1024, or with fewer tiles than three a compute unit, the large ones are faster.
+constexpr int ef_threads(int bm) { return 2 * bm; }
+constexpr int ef_stages(int bm) { return bm == 256 ? 2 * (256 + 256) * 128 : (128 + 128) * 128; }
+constexpr int ef_opan(int bm) { return 2 * bm * 32; }      // outlier panels P[n][16], Q[row][16] (fp16)
+constexpr int ef_lds(int bm) { return ef_stages(bm) + ef_opan(bm) + 2 * bm * 4; }      // and SCB / 127^2, SCA
 
-template <int DT, int BN, int AL>
+template <int DT, int BM, int BN, int AL>
 __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const typename Elem<DT>::T* __restrict__ X,
                                                 int T, const int32_t* __restrict__ rows, const ExpertTile& tile,
-                                                int n0, const int8_t* __restrict__ CBall,
+                                                int n0, int cnt, OutlierCols cols, const int8_t* __restrict__ CBall,
                                                 const float* __restrict__ SCBall, int N, int K,
                                                 typename Elem<DT>::T* __restrict__ out, int8_t* smem) {
-  constexpr int BM = 256, BK = 128, TI = BN / 64, TJ = 2;
-  constexpr int NB = BN / 64;
-  constexpr int STAGE = (BM + BN) * BK, AOFF = BN * BK;
-  static_assert(2 * STAGE <= EF_STAGES && 256 * 512 <= EF_STAGES, "stages and output tile share the same bytes");
+  constexpr int BK = 128, TI = BN / 64, TJ = 2;
+  constexpr int THREADS = ef_threads(BM), RPP = THREADS / 8;      // tile rows a pass loads
+  constexpr int NB = BN / RPP, NA = BM / RPP;
+  constexpr int STAGE = (BM + BN) * BK, AOFF = BN * BK, STAGES = ef_stages(BM), OPAN = ef_opan(BM);
+  static_assert((BM == 256 ? 2 : 1) * STAGE <= STAGES && BM * BN * 2 <= STAGES && BN <= BM,
+                "stages and output tile share the same bytes");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 31, lg = lane >> 5;
@@ -61,13 +70,13 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
   for (int ks = 0; ks < 4; ++ks) roff[ks] = lr * BK + 16 * ((2 * ks + lg) ^ sw);
   const int pb = wn * (BN / 2) * BK, qb = AOFF + wm * 64 * BK;
 
-  v4u RB[NB], RA[4];
+  v4u RB[NB], RA[NA];
   const __amdgpu_buffer_rsrc_t rB = make_rsrc(CB + (int64_t)n0 * K, AL == 1 ? 0 : min(BN, N - n0) * K);
   const int voff = lrow * K + 16 * lc;
   int boff[NB];
   const int8_t* B0 = CB + (int64_t)n0 * K;
 #pragma unroll
-  for (int i = 0; i < NB; ++i) boff[i] = (min(n0 + lrow + 64 * i, N - 1) - n0) * K;   // past N: not stored
+  for (int i = 0; i < NB; ++i) boff[i] = (min(n0 + lrow + RPP * i, N - 1) - n0) * K;   // past N: not stored
   auto load_b = [&](int kt) {
     if constexpr (AL == 1) {
       const int at = tail_at(kt + 16 * lc, K);
@@ -77,21 +86,21 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
       const int v = lrow * K + tail_at(kt + 16 * lc, K);
 #pragma unroll
       for (int i = 0; i < NB; ++i)
-        RB[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rB, v, 64 * i * K, 0));
+        RB[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rB, v, RPP * i * K, 0));
     } else {
       const int v = (kt + 16 * lc < K) ? voff : OOB_OFFSET;
 #pragma unroll
       for (int i = 0; i < NB; ++i)
-        RB[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rB, v, kt + 64 * i * K, 0));
+        RB[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rB, v, kt + RPP * i * K, 0));
     }
   };
   load_b(0);
   const __amdgpu_buffer_rsrc_t rA = make_rsrc(Q.CA, AL == 1 ? 0 : T * K);
-  int aoff[4];
-  const int8_t* pA[4];
+  int aoff[NA];
+  const int8_t* pA[NA];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + lrow + 64 * i;
+  for (int i = 0; i < NA; ++i) {
+    const int r = r0 + lrow + RPP * i;
     const int t = r < r1 ? row_token(rows, r, T) : -1;
     // no token: its scale is 0, whatever its codes
     if constexpr (AL == 1) pA[i] = Q.CA + (int64_t)max(t, 0) * K;
@@ -103,7 +112,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
     if constexpr (AL < 16) {
       const int k = kt + 16 * lc, at = tail_at(k, K);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < NA; ++i) {
         if constexpr (AL == 1) RA[i] = bytes16(pA[i] + at);
         else RA[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rA, aoff[i] + at, 0, 0));
       }
@@ -111,47 +120,46 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
     } else {
       const bool in = kt + 16 * lc < K;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < NA; ++i)
         RA[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rA, in ? aoff[i] : OOB_OFFSET, kt, 0));
     }
   };
   auto write_b = [&](int st) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) *reinterpret_cast<v4u*>(smem + st * STAGE + woff + i * 64 * BK) = RB[i];
+    for (int i = 0; i < NB; ++i) *reinterpret_cast<v4u*>(smem + st * STAGE + woff + i * RPP * BK) = RB[i];
   };
   auto write_a = [&](int st) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<v4u*>(smem + st * STAGE + AOFF + woff + i * 64 * BK) =
+    for (int i = 0; i < NA; ++i)
+      *reinterpret_cast<v4u*>(smem + st * STAGE + AOFF + woff + i * RPP * BK) =
           AL == 16 ? RA[i] : tail_clear<AL>(RA[i], ka, K);      // every step: a branch costs the loop more
   };
   load_a(0);
 
   // the tile's scales, and the panels of the first 16 outlier columns, while
   // the first operand tiles are in flight
-  char* opan = reinterpret_cast<char*>(smem) + EF_STAGES;
-  float* lsb = reinterpret_cast<float*>(opan + EF_OPAN);
-  float* lsa = lsb + 256;
-  const int cnt = *Q.count;
-  const int orow = tid >> 1, oj = (tid & 1) * 8;
+  char* opan = reinterpret_cast<char*>(smem) + STAGES;
+  float* lsb = reinterpret_cast<float*>(opan + OPAN);
+  float* lsa = lsb + BM;
+  const int orow = tid >> 1, oj = (tid & 1) * 8;      // cols: those of oj
   v8h opP = {}, opQ = {};
   auto panels = [&](int jo) {
     const int n = n0 + orow, r = r0 + orow;
-    opP = expert_out_w8(CB, SCB, K, Q.idx, n, orow < BN && n < N, jo + oj, cnt);
-    opQ = expert_out_a8<DT>(Q.sub, Q.cap, X, K, Q.idx, r < r1 ? row_token(rows, r, T) : -1, jo + oj, cnt);
+    opP = expert_out_w8(CB, SCB, K, cols, n, orow < BN && n < N, jo + oj, cnt);
+    opQ = expert_out_a8<DT>(Q.sub, Q.cap, X, K, cols, r < r1 ? row_token(rows, r, T) : -1, jo + oj, cnt);
   };
   auto put_panels = [&]() {
     *reinterpret_cast<v8h*>(opan + orow * 32 + oj * 2) = opP;
-    *reinterpret_cast<v8h*>(opan + EF_OPAN / 2 + orow * 32 + oj * 2) = opQ;
+    *reinterpret_cast<v8h*>(opan + OPAN / 2 + orow * 32 + oj * 2) = opQ;
   };
   if (cnt > 0) panels(0);
-  if (tid < 256) {
+  if (tid < BM) {
     const int n = n0 + tid;
     lsb[tid] = (tid < BN && n < N) ? SCB[n] * (1.0f / 16129.0f) : 0.0f;
   } else {
-    const int r = r0 + tid - 256;
+    const int r = r0 + tid - BM;
     const int t = r < r1 ? row_token(rows, r, T) : -1;
-    lsa[tid - 256] = t >= 0 ? Q.SCA[t] : 0.0f;
+    lsa[tid - BM] = t >= 0 ? Q.SCA[t] : 0.0f;
   }
 
   v16i acc[TI][TJ];
@@ -194,7 +202,25 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
   load_a(BK);
   if (cnt > 0) put_panels();
   __syncthreads();
-  if (r0 + wm * 64 < r1) {
+  const bool busy = r0 + wm * 64 < r1;
+  if constexpr (BM == 128) {
+    for (int kt = 0; kt < nk; ++kt) {
+      if (busy) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          fread(0, ks, ks & 1);
+          mma(ks & 1);
+        }
+      }
+      if (kt + 1 == nk) break;
+      __syncthreads();
+      write_b(0);
+      write_a(0);
+      __syncthreads();
+      load_b((kt + 2) * BK);
+      load_a((kt + 2) * BK);
+    }
+  } else if (busy) {
     fread(0, 0, 0);
     for (int kt = 0; kt < nk; ++kt) {
       const int st = kt & 1;
@@ -227,7 +253,8 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
     }
   }
 
-  // lane (lr, lg), register r of tile (i, j): feature wn BN / 2 + 32 i + 8 (r / 4) + 4 lg + r % 4, row 64 wm + 32 j + lr
+  // lane (lr, lg), register r of tile (i, j): feature wn BN / 2 + 32 i + 8 (r / 4) + 4 lg + r % 4, row 64 wm + 32 j
+  // + lr
   // (the accumulators become fp32 in place)
   const int nl = wn * (BN / 2), ml = wm * 64;
 #pragma unroll
@@ -247,6 +274,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
   }
   for (int jo = 0; jo < cnt; jo += 16) {
     if (jo > 0) {
+      cols = expert_out_cols(Q.idx, jo + oj, cnt);
       panels(jo);
       __syncthreads();
       put_panels();
@@ -257,7 +285,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
       const v8h P = *reinterpret_cast<const v8h*>(opan + (nl + i * 32 + lr) * 32 + lg * 16);
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
-        const v8h V = *reinterpret_cast<const v8h*>(opan + EF_OPAN / 2 + (ml + j * 32 + lr) * 32 + lg * 16);
+        const v8h V = *reinterpret_cast<const v8h*>(opan + OPAN / 2 + (ml + j * 32 + lr) * 32 + lg * 16);
         acc[i][j] = __builtin_bit_cast(
             v16i, __builtin_amdgcn_mfma_f32_32x32x16_f16(P, V, __builtin_bit_cast(v16f, acc[i][j]), 0, 0, 0));
       }
@@ -297,12 +325,12 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
             w[x] = (uint32_t)__builtin_bit_cast(uint16_t, Elem<DT>::from_f32(a)) |
                    ((uint32_t)__builtin_bit_cast(uint16_t, Elem<DT>::from_f32(b)) << 16);
           }
-          *reinterpret_cast<v2u*>(ot + otile_off(ml + j * 32 + lr, (nl + i * 32 + q * 8) >> 3) + 8 * lg) = w;
+          *reinterpret_cast<v2u*>(ot + etile_off<BN>(ml + j * 32 + lr, (nl + i * 32 + q * 8) >> 3) + 8 * lg) = w;
         }
       __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();
-    otile_store<typename Elem<DT>::T>(ot, out, N, r0, n0, r1, min(N, n0 + BN), wave, lane);
+    etile_store<BM, BN, THREADS>(ot, out, N, r0, n0, r1, min(N, n0 + BN));
   }
 }
 
@@ -313,16 +341,42 @@ __global__ __launch_bounds__(512, 1) void k_expert_fwd(ExpertQuantized Q, const 
                                                        const int8_t* __restrict__ CB, const float* __restrict__ SCB,
                                                        int N, int K, typename Elem<DT>::T* __restrict__ out) {
   extern __shared__ __attribute__((aligned(16))) int8_t smem[];
+  const int cnt = *Q.count;
+  const OutlierCols cols = expert_out_cols(Q.idx, (threadIdx.x & 1) * 8, min(cnt, 16));
   const ExpertScan scan = expert_scan(S, R, 256);
-  const ExpertWork work = expert_work(expert_block(), scan.total, (N + 255) / 256);
+  const ExpertWork work = expert_work<true>(expert_block(), scan.total, (N + 255) / 256);
   if (work.slot < 0) return;
   const ExpertTile tile = expert_tile(S, scan, work.slot, R, 256);
   const int n0 = work.tc * 256 + work.part * (256 / work.parts);
   if (tile.r0 >= tile.r1 || n0 >= N) return;
   if (tile.expert < 0) return expert_zeros(out, N, tile.r0, tile.r1, n0, min(N, n0 + 256 / work.parts));
-  if (work.parts == 1) expert_fwd_tile<DT, 256, AL>(Q, X, T, rows, tile, n0, CB, SCB, N, K, out, smem);
-  else if (work.parts == 2) expert_fwd_tile<DT, 128, AL>(Q, X, T, rows, tile, n0, CB, SCB, N, K, out, smem);
-  else expert_fwd_tile<DT, 64, AL>(Q, X, T, rows, tile, n0, CB, SCB, N, K, out, smem);
+  if (work.parts == 1)
+    expert_fwd_tile<DT, 256, 256, AL>(Q, X, T, rows, tile, n0, cnt, cols, CB, SCB, N, K, out, smem);
+  else if (work.parts == 2)
+    expert_fwd_tile<DT, 256, 128, AL>(Q, X, T, rows, tile, n0, cnt, cols, CB, SCB, N, K, out, smem);
+  else
+    expert_fwd_tile<DT, 256, 64, AL>(Q, X, T, rows, tile, n0, cnt, cols, CB, SCB, N, K, out, smem);
+}
+
+// Tiles 128 x 128.
+template <int DT, int AL>
+__global__ __launch_bounds__(256, 3) void k_expert_fwd_short(ExpertQuantized Q,
+                                                             const typename Elem<DT>::T* __restrict__ X, int T,
+                                                             const int32_t* __restrict__ rows, int R, ExpertSegs S,
+                                                             const int8_t* __restrict__ CB,
+                                                             const float* __restrict__ SCB, int N, int K,
+                                                             typename Elem<DT>::T* __restrict__ out) {
+  __shared__ __attribute__((aligned(16))) int8_t smem[ef_lds(128)];
+  const int cnt = *Q.count;
+  const OutlierCols cols = expert_out_cols(Q.idx, (threadIdx.x & 1) * 8, min(cnt, 16));
+  const ExpertScan scan = expert_scan(S, R, 128);
+  const ExpertWork work = expert_work<false>(expert_block(), scan.total, (N + 127) / 128);
+  if (work.slot < 0) return;
+  const ExpertTile tile = expert_tile(S, scan, work.slot, R, 128);
+  const int n0 = work.tc * 128;
+  if (tile.r0 >= tile.r1) return;
+  if (tile.expert < 0) return expert_zeros(out, N, tile.r0, tile.r1, n0, min(N, n0 + 128));
+  expert_fwd_tile<DT, 128, 128, AL>(Q, X, T, rows, tile, n0, cnt, cols, CB, SCB, N, K, out, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -363,6 +417,8 @@ __global__ __launch_bounds__(256, AL == 1 ? 4 : 8) void k_expert_fwd_thin(Expert
   const int lr = lane & 15, lg = lane >> 4;
   const int64_t ts = bid / tiles_n;
   const int n0 = (int)(bid - ts * tiles_n) * WG_N + (KS == 1 ? wave * BN : 0);
+  const int cnt = *Q.count;
+  const OutlierCols cols = expert_out_cols(Q.idx, lg * 8, cnt);
   const ExpertScan scan = expert_scan(S, R, BM);
   if (ts >= scan.total) return;
   const ExpertTile tile = expert_tile(S, scan, (int)ts, R, BM);
@@ -400,18 +456,16 @@ __global__ __launch_bounds__(256, AL == 1 ? 4 : 8) void k_expert_fwd_thin(Expert
   const int t = r < tile.r1 ? row_token(rows, r, T) : -1;
   // what the wave that finishes the tile needs for that is requested before the contraction
   const int nb = n0 + 4 * lg;
-  int cnt = 0;
   float sa = 0.0f, sb[4] = {};
   v8h P = {}, V = {};
   if (KS == 1 || wave == 0) {
-    cnt = *Q.count;
     if (t >= 0) sa = Q.SCA[t];
 #pragma unroll
     for (int x = 0; x < 4; ++x)
       if (nb + x < N) sb[x] = SCB[nb + x];
     if (cnt > 0) {
-      P = expert_out_w8(CB, SCB, K, Q.idx, n0 + lr, n0 + lr < N, lg * 8, cnt);
-      V = expert_out_a8<DT>(Q.sub, Q.cap, X, K, Q.idx, t, lg * 8, cnt);
+      P = expert_out_w8(CB, SCB, K, cols, n0 + lr, n0 + lr < N, lg * 8, cnt);
+      V = expert_out_a8<DT>(Q.sub, Q.cap, X, K, cols, t, lg * 8, cnt);
     }
   }
   v4i acc = {0, 0, 0, 0};
@@ -468,8 +522,9 @@ __global__ __launch_bounds__(256, AL == 1 ? 4 : 8) void k_expert_fwd_thin(Expert
   for (int x = 0; x < 4; ++x) y[x] = (float)sum[x] * (sa * (sb[x] * (1.0f / 16129.0f)));
   if (cnt > 0) y = __builtin_amdgcn_mfma_f32_16x16x32_f16(P, V, y, 0, 0, 0);
   for (int jo = 32; jo < cnt; jo += 32) {
-    P = expert_out_w8(CB, SCB, K, Q.idx, n0 + lr, n0 + lr < N, jo + lg * 8, cnt);
-    V = expert_out_a8<DT>(Q.sub, Q.cap, X, K, Q.idx, t, jo + lg * 8, cnt);
+    const OutlierCols more = expert_out_cols(Q.idx, jo + lg * 8, cnt);
+    P = expert_out_w8(CB, SCB, K, more, n0 + lr, n0 + lr < N, jo + lg * 8, cnt);
+    V = expert_out_a8<DT>(Q.sub, Q.cap, X, K, more, t, jo + lg * 8, cnt);
     y = __builtin_amdgcn_mfma_f32_16x16x32_f16(P, V, y, 0, 0, 0);
   }
   if (r < tile.r1) {
@@ -721,12 +776,22 @@ static hipError_t launch_fwd_t(const ExpertQuantized& Q, const void* X, int T, c
                        static_cast<const E*>(X), T, rows, R, S, CB, SCB, N, K, tiles_n, static_cast<E*>(out));
     return hipGetLastError();
   }
+  const int64_t tiles = expert_slots(R, S.n_seg, 128) * ((N + 127) / 128);
+  if (K <= 1024 && tiles >= 768) {      // three workgroups on every compute unit
+    auto kern = al == 1   ? k_expert_fwd_short<DT, 1>
+                : al == 4 ? k_expert_fwd_short<DT, 4>
+                          : k_expert_fwd_short<DT, 16>;
+    hipLaunchKernelGGL(kern, expert_grid(tiles), dim3(256), 0, st, Q,
+                       static_cast<const E*>(X), T, rows, R, S, CB, SCB, N, K, static_cast<E*>(out));
+    return hipGetLastError();
+  }
   static std::atomic<uint64_t> lds_set[3];
   auto kern = al == 1 ? k_expert_fwd<DT, 1> : al == 4 ? k_expert_fwd<DT, 4> : k_expert_fwd<DT, 16>;
-  const hipError_t e = lds_limit_once((const void*)kern, EF_LDS, lds_set[al == 1 ? 0 : al == 4 ? 1 : 2]);
+  constexpr int lds = ef_lds(256);
+  const hipError_t e = lds_limit_once((const void*)kern, lds, lds_set[al == 1 ? 0 : al == 4 ? 1 : 2]);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, expert_grid(expert_groups(expert_slots(R, S.n_seg, 256), (N + 255) / 256)), dim3(512),
-                     EF_LDS, st, Q, static_cast<const E*>(X), T, rows, R, S, CB, SCB, N, K, static_cast<E*>(out));
+                     lds, st, Q, static_cast<const E*>(X), T, rows, R, S, CB, SCB, N, K, static_cast<E*>(out));
   return hipGetLastError();
 }
 
