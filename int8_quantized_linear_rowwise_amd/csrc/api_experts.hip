@@ -53,13 +53,14 @@ int product_sizes(int64_t R, int64_t N, int64_t K, int64_t n_experts, int64_t n_
   return I8L_OK;
 }
 
-// Lists of at most GRAD_LIST tensors: f(list, its partial sums' start). I8L_OK, I8L_EINVAL, I8L_EDTYPE or I8L_ESHAPE.
+// Lists of at most GRAD_LIST tensors: f(list, its partial sums' start), and for no tensors one empty list. I8L_OK,
+// I8L_EINVAL, I8L_EDTYPE or I8L_ESHAPE.
 template <typename F>
 int grad_lists(const i8l_grad_tensor* t, int64_t count, F f) {
   if (count < 0 || (count > 0 && t == nullptr)) return I8L_EINVAL;
   if (count > ((int64_t)1 << 24)) return I8L_ESHAPE;
-  int64_t at = 0;
-  for (int64_t i = 0; i < count;) {
+  int64_t at = 0, i = 0;
+  do {
     i8l::GradList l;
     l.count = 0;
     int64_t chunks = 0;
@@ -79,13 +80,15 @@ int grad_lists(const i8l_grad_tensor* t, int64_t count, F f) {
     const int rc = f(l, at);
     if (rc != I8L_OK) return rc;
     at += i8l::grad_groups(chunks);
-  }
+  } while (i < count);
   return I8L_OK;
 }
+// Partial sums of all lists: *n, 0 where a single list is small enough for one launch.
 int grad_partials(const i8l_grad_tensor* t, int64_t count, int64_t* n) {
   *n = 0;
   return grad_lists(t, count, [&](const i8l::GradList& l, int64_t at) {
-    *n = at + i8l::grad_groups(l.start[l.count]);
+    const int chunks = l.start[l.count];
+    *n = at + (at == 0 && count <= i8l::GRAD_LIST && chunks <= i8l::grad_small_chunks() ? 0 : i8l::grad_groups(chunks));
     return *n > INT32_MAX ? I8L_ESHAPE : I8L_OK;
   });
 }
@@ -235,6 +238,11 @@ int int8_grad_norm(const i8l_grad_tensor* grads, int64_t count, int norm_type, d
   if ((uintptr_t)ws % ALIGN) return I8L_EINVAL;
   const bool inf = norm_type == I8L_NORM_INF;
   hipStream_t st = (hipStream_t)stream;
+  if (n == 0 && count <= i8l::GRAD_LIST)
+    return grad_lists(grads, count, [&](const i8l::GradList& l, int64_t) {
+      return hip_status(
+          i8l::launch_grad_small(l, inf, max_norm, grad_scale, clip, norm, factor, found_inf, st));
+    });
   double* partial = static_cast<double*>(ws);
   int e = grad_lists(grads, count, [&](const i8l::GradList& l, int64_t at) {
     return hip_status(i8l::launch_grad_partial(l, inf, partial + at, st));

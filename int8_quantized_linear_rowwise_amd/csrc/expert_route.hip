@@ -13,16 +13,18 @@ namespace i8l {
 // so the sort is stable and the result the same on every run.
 //
 // Bound by launches and by the chains of dependent LDS accesses. One workgroup
-// takes up to 2048 choices in one launch; more take a launch that counts and
+// takes up to 8192 choices in one launch; more take a launch that counts and
 // one that places, in which every workgroup adds up the counts of the others
-// itself instead of waiting for a third.
-constexpr int SORT_WAVES = 8;
-constexpr int SORT_BLOCK = 2048;       // choices of a workgroup, more where there would be over 256 workgroups
+// itself instead of waiting for a third. SORTFIG
+constexpr int SORT_WAVES = 8, SORT_THREADS = 64 * SORT_WAVES;
+constexpr int SORT_ALONE = 16 * SORT_THREADS;     // choices that one workgroup takes
+constexpr int SORT_BLOCK = 4 * SORT_THREADS;      // of each of several, more where there would be over 256
 constexpr int SORT_MAX_BLOCKS = 256;
 
 static int sort_per_block(int64_t R) {
+  if (R <= SORT_ALONE) return SORT_ALONE;
   const int64_t most = (R + SORT_MAX_BLOCKS - 1) / SORT_MAX_BLOCKS;
-  return (int)((most > SORT_BLOCK ? most : SORT_BLOCK) + 511) / 512 * 512;
+  return (int)((most > SORT_BLOCK ? most : SORT_BLOCK) + SORT_BLOCK - 1) / SORT_BLOCK * SORT_BLOCK;
 }
 static int sort_blocks(int64_t R) {
   const int pb = sort_per_block(R);
@@ -33,35 +35,49 @@ size_t expert_sort_ints(int64_t R, int n_experts) {
   return b > 1 ? (size_t)b * (size_t)n_experts : 0;
 }
 
-template <typename ID>
-__device__ __forceinline__ int expert_id(const ID* __restrict__ ids, int i, int E) {
-  const ID v = ids[i];
-  return (v >= 0 && v < (ID)E) ? (int)v : -1;
+// f(choice, its expert or -1, whether there is one) for the wave's choices [lo, hi), 64 at a time in order, PER such
+// groups loaded at once.
+template <int PER, typename ID, typename F>
+__device__ __forceinline__ void each_choice(const ID* __restrict__ ids, int lo, int hi, int E, F f) {
+  const int lane = threadIdx.x & 63;
+  for (int i0 = lo; i0 < hi; i0 += 64 * PER) {
+    ID v[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) {
+      const int i = i0 + 64 * u + lane;
+      v[u] = i < hi ? ids[i] : (ID)-1;
+    }
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+      if (i0 + 64 * u < hi) {
+        const int i = i0 + 64 * u + lane;
+        f(i, (v[u] >= 0 && v[u] < (ID)E) ? (int)v[u] : -1, i < hi);
+      }
+  }
 }
 
 // Counts of the block's choices by wave and expert, in LDS.
-template <typename ID>
+template <int PER, typename ID>
 __device__ __forceinline__ void count_ids(const ID* __restrict__ ids, int lo, int hi, int E, int32_t* hist) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int i = threadIdx.x; i < SORT_WAVES * E; i += 64 * SORT_WAVES) hist[i] = 0;
+  const int wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < SORT_WAVES * E; i += SORT_THREADS) hist[i] = 0;
   __syncthreads();
-  for (int i = lo + lane; i < hi; i += 64) {
-    const int e = expert_id(ids, i, E);
+  each_choice<PER>(ids, lo, hi, E, [&](int, int e, bool) {
     if (e >= 0) atomicAdd(&hist[wave * E + e], 1);
-  }
+  });
   __syncthreads();
 }
 
 template <typename ID>
-__global__ __launch_bounds__(64 * SORT_WAVES) void k_expert_count(const ID* __restrict__ ids, int R, int E,
-                                                                  int per_block, int32_t* __restrict__ counts) {
+__global__ __launch_bounds__(SORT_THREADS) void k_expert_count(const ID* __restrict__ ids, int R, int E,
+                                                               int per_block, int32_t* __restrict__ counts) {
   extern __shared__ int32_t hist[];
   const int run = per_block / SORT_WAVES, wave = threadIdx.x >> 6;
   const int64_t b0 = (int64_t)blockIdx.x * per_block;
   const int lo = (int)min((int64_t)R, b0 + (int64_t)wave * run);
   const int hi = (int)min((int64_t)R, b0 + (int64_t)(wave + 1) * run);
-  count_ids(ids, lo, hi, E, hist);
-  for (int e = threadIdx.x; e < E; e += 64 * SORT_WAVES) {
+  count_ids<4>(ids, lo, hi, E, hist);
+  for (int e = threadIdx.x; e < E; e += SORT_THREADS) {
     int n = 0;
 #pragma unroll
     for (int w = 0; w < SORT_WAVES; ++w) n += hist[w * E + e];
@@ -69,50 +85,45 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void k_expert_count(const ID* __re
   }
 }
 
-template <typename ID>
-__global__ __launch_bounds__(64 * SORT_WAVES) void k_expert_place(const ID* __restrict__ ids, int R, int k, int E,
-                                                                  int per_block, const int32_t* __restrict__ counts,
-                                                                  int32_t* __restrict__ off,
-                                                                  int32_t* __restrict__ token,
-                                                                  int32_t* __restrict__ position) {
+template <int PER, typename ID>
+__global__ __launch_bounds__(SORT_THREADS) void k_expert_place(const ID* __restrict__ ids, int R, int k, int E,
+                                                               int per_block, const int32_t* __restrict__ counts,
+                                                               int32_t* __restrict__ off, int32_t* __restrict__ token,
+                                                               int32_t* __restrict__ position) {
   extern __shared__ int32_t hist[];                // [SORT_WAVES][E], then one total a wave
   int32_t* sums = hist + SORT_WAVES * E;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int run = per_block / SORT_WAVES;
+  // a block's choices are dealt out evenly, so that a few of them take all waves
   const int64_t b0 = (int64_t)blockIdx.x * per_block;
-  const int lo = (int)min((int64_t)R, b0 + (int64_t)wave * run);
-  const int hi = (int)min((int64_t)R, b0 + (int64_t)(wave + 1) * run);
-  count_ids(ids, lo, hi, E, hist);
+  const int mine = (int)min((int64_t)per_block, R - b0);
+  const int run = ((mine + SORT_WAVES - 1) / SORT_WAVES + 63) / 64 * 64;
+  const int lo = (int)b0 + min(mine, wave * run), hi = (int)b0 + min(mine, (wave + 1) * run);
+  count_ids<PER>(ids, lo, hi, E, hist);
 
   // per expert: rows of all blocks, and of the blocks before this one
   int carry = 0;                                   // rows of the experts of earlier passes
-  for (int e0 = 0; e0 < E; e0 += 64 * SORT_WAVES) {
+  for (int e0 = 0; e0 < E; e0 += SORT_THREADS) {
     const int e = e0 + tid;
-    int all = 0, before = 0, mine = 0;
+    int all = 0, before = 0, own = 0;
     if (e < E) {
 #pragma unroll
-      for (int w = 0; w < SORT_WAVES; ++w) mine += hist[w * E + e];
+      for (int w = 0; w < SORT_WAVES; ++w) own += hist[w * E + e];
       if (counts) {
-        for (int b0 = 0; b0 < (int)gridDim.x; b0 += 16) {   // 16 loads in flight
+        for (int b1 = 0; b1 < (int)gridDim.x; b1 += 16) {   // 16 loads in flight
           int c[16];
 #pragma unroll
-          for (int u = 0; u < 16; ++u) c[u] = b0 + u < (int)gridDim.x ? counts[(int64_t)(b0 + u) * E + e] : 0;
+          for (int u = 0; u < 16; ++u) c[u] = b1 + u < (int)gridDim.x ? counts[(int64_t)(b1 + u) * E + e] : 0;
 #pragma unroll
           for (int u = 0; u < 16; ++u) {
             all += c[u];
-            before += b0 + u < (int)blockIdx.x ? c[u] : 0;
+            before += b1 + u < (int)blockIdx.x ? c[u] : 0;
           }
         }
       } else {
-        all = mine;
+        all = own;
       }
     }
-    int incl = all;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o, 64);
-      incl += lane >= o ? v : 0;
-    }
+    const int incl = lane_scan(all);
     if (lane == 63) sums[wave] = incl;
     __syncthreads();
     int first = carry, total = 0;
@@ -138,15 +149,12 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void k_expert_place(const ID* __re
   }
   if (blockIdx.x == 0 && tid == 0) off[E] = carry;
   // rows behind the last routed one
-  for (int64_t r = (int64_t)carry + blockIdx.x * (64 * SORT_WAVES) + tid; r < R;
-       r += (int64_t)gridDim.x * (64 * SORT_WAVES))
+  for (int64_t r = (int64_t)carry + blockIdx.x * SORT_THREADS + tid; r < R; r += (int64_t)gridDim.x * SORT_THREADS)
     token[r] = -1;
 
   const int bits = 32 - __clz(E);                  // of the numbers 0 .. E
   volatile int32_t* cursor = hist + wave * E;
-  for (int i0 = lo; i0 < hi; i0 += 64) {
-    const int i = i0 + lane;
-    const int e = i < hi ? expert_id(ids, i, E) : -1;
+  each_choice<PER>(ids, lo, hi, E, [&](int i, int e, bool in) {
     const int key = e < 0 ? E : e;
     uint64_t same = ~0ull;
     for (int b = 0; b < bits; ++b) {
@@ -159,11 +167,11 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void k_expert_place(const ID* __re
     __builtin_amdgcn_wave_barrier();               // every lane has read before the last one of each expert writes
     if (e >= 0 && rank == __popcll(same) - 1) cursor[e] = row + 1;
     __builtin_amdgcn_wave_barrier();
-    if (i < hi) {
+    if (in) {
       position[i] = row;
       if (row >= 0) token[row] = i / k;
     }
-  }
+  });
 }
 
 template <typename ID>
@@ -171,10 +179,14 @@ static hipError_t launch_sort_t(const ID* ids, int R, int k, int E, int32_t* off
                                 int32_t* scratch, hipStream_t st) {
   const int blocks = R > 0 ? sort_blocks(R) : 1, pb = sort_per_block(R);
   const size_t lds = ((size_t)SORT_WAVES * E + SORT_WAVES) * sizeof(int32_t);
-  if (blocks > 1)
-    hipLaunchKernelGGL(k_expert_count<ID>, dim3(blocks), dim3(64 * SORT_WAVES), lds, st, ids, R, E, pb, scratch);
-  hipLaunchKernelGGL(k_expert_place<ID>, dim3(blocks), dim3(64 * SORT_WAVES), lds, st, ids, R, k, E, pb,
-                     blocks > 1 ? scratch : nullptr, off, token, position);
+  if (blocks == 1) {
+    hipLaunchKernelGGL((k_expert_place<16, ID>), dim3(1), dim3(SORT_THREADS), lds, st, ids, R, k, E, pb, nullptr, off,
+                       token, position);
+  } else {
+    hipLaunchKernelGGL(k_expert_count<ID>, dim3(blocks), dim3(SORT_THREADS), lds, st, ids, R, E, pb, scratch);
+    hipLaunchKernelGGL((k_expert_place<4, ID>), dim3(blocks), dim3(SORT_THREADS), lds, st, ids, R, k, E, pb, scratch,
+                       off, token, position);
+  }
   return hipGetLastError();
 }
 

@@ -164,6 +164,10 @@ hipError_t launch_grad_partial(const GradList& list, bool inf, double* partial, 
 hipError_t launch_grad_final(const double* partial, int n, bool inf, double max_norm, const float* grad_scale,
                              float* norm, float* factor, float* found_inf, hipStream_t st);
 hipError_t launch_grad_scale(const GradList& list, const float* factor, hipStream_t st);
+// All of that in one launch, for a single list of up to grad_small_chunks() chunks.
+int grad_small_chunks();
+hipError_t launch_grad_small(const GradList& list, bool inf, double max_norm, const float* grad_scale, int clip,
+                             float* norm, float* factor, float* found_inf, hipStream_t st);
 
 // AdamW over a table of tensors: chunk c is values [chunk * adamw_chunk(), ...)
 // of its tensor, one workgroup each.

@@ -109,14 +109,16 @@ def test_grad_norm_host_errors(L):  # noqa: F811
 
     def call(t, count=None, kind=2, top=1.0, norm=FAKE, factor=FAKE, bad=FAKE, ws=FAKE, wsb=1 << 30):
         return f(t, len(t) if count is None else count, kind, top, None, 0, norm, factor, bad, ws, wsb, None)
-    ok = table((FAKE, 100, 2), (FAKE, 5, 0))
+    ok = table((FAKE, 1 << 20, 2), (FAKE, 5, 0))
     assert call(ok, count=-1) == L.I8L_EINVAL and call(ok, count=(1 << 24) + 1) == L.I8L_ESHAPE
     assert call(ok, kind=1) == L.I8L_EINVAL
     assert call(ok, top=-1.0) == L.I8L_EINVAL and call(ok, top=math.nan) == L.I8L_EINVAL
     for k in ("norm", "factor", "bad"):
         assert call(ok, **{k: 0}) == L.I8L_EINVAL, k
-    assert need(ok, 2) == 256 and need(ok, -1) == 0
-    assert call(ok, wsb=15) == L.I8L_EWORKSPACE and call(ok, ws=0) == L.I8L_EWORKSPACE
+    assert need(ok, 2) == 1280 and need(ok, -1) == 0           # 129 partial sums
+    assert need(table((FAKE, 100, 2)), 1) == 0 and need(table((FAKE, 1 << 17, 2)), 1) == 0
+    assert need(table((FAKE, (1 << 17) + 1, 2)), 1) == 256 and need(table(*[(FAKE, 1, 0)] * 17), 17) == 256
+    assert call(ok, wsb=129 * 8 - 1) == L.I8L_EWORKSPACE and call(ok, ws=0) == L.I8L_EWORKSPACE
     assert call(ok, ws=FAKE + 8) == L.I8L_EINVAL
     assert call(table((FAKE, 100, 3))) == L.I8L_EDTYPE
     assert call(table((FAKE, -1, 2))) == L.I8L_EINVAL and call(table((0, 1, 2))) == L.I8L_EINVAL

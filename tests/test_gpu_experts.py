@@ -26,7 +26,7 @@ def gpu(*ts):
 @pytest.mark.parametrize("T,k,E,drop", [
     (1, 2, 8, 0), (0, 2, 4, 0), (5, 0, 4, 0), (3, 1, 1, 0), (7, 3, 0, 0), (64, 4, 64, 0), (257, 2, 5, 0.5),
     (1024, 2, 128, 0), (1025, 2, 128, 0.1), (3000, 8, 1000, 0.1), (2048, 1, 1024, 0), (777, 3, 7, 1.0),
-    (5000, 8, 3, 0.02),
+    (5000, 8, 3, 0.02), (8192, 1, 40, 0.1), (4097, 2, 9, 0), (1, 1, 1024, 0), (129, 63, 100, 0.3),
 ])
 def test_sort(I8, T, k, E, drop, dtype):
     ids = X.choices(T, k, E, T + k, drop).to(dtype)

@@ -28,7 +28,8 @@ def near(got, want):
     return abs(float(got) - want) <= 2.0 ** -23 * abs(want)
 
 
-LISTS = [[1], [0, 5, 0], [8191, 8192, 8193], [31] * 200, [100000, 1, 7, 65536], [3] * 161 + [0] * 160 + [9], [20_000_003]]
+LISTS = [[1], [0, 5, 0], [8191, 8192, 8193], [31] * 200, [100000, 1, 7, 65536], [3] * 161 + [0] * 160 + [9],
+         [20_000_003], [131072], [131073], [5] * 16, [5] * 17, [0] * 170, [0] * 165 + [4]]
 
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16", "mixed"])
@@ -42,7 +43,7 @@ def test_norm_and_clip(I8, dt, sizes, kind):
         want, factor = X.grad_norm(g, math.inf if top is None else top, kind, 1.0 if c is None else c)
         scale = None if c is None else torch.tensor(c, device=DEV)
         norm, f, bad = plan.norm(top, kind, scale)
-        assert near(norm, want) and near(f, factor) and float(bad) == 0
+        assert near(norm, want) and near(f, factor) and float(bad) == 0, (top, c)
         again = plan.norm(top, kind, scale)
         assert all(torch.equal(a, b) for a, b in zip((norm, f, bad), again))
     before = [x.clone() for x in g]
@@ -141,7 +142,7 @@ def test_refusals(I8):
     with pytest.raises(ValueError):
         I8.GradNormPlan([g, torch.zeros(3)])
     with pytest.raises(ValueError, match="workspace"):
-        I8.GradNormPlan([g]).norm(1.0, workspace=torch.zeros(4, dtype=torch.uint8, device=DEV))
+        I8.GradNormPlan([torch.zeros(1 << 20, device=DEV)]).norm(1.0, workspace=torch.zeros(4, dtype=torch.uint8, device=DEV))
 
 
 def test_replays(I8):
