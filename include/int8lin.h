@@ -450,7 +450,7 @@ int int8_adamw_step(const void* table, int64_t count, int64_t chunks, double lr,
  * found_inf: one fp32 each on the device, none NULL. count = 0 is fine (norm 0).
  * With clip no two tensors may overlap. A norm_type that is neither, or a
  * max_norm that is negative or NaN, is I8L_EINVAL; more than 2^42 values in one
- * launch's 160 tensors are I8L_ESHAPE. Few values need no workspace (its size is
+ * launch's 280 tensors are I8L_ESHAPE. Few values need no workspace (its size is
  * 0, it may be NULL).
  * ------------------------------------------------------------------------ */
 #define I8L_NORM_INF 0

@@ -71,9 +71,10 @@ int grad_lists(const i8l_grad_tensor* t, int64_t count, F f) {
       if (t[i].g == nullptr || (uintptr_t)t[i].g % (t[i].dtype == I8L_F32 ? 4 : 2)) return I8L_EINVAL;
       if (t[i].n > MAX_VALUES) return I8L_ESHAPE;
       l.p[l.count] = t[i].g;
-      l.n[l.count] = t[i].n << 2 | t[i].dtype;
+      const int64_t c = (t[i].n + i8l::grad_chunk() - 1) / i8l::grad_chunk();
+      l.last[l.count] = (uint16_t)((t[i].n - (c - 1) * i8l::grad_chunk()) << 2 | t[i].dtype);
       l.start[l.count++] = (int32_t)chunks;
-      chunks += (t[i].n + i8l::grad_chunk() - 1) / i8l::grad_chunk();
+      chunks += c;
       if (chunks > (1 << 29)) return I8L_ESHAPE;
     }
     l.start[l.count] = (int32_t)chunks;

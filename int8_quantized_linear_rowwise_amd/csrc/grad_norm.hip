@@ -28,13 +28,17 @@ int grad_groups(int64_t chunks) { return (int)(chunks < GN_GROUPS ? chunks : GN_
 // The list in LDS, and the tensor of a chunk.
 struct ListLds {
   const void* p[GRAD_LIST];
-  int64_t n[GRAD_LIST];
   int32_t start[GRAD_LIST + 1];
+  uint16_t last[GRAD_LIST];
+  __device__ __forceinline__ int64_t values(int t) const {
+    return (int64_t)(start[t + 1] - start[t] - 1) * GN_CHUNK + (last[t] >> 2);
+  }
 };
+static_assert(GN_CHUNK << 2 < 65536 && sizeof(GradList) + 64 <= 4096, "packed sizes");
 __device__ __forceinline__ void list_to_lds(const GradList& list, ListLds& s) {
   for (int i = threadIdx.x; i < list.count; i += blockDim.x) {
     s.p[i] = list.p[i];
-    s.n[i] = list.n[i];
+    s.last[i] = list.last[i];
   }
   for (int i = threadIdx.x; i <= list.count; i += blockDim.x) s.start[i] = list.start[i];
   __syncthreads();
@@ -102,7 +106,7 @@ __device__ __forceinline__ double sum_chunks(const ListLds& s, int count, int fi
   double sum = 0.0;
   for (int c = first; c < total; c += step) {
     const int t = tensor_of(s, count, c);
-    const int64_t n = s.n[t] >> 2, at = (int64_t)(c - s.start[t]) * GN_CHUNK;
+    const int64_t n = s.values(t), at = (int64_t)(c - s.start[t]) * GN_CHUNK;
     const bool vec = (uintptr_t)s.p[t] % 16 == 0;
     auto one = [&](auto dt) {
       constexpr int DT = decltype(dt)::value;
@@ -121,7 +125,7 @@ __device__ __forceinline__ double sum_chunks(const ListLds& s, int count, int fi
         }
       });
     };
-    switch ((int)(s.n[t] & 3)) {
+    switch (s.last[t] & 3) {
       case DT_F32: one(std::integral_constant<int, DT_F32>{}); break;
       case DT_F16: one(std::integral_constant<int, DT_F16>{}); break;
       default: one(std::integral_constant<int, DT_BF16>{}); break;
@@ -135,7 +139,7 @@ __device__ __forceinline__ void scale_chunks(const ListLds& s, int count, int fi
   const int total = s.start[count];
   for (int c = first; c < total; c += step) {
     const int t = tensor_of(s, count, c);
-    const int64_t n = s.n[t] >> 2, from = (int64_t)(c - s.start[t]) * GN_CHUNK;
+    const int64_t n = s.values(t), from = (int64_t)(c - s.start[t]) * GN_CHUNK;
     const bool vec = (uintptr_t)s.p[t] % 16 == 0;
     auto one = [&](auto dt) {
       constexpr int DT = decltype(dt)::value;
@@ -164,7 +168,7 @@ __device__ __forceinline__ void scale_chunks(const ListLds& s, int count, int fi
         }
       });
     };
-    switch ((int)(s.n[t] & 3)) {
+    switch (s.last[t] & 3) {
       case DT_F32: one(std::integral_constant<int, DT_F32>{}); break;
       case DT_F16: one(std::integral_constant<int, DT_F16>{}); break;
       default: one(std::integral_constant<int, DT_BF16>{}); break;

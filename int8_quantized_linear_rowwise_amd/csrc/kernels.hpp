@@ -150,11 +150,11 @@ hipError_t launch_expert_combine_bwd(int dt, const void* G, int T, int N, const 
 
 // Norm of many tensors: the list travels in the kernels' arguments, GRAD_LIST
 // tensors a launch.
-constexpr int GRAD_LIST = 160;
+constexpr int GRAD_LIST = 280;   // the arguments of a launch have to stay within 4 KB
 struct GradList {
   const void* p[GRAD_LIST];
-  int64_t n[GRAD_LIST];          // values << 2 | dtype
   int32_t start[GRAD_LIST + 1];  // first chunk of each tensor; [count]: all of them
+  uint16_t last[GRAD_LIST];      // values of its last chunk << 2 | dtype
   int32_t count;
 };
 int grad_chunk();

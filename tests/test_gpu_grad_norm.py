@@ -29,7 +29,8 @@ def near(got, want):
 
 
 LISTS = [[1], [0, 5, 0], [8191, 8192, 8193], [31] * 200, [100000, 1, 7, 65536], [3] * 161 + [0] * 160 + [9],
-         [20_000_003], [131072], [131073], [5] * 16, [5] * 17, [0] * 170, [0] * 165 + [4]]
+         [20_000_003], [131072], [131073], [5] * 16, [5] * 17, [0] * 290, [0] * 285 + [4],
+         [3] * 281 + [0] * 280 + [9], [4, 16384] * 150]
 
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16", "mixed"])
