@@ -20,7 +20,7 @@ namespace i8l {
 
 constexpr int GN_VALUES = 32;                 // values of a thread in one chunk
 constexpr int GN_CHUNK = 256 * GN_VALUES;
-constexpr int GN_GROUPS = 2048;               // workgroups of a launch: eight on each compute unit
+constexpr int GN_GROUPS = 1024;               // workgroups of a launch: as many as are at work at once
 
 int grad_chunk() { return GN_CHUNK; }
 int grad_groups(int64_t chunks) { return (int)(chunks < GN_GROUPS ? chunks : GN_GROUPS); }
