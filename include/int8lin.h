@@ -500,7 +500,7 @@ int int8_expert_sort(const void* experts, int id_bytes, int64_t T, int64_t k, in
  * CB: n_experts x N x K int8, SCB: n_experts x N fp32 (int8_quantize_rowwise of
  * the n_experts N rows, tau off). rows: R int32 on the device; a value outside
  * [0, T) makes a row of zeros, and a token may be named any number of times.
- * out: R x N of `dtype`. K <= I8L_MAX_K, N <= I8L_MAX_COLS, T, R <= 2^24,
+ * out: R x N of `dtype`, no part of an input. K <= I8L_MAX_K, N <= I8L_MAX_COLS, T, R <= 2^24,
  * n_seg, n_experts <= 65536, else I8L_ESHAPE. The size query takes the call's own
  * sizes and looks at no more of CB than its address; it returns 0 for a few
  * tokens (workspace may then be NULL).
@@ -533,7 +533,8 @@ int int8_expert_backward(const void* G, int dtype, int64_t R, int64_t N, const i
  * only. No two positions may name the same row. Rows of grad_Y that no position
  * names are left as they were, but with n_rows (one int32 on the device: the
  * sort's last offset) the rows from *n_rows on get 0. grad_gate is 0 where the
- * position is left out. k <= 64, N <= I8L_MAX_COLS, T, R <= 2^24, else I8L_ESHAPE. */
+ * position is left out. Apart from base no output may overlap an input.
+ * k <= 64, N <= I8L_MAX_COLS, T, R <= 2^24, else I8L_ESHAPE. */
 int int8_expert_combine(const void* Y, int dtype, int64_t R, int64_t N, const int32_t* position, const float* gate,
                         const void* base, int64_t T, int64_t k, void* out, void* stream);
 int int8_expert_combine_backward(const void* G, int dtype, int64_t T, int64_t N, const int32_t* position,

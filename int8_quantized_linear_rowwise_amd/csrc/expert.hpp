@@ -244,15 +244,20 @@ __device__ __forceinline__ void expert_zeros(E* out, int64_t ld, int r0, int r1,
     for (int c = c0 + threadIdx.x; c < c1; c += blockDim.x) out[r * ld + c] = E{};
 }
 
+// Scale of a row without a token: such a row is zeros, whatever its expert's weights hold.
+constexpr float NO_TOKEN = -0.0f;
+__device__ __forceinline__ bool no_token(float sa) { return __float_as_uint(sa) == 0x80000000u; }
+
 // Output tiles of BM rows by BN 16-bit values in LDS, so that global stores cover
 // whole rows: 16-byte chunk c of row r at chunk position c ^ (r mod BN / 8).
 template <int BN>
 __device__ __forceinline__ int etile_off(int row, int chunk) {
   return row * (2 * BN) + 16 * (chunk ^ (row & (BN / 8 - 1)));
 }
+// Rows whose scale in `lsa` says that they have no token are stored as zeros.
 template <int BM, int BN, int THREADS, typename E>
-__device__ __forceinline__ void etile_store(const char* ot, E* __restrict__ dst, int64_t ld, int r0, int c0, int r1,
-                                            int c1) {
+__device__ __forceinline__ void etile_store(const char* ot, const float* lsa, E* __restrict__ dst, int64_t ld, int r0,
+                                            int c0, int r1, int c1) {
   static_assert(sizeof(E) == 2, "16-bit outputs");
   constexpr int CPR = BN / 8;
   const bool vec = ld % 8 == 0 && (uintptr_t)dst % 16 == 0;
@@ -260,7 +265,8 @@ __device__ __forceinline__ void etile_store(const char* ot, E* __restrict__ dst,
   for (int i = threadIdx.x; i < BM * CPR; i += THREADS) {
     const int row = i / CPR, ch = i % CPR, r = r0 + row, c = c0 + ch * 8;
     if (r >= r1) continue;
-    const v4u v = *reinterpret_cast<const v4u*>(ot + etile_off<BN>(row, ch));
+    v4u v = *reinterpret_cast<const v4u*>(ot + etile_off<BN>(row, ch));
+    if (no_token(lsa[row])) v = v4u{0u, 0u, 0u, 0u};
     E* p = dst + (int64_t)r * ld + c;
     if (vec && c + 8 <= c1) {
       *reinterpret_cast<v4u*>(p) = v;

@@ -102,7 +102,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
   for (int i = 0; i < NA; ++i) {
     const int r = r0 + lrow + RPP * i;
     const int t = r < r1 ? row_token(rows, r, T) : -1;
-    // no token: its scale is 0, whatever its codes
+    // no token: the row is stored as zeros, whatever its codes
     if constexpr (AL == 1) pA[i] = Q.CA + (int64_t)max(t, 0) * K;
     else if constexpr (AL == 4) aoff[i] = max(t, 0) * K;
     else aoff[i] = t >= 0 ? t * K + 16 * lc : OOB_OFFSET;
@@ -159,7 +159,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
   } else {
     const int r = r0 + tid - BM;
     const int t = r < r1 ? row_token(rows, r, T) : -1;
-    lsa[tid - BM] = t >= 0 ? Q.SCA[t] : 0.0f;
+    lsa[tid - BM] = t >= 0 ? Q.SCA[t] : NO_TOKEN;
   }
 
   v16i acc[TI][TJ];
@@ -297,6 +297,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
     for (int j = 0; j < TJ; ++j) {
       const int r = r0 + ml + j * 32 + lr;
       if (r >= r1) continue;
+      const bool none = no_token(lsa[ml + j * 32 + lr]);
 #pragma unroll
       for (int i = 0; i < TI; ++i)
 #pragma unroll
@@ -304,7 +305,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
           const int n = n0 + nl + i * 32 + q * 8 + lg * 4;
           float y[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) y[x] = __int_as_float(acc[i][j][4 * q + x]);
+          for (int x = 0; x < 4; ++x) y[x] = none ? 0.0f : __int_as_float(acc[i][j][4 * q + x]);
           expert_store4<DT>(out + (int64_t)r * N + n, y, N - n, ov);
         }
     }
@@ -330,7 +331,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
       __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();
-    etile_store<BM, BN, THREADS>(ot, out, N, r0, n0, r1, min(N, n0 + BN));
+    etile_store<BM, BN, THREADS>(ot, lsa, out, N, r0, n0, r1, min(N, n0 + BN));
   }
 }
 
@@ -528,7 +529,9 @@ __global__ __launch_bounds__(256, AL == 1 ? 4 : 8) void k_expert_fwd_thin(Expert
     y = __builtin_amdgcn_mfma_f32_16x16x32_f16(P, V, y, 0, 0, 0);
   }
   if (r < tile.r1) {
-    const float v[4] = {y[0], y[1], y[2], y[3]};
+    float v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = t >= 0 ? y[x] : 0.0f;
     expert_store4<DT>(out + (int64_t)r * N + nb, v, N - nb, N % 4 == 0 && (uintptr_t)out % (4 * sizeof(E)) == 0);
   }
 }
@@ -684,7 +687,7 @@ __global__ __launch_bounds__(256, TM == 1 ? 6 : 4) void k_expert_fwd_tiny(
     }
   }
   v4i acc = {0, 0, 0, 0};
-  const int8_t* mycodes = codes + max(t, 0) * kp;      // no token: its scale is 0
+  const int8_t* mycodes = codes + max(t, 0) * kp;
   for (int c = wave; c < nc; c += 4) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
@@ -715,7 +718,9 @@ __global__ __launch_bounds__(256, TM == 1 ? 6 : 4) void k_expert_fwd_tiny(
     y = __builtin_amdgcn_mfma_f32_16x16x32_f16(P, V, y, 0, 0, 0);
   }
   if (r < tile.r1) {
-    const float v[4] = {y[0], y[1], y[2], y[3]};
+    float v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = t >= 0 ? y[x] : 0.0f;
     expert_store4<DT>(out + (int64_t)r * N + nb, v, N - nb, N % 4 == 0 && (uintptr_t)out % (4 * sizeof(E)) == 0);
   }
 }

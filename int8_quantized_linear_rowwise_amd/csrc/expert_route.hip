@@ -242,14 +242,14 @@ __global__ __launch_bounds__(256) void k_expert_combine(const typename Elem<DT>:
                                                         const typename Elem<DT>::T* base, int T, int k, int txs,
                                                         typename Elem<DT>::T* out) {
   const int tx = threadIdx.x & ((1 << txs) - 1), ty = threadIdx.x >> txs;
-  const int t = blockIdx.x * (256 >> txs) + ty;
+  const int64_t t = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * (256 >> txs) + ty;
   const int c = (blockIdx.y * (1 << txs) + tx) * 8;
   if (t >= T || c >= N) return;
   const int n = min(8, N - c);
   float s[8] = {};
-  if (base) cld<DT>(base + (int64_t)t * N + c, n, VEC, s);
-  const int32_t* pos = position + (int64_t)t * k;
-  const float* gt = gate ? gate + (int64_t)t * k : nullptr;
+  if (base) cld<DT>(base + t * N + c, n, VEC, s);
+  const int32_t* pos = position + t * k;
+  const float* gt = gate ? gate + t * k : nullptr;
   for (int j0 = 0; j0 < k; j0 += 4) {
     float f[4][8], w[4];
     bool has[4];
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(256) void k_expert_combine(const typename Elem<DT>:
         for (int e = 0; e < 8; ++e) s[e] = __builtin_fmaf(w[u], f[u][e], s[e]);
       }
   }
-  cst<DT>(out + (int64_t)t * N + c, n, VEC, s);
+  cst<DT>(out + t * N + c, n, VEC, s);
 }
 
 template <int DT>
@@ -278,7 +278,9 @@ static hipError_t launch_combine_t(const void* Y, int R, int N, const int32_t* p
   const int chunks = (N + 7) / 8;
   int txs = 3;
   while (txs < 8 && (1 << txs) < chunks) ++txs;
-  const dim3 grid((unsigned)((T + (256 >> txs) - 1) / (256 >> txs)), (unsigned)((chunks + (1 << txs) - 1) >> txs));
+  // workgroups of tokens in x and, over 2^20, in z: a grid axis holds fewer than 2^32 threads
+  const dim3 tokens = expert_grid((T + (256 >> txs) - 1) / (256 >> txs));
+  const dim3 grid(tokens.x, (unsigned)((chunks + (1 << txs) - 1) >> txs), tokens.y);
   auto kern = vec ? k_expert_combine<DT, true> : k_expert_combine<DT, false>;
   hipLaunchKernelGGL(kern, grid, dim3(256), 0, st, static_cast<const E*>(Y), R, N, position, gate,
                      static_cast<const E*>(base), T, k, txs, static_cast<E*>(out));
@@ -310,12 +312,14 @@ __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<
                                                             float* __restrict__ ggate) {
   constexpr int PER = 256 / TT;
   const int blocks = (T + PER - 1) / PER;
-  if ((int)blockIdx.x >= blocks) {
+  const int64_t bid = expert_block();
+  if (bid >= blocks) {
+    if (!n_rows || bid >= blocks + ZERO_BLOCKS) return;
     const int64_t from = min(max(n_rows[0], 0), R);
     const float zero[8] = {};
     const int chunks = (N + 7) / 8;
     const int64_t items = (R - from) * (int64_t)chunks;
-    for (int64_t i = (int64_t)(blockIdx.x - blocks) * 256 + threadIdx.x; i < items; i += (int64_t)ZERO_BLOCKS * 256) {
+    for (int64_t i = (bid - blocks) * 256 + threadIdx.x; i < items; i += (int64_t)ZERO_BLOCKS * 256) {
       const int64_t r = i / chunks;
       const int c = (int)(i - r * chunks) * 8;
       cst<DT>(gY + (from + r) * N + c, min(8, N - c), VEC, zero);
@@ -323,7 +327,7 @@ __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<
     return;
   }
   __shared__ float part[4][4];
-  const int tid = threadIdx.x % TT, t = (int)blockIdx.x * PER + threadIdx.x / TT;
+  const int tid = threadIdx.x % TT, t = (int)bid * PER + threadIdx.x / TT;
   const bool live = t < T;
   const int32_t* pos = position + (int64_t)(live ? t : 0) * k;
   const float* gt = gate ? gate + (int64_t)(live ? t : 0) * k : nullptr;
@@ -390,10 +394,11 @@ static hipError_t launch_combine_bwd_t(const void* G, int T, int N, const int32_
                                        hipStream_t st) {
   typedef typename Elem<DT>::T E;
   const bool vec = N % 8 == 0 && (((uintptr_t)G | (uintptr_t)Y | (uintptr_t)gY) % 16 == 0);
-  const unsigned blocks = (unsigned)((T + 256 / TT - 1) / (256 / TT)) + (n_rows && gY ? ZERO_BLOCKS : 0);
+  if (!gY) n_rows = nullptr;
+  const int64_t blocks = (T + 256 / TT - 1) / (256 / TT) + (n_rows ? ZERO_BLOCKS : 0);
   if (blocks == 0) return hipSuccess;
   auto kern = vec ? k_expert_combine_bwd<DT, true, TT> : k_expert_combine_bwd<DT, false, TT>;
-  hipLaunchKernelGGL(kern, dim3(blocks), dim3(256), 0, st, static_cast<const E*>(G), T, N, position, gate, k,
+  hipLaunchKernelGGL(kern, expert_grid(blocks), dim3(256), 0, st, static_cast<const E*>(G), T, N, position, gate, k,
                      static_cast<const E*>(Y), R, n_rows, static_cast<E*>(gY), ggate);
   return hipGetLastError();
 }

@@ -231,7 +231,8 @@ class AdamW(torch.optim.Optimizer):
     def grad_norm(self, max_norm: Optional[float] = None, norm_type: float = 2.0,
                   grad_scale: Optional[torch.Tensor] = None):
         """(norm, factor, found_inf) over the gradients of all groups, as GradNormPlan.norm: `step` takes the factor as
-        its grad_scale, which clips without a pass of its own, and found_inf. All gradients have to be on one GPU."""
+        its grad_scale, which clips without a pass of its own, and found_inf. There has to be a gradient, and all of
+        them on one GPU."""
         grads = [p.grad for group in self.param_groups for p in group["params"] if p.grad is not None]
         plan = GradNormPlan(grads)
         if _capturing(plan.gpu):   # a graph's replays read these very gradients and the scale

@@ -157,6 +157,23 @@ def test_forward_thresholds(I8, tau):
     run_forward(I8, "bf16", 20, 128, 64, [0, 8, 20], tau=tau)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16"])
+@pytest.mark.parametrize("T,K,N,R", [(2, 64, 40, 9), (40, 64, 40, 60), (700, 64, 3000, 2000), (700, 2048, 600, 1200)])
+def test_forward_rows_without_token_hide_weights(I8, dt, T, K, N, R):
+    """Rows without a token are zeros even where the expert's scales are not finite, in every kernel."""
+    CB, SCB = gpu(*X.weights(2, N, K, 1))
+    x = X.inputs(T, K, dt, 2).to(DEV)
+    SCB[:, ::3] = float("inf")
+    SCB[:, 1::3] = float("nan")
+    rows = (torch.arange(R) % T).int()
+    rows[::5] = -1
+    rows[3::7] = T
+    off = torch.tensor([0, R // 3, R], dtype=torch.int32, device=DEV)
+    out = I8.expert_forward(x, CB, SCB, off, rows=rows.to(DEV))
+    none = ((rows < 0) | (rows >= T)).to(DEV)
+    assert (out[none] == 0).all() and (out[~none][:, 1::3]).isnan().all()
+
+
 def test_forward_more_segments_than_experts(I8):
     """Many short segments that share experts, in any order; over 64 and over 4096 segments."""
     for S in (70, 4500):
@@ -344,6 +361,18 @@ def test_combine_backward(I8, dt, T, k, E, N, gated):
     assert none is None and torch.equal(only, gY)
     none, only = I8.expert_combine_backward(G, pos, gate, Y, with_grad_Y=False)
     assert none is None and torch.equal(only, gg)
+
+
+def test_combine_of_very_many_tokens(I8):
+    """The most tokens there can be, and more workgroups than one axis of the grid is given."""
+    for T, N in ((1 << 24, 1), ((1 << 20) + 3, 2048)):
+        pos = torch.arange(T, dtype=torch.int32, device=DEV).view(T, 1).flip(0)
+        Y = torch.arange(T, dtype=torch.float32, device=DEV)[:, None].repeat(1, N).bfloat16()
+        want = Y.flip(0)
+        assert torch.equal(I8.expert_combine(Y, pos), want)
+        gY, gg = I8.expert_combine_backward(want, pos, None, Y, n_rows=pos[:1].view(1) + 1)
+        assert torch.equal(gY, Y)
+        assert torch.equal(gg, want[:, :1].float().square() * N)      # N equal terms, each exact: 16 bits squared
 
 
 def test_combine_backward_leaves_unnamed_rows(I8):

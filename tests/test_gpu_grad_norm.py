@@ -143,7 +143,8 @@ def test_refusals(I8):
     with pytest.raises(ValueError):
         I8.GradNormPlan([g, torch.zeros(3)])
     with pytest.raises(ValueError, match="workspace"):
-        I8.GradNormPlan([torch.zeros(1 << 20, device=DEV)]).norm(1.0, workspace=torch.zeros(4, dtype=torch.uint8, device=DEV))
+        I8.GradNormPlan([torch.zeros(1 << 20, device=DEV)]).norm(
+            1.0, workspace=torch.zeros(4, dtype=torch.uint8, device=DEV))
 
 
 def test_replays(I8):
