@@ -21,6 +21,9 @@ size_t align_up(size_t x) { return (x + ALIGN - 1) / ALIGN * ALIGN; }
 bool valid_dtype(int dt) { return dt == I8L_F32 || dt == I8L_F16 || dt == I8L_BF16; }
 int hip_status(hipError_t e) { return e == hipSuccess ? I8L_OK : I8L_EHIP; }
 
+// Bytes of a row of codes: rows start on 16-byte borders whatever K is.
+int code_row(int64_t K) { return (int)((K + 15) / 16 * 16); }
+
 struct Layout {
   size_t count, idx, scale, codes, sub, scratch, total;
   int32_t cap;
@@ -36,7 +39,7 @@ Layout forward_layout(int64_t T, int64_t K) {
   L.scale = at;
   at += align_up((size_t)T * 4);
   L.codes = at;
-  at += align_up((size_t)T * (size_t)K);
+  at += align_up((size_t)T * (size_t)code_row(K));
   L.sub = at;
   at += align_up((size_t)T * (size_t)L.cap * 2);
   L.scratch = at;
@@ -153,15 +156,17 @@ int int8_expert_forward(const void* X, int dtype, int64_t T, int64_t K, const in
   int32_t* idx = reinterpret_cast<int32_t*>(w + L.idx);
   float* SCA = reinterpret_cast<float*>(w + L.scale);
   int8_t* CA = reinterpret_cast<int8_t*>(w + L.codes);
+  const int lda = code_row(K);
   uint16_t* sub = reinterpret_cast<uint16_t*>(w + L.sub);
   hipStream_t st = (hipStream_t)stream;
   const hipError_t e =
       i8l::quantize_small_fits(T, K, threshold)
-          ? i8l::launch_quantize_small(dtype, X, (int)T, (int)K, threshold, CA, SCA, idx, count, sub, L.cap, st)
+          ? i8l::launch_quantize_small(dtype, X, (int)T, (int)K, threshold, CA, lda, SCA, idx, count, sub, L.cap,
+                                       st)
           : i8l::launch_quantize(dtype, X, T, (int)K, threshold, CA, SCA, idx, count, sub, L.cap,
-                                 reinterpret_cast<uint32_t*>(w + L.scratch), st, nullptr, (int)K);
+                                 reinterpret_cast<uint32_t*>(w + L.scratch), st, nullptr, (int)K, nullptr, lda);
   if (e != hipSuccess) return I8L_EHIP;
-  const i8l::ExpertQuantized Q = {CA, SCA, sub, L.cap, idx, count};
+  const i8l::ExpertQuantized Q = {CA, lda, SCA, sub, L.cap, idx, count};
   return hip_status(i8l::launch_expert_fwd(dtype, Q, X, (int)T, rows, (int)R, S, CB, SCB, (int)N, (int)K, out, st));
 }
 

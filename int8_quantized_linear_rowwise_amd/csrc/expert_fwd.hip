@@ -28,15 +28,20 @@ namespace i8l {
 // time of a full one.
 // AL, what K (16 at least) and the weights' address are multiples of: 16; 4, the
 // same loads and the last piece of a row as tail_at has it; 1, or where the codes
-// pass 2^31 bytes, 16-byte loads at any address. 4096 tokens, two of eight
-// experts, 4096 -> 11008 449 us, 4088 -> 11000 516 us, 4095 -> 11007 626 us.
+// pass 2^31 bytes, 16-byte loads at any address. Rows of codes start on 16-byte
+// borders for every K, so that only a row's last piece is read across them. 4096
+// tokens, two of eight experts, bf16, 4096 -> 11008 431 us, 4088 -> 11000 457 us
+// (500 with rows of K codes), 4095 -> 11007 597 us (688).
 //
 // Short contractions: 128 rows by 128 features, 4 waves of 64 x 64 and one LDS
 // stage, so that three workgroups share a compute unit and their beginnings and
 // ends (tile, tokens, outlier panels; the output's way to memory), which are most
-// of such a tile's time, cover each other: 4096 tokens,
-// eight of 16 experts, bf16, -> 2048: from 128 80 -> 68 us, from 512 104 -> 96; above
-// 1024, or with fewer tiles than three a compute unit, the large ones are faster.
+// of such a tile's time, cover each other. Up to 512 always, up to 1024 where every
+// compute unit gets a tile. bf16, large tiles against these: 4096 tokens, eight of
+// 16 experts, 128 -> 2048 80 us against 68, 512 -> 2048 104 against 91; 777 tokens,
+// three of five, -> 1530: from 128 28 against 24, 1024 34 against 31, 2048 41 against
+// 42; 512 tokens, two of four, -> 1024 (96 tiles): from 512 20.6 against 19.7, 1024
+// 22.5 against 23.3.
 constexpr int ef_threads(int bm) { return 2 * bm; }
 constexpr int ef_stages(int bm) { return bm == 256 ? 2 * (256 + 256) * 128 : (128 + 128) * 128; }
 constexpr int ef_opan(int bm) { return 2 * bm * 32; }      // outlier panels P[n][16], Q[row][16] (fp16)
@@ -95,7 +100,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
     }
   };
   load_b(0);
-  const __amdgpu_buffer_rsrc_t rA = make_rsrc(Q.CA, AL == 1 ? 0 : T * K);
+  const __amdgpu_buffer_rsrc_t rA = make_rsrc(Q.CA, AL == 1 ? 0 : T * Q.lda);
   int aoff[NA];
   const int8_t* pA[NA];
 #pragma unroll
@@ -103,9 +108,9 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
     const int r = r0 + lrow + RPP * i;
     const int t = r < r1 ? row_token(rows, r, T) : -1;
     // no token: the row is stored as zeros, whatever its codes
-    if constexpr (AL == 1) pA[i] = Q.CA + (int64_t)max(t, 0) * K;
-    else if constexpr (AL == 4) aoff[i] = max(t, 0) * K;
-    else aoff[i] = t >= 0 ? t * K + 16 * lc : OOB_OFFSET;
+    if constexpr (AL == 1) pA[i] = Q.CA + (int64_t)max(t, 0) * Q.lda;
+    else if constexpr (AL == 4) aoff[i] = max(t, 0) * Q.lda;
+    else aoff[i] = t >= 0 ? t * Q.lda + 16 * lc : OOB_OFFSET;
   }
   int ka = 0;      // AL < 16: first byte of the codes in RA
   auto load_a = [&](int kt) {
@@ -477,7 +482,7 @@ __global__ __launch_bounds__(256, AL == 1 ? 4 : 8) void k_expert_fwd_thin(Expert
       const int k = c * ET_KC + s * 64 + lg * 16;
       a[s] = v4i{0, 0, 0, 0};
       if (t >= 0) {
-        const int8_t* p = Q.CA + (int64_t)t * K;
+        const int8_t* p = Q.CA + (int64_t)t * Q.lda;
         if constexpr (AL == 16) {
           if (k < K) a[s] = *reinterpret_cast<const v4i*>(p + k);
         } else {
@@ -763,7 +768,7 @@ static hipError_t launch_fwd_t(const ExpertQuantized& Q, const void* X, int T, c
                                const ExpertSegs& S, const int8_t* CB, const float* SCB, int N, int K, void* out,
                                hipStream_t st) {
   typedef typename Elem<DT>::T E;
-  const bool far = (int64_t)T * K >= ((int64_t)1 << 31);
+  const bool far = (int64_t)T * Q.lda >= ((int64_t)1 << 31);
   const int al = K < 16 || K % 4 != 0 || (uintptr_t)CB % 4 != 0 || far ? 1
                  : K % 16 != 0 || (uintptr_t)CB % 16 != 0              ? 4
                                                                        : 16;
@@ -782,7 +787,7 @@ static hipError_t launch_fwd_t(const ExpertQuantized& Q, const void* X, int T, c
     return hipGetLastError();
   }
   const int64_t tiles = expert_slots(R, S.n_seg, 128) * ((N + 127) / 128);
-  if (K <= 1024 && tiles >= 768) {      // three workgroups on every compute unit
+  if (K <= 512 || (K <= 1024 && tiles >= 256)) {
     auto kern = al == 1   ? k_expert_fwd_short<DT, 1>
                 : al == 4 ? k_expert_fwd_short<DT, 4>
                           : k_expert_fwd_short<DT, 16>;

@@ -15,7 +15,9 @@ namespace i8l {
 // Bound by launches and by the chains of dependent LDS accesses. One workgroup
 // takes up to 8192 choices in one launch; more take a launch that counts and
 // one that places, in which every workgroup adds up the counts of the others
-// itself instead of waiting for a third. SORTFIG
+// itself instead of waiting for a third. Two choices of 8 experts 11 us, of which the
+// kernel 4.6; 8192 of 64 15 us; 131072 of 128 17 us (3 and 9 in the kernels), where the
+// bytes alone would take half a microsecond.
 constexpr int SORT_WAVES = 8, SORT_THREADS = 64 * SORT_WAVES;
 constexpr int SORT_ALONE = 16 * SORT_THREADS;     // choices that one workgroup takes
 constexpr int SORT_BLOCK = 4 * SORT_THREADS;      // of each of several, more where there would be over 256

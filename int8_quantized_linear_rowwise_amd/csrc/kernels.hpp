@@ -12,6 +12,8 @@ namespace i8l {
 // 32-bit words.
 // preflags: column flag words ([slabs][words], the layout of the scratch)
 // handed over by the producer of X; the flags pass is then skipped.
+// ldq: bytes of a row of codes, cols or a larger multiple of 8 (what is behind a
+// row's codes is then not defined); 0 stands for cols.
 //
 // Columns of the weight's dequantized outlier slice kept for a staging width
 // cap: a multiple of 8 (16-byte rows), at most 256.
@@ -34,12 +36,12 @@ size_t quant_scratch_words(int64_t rows, int64_t cols);
 hipError_t launch_quantize(int dt, const void* X, int64_t rows, int cols, float tau, int8_t* codes, float* scale,
                            int32_t* idx, int32_t* count, uint16_t* sub, int cap, uint32_t* scratch,
                            hipStream_t st, const uint32_t* preflags = nullptr, int idx_cap = -1,
-                           const OutlierWeights* ow = nullptr);
+                           const OutlierWeights* ow = nullptr, int ldq = 0);
 
 // The same in one launch for a few rows (idx holds cols entries), where quantize_small_fits().
 bool quantize_small_fits(int64_t rows, int64_t cols, float tau);
-hipError_t launch_quantize_small(int dt, const void* X, int rows, int cols, float tau, int8_t* codes, float* scale,
-                                 int32_t* idx, int32_t* count, uint16_t* sub, int cap, hipStream_t st);
+hipError_t launch_quantize_small(int dt, const void* X, int rows, int cols, float tau, int8_t* codes, int ldq,
+                                 float* scale, int32_t* idx, int32_t* count, uint16_t* sub, int cap, hipStream_t st);
 
 // Producer of a quantizer input: A = D(SiLU(H)) and A's column flag words
 // (quant_scratch_words(rows, cols) words) for tau.
@@ -121,7 +123,8 @@ hipError_t launch_expert_sort(const void* experts, int id_bytes, int R, int k, i
 // out (R x N of dt) = products of the quantized tokens (codes CA, scales SCA, outlier columns) with their rows'
 // experts (CB: n_experts x N x K); row r is token rows[r] (r itself when rows is NULL).
 struct ExpertQuantized {
-  const int8_t* CA;
+  const int8_t* CA;      // rows of lda bytes, a multiple of 16
+  int lda;
   const float* SCA;
   const uint16_t* sub;
   int cap;

@@ -222,12 +222,13 @@ __global__ __launch_bounds__(256) void k_colflags(const typename Elem<DT>::T* __
 // ---------------------------------------------------------------------------
 // Per-chunk pieces of the row kernels (a chunk: 8 consecutive columns; the rest in quantize.hpp).
 
-// chunk ci of row `row` to memory: codes, 0 on outlier columns, whose fp16
+// chunk ci of row `row` to memory: codes (rows of ldq bytes; where they are longer than
+// cols, of whole 8-byte pieces with anything behind), 0 on outlier columns, whose fp16
 // values go to the dense sub-matrix at their rank among the outlier columns
 // (the prefix of the column's mask word plus the set bits below it)
 template <int DT, bool VEC>
-__device__ __forceinline__ void chunk_emit(int8_t* __restrict__ codes, uint16_t* __restrict__ sub, int cap,
-                                           int cols, const uint32_t* smask, const int32_t* sprefix, int64_t row,
+__device__ __forceinline__ void chunk_emit(int8_t* __restrict__ codes, int ldq, uint16_t* __restrict__ sub,
+                                           int cap, int cols, const uint32_t* smask, const int32_t* sprefix, int64_t row,
                                            int ci, const v4u& a, const v4u& b, float inv, uint32_t om, bool any) {
   const int c0 = ci * 8;
   uint32_t lo, hi;
@@ -254,8 +255,8 @@ __device__ __forceinline__ void chunk_emit(int8_t* __restrict__ codes, uint16_t*
       if (j < cap) srow[j] = __builtin_bit_cast(uint16_t, (_Float16)chunk_val<DT>(a, b, e));
     }
   }
-  int8_t* cr = codes + row * (int64_t)cols + c0;
-  if constexpr (VEC) {
+  int8_t* cr = codes + row * (int64_t)ldq + c0;
+  if (VEC || ldq > cols) {
     *reinterpret_cast<v2u*>(cr) = v2u{lo, hi};
   } else {
     for (int e = 0; e < 8; ++e)
@@ -366,7 +367,8 @@ __device__ __forceinline__ void weight_slice(const int8_t* __restrict__ wCB, con
 template <int DT, int NCH, bool VEC, bool WG = false>
 __global__ __launch_bounds__(256) void k_rowquant(const typename Elem<DT>::T* __restrict__ X, int64_t rows,
                                                   int cols, int tau_on, const uint32_t* __restrict__ bits,
-                                                  int slabs, int8_t* __restrict__ codes, float* __restrict__ scale,
+                                                  int slabs, int8_t* __restrict__ codes, int ldq,
+                                                  float* __restrict__ scale,
                                                   int32_t* __restrict__ idx, int idx_cap,
                                                   int32_t* __restrict__ count, uint16_t* __restrict__ sub, int cap,
                                                   const int8_t* __restrict__ wCB, const float* __restrict__ wSCB,
@@ -449,7 +451,7 @@ __global__ __launch_bounds__(256) void k_rowquant(const typename Elem<DT>::T* __
     return chunk_absmax<DT, VEC>(a, b, om, any);
   };
   auto emit = [&](int64_t row, int ci, const v4u& a, const v4u& b, float inv, uint32_t om, bool any) {
-    chunk_emit<DT, VEC>(codes, sub, cap, cols, smask, sprefix, row, ci, a, b, inv, om, any);
+    chunk_emit<DT, VEC>(codes, ldq, sub, cap, cols, smask, sprefix, row, ci, a, b, inv, om, any);
   };
   // with WG the wave maxima meet in LDS; the two slots alternate by row, so
   // one barrier per row suffices
@@ -558,7 +560,7 @@ constexpr int QS_THREADS = 512, QS_CHUNKS = 2;
 template <int DT, bool VEC>
 __global__ __launch_bounds__(QS_THREADS) void k_quant_small(const typename Elem<DT>::T* __restrict__ X, int rows,
                                                             int cols, float tau, int cps, int8_t* __restrict__ codes,
-                                                            float* __restrict__ scale, int32_t* __restrict__ idx,
+                                                            int ldq, float* __restrict__ scale, int32_t* __restrict__ idx,
                                                             int idx_cap, int32_t* __restrict__ count,
                                                             uint16_t* __restrict__ sub, int cap) {
 #pragma clang fp contract(off)
@@ -635,7 +637,7 @@ __global__ __launch_bounds__(QS_THREADS) void k_quant_small(const typename Elem<
   for (int i = 0; i < QS_CHUNKS; ++i) {
     const int ci = t + i * QS_THREADS;
     if (ci < nchunk)
-      chunk_emit<DT, VEC>(codes, sub, cap, cols, smask, sprefix, row, ci, ra[i], rb[i], inv, om[i], true);
+      chunk_emit<DT, VEC>(codes, ldq, sub, cap, cols, smask, sprefix, row, ci, ra[i], rb[i], inv, om[i], true);
   }
   if (t == 0) scale[row] = s;
 }
@@ -652,7 +654,7 @@ size_t quant_scratch_words(int64_t rows, int64_t cols) {
 }
 
 template <int DT>
-static hipError_t launch_quantize_t(const void* Xv, int64_t rows, int cols, float tau, int8_t* codes,
+static hipError_t launch_quantize_t(const void* Xv, int64_t rows, int cols, float tau, int8_t* codes, int ldq,
                                     float* scale, int32_t* idx, int idx_cap, int32_t* count, uint16_t* sub, int cap,
                                     uint32_t* scratch, const uint32_t* preflags, const OutlierWeights* ow,
                                     hipStream_t st) {
@@ -696,7 +698,7 @@ static hipError_t launch_quantize_t(const void* Xv, int64_t rows, int cols, floa
     int64_t nb = WGM ? wblocks : rblocks;                                                                       \
     if (fblocks > nb) nb = fblocks < RQ_MAX_BLOCKS ? fblocks : RQ_MAX_BLOCKS;                                   \
     hipLaunchKernelGGL(kern, dim3((unsigned)nb), dim3(256), lds, st, X, rows, cols, (int)tau_on, bits, slabs,   \
-                       codes, scale, idx, idx_cap, count, sub, cap, wCB, wSCB, wN, wsub, wcap);                 \
+                       codes, ldq, scale, idx, idx_cap, count, sub, cap, wCB, wSCB, wN, wsub, wcap);                 \
   } while (0)
   // 16-bit rows stay in registers between the absmax and the quantization:
   // rows of up to 4096 values in one wave, up to 32768 values spread over a
@@ -732,40 +734,45 @@ bool quantize_small_fits(int64_t rows, int64_t cols, float tau) {
 }
 
 template <int DT>
-static hipError_t launch_quantize_small_t(const void* Xv, int rows, int cols, float tau, int8_t* codes, float* scale,
-                                          int32_t* idx, int32_t* count, uint16_t* sub, int cap, hipStream_t st) {
+static hipError_t launch_quantize_small_t(const void* Xv, int rows, int cols, float tau, int8_t* codes, int ldq,
+                                          float* scale, int32_t* idx, int32_t* count, uint16_t* sub, int cap, hipStream_t st) {
   typedef typename Elem<DT>::T T;
   const T* X = static_cast<const T*>(Xv);
   const bool vec = (cols % 8 == 0) && aligned(X, 16) && aligned(codes, 8);
   int cps = 0;
   while ((1 << cps) < (cols + 7) / 8 && (1 << cps) < QS_THREADS) ++cps;
   auto kern = vec ? k_quant_small<DT, true> : k_quant_small<DT, false>;
-  hipLaunchKernelGGL(kern, dim3((unsigned)rows), dim3(QS_THREADS), 0, st, X, rows, cols, tau, cps, codes, scale, idx,
-                     cols, count, sub, cap);
+  hipLaunchKernelGGL(kern, dim3((unsigned)rows), dim3(QS_THREADS), 0, st, X, rows, cols, tau, cps, codes, ldq, scale,
+                     idx, cols, count, sub, cap);
   return hipGetLastError();
 }
 
-hipError_t launch_quantize_small(int dt, const void* X, int rows, int cols, float tau, int8_t* codes, float* scale,
-                                 int32_t* idx, int32_t* count, uint16_t* sub, int cap, hipStream_t st) {
-  if (dt == DT_F32) return launch_quantize_small_t<DT_F32>(X, rows, cols, tau, codes, scale, idx, count, sub, cap, st);
-  if (dt == DT_F16) return launch_quantize_small_t<DT_F16>(X, rows, cols, tau, codes, scale, idx, count, sub, cap, st);
-  return launch_quantize_small_t<DT_BF16>(X, rows, cols, tau, codes, scale, idx, count, sub, cap, st);
+hipError_t launch_quantize_small(int dt, const void* X, int rows, int cols, float tau, int8_t* codes, int ldq,
+                                 float* scale, int32_t* idx, int32_t* count, uint16_t* sub, int cap,
+                                 hipStream_t st) {
+  if (dt == DT_F32)
+    return launch_quantize_small_t<DT_F32>(X, rows, cols, tau, codes, ldq, scale, idx, count, sub, cap, st);
+  if (dt == DT_F16)
+    return launch_quantize_small_t<DT_F16>(X, rows, cols, tau, codes, ldq, scale, idx, count, sub, cap, st);
+  return launch_quantize_small_t<DT_BF16>(X, rows, cols, tau, codes, ldq, scale, idx, count, sub, cap, st);
 }
 
 hipError_t launch_quantize(int dt, const void* X, int64_t rows, int cols, float tau, int8_t* codes, float* scale,
                            int32_t* idx, int32_t* count, uint16_t* sub, int cap, uint32_t* scratch,
-                           hipStream_t st, const uint32_t* preflags, int idx_cap, const OutlierWeights* ow) {
+                           hipStream_t st, const uint32_t* preflags, int idx_cap, const OutlierWeights* ow,
+                           int ldq) {
   if (idx_cap < 0) idx_cap = cap;
+  if (ldq <= 0) ldq = cols;
   if (ow != nullptr && (ow->K != cols || ow->wcap > 256)) return hipErrorInvalidValue;
   switch (dt) {
     case DT_F32:
-      return launch_quantize_t<DT_F32>(X, rows, cols, tau, codes, scale, idx, idx_cap, count, sub, cap, scratch,
+      return launch_quantize_t<DT_F32>(X, rows, cols, tau, codes, ldq, scale, idx, idx_cap, count, sub, cap, scratch,
                                        preflags, ow, st);
     case DT_F16:
-      return launch_quantize_t<DT_F16>(X, rows, cols, tau, codes, scale, idx, idx_cap, count, sub, cap, scratch,
+      return launch_quantize_t<DT_F16>(X, rows, cols, tau, codes, ldq, scale, idx, idx_cap, count, sub, cap, scratch,
                                        preflags, ow, st);
     default:
-      return launch_quantize_t<DT_BF16>(X, rows, cols, tau, codes, scale, idx, idx_cap, count, sub, cap, scratch,
+      return launch_quantize_t<DT_BF16>(X, rows, cols, tau, codes, ldq, scale, idx, idx_cap, count, sub, cap, scratch,
                                         preflags, ow, st);
   }
 }
