@@ -172,18 +172,14 @@ __device__ __forceinline__ v4u bytes16(const int8_t* p) {
   __builtin_memcpy(&v, p, 16);
   return v;
 }
-// Rows of K >= 16 bytes that are no multiple of 16: the last piece is loaded so
-// that it ends with the row (at tail_at(k)), in both operands alike; in the
-// codes, the bytes that the piece before holds already are cleared.
+// Rows of K >= 16 bytes at any address: the last piece is loaded so that it ends
+// with the row (at tail_at(k)), in both operands alike; in the codes, the bytes
+// that the piece before holds already are cleared.
 __device__ __forceinline__ int tail_at(int k, int K) { return min(k, K - 16); }
-template <int AL>
 __device__ __forceinline__ v4u tail_clear(v4u v, int k, int K) {
   const int d = k - tail_at(k, K);      // bytes to clear
 #pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    if constexpr (AL == 4) v[x] = d > 4 * x ? 0u : v[x];
-    else v[x] &= (uint32_t)(0xffffffffull << min(max(8 * (d - 4 * x), 0), 32));
-  }
+  for (int x = 0; x < 4; ++x) v[x] &= (uint32_t)(0xffffffffull << min(max(8 * (d - 4 * x), 0), 32));
   return v;
 }
 // Bytes k .. k + 15 of a row of fewer than 16, zero past its end.

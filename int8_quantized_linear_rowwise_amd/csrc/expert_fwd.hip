@@ -26,12 +26,11 @@ namespace i8l {
 // tokens, so the gather costs nothing in the loop. Waves whose 64 rows all lie
 // past the segment only move tiles: a tile of 100 rows takes about half the
 // time of a full one.
-// AL, what K (16 at least) and the weights' address are multiples of: 16; 4, the
-// same loads and the last piece of a row as tail_at has it; 1, or where the codes
-// pass 2^31 bytes, 16-byte loads at any address. Rows of codes start on 16-byte
-// borders for every K, so that only a row's last piece is read across them. 4096
-// tokens, two of eight experts, bf16, 4096 -> 11008 431 us, 4088 -> 11000 457 us
-// (500 with rows of K codes), 4095 -> 11007 597 us (688).
+// AL, what K and the weights' address are multiples of: 4, buffer loads, whose
+// last piece of a weight row may go on into the next row (zeros behind the last
+// one) against the zeros that a row of codes ends with; 1, or where the codes pass
+// 2^31 bytes, 16-byte loads at any address, for K of 16 at least. 4096 tokens, two
+// of eight experts, bf16, 4096 -> 11008 443 us, 4088 -> 11000 476, 4095 -> 11007 614.
 //
 // Short contractions: 128 rows by 128 features, 4 waves of 64 x 64 and one LDS
 // stage, so that three workgroups share a compute unit and their beginnings and
@@ -87,11 +86,6 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
       const int at = tail_at(kt + 16 * lc, K);
 #pragma unroll
       for (int i = 0; i < NB; ++i) RB[i] = bytes16(B0 + (boff[i] + at));
-    } else if constexpr (AL == 4) {
-      const int v = lrow * K + tail_at(kt + 16 * lc, K);
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-        RB[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rB, v, RPP * i * K, 0));
     } else {
       const int v = (kt + 16 * lc < K) ? voff : OOB_OFFSET;
 #pragma unroll
@@ -109,18 +103,14 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
     const int t = r < r1 ? row_token(rows, r, T) : -1;
     // no token: the row is stored as zeros, whatever its codes
     if constexpr (AL == 1) pA[i] = Q.CA + (int64_t)max(t, 0) * Q.lda;
-    else if constexpr (AL == 4) aoff[i] = max(t, 0) * Q.lda;
     else aoff[i] = t >= 0 ? t * Q.lda + 16 * lc : OOB_OFFSET;
   }
-  int ka = 0;      // AL < 16: first byte of the codes in RA
+  int ka = 0;      // AL 1: first byte of the codes in RA
   auto load_a = [&](int kt) {
-    if constexpr (AL < 16) {
+    if constexpr (AL == 1) {
       const int k = kt + 16 * lc, at = tail_at(k, K);
 #pragma unroll
-      for (int i = 0; i < NA; ++i) {
-        if constexpr (AL == 1) RA[i] = bytes16(pA[i] + at);
-        else RA[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rA, aoff[i] + at, 0, 0));
-      }
+      for (int i = 0; i < NA; ++i) RA[i] = bytes16(pA[i] + at);
       ka = k;
     } else {
       const bool in = kt + 16 * lc < K;
@@ -137,7 +127,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
 #pragma unroll
     for (int i = 0; i < NA; ++i)
       *reinterpret_cast<v4u*>(smem + st * STAGE + AOFF + woff + i * RPP * BK) =
-          AL == 16 ? RA[i] : tail_clear<AL>(RA[i], ka, K);      // every step: a branch costs the loop more
+          AL == 4 ? RA[i] : tail_clear(RA[i], ka, K);      // every step: a branch costs the loop more
   };
   load_a(0);
 
@@ -398,7 +388,7 @@ __global__ __launch_bounds__(256, 3) void k_expert_fwd_short(ExpertQuantized Q,
 // that eight workgroups on a compute unit cover each other's beginnings and
 // ends: 512 bytes at a time, five workgroups, took 28 us for one token of two
 // 4096 -> 11008 experts instead of 22.
-// AL: as above; 1 goes through registers and takes any K.
+// AL: as above; 1 goes through registers, and takes K below 16.
 // KS 1: a wave has a tile of its own and all of its contraction, with no barrier
 // at all; for contractions up to 2048 where that fills the chip. 64 tokens, four
 // of 64 experts, 512 -> 4096: 27 us against 43 with KS 4, 2048: 80 against 90,
@@ -450,8 +440,8 @@ __global__ __launch_bounds__(256, AL == 1 ? 4 : 8) void k_expert_fwd_thin(Expert
         const int8_t* p = CB + (int64_t)min(n0 + row, N - 1) * K;     // past N: not stored
         W[i] = K >= 16 ? bytes16(p + tail_at(k, K)) : short_row(p, k, K);
       } else {
-        const int at = AL == 4 ? row * K + tail_at(k, K) : k < K ? row * K + k : OOB_OFFSET;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr)(mine + i * 1024), 16, at, 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_ptr)(mine + i * 1024), 16, k < K ? row * K + k : OOB_OFFSET,
+                                                 0, 0, 0);
       }
     }
   };
@@ -483,7 +473,7 @@ __global__ __launch_bounds__(256, AL == 1 ? 4 : 8) void k_expert_fwd_thin(Expert
       a[s] = v4i{0, 0, 0, 0};
       if (t >= 0) {
         const int8_t* p = Q.CA + (int64_t)t * Q.lda;
-        if constexpr (AL == 16) {
+        if constexpr (AL == 4) {
           if (k < K) a[s] = *reinterpret_cast<const v4i*>(p + k);
         } else {
           const v4u v = K >= 16 ? bytes16(p + tail_at(k, K)) : short_row(p, k, K);
@@ -495,11 +485,11 @@ __global__ __launch_bounds__(256, AL == 1 ? 4 : 8) void k_expert_fwd_thin(Expert
 #pragma unroll
       for (int i = 0; i < ET_KC / 64; ++i) *reinterpret_cast<v4u*>(mine + i * 1024 + lane * 16) = W[i];
     }
-    if (AL < 16 && K >= 16 && (c + 1) * ET_KC > K) {
+    if (AL == 1 && K >= 16 && (c + 1) * ET_KC > K) {
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
         const int k = c * ET_KC + s * 64 + lg * 16;
-        a[s] = __builtin_bit_cast(v4i, tail_clear<AL>(__builtin_bit_cast(v4u, a[s]), k, K));
+        a[s] = __builtin_bit_cast(v4i, tail_clear(__builtin_bit_cast(v4u, a[s]), k, K));
       }
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -589,7 +579,7 @@ __global__ __launch_bounds__(256, TM == 1 ? 6 : 4) void k_expert_fwd_tiny(
   if (wave < nc) load_w(wave);
 
   // quantization: a thread has chunks tid and tid + 256 of every token
-  const int nchunk = K / 8;
+  const int nchunk = (K + 15) / 16 * 2;      // codes up to a border of 16, zeros past K
   v4u ra[TM][CH], rb[TM][CH] = {};
 #pragma unroll
   for (int t = 0; t < TM; ++t)
@@ -738,7 +728,7 @@ static bool few_rows(int64_t R, int64_t n_seg, int64_t N) {
 }
 
 bool expert_fwd_tiny_fits(int64_t T, int64_t K, const int8_t* CB, int64_t R, int64_t N, int64_t n_seg) {
-  return T > 0 && T <= EQ_TOKENS && K > 0 && K <= EQ_COLS && K % 16 == 0 && (uintptr_t)CB % 4 == 0 &&
+  return T > 0 && T <= EQ_TOKENS && K > 0 && K <= EQ_COLS && K % 4 == 0 && (uintptr_t)CB % 4 == 0 &&
          few_rows(R, n_seg, N);
 }
 
@@ -750,7 +740,7 @@ static hipError_t launch_tiny_t(const void* X, int T, float tau, const int32_t* 
   auto kern = T == 1 ? k_expert_fwd_tiny<DT, 1> : k_expert_fwd_tiny<DT, EQ_TOKENS>;
   const size_t lds = (size_t)tm * ((K + ET_KC - 1) / ET_KC * ET_KC);
   hipLaunchKernelGGL(kern, expert_grid(expert_slots(R, S.n_seg, 16) * tiles_n), dim3(256), lds, st,
-                     static_cast<const E*>(X), T, (uintptr_t)X % 16 == 0, tau, rows, R, S, CB, SCB, N, K, tiles_n,
+                     static_cast<const E*>(X), T, K % 8 == 0 && (uintptr_t)X % 16 == 0, tau, rows, R, S, CB, SCB, N, K, tiles_n,
                      static_cast<E*>(out));
   return hipGetLastError();
 }
@@ -769,36 +759,28 @@ static hipError_t launch_fwd_t(const ExpertQuantized& Q, const void* X, int T, c
                                hipStream_t st) {
   typedef typename Elem<DT>::T E;
   const bool far = (int64_t)T * Q.lda >= ((int64_t)1 << 31);
-  const int al = K < 16 || K % 4 != 0 || (uintptr_t)CB % 4 != 0 || far ? 1
-                 : K % 16 != 0 || (uintptr_t)CB % 16 != 0              ? 4
-                                                                       : 16;
+  const bool words = K % 4 == 0 && (uintptr_t)CB % 4 == 0 && !far;
   if (few_rows(R, S.n_seg, N) || K < 16 || T == 0) {
     const int64_t slots = expert_slots(R, S.n_seg, 16);
     const bool split = K > 2048 || slots * ((N + 63) / 64) < 1024;
     const int tiles_n = split ? (N + 15) / 16 : (N + 63) / 64;
-    auto kern = split ? (al == 1   ? k_expert_fwd_thin<DT, 1, 4>
-                         : al == 4 ? k_expert_fwd_thin<DT, 4, 4>
-                                   : k_expert_fwd_thin<DT, 16, 4>)
-                      : (al == 1   ? k_expert_fwd_thin<DT, 1, 1>
-                         : al == 4 ? k_expert_fwd_thin<DT, 4, 1>
-                                   : k_expert_fwd_thin<DT, 16, 1>);
+    auto kern = split ? (words ? k_expert_fwd_thin<DT, 4, 4> : k_expert_fwd_thin<DT, 1, 4>)
+                      : (words ? k_expert_fwd_thin<DT, 4, 1> : k_expert_fwd_thin<DT, 1, 1>);
     hipLaunchKernelGGL(kern, expert_grid(slots * tiles_n), dim3(256), 0, st, Q,
                        static_cast<const E*>(X), T, rows, R, S, CB, SCB, N, K, tiles_n, static_cast<E*>(out));
     return hipGetLastError();
   }
   const int64_t tiles = expert_slots(R, S.n_seg, 128) * ((N + 127) / 128);
   if (K <= 512 || (K <= 1024 && tiles >= 256)) {
-    auto kern = al == 1   ? k_expert_fwd_short<DT, 1>
-                : al == 4 ? k_expert_fwd_short<DT, 4>
-                          : k_expert_fwd_short<DT, 16>;
+    auto kern = words ? k_expert_fwd_short<DT, 4> : k_expert_fwd_short<DT, 1>;
     hipLaunchKernelGGL(kern, expert_grid(tiles), dim3(256), 0, st, Q,
                        static_cast<const E*>(X), T, rows, R, S, CB, SCB, N, K, static_cast<E*>(out));
     return hipGetLastError();
   }
-  static std::atomic<uint64_t> lds_set[3];
-  auto kern = al == 1 ? k_expert_fwd<DT, 1> : al == 4 ? k_expert_fwd<DT, 4> : k_expert_fwd<DT, 16>;
+  static std::atomic<uint64_t> lds_set[2];
+  auto kern = words ? k_expert_fwd<DT, 4> : k_expert_fwd<DT, 1>;
   constexpr int lds = ef_lds(256);
-  const hipError_t e = lds_limit_once((const void*)kern, lds, lds_set[al == 1 ? 0 : al == 4 ? 1 : 2]);
+  const hipError_t e = lds_limit_once((const void*)kern, lds, lds_set[words]);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kern, expert_grid(expert_groups(expert_slots(R, S.n_seg, 256), (N + 255) / 256)), dim3(512),
                      lds, st, Q, static_cast<const E*>(X), T, rows, R, S, CB, SCB, N, K, static_cast<E*>(out));

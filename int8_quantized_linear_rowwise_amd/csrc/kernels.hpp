@@ -12,8 +12,8 @@ namespace i8l {
 // 32-bit words.
 // preflags: column flag words ([slabs][words], the layout of the scratch)
 // handed over by the producer of X; the flags pass is then skipped.
-// ldq: bytes of a row of codes, cols or a larger multiple of 8 (what is behind a
-// row's codes is then not defined); 0 stands for cols.
+// ldq: bytes of a row of codes, cols or cols rounded up to 16 (with zeros behind
+// a row's codes; the codes then start on an 8-byte border); 0 stands for cols.
 //
 // Columns of the weight's dequantized outlier slice kept for a staging width
 // cap: a multiple of 8 (16-byte rows), at most 256.
@@ -123,7 +123,7 @@ hipError_t launch_expert_sort(const void* experts, int id_bytes, int R, int k, i
 // out (R x N of dt) = products of the quantized tokens (codes CA, scales SCA, outlier columns) with their rows'
 // experts (CB: n_experts x N x K); row r is token rows[r] (r itself when rows is NULL).
 struct ExpertQuantized {
-  const int8_t* CA;      // rows of lda bytes, a multiple of 16
+  const int8_t* CA;      // rows of lda bytes: K rounded up to 16, zeros behind the codes
   int lda;
   const float* SCA;
   const uint16_t* sub;

@@ -222,8 +222,8 @@ __global__ __launch_bounds__(256) void k_colflags(const typename Elem<DT>::T* __
 // ---------------------------------------------------------------------------
 // Per-chunk pieces of the row kernels (a chunk: 8 consecutive columns; the rest in quantize.hpp).
 
-// chunk ci of row `row` to memory: codes (rows of ldq bytes; where they are longer than
-// cols, of whole 8-byte pieces with anything behind), 0 on outlier columns, whose fp16
+// chunk ci of row `row` to memory: codes (in rows of ldq bytes, cols or cols rounded up
+// to 16 with zeros behind), 0 on outlier columns, whose fp16
 // values go to the dense sub-matrix at their rank among the outlier columns
 // (the prefix of the column's mask word plus the set bits below it)
 template <int DT, bool VEC>
@@ -258,6 +258,7 @@ __device__ __forceinline__ void chunk_emit(int8_t* __restrict__ codes, int ldq, 
   int8_t* cr = codes + row * (int64_t)ldq + c0;
   if (VEC || ldq > cols) {
     *reinterpret_cast<v2u*>(cr) = v2u{lo, hi};
+    if (ldq > cols && c0 + 8 >= cols && c0 + 16 <= ldq) *reinterpret_cast<v2u*>(cr + 8) = v2u{0u, 0u};
   } else {
     for (int e = 0; e < 8; ++e)
       if (c0 + e < cols) cr[e] = (int8_t)(((e < 4 ? lo : hi) >> (8 * (e & 3))) & 0xffu);

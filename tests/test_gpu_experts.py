@@ -152,6 +152,32 @@ def test_forward_few_tokens(I8, dt, T, k, E, K, N, outliers):
         assert torch.equal(I8.expert_forward(five, CB, SCB, off, rows=token), a)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("K,N", [(4, 9), (12, 40), (20, 33), (1004, 31), (4092, 24), (4088, 17)])
+@pytest.mark.parametrize("T", [1, 4])
+def test_forward_few_tokens_between_borders(I8, dt, T, K, N):
+    """Contractions that are whole words and no whole pieces: what follows a row of weights must not reach its sums."""
+    off, token, _ = X.sort(X.choices(T, 2, 3, 7, 0.1), 3)
+    run_forward(I8, dt, T, K, N, off.tolist(), rows=token)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,k,E,K,N,shift", [(700, 2, 3, 1040, 512, 0), (1500, 2, 4, 1100, 1100, 4),
+                                             (1500, 2, 4, 1041, 4101, 0), (900, 2, 3, 2001, 530, 1),
+                                             (2100, 3, 9, 1288, 2304, 0), (600, 1, 1, 1030, 5000, 2),
+                                             (300, 1, 2, 1044, 150, 0), (700, 2, 3, 1028, 300, 12)])
+def test_forward_long_contractions(I8, dt, T, k, E, K, N, shift):
+    """Past what the tiles for short contractions take; weights that begin off a border."""
+    off, token, _ = X.sort(X.choices(T, k, E, 7, 0.1, skew=1.5), E)
+    CB, SCB = X.weights(E, N, K, 3)
+    x, off, token, SCB = gpu(X.inputs(T, K, dt, 4, 5), off, token, SCB)
+    place = torch.zeros(E * N * K + 16, dtype=torch.int8, device=DEV)
+    CB = place[shift:shift + E * N * K].view(E, N, K).copy_(CB)
+    got = I8.expert_forward(x, CB, SCB, off, rows=token)
+    y, slack = X.forward(x, CB, SCB, off, None, token, 6.0)
+    X.check(got, y, X.rounded(y, slack, dt), "out")
+
+
 @pytest.mark.parametrize("tau", [0.0, -1.0, float("inf"), float("nan"), 1.0])
 def test_forward_thresholds(I8, tau):
     run_forward(I8, "bf16", 20, 128, 64, [0, 8, 20], tau=tau)
