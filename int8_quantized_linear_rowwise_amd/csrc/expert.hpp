@@ -250,7 +250,7 @@ template <int BN>
 __device__ __forceinline__ int etile_off(int row, int chunk) {
   return row * (2 * BN) + 16 * (chunk ^ (row & (BN / 8 - 1)));
 }
-// Rows whose scale in `lsa` says that they have no token are stored as zeros.
+// Rows whose scale in `lsa` (if any) says that they have no token are stored as zeros.
 template <int BM, int BN, int THREADS, typename E>
 __device__ __forceinline__ void etile_store(const char* ot, const float* lsa, E* __restrict__ dst, int64_t ld, int r0,
                                             int c0, int r1, int c1) {
@@ -262,7 +262,7 @@ __device__ __forceinline__ void etile_store(const char* ot, const float* lsa, E*
     const int row = i / CPR, ch = i % CPR, r = r0 + row, c = c0 + ch * 8;
     if (r >= r1) continue;
     v4u v = *reinterpret_cast<const v4u*>(ot + etile_off<BN>(row, ch));
-    if (no_token(lsa[row])) v = v4u{0u, 0u, 0u, 0u};
+    if (lsa != nullptr && no_token(lsa[row])) v = v4u{0u, 0u, 0u, 0u};
     E* p = dst + (int64_t)r * ld + c;
     if (vec && c + 8 <= c1) {
       *reinterpret_cast<v4u*>(p) = v;

@@ -10,6 +10,20 @@
 // own kernel: the next stage's weights and gradients are loaded two steps
 // ahead, and converted and written between the matrix instructions. Waves whose
 // 64 rows all lie past the segment only move and convert tiles.
+// Bound by the matrix instructions and the conversions beside them (32 weights and
+// 32 gradients a lane for 32 matrix instructions): 4096 tokens, two of eight
+// 4096 -> 11008 experts, bf16 790 us (0.94 PF/s; the projection's own kernel, with
+// no tile cut short by a segment's end, 640 to 670), fp16 780, fp32 874 with the cast;
+// 4092 -> 11004 877, 4095 -> 11007 1031.
+//
+// Short contractions (up to 512), and few rows an expert (up to 64 on average)
+// where every compute unit gets three tiles: tiles of 128 by 128, 4 waves, one LDS
+// stage, three workgroups a compute unit, whose beginnings and ends cover each
+// other. Large tiles against these: 4096 tokens, four of 64 experts, fp16, K 2048: N 64
+// 42 us against 29, 512 81 against 73, 768 107 against 102, 1408 169 against 171, 4096
+// 420 against 454; two of eight, bf16, K 4096, N 1024: 99 against 106. 64 tokens, four of
+// 64 experts, K and N 4096: 234 against 193 (the weights alone take 199 at a large
+// copy's rate); 16 tokens, two of eight, K 4096, N 11008 (256 tiles): 149 against 224.
 //
 // fp32 gradients, and those whose rows do not start on 16-byte borders, are cast
 // to rows of fp16 first (the same cast that the tiles would do).
@@ -19,20 +33,25 @@
 
 namespace i8l {
 
+// Bytes of a stage: rows of 64 fp16 values.
+constexpr int eb_stage(int bm, int bk) { return (bm + bk) * 128; }
+
 // G is fp16 or bf16 (GT), R rows of ng values (N, or N rounded up to 8 with
 // zeros behind it); the result is OT.
 // AL: 0, N is a multiple of 8, K of 4, the weights lie on 4-byte borders and an
 // expert's weight stays within 32-bit offsets; 1, but for N; 2, none of that:
 // loads at any address, a row's last piece loaded so that it ends with the row
 // and shifted into place.
-template <int GT, int OT, int BK, int AL>
+template <int GT, int OT, int BM, int BK, int AL>
 __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __restrict__ G, int ng,
                                                 const ExpertTile& tile, int k0, const int8_t* __restrict__ CBall,
                                                 const float* __restrict__ SCBall, int N, int K,
                                                 typename Elem<OT>::T* __restrict__ gX, char* bsm) {
   static_assert(GT == DT_F16 || GT == DT_BF16, "16-bit gradients only");
-  constexpr int BM = 256, BNC = 64, TI = BK / 64, TJ = 2;
-  constexpr int WR = BK / 32;                  // weight rows a lane converts in a step
+  constexpr int BNC = 64, TI = BK / 64, TJ = 2, THREADS = 2 * BM;
+  constexpr int WROWS = BNC / (THREADS / 64);      // weight rows of a wave in a step
+  constexpr int WR = BK * BNC / (4 * THREADS);     // and of a lane, which converts four columns of them
+  constexpr int NG = BM * BNC / (8 * THREADS);     // gradient pieces of a lane
   constexpr int ROW = BNC * 2;
   constexpr int STAGE = (BK + BM) * ROW, GOFF = BK * ROW;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -47,11 +66,11 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
   const __amdgpu_buffer_rsrc_t rW = make_rsrc(CB + k0, AL == 2 ? 0 : N * K - k0);
   const __amdgpu_buffer_rsrc_t rS = make_rsrc(SCB, AL == 2 ? 0 : N * 4);
 
-  // gradient slots: 16-byte chunk gc of rows grow + 64 i (i < 4)
+  // gradient slots: 16-byte chunk gc of rows grow + THREADS / 8 i (i < NG)
   const int grow = tid >> 3, gc = tid & 7;
   const int gvoff = grow * ng * 2 + 16 * gc;
   const int gwoff = GOFF + grow * ROW + 16 * (gc ^ lds_swz(grow));
-  // weights: rows nc + 8 wave + wh .. + WR - 1, bytes 4 kq .. 4 kq + 3
+  // weights: rows nc + WROWS wave + wh .. + WR - 1, bytes 4 kq .. 4 kq + 3
   constexpr int QUADS = BK / 4;                // lanes side by side on a weight row
   const int kq = lane % QUADS, wh = WR * (lane / QUADS);
   const int wvoff = 4 * kq + wh * K;
@@ -61,7 +80,7 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const int r = 4 * kq + c;
-    wwoff[c] = r * ROW + 16 * (wave ^ lds_swz(r)) + 2 * wh;
+    wwoff[c] = r * ROW + 16 * (((WROWS * wave + wh) >> 3) ^ lds_swz(r)) + 2 * (wh & 7);
   }
   const int sw = lds_swz(lr);
   int roff[4];
@@ -69,11 +88,11 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
   for (int ks = 0; ks < 4; ++ks) roff[ks] = lr * ROW + 16 * ((2 * ks + lg) ^ sw);
   const int pb = wk * (BK / 2) * ROW, qb = GOFF + wm * 64 * ROW;
 
-  v4u RG[4];
+  v4u RG[NG];
   uint32_t RW[WR];
   float SG[WR];
   auto load_w = [&](int nc) {
-    const int n8 = nc + 8 * wave;
+    const int n8 = nc + WROWS * wave;
     if constexpr (AL == 2) {
 #pragma unroll
       for (int e = 0; e < WR; ++e) {
@@ -89,8 +108,8 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
     } else {
 #pragma unroll
       for (int e = 0; e < WR; ++e) RW[e] = __builtin_amdgcn_raw_buffer_load_b32(rW, wvoff, (n8 + e) * K, 0);
-      // N % 8 == 0: the eight rows from n8 are all in the matrix or all past it
-      const int so = (n8 < N) ? 4 * (n8 + wh) : OOB_OFFSET;
+      // N % 8 == 0: the eight rows from a multiple of 8 are all in the matrix or all past it
+      const int so = (n8 + (wh & ~7) < N) ? 4 * (n8 + wh) : OOB_OFFSET;
       if constexpr (AL == 1) {
 #pragma unroll
         for (int e = 0; e < WR; ++e)
@@ -112,8 +131,9 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
   auto load_g = [&](int nc) {
     const int gv = (nc + 8 * gc < ng) ? gvoff : OOB_OFFSET;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      RG[i] = __builtin_bit_cast(v4u, __builtin_amdgcn_raw_buffer_load_b128(rG, gv, 2 * nc + 128 * i * ng, 0));
+    for (int i = 0; i < NG; ++i)
+      RG[i] = __builtin_bit_cast(
+          v4u, __builtin_amdgcn_raw_buffer_load_b128(rG, gv, 2 * nc + THREADS / 4 * i * ng, 0));
   };
   auto write_w = [&](int st, int c0) {
     float sg[WR];
@@ -137,7 +157,7 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
   };
   auto write_g = [&](int st) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < NG; ++i) {
       v4u v;
       if constexpr (GT == DT_F16) {
         v = RG[i];
@@ -145,7 +165,7 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = bf16x2_to_f16x2(RG[i][e]);
       }
-      *reinterpret_cast<v4u*>(bsm + st * STAGE + gwoff + i * 64 * ROW) = v;
+      *reinterpret_cast<v4u*>(bsm + st * STAGE + gwoff + i * (THREADS / 8) * ROW) = v;
     }
   };
 
@@ -192,7 +212,26 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
   load_w(BNC);
   load_g(BNC);
   __syncthreads();
-  if (r0 + wm * 64 < r1) {
+  const bool busy = r0 + wm * 64 < r1;
+  if constexpr (BM == 128) {
+    for (int t = 0; t < nn; ++t) {
+      if (busy) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          fread(0, ks, ks & 1);
+          mma(ks & 1);
+        }
+      }
+      if (t + 1 == nn) break;
+      __syncthreads();
+      write_w(0, 0);
+      write_w(0, 2);
+      write_g(0);
+      __syncthreads();
+      load_w((t + 2) * BNC);
+      load_g((t + 2) * BNC);
+    }
+  } else if (busy) {
     fread(0, 0, 0);
     for (int t = 0; t < nn; ++t) {
       const int st = t & 1;
@@ -258,10 +297,10 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
           for (int e = 0; e < 2; ++e)
             w[e] = (uint32_t)__builtin_bit_cast(uint16_t, Elem<OT>::from_f32(acc[i][j][4 * q + 2 * e])) |
                    ((uint32_t)__builtin_bit_cast(uint16_t, Elem<OT>::from_f32(acc[i][j][4 * q + 2 * e + 1])) << 16);
-          *reinterpret_cast<v2u*>(bsm + otile_off(wm * 64 + j * 32 + lr, wk * (BK / 16) + i * 4 + q) + 8 * lg) = w;
+          *reinterpret_cast<v2u*>(bsm + etile_off<BK>(wm * 64 + j * 32 + lr, wk * (BK / 16) + i * 4 + q) + 8 * lg) = w;
         }
     __syncthreads();
-    otile_store<typename Elem<OT>::T>(bsm, gX, K, r0, k0, r1, min(K, k0 + BK), wave, lane);
+    etile_store<BM, BK, THREADS, typename Elem<OT>::T>(bsm, nullptr, gX, K, r0, k0, r1, min(K, k0 + BK));
   }
 }
 
@@ -279,9 +318,26 @@ __global__ __launch_bounds__(512, 1) void k_expert_bwd(const typename Elem<GT>::
   const int k0 = work.tc * 256 + work.part * (256 / work.parts);
   if (tile.r0 >= tile.r1 || k0 >= K) return;
   if (tile.expert < 0 || N == 0) return expert_zeros(gX, K, tile.r0, tile.r1, k0, min(K, k0 + 256 / work.parts));
-  if (work.parts == 1) expert_bwd_tile<GT, OT, 256, AL>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
-  else if (work.parts == 2) expert_bwd_tile<GT, OT, 128, AL>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
-  else expert_bwd_tile<GT, OT, 64, AL>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
+  if (work.parts == 1) expert_bwd_tile<GT, OT, 256, 256, AL>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
+  else if (work.parts == 2) expert_bwd_tile<GT, OT, 256, 128, AL>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
+  else expert_bwd_tile<GT, OT, 256, 64, AL>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
+}
+
+// Tiles 128 x 128.
+template <int GT, int OT, int AL>
+__global__ __launch_bounds__(256, 3) void k_expert_bwd_short(const typename Elem<GT>::T* __restrict__ G, int ng, int R,
+                                                             ExpertSegs S, const int8_t* __restrict__ CB,
+                                                             const float* __restrict__ SCB, int N, int K,
+                                                             typename Elem<OT>::T* __restrict__ gX) {
+  __shared__ __attribute__((aligned(16))) char bsm[eb_stage(128, 128)];
+  const ExpertScan scan = expert_scan(S, R, 128);
+  const ExpertWork work = expert_work<false>(expert_block(), scan.total, (K + 127) / 128);
+  if (work.slot < 0) return;
+  const ExpertTile tile = expert_tile(S, scan, work.slot, R, 128);
+  const int k0 = work.tc * 128;
+  if (tile.r0 >= tile.r1) return;
+  if (tile.expert < 0 || N == 0) return expert_zeros(gX, K, tile.r0, tile.r1, k0, min(K, k0 + 128));
+  expert_bwd_tile<GT, OT, 128, 128, AL>(G, ng, tile, k0, CB, SCB, N, K, gX, bsm);
 }
 
 // Rows of G as fp16, ng values each, zeros behind the N-th.
@@ -319,9 +375,18 @@ size_t expert_bwd_bytes(const void* G, int dt, int64_t R, int64_t N) {
 template <int GT, int OT>
 static hipError_t launch_bwd_t(const void* G, int ng, int R, const ExpertSegs& S, const int8_t* CB, const float* SCB,
                                int N, int K, void* gX, hipStream_t st) {
-  constexpr int lds = 2 * (256 + 256) * 128;      // operand stages; the output tile takes their place
+  constexpr int lds = 2 * eb_stage(256, 256);      // operand stages; the output tile takes their place
   const bool words = K % 4 == 0 && (uintptr_t)CB % 4 == 0 && (N + (int64_t)128) * K < ((int64_t)1 << 31) - 4096;
   const int al = !words ? 2 : N % 8 != 0 ? 1 : 0;
+  const int64_t tiles = expert_slots(R, S.n_seg, 128) * ((K + 127) / 128);
+  if (N <= 512 || (R <= 64 * (int64_t)S.n_seg && tiles >= 768)) {
+    auto kern = al == 2   ? k_expert_bwd_short<GT, OT, 2>
+                : al == 1 ? k_expert_bwd_short<GT, OT, 1>
+                          : k_expert_bwd_short<GT, OT, 0>;
+    hipLaunchKernelGGL(kern, expert_grid(tiles), dim3(256), 0, st, static_cast<const typename Elem<GT>::T*>(G), ng, R, S,
+                       CB, SCB, N, K, static_cast<typename Elem<OT>::T*>(gX));
+    return hipGetLastError();
+  }
   static std::atomic<uint64_t> lds_set[3];
   auto kern = al == 2 ? k_expert_bwd<GT, OT, 2> : al == 1 ? k_expert_bwd<GT, OT, 1> : k_expert_bwd<GT, OT, 0>;
   const hipError_t e = lds_limit_once((const void*)kern, lds, lds_set[al]);

@@ -310,6 +310,16 @@ def test_backward_many_rows(I8, dt, T, k, E, N, K):
     run_backward(I8, dt, T * k, N, K, off.tolist())
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,k,E,N,K", [(1500, 2, 4, 600, 1100), (900, 2, 3, 1041, 2101), (2100, 3, 9, 520, 2304),
+                                       (600, 1, 1, 1028, 5000), (700, 2, 3, 577, 131), (64, 4, 64, 600, 1600),
+                                       (64, 4, 64, 523, 1601), (40, 4, 70, 516, 1410)])
+def test_backward_long_contractions(I8, dt, T, k, E, N, K):
+    """Past what the tiles for short contractions take, with many rows an expert, and with few of them."""
+    off, _, _ = X.sort(X.choices(T, k, E, 7, 0.1, skew=1.5), E)
+    run_backward(I8, dt, T * k, N, K, off.tolist())
+
+
 def test_backward_rows_without_expert(I8):
     got = run_backward(I8, "bf16", 11, 80, 96, [0, 3, 6, 9], ids=[1, -1, 5], E=2)
     assert (got[3:] == 0).all() and (got[:3] != 0).any()
