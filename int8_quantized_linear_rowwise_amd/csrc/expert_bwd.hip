@@ -14,7 +14,7 @@
 // 32 gradients a lane for 32 matrix instructions): 4096 tokens, two of eight
 // 4096 -> 11008 experts, bf16 790 us (0.94 PF/s; the projection's own kernel, with
 // no tile cut short by a segment's end, 640 to 670), fp16 780, fp32 874 with the cast;
-// 4092 -> 11004 877, 4095 -> 11007 1031.
+// 4092 -> 11004 877, 4095 -> 11007 995.
 //
 // Short contractions (up to 512), and few rows an expert (up to 64 on average)
 // where every compute unit gets three tiles: tiles of 128 by 128, 4 waves, one LDS
@@ -270,6 +270,13 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
   // lane (lr, lg), register r of tile (i, j): column wk BK / 2 + i 32 + (r / 4) 8 + lg 4 + r % 4, row wm 64 + j 32 + lr
   if constexpr (OT == DT_F32) {
     const bool ov = K % 4 == 0 && (uintptr_t)gX % 16 == 0;
+    if (!ov) {
+      auto value = [&](int i, int j, int q) {
+        return v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      };
+      return etile_f32<BM, BK, THREADS, (BM == 256 ? 2 : 1) * eb_stage(BM, BM)>(bsm, value, nullptr, gX, K, r0, k0, r1,
+                                                                              min(K, k0 + BK), wk, wm, lr, lg);
+    }
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const int r = r0 + wm * 64 + j * 32 + lr;
@@ -280,7 +287,7 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
         for (int q = 0; q < 4; ++q) {
           const int k = k0 + wk * (BK / 2) + i * 32 + q * 8 + lg * 4;
           const float y[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-          expert_store4<OT>(gX + (int64_t)r * K + k, y, K - k, ov);
+          expert_store4<OT>(gX + (int64_t)r * K + k, y, K - k, true);
         }
     }
   } else {
@@ -297,7 +304,7 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
           for (int e = 0; e < 2; ++e)
             w[e] = (uint32_t)__builtin_bit_cast(uint16_t, Elem<OT>::from_f32(acc[i][j][4 * q + 2 * e])) |
                    ((uint32_t)__builtin_bit_cast(uint16_t, Elem<OT>::from_f32(acc[i][j][4 * q + 2 * e + 1])) << 16);
-          *reinterpret_cast<v2u*>(bsm + etile_off<BK>(wm * 64 + j * 32 + lr, wk * (BK / 16) + i * 4 + q) + 8 * lg) = w;
+          *reinterpret_cast<v2u*>(bsm + etile_off<2 * BK>(wm * 64 + j * 32 + lr, wk * (BK / 16) + i * 4 + q) + 8 * lg) = w;
         }
     __syncthreads();
     etile_store<BM, BK, THREADS, typename Elem<OT>::T>(bsm, nullptr, gX, K, r0, k0, r1, min(K, k0 + BK));

@@ -30,7 +30,7 @@ namespace i8l {
 // last piece of a weight row may go on into the next row (zeros behind the last
 // one) against the zeros that a row of codes ends with; 1, or where the codes pass
 // 2^31 bytes, 16-byte loads at any address, for K of 16 at least. 4096 tokens, two
-// of eight experts, bf16, 4096 -> 11008 443 us, 4088 -> 11000 476, 4095 -> 11007 614.
+// of eight experts, bf16, 4096 -> 11008 443 us, 4088 -> 11000 476, 4095 -> 11007 561.
 //
 // Short contractions: 128 rows by 128 features, 4 waves of 64 x 64 and one LDS
 // stage, so that three workgroups share a compute unit and their beginnings and
@@ -288,6 +288,14 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
   }
   if constexpr (DT == DT_F32) {
     const bool ov = N % 4 == 0 && (uintptr_t)out % 16 == 0;
+    if (!ov) {
+      auto value = [&](int i, int j, int q) {
+        return v4f{__int_as_float(acc[i][j][4 * q]), __int_as_float(acc[i][j][4 * q + 1]),
+                   __int_as_float(acc[i][j][4 * q + 2]), __int_as_float(acc[i][j][4 * q + 3])};
+      };
+      return etile_f32<BM, BN, THREADS, STAGES>(reinterpret_cast<char*>(smem), value, lsa, out, N, r0, n0, r1,
+                                                min(N, n0 + BN), wn, wm, lr, lg);
+    }
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const int r = r0 + ml + j * 32 + lr;
@@ -301,7 +309,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
           float y[4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) y[x] = none ? 0.0f : __int_as_float(acc[i][j][4 * q + x]);
-          expert_store4<DT>(out + (int64_t)r * N + n, y, N - n, ov);
+          expert_store4<DT>(out + (int64_t)r * N + n, y, N - n, true);
         }
     }
   } else {
@@ -321,7 +329,7 @@ __device__ __forceinline__ void expert_fwd_tile(const ExpertQuantized& Q, const 
             w[x] = (uint32_t)__builtin_bit_cast(uint16_t, Elem<DT>::from_f32(a)) |
                    ((uint32_t)__builtin_bit_cast(uint16_t, Elem<DT>::from_f32(b)) << 16);
           }
-          *reinterpret_cast<v2u*>(ot + etile_off<BN>(ml + j * 32 + lr, (nl + i * 32 + q * 8) >> 3) + 8 * lg) = w;
+          *reinterpret_cast<v2u*>(ot + etile_off<2 * BN>(ml + j * 32 + lr, (nl + i * 32 + q * 8) >> 3) + 8 * lg) = w;
         }
       __builtin_amdgcn_sched_barrier(0);
     }
