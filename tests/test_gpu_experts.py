@@ -320,6 +320,15 @@ def test_backward_long_contractions(I8, dt, T, k, E, N, K):
     run_backward(I8, dt, T * k, N, K, off.tolist())
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("width", [1101, 1102, 300, 2307])
+def test_rows_off_borders(I8, dt, width):
+    """Outputs whose rows start anywhere, from whole tiles, halves and quarters."""
+    off, token, _ = X.sort(X.choices(1500, 2, 4, 7, 0.1, skew=1.5), 4)
+    run_forward(I8, dt, 1500, 1040, width, off.tolist(), rows=token)
+    run_backward(I8, dt, 3000, 600, width, off.tolist())
+
+
 def test_backward_rows_without_expert(I8):
     got = run_backward(I8, "bf16", 11, 80, 96, [0, 3, 6, 9], ids=[1, -1, 5], E=2)
     assert (got[3:] == 0).all() and (got[:3] != 0).any()
