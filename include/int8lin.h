@@ -500,14 +500,14 @@ int int8_expert_sort(const void* experts, int id_bytes, int64_t T, int64_t k, in
  * CB: n_experts x N x K int8, SCB: n_experts x N fp32 (int8_quantize_rowwise of
  * the n_experts N rows, tau off). rows: R int32 on the device; a value outside
  * [0, T) makes a row of zeros, and a token may be named any number of times.
- * out: R x N of `dtype`, no part of an input. K <= I8L_MAX_K, N <= I8L_MAX_COLS, T, R <= 2^24,
- * n_seg, n_experts <= 65536, else I8L_ESHAPE. The size query takes the call's own
- * sizes and looks at no more of CB than its address; it returns 0 for a few
- * tokens (workspace may then be NULL).
+ * out: R x N of `dtype`, no part of an input. K <= I8L_MAX_K, N <= I8L_MAX_COLS,
+ * T, R <= 2^24, n_seg, n_experts <= 65536, else I8L_ESHAPE. The size query takes
+ * the call's own sizes and looks at no more of CB than its address; it returns 0
+ * for a few tokens (workspace may then be NULL).
  *
  * Input gradient (the weights are frozen): grad_X[r, k] = D(sum_n fp16(G[r, n]) *
- * Wdq[e, n, k]), R rows; the rows of a token are added up by int8_expert_combine
- * with gate = NULL. It needs a workspace (for rows of fp16) where G is fp32, N is
+ * Wdq[e, n, k]), R rows, no part of an input; the rows of a token are added up by
+ * int8_expert_combine with gate = NULL. It needs a workspace (for rows of fp16) where G is fp32, N is
  * no multiple of 8 or G lies off a 16-byte border; the size query looks at no more
  * of G than its address, and returns 0 otherwise (workspace may then be NULL). */
 size_t int8_expert_forward_workspace_bytes(int64_t T, int64_t K, const int8_t* CB, int64_t R, int64_t N,

@@ -304,7 +304,8 @@ __device__ __forceinline__ void etile_f32(char* ot, V value, const float* lsa, f
       for (int i = 0; i < TIP; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<v4f*>(ot + etile_off<4 * CP>(wm * 64 + j * 32 + lr, (wn * HALF + i * 32 + q * 8) / 4 + lg)) =
+          *reinterpret_cast<v4f*>(
+              ot + etile_off<4 * CP>(wm * 64 + j * 32 + lr, (wn * HALF + i * 32 + q * 8) / 4 + lg)) =
               value(h * TIP + i, j, q);
     __syncthreads();
 #pragma unroll 4

@@ -304,7 +304,8 @@ __device__ __forceinline__ void expert_bwd_tile(const typename Elem<GT>::T* __re
           for (int e = 0; e < 2; ++e)
             w[e] = (uint32_t)__builtin_bit_cast(uint16_t, Elem<OT>::from_f32(acc[i][j][4 * q + 2 * e])) |
                    ((uint32_t)__builtin_bit_cast(uint16_t, Elem<OT>::from_f32(acc[i][j][4 * q + 2 * e + 1])) << 16);
-          *reinterpret_cast<v2u*>(bsm + etile_off<2 * BK>(wm * 64 + j * 32 + lr, wk * (BK / 16) + i * 4 + q) + 8 * lg) = w;
+          *reinterpret_cast<v2u*>(
+              bsm + etile_off<2 * BK>(wm * 64 + j * 32 + lr, wk * (BK / 16) + i * 4 + q) + 8 * lg) = w;
         }
     __syncthreads();
     etile_store<BM, BK, THREADS, typename Elem<OT>::T>(bsm, nullptr, gX, K, r0, k0, r1, min(K, k0 + BK));
@@ -390,8 +391,8 @@ static hipError_t launch_bwd_t(const void* G, int ng, int R, const ExpertSegs& S
     auto kern = al == 2   ? k_expert_bwd_short<GT, OT, 2>
                 : al == 1 ? k_expert_bwd_short<GT, OT, 1>
                           : k_expert_bwd_short<GT, OT, 0>;
-    hipLaunchKernelGGL(kern, expert_grid(tiles), dim3(256), 0, st, static_cast<const typename Elem<GT>::T*>(G), ng, R, S,
-                       CB, SCB, N, K, static_cast<typename Elem<OT>::T*>(gX));
+    hipLaunchKernelGGL(kern, expert_grid(tiles), dim3(256), 0, st, static_cast<const typename Elem<GT>::T*>(G), ng, R,
+                       S, CB, SCB, N, K, static_cast<typename Elem<OT>::T*>(gX));
     return hipGetLastError();
   }
   static std::atomic<uint64_t> lds_set[3];

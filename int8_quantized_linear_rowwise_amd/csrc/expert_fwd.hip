@@ -748,8 +748,8 @@ static hipError_t launch_tiny_t(const void* X, int T, float tau, const int32_t* 
   auto kern = T == 1 ? k_expert_fwd_tiny<DT, 1> : k_expert_fwd_tiny<DT, EQ_TOKENS>;
   const size_t lds = (size_t)tm * ((K + ET_KC - 1) / ET_KC * ET_KC);
   hipLaunchKernelGGL(kern, expert_grid(expert_slots(R, S.n_seg, 16) * tiles_n), dim3(256), lds, st,
-                     static_cast<const E*>(X), T, K % 8 == 0 && (uintptr_t)X % 16 == 0, tau, rows, R, S, CB, SCB, N, K, tiles_n,
-                     static_cast<E*>(out));
+                     static_cast<const E*>(X), T, K % 8 == 0 && (uintptr_t)X % 16 == 0, tau, rows, R, S, CB, SCB, N, K,
+                     tiles_n, static_cast<E*>(out));
   return hipGetLastError();
 }
 

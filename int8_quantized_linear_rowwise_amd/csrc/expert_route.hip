@@ -201,7 +201,8 @@ hipError_t launch_expert_sort(const void* experts, int id_bytes, int R, int k, i
 
 // ---------------------------------------------------------------------------
 // Weighted sum. A thread takes 8 columns of one token and adds its k rows in
-// order, in fp32, then rounds once. Bound by memory: every row is read once.
+// order, in fp32, then rounds once. Bound by memory: every row is read once. 4096
+// tokens with two rows of 4096 and a base, bf16: 24.6 us, 5.4 TB/s.
 
 template <int DT>
 __device__ __forceinline__ void cld(const typename Elem<DT>::T* __restrict__ p, int n, bool vec, float (&f)[8]) {
@@ -301,7 +302,8 @@ hipError_t launch_expert_combine(int dt, const void* Y, int R, int N, const int3
 // read once for four rows at a time, whose products with Y stay in registers
 // until the end of the row; the gradient of each row is written as it is
 // formed. Sums run in a fixed order. The last ZERO_BLOCKS workgroups write
-// zeros into the rows behind the last routed one.
+// zeros into the rows behind the last routed one. 8192 tokens with eight rows of
+// 2048, bf16: 119 us, 4.7 TB/s (reads and writes of 2 KB-rows in turn).
 constexpr int ZERO_BLOCKS = 256;
 
 template <int DT, bool VEC, int TT>   // TT threads a token: 64 or 256

@@ -222,14 +222,14 @@ __global__ __launch_bounds__(256) void k_colflags(const typename Elem<DT>::T* __
 // ---------------------------------------------------------------------------
 // Per-chunk pieces of the row kernels (a chunk: 8 consecutive columns; the rest in quantize.hpp).
 
-// chunk ci of row `row` to memory: codes (in rows of ldq bytes, cols or cols rounded up
-// to 16 with zeros behind), 0 on outlier columns, whose fp16
-// values go to the dense sub-matrix at their rank among the outlier columns
-// (the prefix of the column's mask word plus the set bits below it)
+// chunk ci of row `row` to memory: codes (in rows of ldq bytes, cols or cols
+// rounded up to 16 with zeros behind), 0 on outlier columns, whose fp16 values go
+// to the dense sub-matrix at their rank among the outlier columns (the prefix of
+// the column's mask word plus the set bits below it)
 template <int DT, bool VEC>
 __device__ __forceinline__ void chunk_emit(int8_t* __restrict__ codes, int ldq, uint16_t* __restrict__ sub,
-                                           int cap, int cols, const uint32_t* smask, const int32_t* sprefix, int64_t row,
-                                           int ci, const v4u& a, const v4u& b, float inv, uint32_t om, bool any) {
+                                           int cap, int cols, const uint32_t* smask, const int32_t* sprefix,
+                                           int64_t row, int ci, const v4u& a, const v4u& b, float inv, uint32_t om, bool any) {
   const int c0 = ci * 8;
   uint32_t lo, hi;
   chunk_quant8<DT>(a, b, inv, lo, hi);
@@ -561,7 +561,8 @@ constexpr int QS_THREADS = 512, QS_CHUNKS = 2;
 template <int DT, bool VEC>
 __global__ __launch_bounds__(QS_THREADS) void k_quant_small(const typename Elem<DT>::T* __restrict__ X, int rows,
                                                             int cols, float tau, int cps, int8_t* __restrict__ codes,
-                                                            int ldq, float* __restrict__ scale, int32_t* __restrict__ idx,
+                                                            int ldq, float* __restrict__ scale,
+                                                            int32_t* __restrict__ idx,
                                                             int idx_cap, int32_t* __restrict__ count,
                                                             uint16_t* __restrict__ sub, int cap) {
 #pragma clang fp contract(off)
@@ -736,7 +737,8 @@ bool quantize_small_fits(int64_t rows, int64_t cols, float tau) {
 
 template <int DT>
 static hipError_t launch_quantize_small_t(const void* Xv, int rows, int cols, float tau, int8_t* codes, int ldq,
-                                          float* scale, int32_t* idx, int32_t* count, uint16_t* sub, int cap, hipStream_t st) {
+                                          float* scale, int32_t* idx, int32_t* count, uint16_t* sub, int cap,
+                                          hipStream_t st) {
   typedef typename Elem<DT>::T T;
   const T* X = static_cast<const T*>(Xv);
   const bool vec = (cols % 8 == 0) && aligned(X, 16) && aligned(codes, 8);
