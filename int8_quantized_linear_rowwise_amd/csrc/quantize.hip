@@ -222,6 +222,12 @@ __global__ __launch_bounds__(256) void k_colflags(const typename Elem<DT>::T* __
 // ---------------------------------------------------------------------------
 // Per-chunk pieces of the row kernels (a chunk: 8 consecutive columns; the rest in quantize.hpp).
 
+// the zeros with which a row of codes of ldq bytes ends, if there are any past its last chunk
+__device__ __forceinline__ void codes_end(int8_t* __restrict__ codes, int ldq, int cols, int64_t row) {
+  const int end = (cols + 7) & ~7;
+  if (end + 8 <= ldq) *reinterpret_cast<v2u*>(codes + row * (int64_t)ldq + end) = v2u{0u, 0u};
+}
+
 // chunk ci of row `row` to memory: codes (in rows of ldq bytes, cols or cols
 // rounded up to 16 with zeros behind), 0 on outlier columns, whose fp16 values go
 // to the dense sub-matrix at their rank among the outlier columns (the prefix of
@@ -258,7 +264,6 @@ __device__ __forceinline__ void chunk_emit(int8_t* __restrict__ codes, int ldq, 
   int8_t* cr = codes + row * (int64_t)ldq + c0;
   if (VEC || ldq > cols) {
     *reinterpret_cast<v2u*>(cr) = v2u{lo, hi};
-    if (ldq > cols && c0 + 8 >= cols && c0 + 16 <= ldq) *reinterpret_cast<v2u*>(cr + 8) = v2u{0u, 0u};
   } else {
     for (int e = 0; e < 8; ++e)
       if (c0 + e < cols) cr[e] = (int8_t)(((e < 4 ? lo : hi) >> (8 * (e & 3))) & 0xffu);
@@ -504,7 +509,10 @@ __global__ __launch_bounds__(256) void k_rowquant(const typename Elem<DT>::T* __
         const int ci = i * TPR + me;
         if (ci < nchunk) emit(row, ci, ra[i], rb[i], inv, rmask(i), (anyb >> i) & 1u);
       }
-      if (me == 0) scale[row] = sv;
+      if (me == 0) {
+        scale[row] = sv;
+        codes_end(codes, ldq, cols, row);
+      }
     }
   } else {
     for (int64_t row = row0; row < rows; row += wstride) {
@@ -542,7 +550,10 @@ __global__ __launch_bounds__(256) void k_rowquant(const typename Elem<DT>::T* __
             if (ci < nchunk) emit(row, ci, a[u], b[u], inv, om, any);
           }
         }
-      if (lane == 0) scale[row] = sv;
+      if (lane == 0) {
+        scale[row] = sv;
+        codes_end(codes, ldq, cols, row);
+      }
     }
   }
 
@@ -641,7 +652,10 @@ __global__ __launch_bounds__(QS_THREADS) void k_quant_small(const typename Elem<
     if (ci < nchunk)
       chunk_emit<DT, VEC>(codes, ldq, sub, cap, cols, smask, sprefix, row, ci, ra[i], rb[i], inv, om[i], true);
   }
-  if (t == 0) scale[row] = s;
+  if (t == 0) {
+    scale[row] = s;
+    codes_end(codes, ldq, cols, row);
+  }
 }
 
 // ---------------------------------------------------------------------------
