@@ -384,7 +384,7 @@ template <int GT, int OT>
 static hipError_t launch_bwd_t(const void* G, int ng, int R, const ExpertSegs& S, const int8_t* CB, const float* SCB,
                                int N, int K, void* gX, hipStream_t st) {
   constexpr int lds = 2 * eb_stage(256, 256);      // operand stages; the output tile takes their place
-  const bool words = K % 4 == 0 && (uintptr_t)CB % 4 == 0 && (N + (int64_t)128) * K < ((int64_t)1 << 31) - 4096;
+  const bool words = K % 4 == 0 && (uintptr_t)CB % 4 == 0 && (N + (int64_t)256) * K < ((int64_t)1 << 31) - 4096;
   const int al = !words ? 2 : N % 8 != 0 ? 1 : 0;
   const int64_t tiles = expert_slots(R, S.n_seg, 128) * ((K + 127) / 128);
   if (N <= 512 || (R <= 64 * (int64_t)S.n_seg && tiles >= 768)) {

@@ -178,6 +178,54 @@ def test_forward_long_contractions(I8, dt, T, k, E, K, N, shift):
     X.check(got, y, X.rounded(y, slack, dt), "out")
 
 
+def _codes(*shape):
+    g = torch.Generator(device=DEV).manual_seed(5)
+    return torch.randint(-127, 128, shape, dtype=torch.int8, device=DEV, generator=g)
+
+
+@pytest.mark.parametrize("T,E,N,K", [(5, 17, 8192, 16384), (40, 17, 8192, 16384), (600, 17, 8192, 16384),
+                                     (600, 600, 8192, 512)])
+def test_weights_past_32_bits(I8, T, E, N, K):
+    """Weights of over 2^31 bytes: the last expert's products and gradients are those of that expert alone."""
+    CB, SCB = _codes(E, N, K), torch.rand((E, N), device=DEV) + 0.5
+    x, G = X.inputs(T, K, "bf16", 1).to(DEV), X.inputs(T, N, "bf16", 2, 0).to(DEV)
+    for ids in ([E - 1], [0]):
+        off, seg = torch.tensor([0, T], dtype=torch.int32, device=DEV), torch.tensor(ids, dtype=torch.int32, device=DEV)
+        one = slice(ids[0], ids[0] + 1)
+        assert torch.equal(I8.expert_forward(x, CB, SCB, off, seg), I8.expert_forward(x, CB[one], SCB[one], off))
+        assert torch.equal(I8.expert_backward(G, CB, SCB, off, seg), I8.expert_backward(G, CB[one], SCB[one], off))
+
+
+@pytest.mark.parametrize("N", [262144, 262143])
+def test_rows_past_32_bits(I8, N):
+    """Over 2^31 outputs, and gradients: the last rows are those of a call with these rows alone."""
+    T, K, last = 9000, 16, 300
+    CB, SCB = _codes(1, N, K), torch.rand((1, N), device=DEV) + 0.5
+    x = X.inputs(T, K, "bf16", 1, 0).to(DEV)
+    off, few = (torch.tensor([0, n], dtype=torch.int32, device=DEV) for n in (T, last))
+    out = I8.expert_forward(x, CB, SCB, off, threshold=0.0)
+    assert torch.equal(out[-last:], I8.expert_forward(x[-last:], CB, SCB, few, threshold=0.0))
+    g = I8.expert_backward(out, CB, SCB, off)
+    assert torch.equal(g[-last:], I8.expert_backward(out[-last:].contiguous(), CB, SCB, few))
+    pos = torch.arange(T, dtype=torch.int32, device=DEV).view(T, 1)
+    assert torch.equal(I8.expert_combine(out, pos[-last:]), out[-last:])
+    gY, gg = I8.expert_combine_backward(out, pos, None, out)
+    assert torch.equal(gY, out) and bool((gg[-last:] > 0).all())
+
+
+def test_tokens_past_32_bits(I8):
+    """Over 2^31 codes: the last tokens' products are those of these tokens alone."""
+    T, K, N, last = 140000, 16384, 256, 700
+    x = X.inputs(1000, K, "bf16", 1, 0).to(DEV).repeat(T // 1000, 1)
+    x[-last:] *= torch.linspace(0.5, 2.0, last, device=DEV, dtype=torch.bfloat16)[:, None]
+    CB, SCB = _codes(2, N, K), torch.rand((2, N), device=DEV) + 0.5
+    for n in (12, last):
+        off = torch.tensor([0, n // 3, n], dtype=torch.int32, device=DEV)
+        rows = torch.arange(T - n, T, dtype=torch.int32, device=DEV).flip(0)
+        got = I8.expert_forward(x, CB, SCB, off, rows=rows, threshold=0.0)
+        assert torch.equal(got, I8.expert_forward(x[-n:], CB, SCB, off, rows=rows - (T - n), threshold=0.0))
+
+
 @pytest.mark.parametrize("tau", [0.0, -1.0, float("inf"), float("nan"), 1.0])
 def test_forward_thresholds(I8, tau):
     run_forward(I8, "bf16", 20, 128, 64, [0, 8, 20], tau=tau)
