@@ -236,8 +236,16 @@ __device__ __forceinline__ v8h expert_out_w8(const int8_t* __restrict__ CB, cons
 // Zeros into columns [c0, c1) of rows [r0, r1), by the whole workgroup: rows without an expert.
 template <typename E>
 __device__ __forceinline__ void expert_zeros(E* out, int64_t ld, int r0, int r1, int c0, int c1) {
-  for (int r = r0; r < r1; ++r)
-    for (int c = c0 + threadIdx.x; c < c1; c += blockDim.x) out[r * ld + c] = E{};
+  constexpr int V = 16 / sizeof(E);
+  const int step = blockDim.x;
+  if (ld % V == 0 && (uintptr_t)out % 16 == 0 && (c1 - c0) % V == 0) {      // c0 is on a border of 16 values
+    const int w = (c1 - c0) / V, n = (r1 - r0) * w;
+    for (int i = threadIdx.x; i < n; i += step)
+      *reinterpret_cast<v4u*>(out + (int64_t)(r0 + i / w) * ld + c0 + i % w * V) = v4u{0u, 0u, 0u, 0u};
+  } else {
+    const int w = c1 - c0, n = (r1 - r0) * w;
+    for (int i = threadIdx.x; i < n; i += step) out[(int64_t)(r0 + i / w) * ld + c0 + i % w] = E{};
+  }
 }
 
 // Scale of a row without a token: such a row is zeros, whatever its expert's weights hold.
