@@ -320,7 +320,7 @@ __global__ __launch_bounds__(512, 1) void k_expert_bwd(const typename Elem<GT>::
                                                        typename Elem<OT>::T* __restrict__ gX) {
   extern __shared__ __attribute__((aligned(16))) char bsm[];
   const ExpertScan scan = expert_scan(S, R, 256);
-  const ExpertWork work = expert_work<true>(expert_block(), scan.total, (K + 255) / 256);
+  const ExpertWork work = expert_work<true>(expert_block(), scan, (K + 255) / 256);
   if (work.slot < 0) return;
   const ExpertTile tile = expert_tile(S, scan, work.slot, R, 256);
   const int k0 = work.tc * 256 + work.part * (256 / work.parts);
@@ -339,7 +339,7 @@ __global__ __launch_bounds__(256, 3) void k_expert_bwd_short(const typename Elem
                                                              typename Elem<OT>::T* __restrict__ gX) {
   __shared__ __attribute__((aligned(16))) char bsm[eb_stage(128, 128)];
   const ExpertScan scan = expert_scan(S, R, 128);
-  const ExpertWork work = expert_work<false>(expert_block(), scan.total, (K + 127) / 128);
+  const ExpertWork work = expert_work<false>(expert_block(), scan, (K + 127) / 128);
   if (work.slot < 0) return;
   const ExpertTile tile = expert_tile(S, scan, work.slot, R, 128);
   const int k0 = work.tc * 128;

@@ -348,7 +348,7 @@ __global__ __launch_bounds__(512, 1) void k_expert_fwd(ExpertQuantized Q, const 
   const int cnt = *Q.count;
   const OutlierCols cols = expert_out_cols(Q.idx, (threadIdx.x & 1) * 8, min(cnt, 16));
   const ExpertScan scan = expert_scan(S, R, 256);
-  const ExpertWork work = expert_work<true>(expert_block(), scan.total, (N + 255) / 256);
+  const ExpertWork work = expert_work<true>(expert_block(), scan, (N + 255) / 256);
   if (work.slot < 0) return;
   const ExpertTile tile = expert_tile(S, scan, work.slot, R, 256);
   const int n0 = work.tc * 256 + work.part * (256 / work.parts);
@@ -374,7 +374,7 @@ __global__ __launch_bounds__(256, 3) void k_expert_fwd_short(ExpertQuantized Q,
   const int cnt = *Q.count;
   const OutlierCols cols = expert_out_cols(Q.idx, (threadIdx.x & 1) * 8, min(cnt, 16));
   const ExpertScan scan = expert_scan(S, R, 128);
-  const ExpertWork work = expert_work<false>(expert_block(), scan.total, (N + 127) / 128);
+  const ExpertWork work = expert_work<false>(expert_block(), scan, (N + 127) / 128);
   if (work.slot < 0) return;
   const ExpertTile tile = expert_tile(S, scan, work.slot, R, 128);
   const int n0 = work.tc * 128;
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(256, AL == 1 ? 4 : 8) void k_expert_fwd_thin(Expert
   const int cnt = *Q.count;
   const OutlierCols cols = expert_out_cols(Q.idx, lg * 8, cnt);
   const ExpertScan scan = expert_scan(S, R, BM);
-  if (ts >= scan.total) return;
+  if (ts >= scan.total + scan.zeros) return;
   const ExpertTile tile = expert_tile(S, scan, (int)ts, R, BM);
   if (tile.r0 >= tile.r1) return;
   if (tile.expert < 0) {
@@ -566,7 +566,7 @@ __global__ __launch_bounds__(256, TM == 1 ? 6 : 4) void k_expert_fwd_tiny(
   const int64_t ts = bid / tiles_n;
   const int n0 = (int)(bid - ts * tiles_n) * BN;
   const ExpertScan scan = expert_scan(S, R, 16);
-  if (ts >= scan.total) return;
+  if (ts >= scan.total + scan.zeros) return;
   const ExpertTile tile = expert_tile(S, scan, (int)ts, R, 16);
   if (tile.r0 >= tile.r1) return;
   if (tile.expert < 0) return expert_zeros(out, N, tile.r0, tile.r1, n0, min(N, n0 + BN));

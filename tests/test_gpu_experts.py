@@ -377,6 +377,20 @@ def test_rows_off_borders(I8, dt, width):
     run_backward(I8, dt, 3000, 600, width, off.tolist())
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,K,N", [(2100, 1040, 900), (2100, 256, 1100), (60, 96, 80)])
+@pytest.mark.parametrize("ids", [[-1, 0, -1, 1, 2, -1], [9, 9, 9, 9, 9, 2], [0, -1, -1, -1, -1, -1], [-1] * 6])
+def test_segments_without_expert_among_others(I8, dt, T, K, N, ids):
+    """Some of the experts are elsewhere: their rows are zeros, in every form, wherever they lie."""
+    off = [0, T // 5, T // 5, T // 2, T // 2 + 3, T - 7, T - 2]
+    got = run_forward(I8, dt, T, K, N, off, ids=ids, E=3)
+    back = run_backward(I8, dt, T, N, K, off, ids=ids, E=3)
+    for j, e in enumerate(ids):
+        if not 0 <= e < 3:
+            assert (got[off[j]:off[j + 1]] == 0).all() and (back[off[j]:off[j + 1]] == 0).all()
+    assert (got[off[-1]:] == 0).all() and (back[off[-1]:] == 0).all()
+
+
 def test_backward_rows_without_expert(I8):
     got = run_backward(I8, "bf16", 11, 80, 96, [0, 3, 6, 9], ids=[1, -1, 5], E=2)
     assert (got[3:] == 0).all() and (got[:3] != 0).any()
