@@ -233,8 +233,8 @@ class Int8ExpertsFunction(torch.autograd.Function):
 class ExpertCombineFunction(torch.autograd.Function):
     """Weighted sum of each token's rows plus base: gradients for the rows, the gate and base.
 
-    n_rows: the sort's last offset (one int32), behind which the rows' gradient is 0; without it all of the rows'
-    gradient is cleared first."""
+    Rows that no position names get a gradient of 0, also where positions of the sort were taken out (-1) after it.
+    n_rows (the sort's last offset) is not needed for that; it may be None."""
 
     @staticmethod
     def forward(ctx, Y, position, gate, base, n_rows):
@@ -242,21 +242,21 @@ class ExpertCombineFunction(torch.autograd.Function):
         gate_c = None if gate is None else gate.contiguous()
         out = expert_combine(Yc, position, gate_c, None if base is None else base.contiguous())
         ctx.rows = Y.shape[0]
-        ctx.save_for_backward(Yc if gate is not None and ctx.needs_input_grad[2] else None, position, gate_c, n_rows)
+        ctx.save_for_backward(Yc if gate is not None and ctx.needs_input_grad[2] else None, position, gate_c)
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, g):
-        Y, position, gate, n_rows = ctx.saved_tensors
+        Y, position, gate = ctx.saved_tensors
         need = ctx.needs_input_grad
         gY = gg = None
         if need[0] or need[2]:
             g2 = g.contiguous()
-            # without n_rows there is no telling which rows no position names: all start at 0
-            zeros = torch.zeros((ctx.rows, g.shape[1]), dtype=g.dtype, device=g.device) \
-                if need[0] and n_rows is None else None
-            gY, gg = expert_combine_backward(g2, position, gate, Y, n_rows, rows=ctx.rows, with_grad_Y=need[0],
+            # there is no telling which rows no position names (some may have been taken out after the sort): all start
+            # at 0
+            zeros = torch.zeros((ctx.rows, g.shape[1]), dtype=g.dtype, device=g.device) if need[0] else None
+            gY, gg = expert_combine_backward(g2, position, gate, Y, rows=ctx.rows, with_grad_Y=need[0],
                                              with_grad_gate=need[2], grad_Y=zeros)
         return gY, None, gg, g if need[3] else None, None
 

@@ -180,6 +180,23 @@ def combine_backward(G, position, gate, Y, R):
     return gY, gg, (N / 64 + 16) * 2.0 ** -24 * mag
 
 
+def combine_gradient(G, position, gate, R):
+    """(grad_Y, slack) for positions of any kind: each row gets the sum over all that name it, none 0. One rounding a
+    term, of the product or of the sum so far."""
+    T, k = position.shape
+    gY = torch.zeros((R, G.shape[1]), dtype=d, device=G.device)
+    mag = torch.zeros_like(gY)
+    named = torch.zeros(R, dtype=d, device=G.device)
+    has = (position >= 0) & (position < R)
+    for j in range(k):
+        t = has[:, j].nonzero()[:, 0]
+        r = position[t, j].long()
+        part = G[t].to(d) * (1.0 if gate is None else gate[t, j].to(d)[:, None])
+        gY, mag = gY.index_add(0, r, part), mag.index_add(0, r, part.abs())
+        named = named.index_add(0, r, torch.ones_like(r, dtype=d))
+    return gY, named[:, None] * 2.0 ** -24 * mag
+
+
 # ---- gradient norm --------------------------------------------------------------------------------------------------
 
 
