@@ -534,7 +534,14 @@ int int8_expert_backward(const void* G, int dtype, int64_t R, int64_t N, const i
  * names are left as they were, but with n_rows (one int32 on the device: the
  * sort's last offset) the rows from *n_rows on get 0. grad_gate is 0 where the
  * position is left out. Apart from base no output may overlap an input.
- * k <= 64, N <= I8L_MAX_COLS, T, R <= 2^24, else I8L_ESHAPE. */
+ * k <= 64, N <= I8L_MAX_COLS, T, R <= 2^24, else I8L_ESHAPE.
+ * With dtype | I8L_ANY_POSITIONS the positions may be any: a row that several
+ * name gets the sum of their terms, in the order of the choices (fp32, rounded
+ * once), a row that none names 0. n_rows is then scratch of 2 R int32 that the
+ * call writes (2 R words at any 4-byte address, I8L_EINVAL where it is missing
+ * and grad_Y is asked for); sums are the same on every run. */
+#define I8L_ANY_POSITIONS 256
+
 int int8_expert_combine(const void* Y, int dtype, int64_t R, int64_t N, const int32_t* position, const float* gate,
                         const void* base, int64_t T, int64_t k, void* out, void* stream);
 int int8_expert_combine_backward(const void* G, int dtype, int64_t T, int64_t N, const int32_t* position,

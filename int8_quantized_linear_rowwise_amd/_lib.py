@@ -20,6 +20,7 @@ I8L_MAX_COLS = 262144
 I8L_LORA_MAX_RANK = 128
 I8L_SORT_MAX_EXPERTS = 1024
 I8L_NORM_INF = 0
+I8L_ANY_POSITIONS = 256
 
 # every symbol the header declares, with (restype, argtypes)
 _vp, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t

@@ -215,15 +215,20 @@ int int8_expert_combine(const void* Y, int dtype, int64_t R, int64_t N, const in
 int int8_expert_combine_backward(const void* G, int dtype, int64_t T, int64_t N, const int32_t* position,
                                  const float* gate, int64_t k, const void* Y, int64_t R, const int32_t* n_rows,
                                  void* grad_Y, float* grad_gate, void* stream) {
+  const bool any = dtype >= 0 && (dtype & I8L_ANY_POSITIONS) != 0;
+  if (any) dtype &= ~I8L_ANY_POSITIONS;
   const int rc = combine_sizes(dtype, R, N, T, k);
   if (rc != I8L_OK) return rc;
   if (T > 0 && k > 0) {
     if (position == nullptr || (N > 0 && G == nullptr)) return I8L_EINVAL;
     if (grad_gate && N > 0 && R > 0 && Y == nullptr) return I8L_EINVAL;
   }
+  if (any && grad_Y && R > 0 && (n_rows == nullptr || (uintptr_t)n_rows % 4)) return I8L_EINVAL;
   if (!grad_Y && !grad_gate) return I8L_OK;
+  int32_t* named = any ? const_cast<int32_t*>(n_rows) : nullptr;
   return hip_status(i8l::launch_expert_combine_bwd(dtype, G, k > 0 ? (int)T : 0, (int)N, position, gate, (int)k, Y,
-                                                   (int)R, n_rows, grad_Y, grad_gate, (hipStream_t)stream));
+                                                   (int)R, any ? nullptr : n_rows, named, grad_Y, grad_gate,
+                                                   (hipStream_t)stream));
 }
 
 size_t int8_grad_norm_workspace_bytes(const i8l_grad_tensor* grads, int64_t count) {

@@ -304,23 +304,57 @@ hipError_t launch_expert_combine(int dt, const void* Y, int R, int N, const int3
 // formed. Sums run in a fixed order. The last ZERO_BLOCKS workgroups write
 // zeros into the rows behind the last routed one. 8192 tokens with eight rows of
 // 2048, bf16: 119 us, 4.7 TB/s (reads and writes of 2 KB-rows in turn).
+//
+// ANY, positions of any kind: `named` holds the first and the last choice that
+// names each row, by integer atomics, so that their order is nothing to the
+// result. The first choice writes the row; where it is not the last one too, it
+// looks through the choices between them, 256 at a time, and adds theirs in
+// order. The zeros go to rows without a first choice.
 constexpr int ZERO_BLOCKS = 256;
+constexpr int NO_CHOICE = 0x7fffffff;
 
-template <int DT, bool VEC, int TT>   // TT threads a token: 64 or 256
+__global__ __launch_bounds__(256) void k_named_clear(int32_t* __restrict__ named, int R) {
+  for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < R; r += (int64_t)gridDim.x * 256) {
+    named[r] = NO_CHOICE;
+    named[R + r] = -1;
+  }
+}
+__global__ __launch_bounds__(256) void k_named(const int32_t* __restrict__ position, int choices, int R,
+                                               int32_t* __restrict__ named) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < choices; i += (int64_t)gridDim.x * 256) {
+    const int r = position[i];
+    if (r >= 0 && r < R) {
+      atomicMin(&named[r], (int)i);
+      atomicMax(&named[R + r], (int)i);
+    }
+  }
+}
+
+template <int DT, bool VEC, int TT, bool ANY>   // TT threads a token: 64 or 256
 __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<DT>::T* __restrict__ G, int T, int N,
                                                             const int32_t* __restrict__ position,
                                                             const float* __restrict__ gate, int k,
                                                             const typename Elem<DT>::T* __restrict__ Y, int R,
-                                                            const int32_t* __restrict__ n_rows,
+                                                            const int32_t* __restrict__ n_rows,   // ANY: named
                                                             typename Elem<DT>::T* __restrict__ gY,
                                                             float* __restrict__ ggate) {
   constexpr int PER = 256 / TT;
-  const int blocks = (T + PER - 1) / PER;
+  const int blocks = (T + PER - 1) / PER, lane = threadIdx.x & 63;
   const int64_t bid = expert_block();
   if (bid >= blocks) {
     if (!n_rows || bid >= blocks + ZERO_BLOCKS) return;
-    const int64_t from = min(max(n_rows[0], 0), R);
     const float zero[8] = {};
+    if constexpr (ANY) {
+      for (int64_t r0 = ((bid - blocks) * 4 + (threadIdx.x >> 6)) * 64; r0 < R; r0 += (int64_t)ZERO_BLOCKS * 256) {
+        uint64_t none = __ballot(r0 + lane < R && n_rows[r0 + lane] == NO_CHOICE);
+        for (; none != 0; none &= none - 1) {
+          const int64_t r = r0 + __builtin_ctzll(none);
+          for (int c = lane * 8; c < N; c += 512) cst<DT>(gY + r * N + c, min(8, N - c), VEC, zero);
+        }
+      }
+      return;
+    }
+    const int64_t from = min(max(n_rows[0], 0), R);
     const int chunks = (N + 7) / 8;
     const int64_t items = (R - from) * (int64_t)chunks;
     for (int64_t i = (bid - blocks) * 256 + threadIdx.x; i < items; i += (int64_t)ZERO_BLOCKS * 256) {
@@ -339,11 +373,22 @@ __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<
   for (int j0 = 0; j0 < k; j0 += 4) {
     int64_t row[4];
     float w[4], dot[4] = {};
+    bool writes[4];
+    int to[4];      // ANY: the last choice that names the row, where this one is the first of several, else 0
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int r = live && j0 + u < k ? pos[j0 + u] : -1;
       row[u] = (r >= 0 && r < R) ? (int64_t)r * N : -1;
       w[u] = row[u] >= 0 ? (gt ? gt[j0 + u] : 1.0f) : 0.0f;
+      writes[u] = gY && row[u] >= 0;
+      to[u] = 0;
+      if constexpr (ANY) {
+        if (writes[u]) {
+          const int i = t * k + j0 + u, last = n_rows[R + r];
+          writes[u] = n_rows[r] == i && last == i;
+          if (n_rows[r] == i && last != i) to[u] = last;
+        }
+      }
     }
     for (int c = tid * 8; c < N; c += TT * 8) {
       const int n = min(8, N - c);
@@ -358,7 +403,7 @@ __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (row[u] >= 0) {
-          if (gY) {
+          if (writes[u]) {
             float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = w[u] * f[e];
@@ -367,6 +412,39 @@ __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<
           if (ggate) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) dot[u] = __builtin_fmaf(f[e], y[u][e], dot[u]);
+          }
+        }
+    }
+    if constexpr (ANY) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (to[u] > 0) {      // alike in all of the token's threads; no barrier follows
+          const int r = pos[j0 + u], from = t * k + j0 + u + 1;
+          for (int c0 = 0; c0 < N; c0 += TT * 8) {
+            const int c = c0 + tid * 8, n = min(8, N - c);
+            float s[8] = {}, f[8];
+            if (c < N) {
+              cld<DT>(g + c, n, VEC, f);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) s[e] = w[u] * f[e];
+            }
+            for (int i0 = from; i0 <= to[u]; i0 += 256) {      // to[u] < 2^30
+              int p[4];
+#pragma unroll
+              for (int b = 0; b < 4; ++b) p[b] = i0 + 64 * b + lane <= to[u] ? position[i0 + 64 * b + lane] : -1;
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                for (uint64_t same = __ballot(p[b] == r); same != 0; same &= same - 1) {
+                  const int i = i0 + 64 * b + __builtin_ctzll(same);
+                  const float wi = gate ? gate[i] : 1.0f;
+                  if (c < N) {
+                    cld<DT>(G + (int64_t)(i / k) * N + c, n, VEC, f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[e] = __builtin_fmaf(wi, f[e], s[e]);
+                  }
+                }
+            }
+            if (c < N) cst<DT>(gY + row[u] + c, n, VEC, s);
           }
         }
     }
@@ -394,25 +472,32 @@ __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<
 
 template <int DT, int TT>
 static hipError_t launch_combine_bwd_t(const void* G, int T, int N, const int32_t* position, const float* gate, int k,
-                                       const void* Y, int R, const int32_t* n_rows, void* gY, float* ggate,
-                                       hipStream_t st) {
+                                       const void* Y, int R, const int32_t* n_rows, int32_t* named, void* gY,
+                                       float* ggate, hipStream_t st) {
   typedef typename Elem<DT>::T E;
   const bool vec = N % 8 == 0 && (((uintptr_t)G | (uintptr_t)Y | (uintptr_t)gY) % 16 == 0);
-  if (!gY) n_rows = nullptr;
-  const int64_t blocks = (T + 256 / TT - 1) / (256 / TT) + (n_rows ? ZERO_BLOCKS : 0);
+  if (!gY || R == 0) n_rows = named = nullptr;
+  const int64_t blocks = (T + 256 / TT - 1) / (256 / TT) + (n_rows || named ? ZERO_BLOCKS : 0);
   if (blocks == 0) return hipSuccess;
-  auto kern = vec ? k_expert_combine_bwd<DT, true, TT> : k_expert_combine_bwd<DT, false, TT>;
+  auto kern = vec ? k_expert_combine_bwd<DT, true, TT, false> : k_expert_combine_bwd<DT, false, TT, false>;
+  if (named) {
+    auto grid = [](int64_t n) { return dim3((unsigned)(n < 4096 * 256 ? (n + 255) / 256 : 4096)); };
+    hipLaunchKernelGGL(k_named_clear, grid(R), dim3(256), 0, st, named, R);
+    if (T > 0) hipLaunchKernelGGL(k_named, grid((int64_t)T * k), dim3(256), 0, st, position, T * k, R, named);
+    kern = vec ? k_expert_combine_bwd<DT, true, TT, true> : k_expert_combine_bwd<DT, false, TT, true>;
+    n_rows = named;
+  }
   hipLaunchKernelGGL(kern, expert_grid(blocks), dim3(256), 0, st, static_cast<const E*>(G), T, N, position, gate, k,
                      static_cast<const E*>(Y), R, n_rows, static_cast<E*>(gY), ggate);
   return hipGetLastError();
 }
 
 hipError_t launch_expert_combine_bwd(int dt, const void* G, int T, int N, const int32_t* position, const float* gate,
-                                     int k, const void* Y, int R, const int32_t* n_rows, void* gY, float* ggate,
-                                     hipStream_t st) {
-#define I8L_CB(D)                                                                                           \
-  return N <= 1024 ? launch_combine_bwd_t<D, 64>(G, T, N, position, gate, k, Y, R, n_rows, gY, ggate, st)   \
-                   : launch_combine_bwd_t<D, 256>(G, T, N, position, gate, k, Y, R, n_rows, gY, ggate, st)
+                                     int k, const void* Y, int R, const int32_t* n_rows, int32_t* named, void* gY,
+                                     float* ggate, hipStream_t st) {
+#define I8L_CB(D)                                                                                                  \
+  return N <= 1024 ? launch_combine_bwd_t<D, 64>(G, T, N, position, gate, k, Y, R, n_rows, named, gY, ggate, st)   \
+                   : launch_combine_bwd_t<D, 256>(G, T, N, position, gate, k, Y, R, n_rows, named, gY, ggate, st)
   if (dt == DT_F32) I8L_CB(DT_F32);
   if (dt == DT_F16) I8L_CB(DT_F16);
   I8L_CB(DT_BF16);

@@ -144,12 +144,13 @@ hipError_t launch_expert_fwd_tiny(int dt, const void* X, int T, float tau, const
 size_t expert_bwd_bytes(const void* G, int dt, int64_t R, int64_t N);
 hipError_t launch_expert_bwd(int dt, const void* G, int R, const ExpertSegs& S, const int8_t* CB, const float* SCB,
                              int N, int K, void* gX, void* ws, hipStream_t st);
-// out[t] = D(base[t] + sum_j gate[t, j] Y[position[t, j]]) and its gradients.
+// out[t] = D(base[t] + sum_j gate[t, j] Y[position[t, j]]) and its gradients. named (2 R int32, or NULL): scratch with
+// which the positions may be any; n_rows is not read then.
 hipError_t launch_expert_combine(int dt, const void* Y, int R, int N, const int32_t* position, const float* gate,
                                  const void* base, int T, int k, void* out, hipStream_t st);
 hipError_t launch_expert_combine_bwd(int dt, const void* G, int T, int N, const int32_t* position, const float* gate,
-                                     int k, const void* Y, int R, const int32_t* n_rows, void* gY, float* ggate,
-                                     hipStream_t st);
+                                     int k, const void* Y, int R, const int32_t* n_rows, int32_t* named, void* gY,
+                                     float* ggate, hipStream_t st);
 
 // Norm of many tensors: the list travels in the kernels' arguments, GRAD_LIST
 // tensors a launch.

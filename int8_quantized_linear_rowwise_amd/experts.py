@@ -13,7 +13,7 @@ from typing import Optional
 
 import torch
 
-from ._lib import I8L_SORT_MAX_EXPERTS, check, lib
+from ._lib import I8L_ANY_POSITIONS, I8L_SORT_MAX_EXPERTS, check, lib
 from ._tensors import _check_out, _code, _empty, _gpu, _on_gpu, _ptr, _raw_stream, _workspace
 
 
@@ -167,12 +167,15 @@ def expert_combine(Y: torch.Tensor, position: torch.Tensor, gate: Optional[torch
 def expert_combine_backward(G: torch.Tensor, position: torch.Tensor, gate: Optional[torch.Tensor] = None,
                             Y: Optional[torch.Tensor] = None, n_rows: Optional[torch.Tensor] = None,
                             rows: Optional[int] = None, with_grad_Y: bool = True, with_grad_gate: bool = True,
-                            grad_Y: Optional[torch.Tensor] = None, grad_gate: Optional[torch.Tensor] = None):
+                            grad_Y: Optional[torch.Tensor] = None, grad_gate: Optional[torch.Tensor] = None,
+                            any_positions: bool = False, workspace: Optional[torch.Tensor] = None):
     """(grad_Y, grad_gate) of expert_combine, None where not asked for.
 
     G: T x N. Y, the forward's, is read for grad_gate only; without it `rows` is the number of its rows (default: T k).
-    Each position is named once. Rows of grad_Y that no position names are left as they were, in a new grad_Y
-    uninitialised; with n_rows (one int32 on the GPU: the sort's last offset) the rows from there on are 0."""
+    Without any_positions, no two positions may name the same row, and rows of grad_Y that no position names are left
+    as they were, in a new grad_Y uninitialised; with n_rows (one int32 on the GPU: the sort's last offset) the rows
+    from there on are 0. With any_positions a row that several name gets the sum of their terms, a row that none names
+    0, n_rows is not needed, and the workspace takes 8 bytes a row of grad_Y."""
     if G.dim() != 2:
         raise ValueError("G must be 2-D")
     T, k = _positions(position, gate)
@@ -186,6 +189,8 @@ def expert_combine_backward(G: torch.Tensor, position: torch.Tensor, gate: Optio
     R = Y.shape[0] if Y is not None else T * k if rows is None else int(rows)
     if n_rows is not None and (n_rows.dtype != torch.int32 or n_rows.numel() != 1):
         raise ValueError("n_rows must be one int32 value")
+    if any_positions and n_rows is not None:
+        raise ValueError("n_rows says which rows no position names; with any_positions that is found out")
     _check_out(grad_Y, (R, N), G.dtype, "grad_Y")
     _check_out(grad_gate, (T, k), torch.float32, "grad_gate")
     dev = _gpu(G, "G")
@@ -193,10 +198,14 @@ def expert_combine_backward(G: torch.Tensor, position: torch.Tensor, gate: Optio
         grad_Y = _empty((R, N), G.dtype, G.device)
     if grad_gate is None and with_grad_gate:
         grad_gate = _empty((T, k), torch.float32, G.device)
+    code = _code(G)
+    if any_positions:
+        code |= I8L_ANY_POSITIONS
+        n_rows = _workspace(workspace, 8 * R if with_grad_Y else 0, G.device, dev)
     with _on_gpu(dev):
-        check(lib.int8_expert_combine_backward(_ptr(G, "G", dev), _code(G), T, N, _ptr(position, "position", dev),
+        check(lib.int8_expert_combine_backward(_ptr(G, "G", dev), code, T, N, _ptr(position, "position", dev),
                                                _ptr(gate, "gate", dev), k, _ptr(Y, "Y", dev), R,
-                                               _ptr(n_rows, "n_rows", dev),
+                                               _ptr(n_rows, "workspace" if any_positions else "n_rows", dev),
                                                _ptr(grad_Y, "grad_Y", dev) if with_grad_Y else 0,
                                                _ptr(grad_gate, "grad_gate", dev) if with_grad_gate else 0,
                                                _raw_stream(dev)),
@@ -233,8 +242,8 @@ class Int8ExpertsFunction(torch.autograd.Function):
 class ExpertCombineFunction(torch.autograd.Function):
     """Weighted sum of each token's rows plus base: gradients for the rows, the gate and base.
 
-    Rows that no position names get a gradient of 0, also where positions of the sort were taken out (-1) after it.
-    n_rows (the sort's last offset) is not needed for that; it may be None."""
+    Positions may be any: a row that several name gets the sum of their terms, a row that none names (also one whose
+    position was taken out after the sort) 0. n_rows (the sort's last offset) is not needed for that; it may be None."""
 
     @staticmethod
     def forward(ctx, Y, position, gate, base, n_rows):
@@ -253,11 +262,8 @@ class ExpertCombineFunction(torch.autograd.Function):
         gY = gg = None
         if need[0] or need[2]:
             g2 = g.contiguous()
-            # there is no telling which rows no position names (some may have been taken out after the sort): all start
-            # at 0
-            zeros = torch.zeros((ctx.rows, g.shape[1]), dtype=g.dtype, device=g.device) if need[0] else None
             gY, gg = expert_combine_backward(g2, position, gate, Y, rows=ctx.rows, with_grad_Y=need[0],
-                                             with_grad_gate=need[2], grad_Y=zeros)
+                                             with_grad_gate=need[2], any_positions=need[0])
         return gY, None, gg, g if need[3] else None, None
 
 
