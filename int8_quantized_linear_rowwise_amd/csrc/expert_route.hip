@@ -309,7 +309,9 @@ hipError_t launch_expert_combine(int dt, const void* Y, int R, int N, const int3
 // names each row, by integer atomics, so that their order is nothing to the
 // result. The first choice writes the row; where it is not the last one too, it
 // looks through the choices between them, 256 at a time, and adds theirs in
-// order. The zeros go to rows without a first choice.
+// order. The zeros go to rows without a first choice. The same 8192 tokens, no row
+// named twice: 148 us, of which 9 for `named`; every row twice 450; all 65536
+// choices on one row, which one workgroup adds up, 20 ms.
 constexpr int ZERO_BLOCKS = 256;
 constexpr int NO_CHOICE = 0x7fffffff;
 
@@ -345,10 +347,13 @@ __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<
     if (!n_rows || bid >= blocks + ZERO_BLOCKS) return;
     const float zero[8] = {};
     if constexpr (ANY) {
-      for (int64_t r0 = ((bid - blocks) * 4 + (threadIdx.x >> 6)) * 64; r0 < R; r0 += (int64_t)ZERO_BLOCKS * 256) {
-        uint64_t none = __ballot(r0 + lane < R && n_rows[r0 + lane] == NO_CHOICE);
+      // rows side by side go to different waves: those behind the last routed one lie together
+      constexpr int64_t WAVES = ZERO_BLOCKS * 4;
+      for (int64_t r0 = (bid - blocks) * 4 + (threadIdx.x >> 6); r0 < R; r0 += 64 * WAVES) {
+        const int64_t mine = r0 + lane * WAVES;
+        uint64_t none = __ballot(mine < R && n_rows[mine] == NO_CHOICE);
         for (; none != 0; none &= none - 1) {
-          const int64_t r = r0 + __builtin_ctzll(none);
+          const int64_t r = r0 + __builtin_ctzll(none) * WAVES;
           for (int c = lane * 8; c < N; c += 512) cst<DT>(gY + r * N + c, min(8, N - c), VEC, zero);
         }
       }
@@ -370,25 +375,26 @@ __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<
   const int32_t* pos = position + (int64_t)(live ? t : 0) * k;
   const float* gt = gate ? gate + (int64_t)(live ? t : 0) * k : nullptr;
   const typename Elem<DT>::T* g = G + (int64_t)(live ? t : 0) * N;
+  // ANY: the token's choices (at most 64) that alone name their rows, and those that are the first of several; looked up
+  // together, once, so that rows and products wait for nothing (172 us against 148 where every four choices asked)
+  uint64_t single = 0, several = 0;
+  if constexpr (ANY) {
+    if (gY) {
+      const int r = live && lane < k ? pos[lane] : -1, i = t * k + lane;
+      const bool has = r >= 0 && r < R;
+      const int first = has ? n_rows[r] : -1, last = has ? n_rows[R + r] : -1;
+      single = __ballot(first == i && last == i);
+      several = __ballot(first == i && last > i);
+    }
+  }
   for (int j0 = 0; j0 < k; j0 += 4) {
     int64_t row[4];
     float w[4], dot[4] = {};
-    bool writes[4];
-    int to[4];      // ANY: the last choice that names the row, where this one is the first of several, else 0
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int r = live && j0 + u < k ? pos[j0 + u] : -1;
       row[u] = (r >= 0 && r < R) ? (int64_t)r * N : -1;
       w[u] = row[u] >= 0 ? (gt ? gt[j0 + u] : 1.0f) : 0.0f;
-      writes[u] = gY && row[u] >= 0;
-      to[u] = 0;
-      if constexpr (ANY) {
-        if (writes[u]) {
-          const int i = t * k + j0 + u, last = n_rows[R + r];
-          writes[u] = n_rows[r] == i && last == i;
-          if (n_rows[r] == i && last != i) to[u] = last;
-        }
-      }
     }
     for (int c = tid * 8; c < N; c += TT * 8) {
       const int n = min(8, N - c);
@@ -403,7 +409,7 @@ __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (row[u] >= 0) {
-          if (writes[u]) {
+          if (gY && (!ANY || (single >> (j0 + u)) & 1)) {
             float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = w[u] * f[e];
@@ -418,8 +424,8 @@ __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<
     if constexpr (ANY) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (to[u] > 0) {      // alike in all of the token's threads; no barrier follows
-          const int r = pos[j0 + u], from = t * k + j0 + u + 1;
+        if (j0 + u < k && (several >> (j0 + u)) & 1) {      // alike in all of the token's threads
+          const int r = pos[j0 + u], from = t * k + j0 + u + 1, to = n_rows[R + r];      // below 2^30
           for (int c0 = 0; c0 < N; c0 += TT * 8) {
             const int c = c0 + tid * 8, n = min(8, N - c);
             float s[8] = {}, f[8];
@@ -428,10 +434,10 @@ __global__ __launch_bounds__(256) void k_expert_combine_bwd(const typename Elem<
 #pragma unroll
               for (int e = 0; e < 8; ++e) s[e] = w[u] * f[e];
             }
-            for (int i0 = from; i0 <= to[u]; i0 += 256) {      // to[u] < 2^30
+            for (int i0 = from; i0 <= to; i0 += 256) {
               int p[4];
 #pragma unroll
-              for (int b = 0; b < 4; ++b) p[b] = i0 + 64 * b + lane <= to[u] ? position[i0 + 64 * b + lane] : -1;
+              for (int b = 0; b < 4; ++b) p[b] = i0 + 64 * b + lane <= to ? position[i0 + 64 * b + lane] : -1;
 #pragma unroll
               for (int b = 0; b < 4; ++b)
                 for (uint64_t same = __ballot(p[b] == r); same != 0; same &= same - 1) {
