@@ -213,10 +213,25 @@ def expert_combine_backward(G: torch.Tensor, position: torch.Tensor, gate: Optio
     return grad_Y if with_grad_Y else None, grad_gate if with_grad_gate else None
 
 
+MAX_CHOICES = 64     # rows of a token that one weighted sum takes
+
+
+def _sum_of_rows(gX, position):
+    """Each token's rows added up; more of them than one sum takes in fp32, rounded once at the end."""
+    k = position.shape[1]
+    if k <= MAX_CHOICES:
+        return expert_combine(gX, position)
+    rows, total = gX.float(), None
+    for j in range(0, k, MAX_CHOICES):
+        total = expert_combine(rows, position[:, j:j + MAX_CHOICES].contiguous(), base=total, out=total)
+    return total.to(gX.dtype)
+
+
 class Int8ExpertsFunction(torch.autograd.Function):
     """The experts' products in int8, with the memory-efficient input gradient: tokens (T x K) to rows (R x N).
 
-    position (T x k): the rows of each token, needed for the gradient where `rows` is given."""
+    position (T x k): the rows of each token, needed for the gradient where `rows` is given. Each row's gradient is
+    rounded to x's dtype, then a token's rows are added in fp32 and rounded again."""
 
     @staticmethod
     def forward(ctx, x, CB, SCB, seg_offsets, seg_expert, rows, position, threshold):
@@ -235,7 +250,7 @@ class Int8ExpertsFunction(torch.autograd.Function):
             raise ValueError("the gradient of gathered tokens needs position, the rows of each token")
         gX = expert_backward(g.contiguous(), CB, SCB, seg_offsets, seg_expert)
         if rows is not None:
-            gX = expert_combine(gX, position)
+            gX = _sum_of_rows(gX, position)
         return gX, None, None, None, None, None, None, None
 
 

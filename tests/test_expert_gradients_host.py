@@ -54,3 +54,18 @@ def test_plain_gradient_of_repeats_against_differences():
             sides.append(float((X.combine(b, pos, gate, base)[0] * G).sum()))
         # linear in Y: what is left is cancellation, 2^-52 |loss| / h
         assert abs((sides[0] - sides[1]) / (2 * h) - float(gY.view(-1)[i])) < 1e-8
+
+
+@pytest.mark.parametrize("k,sums", [(1, 1), (64, 1), (65, 2), (150, 3)])
+def test_token_gradient_takes_any_number_of_choices(stub, L, monkeypatch, k, sums):  # noqa: F811
+    calls = []
+    for name in ("int8_expert_forward", "int8_expert_backward", "int8_expert_combine"):
+        monkeypatch.setattr(L.lib, name, lambda *a, n=name: calls.append((n, a)) or 0)
+    x = torch.zeros((8, 32), dtype=torch.bfloat16, requires_grad=True)
+    CB, SCB = torch.zeros((2, 16, 32), dtype=torch.int8), torch.zeros((2, 16))
+    off, rows = torch.zeros(3, dtype=torch.int32), torch.zeros(8 * k, dtype=torch.int32)
+    pos = torch.zeros((8, k), dtype=torch.int32)
+    stub.I8.Int8ExpertsFunction.apply(x, CB, SCB, off, None, rows, pos, 6.0).sum().backward()
+    assert [n for n, _ in calls] == ["int8_expert_forward", "int8_expert_backward"] + ["int8_expert_combine"] * sums
+    took = [a[8] for n, a in calls if n == "int8_expert_combine"]
+    assert sum(took) == k and max(took) <= 64 and x.grad.dtype == x.dtype

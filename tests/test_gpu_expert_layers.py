@@ -73,6 +73,22 @@ def test_mixture_stage_by_stage(I8, dt, T, k, E, K, H):
     X.check(x.grad, total, X.rounded(total, bound, dt), "x.grad")
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("k", [64, 65, 150])
+def test_token_gradient_of_many_choices(I8, dt, k):
+    """More rows a token than one weighted sum takes."""
+    T, E, K, N = 20, 3, 72, 40
+    CB, SCB = X.weights(E, N, K, 1)
+    ids = X.choices(T, k, E, 2, 0.2)
+    CB, SCB, ids = CB.to(DEV), SCB.to(DEV), ids.to(DEV)
+    x, G = X.inputs(T, K, dt, 3).to(DEV).requires_grad_(), X.inputs(T * k, N, dt, 4, 0).to(DEV)
+    off, token, pos = I8.expert_sort(ids, E)
+    y = I8.Int8ExpertsFunction.apply(x, CB, SCB, off, None, token, pos, 6.0)
+    y.backward(G)
+    want, bound = token_gradient(G, CB, SCB, off, pos, dt)
+    X.check(x.grad, want, bound, "x.grad")
+
+
 # ---- segments -------------------------------------------------------------------------------------------------------
 
 
