@@ -9,7 +9,7 @@ from typing import Iterable, Optional, Sequence, Tuple
 
 import torch
 
-from ._lib import I8L_NORM_INF, GradTensor, check, lib
+from ._lib import I8L_F32, I8L_NORM_INF, GradTensor, check, lib
 from ._tensors import DTYPE_CODE, _empty, _on_gpu, _ptr, _raw_stream, _workspace
 
 
@@ -37,21 +37,26 @@ class GradNormPlan:
         if self.gpu < 0:
             raise ValueError("gradients must be on a GPU")
         self.count, self._keep = len(grads), grads
-        rows, seen = [], set()
-        self._twice = False
+        rows = []
         for g in grads:
             code = DTYPE_CODE.get(g.dtype)
             if code is None:
                 raise TypeError(f"unsupported dtype {g.dtype}; expected float32, float16 or bfloat16")
-            n, p = g.numel(), _ptr(g, "every gradient", self.gpu)
-            if n:
-                self._twice = self._twice or p in seen
-                seen.add(p)
-            rows += (p, n, code)
+            rows += (_ptr(g, "every gradient", self.gpu), g.numel(), code)
         # i8l_grad_tensor is three 64-bit words, the dtype in the last one's lower half
         self._table = (ctypes.c_int64 * len(rows))(*rows)
+        self._overlap: Optional[bool] = None      # found out by the first clipping
         assert ctypes.sizeof(GradTensor) == 24
         self.workspace_bytes = lib.int8_grad_norm_workspace_bytes(self._table, self.count)
+
+    def _overlapping(self) -> bool:
+        t, end = self._table, 0
+        for p, n, code in sorted(zip(t[::3], t[1::3], t[2::3])):
+            if n:
+                if p < end:
+                    return True
+                end = p + n * (4 if code == I8L_F32 else 2)
+        return False
 
     def _run(self, max_norm, norm_type, grad_scale, clip, workspace):
         max_norm, kind = _numbers(max_norm, norm_type)
@@ -60,8 +65,11 @@ class GradNormPlan:
             if grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or grad_scale.get_device() != self.gpu:
                 raise ValueError(f"grad_scale must be one float32 value on {self.device}")
             scale = grad_scale.data_ptr()
-        if clip and self._twice:
-            raise ValueError("a gradient that is in the list twice would be clipped twice")
+        if clip:
+            if self._overlap is None:
+                self._overlap = self._overlapping()
+            if self._overlap:
+                raise ValueError("gradients that overlap, or are in the list twice, would be clipped twice")
         out = _empty((3,), torch.float32, self.device)
         ws = _workspace(workspace, self.workspace_bytes, self.device, self.gpu)
         at = out.data_ptr()
@@ -81,7 +89,7 @@ class GradNormPlan:
 
     def clip(self, max_norm: Optional[float] = None, norm_type: float = 2.0,
              grad_scale: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
-        """`norm`, and the gradients multiplied by the factor in place."""
+        """`norm`, and the gradients multiplied by the factor in place. No two of them may overlap."""
         return self._run(max_norm, norm_type, grad_scale, 1, workspace)
 
 
