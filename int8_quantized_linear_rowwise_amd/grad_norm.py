@@ -23,9 +23,11 @@ def _numbers(max_norm: Optional[float], norm_type: float) -> Tuple[float, int]:
 
 
 class GradNormPlan:
-    """The gradients of a step, checked once; `norm` and `clip` read (and write) these very tensors at every call and
-    the plan keeps them alive. Nothing of it lies on the device: every call has outputs and workspace of its own, so
-    calls on different streams, or captured into different graphs, do not meet.
+    """The gradients of a step, checked once; `norm` and `clip` read (and write) the memory that these tensors have now
+    at every call, and the plan keeps it alive: a gradient that is replaced, or given other memory (g.data = ...), needs
+    a new plan, and one whose storage is resized leaves this one without. A captured call's plan is kept as long as the
+    graph. Nothing of it lies on the device: every call has outputs and workspace of its own, so calls on different
+    streams, or captured into different graphs, do not meet.
 
     grads: contiguous tensors on one GPU, each fp32, fp16 or bf16."""
 
@@ -36,13 +38,14 @@ class GradNormPlan:
         self.device, self.gpu = grads[0].device, grads[0].get_device()
         if self.gpu < 0:
             raise ValueError("gradients must be on a GPU")
-        self.count, self._keep = len(grads), grads
+        self.count = len(grads)
         rows = []
         for g in grads:
             code = DTYPE_CODE.get(g.dtype)
             if code is None:
                 raise TypeError(f"unsupported dtype {g.dtype}; expected float32, float16 or bfloat16")
             rows += (_ptr(g, "every gradient", self.gpu), g.numel(), code)
+        self._keep = grads, [g.untyped_storage() for g in grads]
         # i8l_grad_tensor is three 64-bit words, the dtype in the last one's lower half
         self._table = (ctypes.c_int64 * len(rows))(*rows)
         self._overlap: Optional[bool] = None      # found out by the first clipping
@@ -96,7 +99,8 @@ class GradNormPlan:
 def clip_grad_norm_(parameters: Iterable[torch.Tensor], max_norm: float, norm_type: float = 2.0,
                     grad_scale: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Clips the gradients of `parameters` (those that have one) in place to a norm of max_norm over all of them, after
-    multiplying them by grad_scale if there is one; returns their norm before the clipping."""
+    multiplying them by grad_scale if there is one; returns their norm before the clipping. It keeps nothing: where the
+    call is captured, the gradients and grad_scale are kept by the caller as long as the graph."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads = [p.grad for p in parameters if p.grad is not None]

@@ -39,3 +39,22 @@ def test_neighbours_do_not_overlap(stub, calls):  # noqa: F811
     flat, half = torch.zeros(100), torch.zeros(100, dtype=torch.bfloat16)
     stub.I8.GradNormPlan([flat[50:], flat[:50], flat[20:20], half[:1], half[1:], half[7:7]]).clip(1.0)
     assert len(calls) == 1
+
+
+@pytest.mark.parametrize("move", ["data", "set_"])
+def test_a_plan_holds_the_memory_that_it_names(stub, calls, move):  # noqa: F811
+    """A gradient that is given other memory later: the plan's calls go on with what it was laid out for, which nobody
+    else has been given meanwhile."""
+    g = [torch.zeros(300), torch.zeros(40)]
+    plan = stub.I8.GradNormPlan(g)
+    memory = g[0].untyped_storage()._weak_ref()
+    address = g[0].data_ptr()
+    if move == "data":
+        g[0].data = torch.ones(300)
+    else:
+        g[0].set_(torch.ones(300))
+    plan.norm(1.0)
+    assert calls[-1][0][0] == address and not torch.UntypedStorage._expired(memory)
+    del plan
+    calls.clear()
+    assert torch.UntypedStorage._expired(memory)
