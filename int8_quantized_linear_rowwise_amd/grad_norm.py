@@ -52,6 +52,10 @@ class GradNormPlan:
         assert ctypes.sizeof(GradTensor) == 24
         self.workspace_bytes = lib.int8_grad_norm_workspace_bytes(self._table, self.count)
 
+    def __reduce__(self):
+        """A copy is laid out for the copied gradients, not for the addresses of these."""
+        return GradNormPlan, (list(self._keep[0]),)
+
     def _overlapping(self) -> bool:
         t, end = self._table, 0
         for p, n, code in sorted(zip(t[::3], t[1::3], t[2::3])):

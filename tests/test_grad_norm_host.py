@@ -58,3 +58,19 @@ def test_a_plan_holds_the_memory_that_it_names(stub, calls, move):  # noqa: F811
     del plan
     calls.clear()
     assert torch.UntypedStorage._expired(memory)
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "copy", "pickle"])
+def test_a_copied_plan_names_its_own_gradients(stub, calls, how):  # noqa: F811
+    import copy
+    import pickle
+    g = [torch.arange(300.0), torch.zeros(40)]
+    plan = stub.I8.GradNormPlan(g)
+    plan.norm(1.0)
+    other = {"deepcopy": copy.deepcopy, "copy": copy.copy,
+             "pickle": lambda p: pickle.loads(pickle.dumps(p))}[how](plan)
+    other.norm(1.0)
+    mine, theirs = calls[-2][0], calls[-1][0]
+    held = other._keep[0]
+    assert [theirs[0], theirs[3]] == [t.data_ptr() for t in held] and torch.equal(held[0], g[0])
+    assert (mine[0] == theirs[0]) == (how == "copy")
