@@ -220,7 +220,7 @@ def _sum_of_rows(gX, position):
     """Each token's rows added up; more of them than one sum takes in fp32, rounded once at the end."""
     k = position.shape[1]
     if k <= MAX_CHOICES:
-        return expert_combine(gX, position)
+        return expert_combine(gX, position.contiguous())
     rows, total = gX.float(), None
     for j in range(0, k, MAX_CHOICES):
         total = expert_combine(rows, position[:, j:j + MAX_CHOICES].contiguous(), base=total, out=total)

@@ -69,3 +69,14 @@ def test_token_gradient_takes_any_number_of_choices(stub, L, monkeypatch, k, sum
     assert [n for n, _ in calls] == ["int8_expert_forward", "int8_expert_backward"] + ["int8_expert_combine"] * sums
     took = [a[8] for n, a in calls if n == "int8_expert_combine"]
     assert sum(took) == k and max(took) <= 64 and x.grad.dtype == x.dtype
+
+
+def test_token_gradient_takes_positions_of_any_layout(stub, L, monkeypatch):  # noqa: F811
+    """A slice of the positions, which the forward takes, is no reason to refuse the gradient."""
+    for name in ("int8_expert_forward", "int8_expert_backward", "int8_expert_combine"):
+        monkeypatch.setattr(L.lib, name, lambda *a: 0)
+    x = torch.zeros((8, 32), requires_grad=True)
+    CB, SCB = torch.zeros((2, 16, 32), dtype=torch.int8), torch.zeros((2, 16))
+    off, rows = torch.zeros(3, dtype=torch.int32), torch.zeros(16, dtype=torch.int32)
+    for pos in (torch.zeros((8, 4), dtype=torch.int32)[:, ::2], torch.zeros((2, 8), dtype=torch.int32).t()):
+        stub.I8.Int8ExpertsFunction.apply(x, CB, SCB, off, None, rows, pos, 6.0).sum().backward()
