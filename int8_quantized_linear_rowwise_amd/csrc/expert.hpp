@@ -28,7 +28,11 @@ __device__ __forceinline__ int expert_of(const ExpertSegs& S, int s) {
 // of eight experts to one XCD of eight (8192 rows, 4096 -> 11008, bf16: 303 us
 // against 117, the gradient 502 against 142). More: segment s owns the slots from start(s) / tm + s on; its
 // ceil(len / tm) tiles never reach the next segment's, so a search 64 wide finds
-// the segment in two or three loads, and slots that hold no tile end at once.
+// the segment in two or three loads, and slots that hold no tile end at once. There
+// the tiles of rows without an expert stay in the rows' order and the empty slots
+// count as tiles: 4096 tokens, eight of 255 experts against eight of 256, 2048 ->
+// 1408, bf16: 266 us against 270, gradient 394 against 431, but on a rank that holds
+// an eighth of them 90 against 220 and 108 against 370.
 struct ExpertTile {
   int r0, r1, expert;   // rows [r0, r1), none where r1 <= r0; expert -1: rows of zeros
 };

@@ -9,8 +9,16 @@
 // weights on the matrix core's row side), so that a lane owns four
 // consecutive features of one row.
 //
-// Two kernels. Few rows an expert: bound by reading the weights once. Many:
-// bound by the matrix cores as the projection's kernel is, at its rate.
+// Four forms, taken in this order (the sizes on both sides of each rule are at the
+// forms):
+//   k_expert_fwd_tiny    up to 4 tokens with few rows an expert, K up to 4096 in whole
+//                        words: quantized in the same launch
+//   k_expert_fwd_thin    few rows an expert (few_rows), or K below 16: tiles of 16 x 16,
+//                        bound by reading the weights once
+//   k_expert_fwd_short   K up to 512, or up to 1024 where every compute unit gets a
+//                        tile: 128 x 128, three workgroups a compute unit
+//   k_expert_fwd         all others: 256 x 256, bound by the matrix cores as the
+//                        projection's kernel is, at its rate
 #include <type_traits>
 
 #include "expert.hpp"
@@ -545,6 +553,9 @@ __global__ __launch_bounds__(256, AL == 1 ? 4 : 8) void k_expert_fwd_thin(Expert
 // weights are on their way: one launch, and nothing to wait for between two. The
 // same flags, scales, codes and outlier values as the quantizer's.
 // One token of two 4096 -> 11008 experts, bf16: 20 us against 26 in two launches.
+// Contractions past 4096 are more than a thread's two pieces of a token: they take
+// the launches above (11008 -> 4096: 30 to 37 us for one token, 68 for four; up to 8192
+// the quantizer is one launch, past that two).
 constexpr int EQ_TOKENS = 4, EQ_COLS = 4096, EQ_LIST = 256;
 template <int DT, int TM>      // TM: 1 or EQ_TOKENS, at least T
 __global__ __launch_bounds__(256, TM == 1 ? 6 : 4) void k_expert_fwd_tiny(

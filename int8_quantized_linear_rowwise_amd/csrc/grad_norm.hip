@@ -11,8 +11,10 @@
 // Bound by memory. The list of tensors travels in the kernels' arguments and
 // is put into LDS by every workgroup, so a call needs no table on the device:
 // nothing to lay out, nothing to keep between calls. The norm of 202 M
-// bf16 values takes 66 us and 4.6 to add the workgroups' sums (6.1 TB/s), clipping
-// 20 M in 224 tensors 11 + 15 us (3.6 and 5.3 TB/s).
+// bf16 values takes 67 us and 4.8 to add the workgroups' sums (6.0 TB/s). Clipping
+// 40 M bf16 values of 448 tensors: launches of 280 tensors with 18 M values and of
+// 168 with 22 M, 10.0 and 10.8 us for their sums (3.7 and 4.0 TB/s), 3.6 to add them
+// up, 15.1 and 15.4 for the scaling (4.9 and 5.6 TB/s).
 #include <type_traits>
 
 #include "common.hpp"

@@ -5,7 +5,7 @@ Binding of int8_expert_* (include/int8lin.h), autograd functions and a module.
     ids, gate = ...                                    # (T, k): each token's experts and their weights
     off, token, position = expert_sort(ids, E)
     h = experts(x, off, rows=token, position=position)     # Int8Experts: (T, K) -> (T k, N), sorted by expert
-    y = ExpertCombineFunction.apply(h, position, gate, residual, off[-1:])
+    y = ExpertCombineFunction.apply(h, position, gate, residual, None)
 """
 from __future__ import annotations
 

@@ -232,7 +232,8 @@ class AdamW(torch.optim.Optimizer):
                   grad_scale: Optional[torch.Tensor] = None):
         """(norm, factor, found_inf) over the gradients of all groups, as GradNormPlan.norm: `step` takes the factor as
         its grad_scale, which clips without a pass of its own, and found_inf. There has to be a gradient, and all of
-        them on one GPU."""
+        them on one GPU. The list is laid out at every call (0.24 ms of host time for 448 tensors; a GradNormPlan over
+        gradients that stay in place is laid out once)."""
         grads = [p.grad for group in self.param_groups for p in group["params"] if p.grad is not None]
         plan = GradNormPlan(grads)
         if _capturing(plan.gpu):   # a graph's replays read these very gradients and the scale
