@@ -162,3 +162,15 @@ def test_any_positions_replayed(I8):
         here = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(here, there)), kind
+
+
+@pytest.mark.parametrize("T,N", [(1 << 24, 1), ((1 << 20) + 3, 2048)])
+def test_any_positions_of_very_many_tokens(I8, T, N):
+    """The most tokens there can be, and more workgroups than one axis of the grid is given; the last two tokens name
+    one row, so that the first token's row is named by none."""
+    pos = torch.arange(T, dtype=torch.int32, device=DEV).view(T, 1).flip(0)
+    pos[-1] = 1
+    G = torch.ones((T, N), dtype=torch.bfloat16, device=DEV)
+    gate = torch.full((T, 1), 0.5, device=DEV)
+    gY, none = I8.expert_combine_backward(G, pos, gate, rows=T, with_grad_gate=False, any_positions=True)
+    assert none is None and (gY[0] == 0).all() and (gY[1] == 1).all() and bool((gY[2:] == 0.5).all())
