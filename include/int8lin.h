@@ -500,6 +500,9 @@ int int8_expert_sort(const void* experts, int id_bytes, int64_t T, int64_t k, in
  * CB: n_experts x N x K int8, SCB: n_experts x N fp32 (int8_quantize_rowwise of
  * the n_experts N rows, tau off). rows: R int32 on the device; a value outside
  * [0, T) makes a row of zeros, and a token may be named any number of times.
+ * Tokens that no row names count for the outlier columns too: their values, like
+ * all of X, have to be finite in fp16 (a NaN hides its column's outliers, an
+ * infinity makes its column one; no other row's codes depend on either).
  * out: R x N of `dtype`, no part of an input. K <= I8L_MAX_K, N <= I8L_MAX_COLS,
  * T, R <= 2^24, n_seg, n_experts <= 65536, else I8L_ESHAPE. The size query takes
  * the call's own sizes and looks at no more of CB than its address; it returns 0
@@ -537,9 +540,9 @@ int int8_expert_backward(const void* G, int dtype, int64_t R, int64_t N, const i
  * k <= 64, N <= I8L_MAX_COLS, T, R <= 2^24, else I8L_ESHAPE.
  * With dtype | I8L_ANY_POSITIONS the positions may be any: a row that several
  * name gets the sum of their terms, in the order of the choices (fp32, rounded
- * once), a row that none names 0. n_rows is then scratch of 2 R int32 that the
- * call writes (2 R words at any 4-byte address, I8L_EINVAL where it is missing
- * and grad_Y is asked for); sums are the same on every run. */
+ * once, the same on every run), a row that none names 0. n_rows is then scratch
+ * that the call writes, 2 R int32 on a 4-byte border; where it is missing and
+ * grad_Y is asked for: I8L_EINVAL. */
 #define I8L_ANY_POSITIONS 256
 
 int int8_expert_combine(const void* Y, int dtype, int64_t R, int64_t N, const int32_t* position, const float* gate,

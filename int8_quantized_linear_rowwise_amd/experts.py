@@ -79,7 +79,8 @@ def expert_forward(X: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor, seg_off
     X: T x K; CB: experts x N x K int8 and SCB: experts x N fp32 (quantize_weight of the experts' rows). seg_offsets:
     int32, segments + 1 row offsets; seg_expert: int32, each segment's expert (None: segment j uses expert j; any value
     outside [0, experts): none). rows: int32, the token of each row, any value outside [0, T) for none (None: row r is
-    token r). A row without expert or token, and every row behind the last offset, becomes 0."""
+    token r). A row without expert or token, and every row behind the last offset, becomes 0. Tokens that no row names
+    (padding) count for the outlier columns too: fill them with finite values."""
     if X.dim() != 2:
         raise ValueError("X must be 2-D (flatten leading dimensions)")
     T, K = X.shape
