@@ -501,8 +501,8 @@ int int8_expert_sort(const void* experts, int id_bytes, int64_t T, int64_t k, in
  * the n_experts N rows, tau off). rows: R int32 on the device; a value outside
  * [0, T) makes a row of zeros, and a token may be named any number of times.
  * Tokens that no row names count for the outlier columns too: their values, like
- * all of X, have to be finite in fp16 (a NaN hides its column's outliers, an
- * infinity makes its column one; no other row's codes depend on either).
+ * all of X, have to be finite in fp16 (a NaN hides the outliers of its column in
+ * all tokens, an infinity makes its column one).
  * out: R x N of `dtype`, no part of an input. K <= I8L_MAX_K, N <= I8L_MAX_COLS,
  * T, R <= 2^24, n_seg, n_experts <= 65536, else I8L_ESHAPE. The size query takes
  * the call's own sizes and looks at no more of CB than its address; it returns 0
